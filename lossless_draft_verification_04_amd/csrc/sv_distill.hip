@@ -1,0 +1,369 @@
+// sv_distill.hip -- distillation from a teacher's top logits on gfx950: the
+// loss KL(p || q) over the teacher's k tokens I and one class for all others,
+// and its gradient.
+//
+//   p_i = exp(t_i / T) / Z, p_0 = exp(rest) / Z, Z = sum_i exp(t_i / T) + exp(rest)
+//   q = softmax(z / T), q_0 = sum_{v not in I} q_v
+//   loss = sum_i p_i log(p_i / q_i) + p_0 log(p_0 / q_0)
+//   dz_v = (g / T) (q_v - p_v) in I, (g / T) q_v (1 - p_0 / q_0) elsewhere
+//
+// Both passes stream V logits a row and are bound by memory; an exponential
+// a logit (a quarter-rate instruction) and the conversion of bf16 pairs are
+// most of the arithmetic.
+//
+// Everything of size k is computed in 64 bits: the loss is a difference of
+// logarithms near 10 that may be 1e-2 itself.  The row's sums are 32-bit per
+// thread and 64-bit across threads.  The sum outside I is formed without the
+// tokens of I (a byte of LDS per 16-byte vector marks them), so q_0 keeps its
+// digits where I holds nearly everything, and the error that the sum's
+// elements share (that of log2(e) / T in 32 bits) enters the loss only times
+// q_0 - p_0.
+#include "sv_draft.h"
+#include "sv_topmass.hpp"
+
+namespace sv {
+
+constexpr int kDNT = 256;
+constexpr int kDU = 4;     // vectors in flight per thread
+constexpr int kTeach = SV_MAX_TEACHER / kWave;  // teacher tokens per lane of the finishing wave
+static_assert(SV_MAX_TEACHER <= kDNT, "a thread a teacher token");
+
+// A row's teacher tokens in LDS: id (-1: absent), value, the drafter's logit.
+struct Teacher {
+  int32_t id[SV_MAX_TEACHER];
+  float t[SV_MAX_TEACHER];
+  float z[SV_MAX_TEACHER];
+  int live;
+};
+
+// Loads them (every thread of a block of at least SV_MAX_TEACHER threads).
+// Out-of-range and repeated ids are flagged and become absent.  Returns
+// whether the row has teacher mass, in every thread.
+template <int DT>
+__device__ __forceinline__ bool load_teacher(const DistillParams& a, int r, const void* row, Teacher& s, bool report) {
+  const int i = threadIdx.x;
+  int32_t id = -1;
+  float t = kNegInf;
+  if (i < a.k) {
+    id = a.ids[(int64_t)r * a.k + i];
+    t = a.vals[(int64_t)r * a.k + i];
+  }
+  const float rest = a.rest ? a.rest[r] : kNegInf;
+  bool bad = id < -1 || id >= a.V;
+  if (bad) id = -1;
+  if (i < SV_MAX_TEACHER) s.id[i] = id;
+  if (i == 0) s.live = rest > kNegInf;
+  lds_sync();
+  bool twice = false;
+  if (id >= 0)
+    for (int j = 0; j < i; ++j) twice |= s.id[j] == id;
+  if (report && (bad || twice)) set_error(a.err, SV_DERR_TOKEN);
+  lds_sync();
+  if (twice) id = -1;
+  if (i < SV_MAX_TEACHER) {
+    s.id[i] = id;
+    s.t[i] = id >= 0 ? t : kNegInf;
+    if (id >= 0 && t > kNegInf) s.live = 1;
+    s.z[i] = id >= 0 ? load_elem<DT>(row, id) : kNegInf;
+  }
+  lds_sync();
+  return s.live != 0;
+}
+
+// The teacher's normaliser: its largest exponent m and Z relative to it.
+struct Norm {
+  double m, z;
+};
+__device__ __forceinline__ Norm wave_teacher_norm(const Teacher& s, int k, double rest, double invT, int lane) {
+  float tm = kNegInf;
+  for (int i = lane; i < k; i += kWave) tm = fmaxf(tm, s.t[i]);
+  tm = wave_fmax(tm);
+  Norm n;
+  n.m = fmax((double)tm * invT, rest);
+  double z = 0.0;
+  for (int i = lane; i < k; i += kWave)
+    if (s.t[i] > kNegInf) z += exp((double)s.t[i] * invT - n.m);
+  n.z = wave_sum(z) + exp(rest - n.m);
+  return n;
+}
+
+// The loss and the statistics of one row from the sum outside I, by one wave.
+__device__ __forceinline__ void finish_loss(const DistillParams& a, int r, const Teacher& s, const Partial& out,
+                                            int lane) {
+  const double rest = a.rest ? (double)a.rest[r] : -__builtin_huge_val();
+  const Norm n = wave_teacher_norm(s, a.k, rest, a.invT, lane);
+  float m = kNegInf;
+  for (int i = lane; i < a.k; i += kWave) m = fmaxf(m, s.z[i]);
+  m = fmaxf(wave_fmax(m), out.m);
+  if (m == kNegInf) {
+    if (lane == 0) {
+      set_error(a.err, SV_DERR_ROW);
+      a.out_loss[r] = 0.f;
+      reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+  double sum = 0.0;
+  for (int i = lane; i < a.k; i += kWave)
+    if (s.z[i] > kNegInf) sum += exp(((double)s.z[i] - (double)m) * a.invT);
+  sum = wave_sum(sum);
+  if (out.s > 0.0) sum += out.s * exp(((double)out.m - (double)m) * a.invT);
+  const double lt = n.m + log(n.z);
+  const double lq = (double)m * a.invT + log(sum);
+  double loss = 0.0;
+  for (int i = lane; i < a.k; i += kWave) {
+    const double lp = (double)s.t[i] * a.invT - lt;
+    const double p = s.t[i] > kNegInf ? exp(lp) : 0.0;
+    if (p > 0.0) loss += p * (lp - ((double)s.z[i] * a.invT - lq));
+  }
+  loss = wave_sum(loss);
+  const double p0 = exp(rest - lt);
+  if (p0 > 0.0) loss += p0 * ((rest - lt) - ((double)out.m * a.invT + log(out.s) - lq));
+  if (lane == 0) {
+    a.out_loss[r] = (float)loss;
+    reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(m, (float)sum, out.m, (float)out.s);
+  }
+}
+
+// kDU vectors of a row; tokens of I and elements past V become -inf.
+template <int DT, bool LAST>
+__device__ __forceinline__ void fold_group(const u32x4 (&d)[kDU], const uint8_t* mark, int64_t first, int64_t nv,
+                                           int64_t v0, int V, float c, Mass& acc) {
+  constexpr int E = Fmt<DT>::kPerVec;
+  float x[kDU * E];
+#pragma unroll
+  for (int u = 0; u < kDU; ++u) unpack<DT>(d[u], x + u * E);
+  uint32_t mk[kDU];
+#pragma unroll
+  for (int u = 0; u < kDU; ++u) {
+    const int64_t i = first + (int64_t)u * kDNT;
+    mk[u] = !LAST || i < nv ? mark[i] : 0xffu;
+    if (LAST && i < nv && (v0 + i + 1) * E > V) mk[u] |= 0xffu << (V - (v0 + i) * E);
+  }
+  if (mk[0] | mk[1] | mk[2] | mk[3]) {
+#pragma unroll
+    for (int u = 0; u < kDU; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if ((mk[u] >> e) & 1u) x[u * E + e] = kNegInf;
+  }
+  fold_values<kDU * E>(x, c, acc);
+}
+
+template <int DT>
+__global__ __launch_bounds__(kDNT) void distill_loss_kernel(DistillParams a) {
+  constexpr int E = Fmt<DT>::kPerVec;
+  extern __shared__ uint32_t s_mark[];  // a byte per vector of the part: its tokens in I
+  __shared__ Teacher s;
+  const int r = blockIdx.x / a.nch;
+  const int ch = blockIdx.x - r * a.nch;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = threadIdx.x / kWave;
+  const void* row = row_ptr(a.z, r, a.sb);
+  const int64_t v0 = (int64_t)ch * a.vpc;
+  const int64_t nv = (v0 + a.vpc < a.nvec ? v0 + a.vpc : a.nvec) - v0;
+  for (int i = threadIdx.x; i < (int)(nv + 3) / 4; i += kDNT) s_mark[i] = 0u;
+  if (!load_teacher<DT>(a, r, row, s, ch == 0)) {  // block-uniform, the same for all of the row's blocks
+    if (ch == 0 && threadIdx.x == 0) {
+      a.out_loss[r] = 0.f;
+      reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+  if (threadIdx.x < a.k) {
+    const int32_t id = s.id[threadIdx.x];
+    const int64_t i = (int64_t)id / E - v0;
+    if (id >= 0 && i >= 0 && i < nv) atomicOr(&s_mark[i >> 2], 1u << ((i & 3) * 8 + id % E));
+  }
+  lds_sync();
+  const uint8_t* mark = reinterpret_cast<const uint8_t*>(s_mark);
+  Mass acc;
+  {
+    const __amdgpu_buffer_rsrc_t rs = range_rsrc(static_cast<const u32x4*>(row) + v0, (uint32_t)(nv * 16));
+    // groups of kDU * kDNT vectors; the last one is masked (and may hold the row's end)
+    const int64_t full = (nv - 1) / (kDU * kDNT);
+    uint32_t off = threadIdx.x * 16u;
+    u32x4 cur[kDU];
+#pragma unroll
+    for (int u = 0; u < kDU; ++u) cur[u] = load_range(rs, off + (uint32_t)(u * kDNT * 16));
+    for (int64_t k = 0; k < full; ++k) {
+      off += kDU * kDNT * 16;
+      u32x4 nxt[kDU];
+#pragma unroll
+      for (int u = 0; u < kDU; ++u) nxt[u] = load_range(rs, off + (uint32_t)(u * kDNT * 16));
+      fold_group<DT, false>(cur, mark, k * (kDU * kDNT) + threadIdx.x, nv, v0, a.V, a.c, acc);
+#pragma unroll
+      for (int u = 0; u < kDU; ++u) cur[u] = nxt[u];
+    }
+    fold_group<DT, true>(cur, mark, full * (kDU * kDNT) + threadIdx.x, nv, v0, a.V, a.c, acc);
+  }
+  Partial out = block_mass<kDNT>(acc, a.c);
+  if (a.nch > 1) {
+    Partial* parts = static_cast<Partial*>(a.parts) + (int64_t)r * a.nch;
+    if (threadIdx.x == 0) put_partial(parts + ch, out);
+    if (!arrive_last<kDNT>(&a.cnt[r], (uint32_t)a.nch)) return;
+    if (wave == 0) {
+      float m = kNegInf;
+      for (int i = lane; i < a.nch; i += kWave) m = fmaxf(m, get_partial(parts + i).m);
+      out.m = wave_fmax(m);
+      double t = 0.0;
+      for (int i = lane; i < a.nch; i += kWave) {
+        const Partial p = get_partial(parts + i);
+        t += p.s * rescale(p.m, out.m, a.c);
+      }
+      out.s = wave_sum(t);
+      if (lane == 0) __hip_atomic_store(&a.cnt[r], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  if (wave == 0) finish_loss(a, r, s, out, lane);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient.
+// ---------------------------------------------------------------------------
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// E values as one vector of the row's type (bf16: round to nearest even).
+template <int DT>
+__device__ __forceinline__ u32x4 pack(const float* x) {
+  u32x4 d;
+  if constexpr (DT == SV_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      d[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * i], x[2 * i + 1]}, bf16x2));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = __float_as_uint(x[i]);
+  }
+  return d;
+}
+template <int DT>
+__device__ __forceinline__ void store_elem(void* row, int64_t i, float x) {
+  if constexpr (DT == SV_BF16)
+    reinterpret_cast<__bf16*>(row)[i] = (__bf16)x;
+  else
+    reinterpret_cast<float*>(row)[i] = x;
+}
+
+// What the gradient of a row needs: dz_v = each * 2^(c z_v - cm) outside I
+// (each * 2^((z_v - m) c) where cm is not finite), top[i] at token i of I.
+struct GradRow {
+  float m, cm, each;
+};
+
+// One wave: the row's factors, and (q_i - p_i) g / T in place of s.z.
+__device__ __forceinline__ GradRow wave_grad_row(const DistillParams& a, int r, Teacher& s, const float4 st, int lane) {
+  const double rest = a.rest ? (double)a.rest[r] : -__builtin_huge_val();
+  const Norm n = wave_teacher_norm(s, a.k, rest, a.invT, lane);
+  const double scale = (a.g ? (double)a.g[r] : 1.0) * a.invT;
+  const double inv = 1.0 / (double)st.y;
+  for (int i = lane; i < a.k; i += kWave) {
+    const double p = s.t[i] > kNegInf ? exp((double)s.t[i] * a.invT - n.m) / n.z : 0.0;
+    const double q = s.z[i] > kNegInf ? exp(((double)s.z[i] - (double)st.x) * a.invT) * inv : 0.0;
+    s.z[i] = (float)((q - p) * scale);
+  }
+  const double p0 = exp(rest - n.m) / n.z;
+  const double q0 = st.w > 0.f ? (double)st.w * exp(((double)st.z - (double)st.x) * a.invT) * inv : 0.0;
+  GradRow g;
+  g.m = st.x;
+  g.cm = a.c * st.x;
+  double each = p0 > 0.0 ? (q0 > 0.0 ? 1.0 - p0 / q0 : 0.0) : 1.0;
+  each *= scale * inv;
+  // 2^(c z - cm) has the shift cm, which is not quite c m
+  if (fabsf(g.cm) <= 3e38f) each *= exp2((double)g.cm - (double)a.c * (double)st.x);
+  g.each = (float)each;
+  return g;
+}
+
+template <int DT>
+__device__ __forceinline__ u32x4 grad_vec(const u32x4 d, const GradRow& g, float c) {
+  constexpr int E = Fmt<DT>::kPerVec;
+  float x[E];
+  unpack<DT>(d, x);
+  if (__builtin_expect(fabsf(g.cm) <= 3e38f, 1)) {
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = g.each * fast_exp2(__builtin_fmaf(x[e], c, -g.cm));
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) x[e] = g.each * fast_exp2((x[e] - g.m) * c);
+  }
+  return pack<DT>(x);
+}
+
+// A block per (row part): the gradient outside I streams through, then the
+// part's tokens of I are written over it.  In place this holds: the block
+// reads its tokens' logits before it writes, and no other block's.
+template <int DT>
+__global__ __launch_bounds__(kDNT) void distill_grad_kernel(DistillParams a) {
+  constexpr int E = Fmt<DT>::kPerVec;
+  __shared__ Teacher s;
+  __shared__ GradRow s_g;
+  const int r = blockIdx.x / a.nch2;
+  const int ch = blockIdx.x - r * a.nch2;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = threadIdx.x / kWave;
+  const u32x4* row = static_cast<const u32x4*>(row_ptr(a.z, r, a.sb));
+  char* out = static_cast<char*>(a.grad) + (int64_t)r * a.gb;
+  u32x4* outv = reinterpret_cast<u32x4*>(out);
+  const int64_t v0 = (int64_t)ch * a.vpc2;
+  const int64_t v1 = v0 + a.vpc2 < a.nvec ? v0 + a.vpc2 : a.nvec;
+  const int64_t nfull = a.V / E;
+  const int64_t vf = v1 < nfull ? v1 : nfull;  // whole vectors; the row's last one may be shorter
+  const float4 st = reinterpret_cast<const float4*>(a.stat)[r];
+  if (!(st.y > 0.f)) {  // no teacher mass, or no finite logit
+    for (int64_t v = v0 + threadIdx.x; v < vf; v += kDNT) outv[v] = u32x4{0u, 0u, 0u, 0u};
+    if (v1 > nfull && threadIdx.x < a.V - nfull * E) store_elem<DT>(out, nfull * E + threadIdx.x, 0.f);
+    return;
+  }
+  load_teacher<DT>(a, r, row, s, ch == 0);
+  if (wave == 0) {
+    const GradRow g = wave_grad_row(a, r, s, st, lane);
+    if (lane == 0) s_g = g;
+  }
+  lds_sync();
+  const GradRow g = s_g;
+  for (int64_t v = v0 + threadIdx.x; v < vf; v += kDU * kDNT) {
+    u32x4 d[kDU];
+#pragma unroll
+    for (int u = 0; u < kDU; ++u)
+      if (v + u * kDNT < vf) d[u] = load_vec(row, v + u * kDNT);
+#pragma unroll
+    for (int u = 0; u < kDU; ++u)
+      if (v + u * kDNT < vf) outv[v + u * kDNT] = grad_vec<DT>(d[u], g, a.c);
+  }
+  if (v1 > nfull && threadIdx.x < a.V - nfull * E) {
+    float x[E];
+    const int e = threadIdx.x;
+    const float z = load_elem<DT>(row, nfull * E + e);
+    const float arg = fabsf(g.cm) <= 3e38f ? __builtin_fmaf(z, a.c, -g.cm) : (z - g.m) * a.c;
+    store_elem<DT>(out, nfull * E + e, g.each * fast_exp2(arg));
+  }
+  __builtin_amdgcn_s_waitcnt(0);  // the stream's stores are done before any token's
+  __syncthreads();
+  if (threadIdx.x < a.k) {
+    const int32_t id = s.id[threadIdx.x];
+    if (id >= 0 && id / E >= v0 && id / E < v1) store_elem<DT>(out, id, s.z[threadIdx.x]);
+  }
+}
+
+hipError_t launch_distill_loss(const DistillParams& p, sv_dtype dt, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.R * p.nch));
+  const size_t lds = (size_t)((p.vpc + 3) / 4 * 4);
+  if (dt == SV_BF16)
+    distill_loss_kernel<SV_BF16><<<grid, dim3(kDNT), lds, s>>>(p);
+  else
+    distill_loss_kernel<SV_F32><<<grid, dim3(kDNT), lds, s>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_distill_grad(const DistillParams& p, sv_dtype dt, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.R * p.nch2));
+  if (dt == SV_BF16)
+    distill_grad_kernel<SV_BF16><<<grid, dim3(kDNT), 0, s>>>(p);
+  else
+    distill_grad_kernel<SV_F32><<<grid, dim3(kDNT), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace sv

@@ -1,0 +1,71 @@
+// sv_teacher.hip -- the verifier's top logits and the mass outside them, a
+// distillation target per row, on gfx950.
+//
+// Per row: the k largest logits (value descending, index ascending) and
+// rest = log sum over the others of exp(z / T), natural logarithm.  One read
+// of each row bounds it from below; the work beside it is one exponential and
+// about ten other operations a logit.
+//
+// One launch: a block per (row part).  The block finds its part's list and
+// the mass outside it (sv_topmass.hpp); a row in one part is written by its
+// block, otherwise the row's last block merges the parts: what a part listed
+// and the row does not is counted back into the mass.
+#include "sv_draft.h"
+#include "sv_topmass.hpp"
+
+namespace sv {
+
+constexpr int kTNT = 512;
+
+__device__ __forceinline__ void put_target(const TeacherParams& a, int r, int lane, float lv, int32_t li,
+                                           const Partial& rest) {
+  if (lane < a.k) {
+    a.out_ids[(int64_t)r * a.k + lane] = li != kNoIdx ? li : -1;
+    a.out_vals[(int64_t)r * a.k + lane] = li != kNoIdx ? lv : kNegInf;
+  }
+  if (lane == 0) a.out_rest[r] = rest.s > 0.0 ? (float)((double)rest.m * a.invT + log(rest.s)) : kNegInf;
+}
+
+template <int DT>
+__global__ __launch_bounds__(kTNT) void teacher_kernel(TeacherParams a) {
+  constexpr int E = Fmt<DT>::kPerVec;
+  const int r = blockIdx.x / a.nch;
+  const int ch = blockIdx.x - r * a.nch;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = threadIdx.x / kWave;
+  const int64_t v0 = (int64_t)ch * a.vpc;
+  const int64_t v1 = v0 + a.vpc < a.nvec ? v0 + a.vpc : a.nvec;
+  Mass own;
+  const TopPair t =
+      block_topk_mass<kTNT, E>(RowValues<DT>{row_ptr(a.logits, r, a.sb), a.V}, v0, v1, a.V, a.k, a.c, &own);
+  const Partial rest = block_mass<kTNT>(own, a.c);
+  if (a.nch == 1) {
+    if (wave == 0) put_target(a, r, lane, t.v, t.i, rest);
+    return;
+  }
+  TopEntry* lists = static_cast<TopEntry*>(a.lists) + (int64_t)r * a.nch * a.k;
+  Partial* parts = static_cast<Partial*>(a.parts) + (int64_t)r * a.nch;
+  if (wave == 0) {
+    if (lane < a.k) put_entry(lists + (int64_t)ch * a.k + lane, t.v, t.i);
+    if (lane == 0) put_partial(parts + ch, rest);
+  }
+  if (!arrive_last<kTNT>(&a.cnt[r], (uint32_t)a.nch)) return;
+  if (wave == 0) {
+    float lv;
+    int32_t li;
+    const Partial whole = wave_merge_parts(lists, parts, a.nch, a.k, a.c, lane, lv, li);
+    put_target(a, r, lane, lv, li, whole);
+    if (lane == 0) __hip_atomic_store(&a.cnt[r], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+
+hipError_t launch_teacher(const TeacherParams& p, sv_dtype dt, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.R * p.nch));
+  if (dt == SV_BF16)
+    teacher_kernel<SV_BF16><<<grid, dim3(kTNT), 0, s>>>(p);
+  else
+    teacher_kernel<SV_F32><<<grid, dim3(kTNT), 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace sv

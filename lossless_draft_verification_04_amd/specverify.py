@@ -13,6 +13,7 @@ along V and evenly spaced rows whose start addresses are 16-byte aligned
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -34,6 +35,9 @@ SV_F32, SV_BF16 = 0, 1
 (SV_OP_CHAIN, SV_OP_GREEDY, SV_OP_MULTI, SV_OP_TREE, SV_OP_FANOUT, SV_OP_CHAIN_PM, SV_OP_TREE_PM,
  SV_OP_CACHE, SV_OP_PRESTO, SV_OP_BRANCH) = range(10)
 DERR_TOKEN, DERR_TREE, DERR_FANOUT, DERR_ROW, DERR_TIMEOUT = 1, 2, 4, 8, 16
+# the drafter's side (specverify_draft.h)
+SV_DRAFT_TEACHER, SV_DRAFT_DISTILL, SV_DRAFT_BEAM, SV_DRAFT_REORDER = range(4)
+DERR_RANGE = 32
 
 _P = ctypes.c_void_p
 _i32, _i64, _u32, _u64, _f32, _f64, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64,
@@ -67,12 +71,25 @@ _SIGS = {
     "sv_read_probe": ([_P, _sz, _i32, _i32, _i32, _sz, _P, _P], _i32),
     "sv_timeline_set": ([_P, ctypes.c_uint64], _i32),
 }
-for _name, (_args, _res) in _SIGS.items():
+# entry points of specverify_draft.h
+_DRAFT_SIGS = {
+    "sv_draft_workspace_size": ([_i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)], _i32),
+    "sv_teacher_topk": ([_P, _i32, _i64, _i32, _i32, _i32, _f32, _P, _P, _P, _P, _sz, _P], _i32),
+    "sv_distill_topk": ([_P, _i32, _i64, _i32, _i32, _P, _P, _P, _i32, _f32, _P, _P, _P, _P, _i64, _P, _sz, _P],
+                        _i32),
+    "sv_distill_topk_backward": ([_P, _i32, _i64, _i32, _i32, _P, _P, _P, _i32, _f32, _P, _P, _P, _i64, _P, _sz, _P],
+                                 _i32),
+    "sv_beam_select": ([_P, _i32, _i64, _P, _P, _i32, _i32, _i32, _f32, _i32, _i32, _P, _P, _P, _P, _sz, _P], _i32),
+    "sv_beam_reorder": ([_P, ctypes.POINTER(_i64), _P, ctypes.POINTER(_i64), _P, _P, _i32, _i32, _i32, _i32, _i32,
+                         _i64, _i64, _P, _sz, _P], _i32),
+}
+for _name, (_args, _res) in (*_SIGS.items(), *_DRAFT_SIGS.items()):
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
     _fn.restype = _res
 
 EXPORTED = tuple(_SIGS)
+DRAFT_EXPORTED = tuple(_DRAFT_SIGS)
 
 
 class SpecVerifyError(RuntimeError):
@@ -91,7 +108,8 @@ class DeviceError(RuntimeError):
 
     def __init__(self, flags, what):
         names = [n for n, b in (("token", DERR_TOKEN), ("tree", DERR_TREE), ("fanout", DERR_FANOUT),
-                                ("row", DERR_ROW), ("timeout", DERR_TIMEOUT)) if flags & b]
+                                ("row", DERR_ROW), ("timeout", DERR_TIMEOUT),
+                                ("range", DERR_RANGE)) if flags & b]
         super().__init__(f"{what}: device error word {flags} ({', '.join(names)}); outputs of the call are invalid")
         self.flags = flags
 
@@ -446,3 +464,208 @@ def sv_geometric_fanout(F0, a_p, r, K, capped_last=False):
     if s < 0:
         raise SpecVerifyError(SV_EINVAL, "sv_geometric_fanout")
     return list(out)
+
+
+# ---------------------------------------------------------------------------
+# The drafter's side (specverify_draft.h).  Tensors of one call are on one
+# device, which need not be the current one; the call runs on that device's
+# current stream.  The default workspace is the device's: calls that overlap
+# in time on several streams, and graphs that may be replayed together, take a
+# zero-filled one each (workspace=, a uint8 tensor of draft_workspace_size
+# bytes).
+# ---------------------------------------------------------------------------
+
+
+@functools.lru_cache(maxsize=1024)
+def draft_workspace_size(op, dt, rows, W, V, k) -> int:
+    n = _sz(0)
+    _check(_lib.sv_draft_workspace_size(op, dt, rows, W, V, k, ctypes.byref(n)), "sv_draft_workspace_size")
+    return n.value
+
+
+def _one_device(what, first, *others):
+    if not first.is_cuda:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: want tensors on the GPU, got {first.device}")
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise SpecVerifyError(SV_EINVAL, f"{what}: tensors on {first.device} and {t.device}")
+    return first.device
+
+
+def _call(dev, fn, what, *args):
+    """One launch with `dev` current, on its current stream."""
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(dev)), what)
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, _stream(dev)), what)
+
+
+def _f32_tensor(t, shape, what):
+    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise SpecVerifyError(SV_EINVAL, f"{what}: want contiguous float32 {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def _rows_2d(t, what):
+    if t.dim() != 2:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: want [rows, V], got {tuple(t.shape)}")
+    return t.shape
+
+
+def sv_teacher_topk(logits, k, T, workspace=None):
+    """The k largest logits of each row and the logarithm of the mass outside them at temperature T.
+    logits [R, V] -> dict(ids [R, k] int32, vals [R, k], rest [R])."""
+    R, V = _rows_2d(logits, "logits")
+    dt, k = _dtype_code(logits), int(k)
+    dev = _one_device("sv_teacher_topk", logits, workspace)
+    ws = workspace if workspace is not None else Workspace.get(
+        dev, draft_workspace_size(SV_DRAFT_TEACHER, dt, R, 1, V, k))
+    out = dict(ids=torch.empty(R, k, dtype=torch.int32, device=dev),
+               vals=torch.empty(R, k, dtype=torch.float32, device=dev),
+               rest=torch.empty(R, dtype=torch.float32, device=dev))
+    _call(dev, _lib.sv_teacher_topk, "sv_teacher_topk", _ptr(logits), dt, _row_stride(logits, "logits"), R, V, k,
+          float(T), _ptr(out["ids"]), _ptr(out["vals"]), _ptr(out["rest"]), _ptr(ws), ws.numel())
+    _checked(dev, "sv_teacher_topk", workspace)
+    return out
+
+
+def _distill_args(what, z, ids, vals, rest, grad_loss, grad, workspace):
+    R, V = _rows_2d(z, "z")
+    if ids.dim() != 2 or ids.shape[0] != R:
+        raise SpecVerifyError(SV_EINVAL, f"ids: want [{R}, k], got {tuple(ids.shape)}")
+    k = ids.shape[1]
+    _i32_tensor(ids, (R, k), "ids")
+    _f32_tensor(vals, (R, k), "vals")
+    if rest is not None:
+        _f32_tensor(rest, (R,), "rest")
+    if grad_loss is not None:
+        _f32_tensor(grad_loss, (R,), "grad_loss")
+    if grad is not None and (tuple(grad.shape) != (R, V) or grad.dtype != z.dtype):
+        raise SpecVerifyError(SV_EINVAL, f"grad: want {z.dtype} {(R, V)}, got {grad.dtype} {tuple(grad.shape)}")
+    dt = _dtype_code(z)
+    dev = _one_device(what, z, ids, vals, rest, grad_loss, grad, workspace)
+    ws = workspace if workspace is not None else Workspace.get(
+        dev, draft_workspace_size(SV_DRAFT_DISTILL, dt, R, 1, V, k))
+    return R, V, k, dt, dev, ws
+
+
+def _grad_rows(z, R, V):
+    """Gradient rows beside z, 16-byte aligned (a view of padded rows where V needs it)."""
+    per = 16 // z.element_size()
+    return torch.empty(R, -(-V // per) * per, dtype=z.dtype, device=z.device)[:, :V]
+
+
+def sv_distill_topk(z, ids, vals, T, rest=None, grad_loss=None, want_grad=False, grad=None, workspace=None):
+    """KL divergence of a drafter's rows from a teacher's top logits (sv_teacher_topk's ids, vals and rest; rest None:
+    renormalised over the ids), and with want_grad its gradient, times grad_loss [R] (None: 1).
+    z [R, V], ids, vals [R, k] -> dict(loss [R], stat [R, 4] for the backward pass, grad [R, V] or None).
+    grad: where to write the gradient (z itself: in place); hand it on with z.backward(out["grad"])."""
+    R, V, k, dt, dev, ws = _distill_args("sv_distill_topk", z, ids, vals, rest, grad_loss, grad, workspace)
+    if grad is None and want_grad:
+        grad = _grad_rows(z, R, V)
+    out = dict(loss=torch.empty(R, dtype=torch.float32, device=dev),
+               stat=torch.empty(R, 4, dtype=torch.float32, device=dev), grad=grad)
+    _call(dev, _lib.sv_distill_topk, "sv_distill_topk", _ptr(z), dt, _row_stride(z, "z"), R, V, _ptr(ids), _ptr(vals),
+          _ptr(rest), k, float(T), _ptr(grad_loss), _ptr(out["loss"]), _ptr(out["stat"]), _ptr(grad),
+          _row_stride(grad, "grad") if grad is not None else 0, _ptr(ws), ws.numel())
+    _checked(dev, "sv_distill_topk", workspace)
+    return out
+
+
+def sv_distill_topk_backward(z, ids, vals, stat, T, rest=None, grad_loss=None, grad=None, workspace=None):
+    """The gradient of sv_distill_topk from its stat: [R, V] of z's type (grad: where to write it; z itself: in place)."""
+    R, V, k, dt, dev, ws = _distill_args("sv_distill_topk_backward", z, ids, vals, rest, grad_loss, grad, workspace)
+    _f32_tensor(stat, (R, 4), "stat")
+    _one_device("sv_distill_topk_backward", z, stat)
+    if grad is None:
+        grad = _grad_rows(z, R, V)
+    _call(dev, _lib.sv_distill_topk_backward, "sv_distill_topk_backward", _ptr(z), dt, _row_stride(z, "z"), R, V,
+          _ptr(ids), _ptr(vals), _ptr(rest), k, float(T), _ptr(stat), _ptr(grad_loss), _ptr(grad),
+          _row_stride(grad, "grad"), _ptr(ws), ws.numel())
+    _checked(dev, "sv_distill_topk_backward", workspace)
+    return grad
+
+
+def sv_beam_select(logits, scores, N, T=1.0, finished=None, pad_tok=0, workspace=None):
+    """One step of beam search.  logits [B, W, V], scores [B, W] float32, finished [B, W] int32 or None
+    -> dict(beam, tok [B, N] int32, score [B, N])."""
+    if logits.dim() != 3:
+        raise SpecVerifyError(SV_EINVAL, f"logits: want [B, W, V], got {tuple(logits.shape)}")
+    B, W, V = logits.shape
+    _f32_tensor(scores, (B, W), "scores")
+    if finished is not None:
+        _i32_tensor(finished, (B, W), "finished")
+    dt, N, pad = _dtype_code(logits), int(N), int(pad_tok)
+    if not -(1 << 31) <= pad < 1 << 31:
+        raise SpecVerifyError(SV_EINVAL, f"pad_tok {pad} outside int32")
+    dev = _one_device("sv_beam_select", logits, scores, finished, workspace)
+    ws = workspace if workspace is not None else Workspace.get(
+        dev, draft_workspace_size(SV_DRAFT_BEAM, dt, B, W, V, N))
+    out = dict(beam=torch.empty(B, N, dtype=torch.int32, device=dev),
+               tok=torch.empty(B, N, dtype=torch.int32, device=dev),
+               score=torch.empty(B, N, dtype=torch.float32, device=dev))
+    _call(dev, _lib.sv_beam_select, "sv_beam_select", _ptr(logits), dt, _row_stride(logits, "logits"), _ptr(scores),
+          _ptr(finished), B, W, V, float(T), pad, N, _ptr(out["beam"]), _ptr(out["tok"]), _ptr(out["score"]), _ptr(ws),
+          ws.numel())
+    _checked(dev, "sv_beam_select", workspace)
+    return out
+
+
+def _state_layout(t, pos_dim, what):
+    """(L, B, beams, H, S), position bytes and the strides in bytes of a state [L, B, beams, ...]."""
+    shape, st, es = t.shape, t.stride(), t.element_size()
+    if t.dim() < 3:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: want [L, B, beams, ...], got {tuple(shape)}")
+    p = t.dim() if pos_dim is None else int(pos_dim)
+    if pos_dim is not None and not 3 <= p < t.dim():
+        raise SpecVerifyError(SV_EINVAL, f"{what}: pos_dim {pos_dim} of a state of {t.dim()} dimensions")
+    first = 3 if pos_dim is None else p  # dimensions from here on are adjacent in memory
+    run = 1
+    for ax in range(t.dim() - 1, first - 1, -1):
+        if shape[ax] > 1 and st[ax] != run:
+            raise SpecVerifyError(SV_EINVAL, f"{what}: the values of a position and the positions must be adjacent")
+        run *= shape[ax]
+    S = 1 if pos_dim is None else shape[p]
+    H, sh = 1, 0
+    for ax in range(first - 1, 2, -1):  # segments: evenly spaced
+        if shape[ax] == 1:
+            continue
+        if H > 1 and st[ax] != sh * H:
+            raise SpecVerifyError(SV_EINVAL, f"{what}: the dimensions between beams and positions must be evenly spaced")
+        sh = st[ax] if H == 1 else sh
+        H *= shape[ax]
+    pos = (run // S if S else 1) * es
+    return (shape[0], shape[1], shape[2], H, S, pos), (_i64 * 4)(st[0] * es, st[1] * es, st[2] * es, sh * es)
+
+
+def sv_beam_reorder(state, parent, pos_dim=None, lens=None, out=None, workspace=None):
+    """The beams' states after a selection: out[l, b, n] = state[l, b, parent[b, n]] (parent -1: left as it is).
+    state [L, B, W, ...] of any type, parent [B, N] int32; pos_dim names the dimension of the positions, of which only
+    the first lens[b] ([B] int32) move; between the beams and the positions may stand heads, after them a position's
+    values.  out [L, B, N, ...] apart from state, or None: in place (N <= W).  Returns out, or state."""
+    if lens is not None and pos_dim is None:
+        raise SpecVerifyError(SV_EINVAL, "lens: want pos_dim with it")
+    dst = state if out is None else out
+    if dst.dim() != state.dim() or dst.dtype != state.dtype:
+        raise SpecVerifyError(SV_EINVAL, f"out: want {state.dtype} of {state.dim()} dimensions")
+    (L, B, W, H, S, pos), ss = _state_layout(state, pos_dim, "state")
+    (_, _, Nd, Hd, Sd, posd), ds = _state_layout(dst, pos_dim, "out")
+    if parent.dim() != 2:
+        raise SpecVerifyError(SV_EINVAL, f"parent: want [B, N], got {tuple(parent.shape)}")
+    N = parent.shape[1]
+    _i32_tensor(parent, (B, N), "parent")
+    if lens is not None:
+        _i32_tensor(lens, (B,), "lens")
+    if out is None:
+        if N > W:
+            raise SpecVerifyError(SV_EINVAL, f"parent: {N} beams in place of {W}")
+    elif Nd != N or dst.shape[:2] != state.shape[:2] or dst.shape[3:] != state.shape[3:]:
+        raise SpecVerifyError(SV_EINVAL, f"out: shape {tuple(dst.shape)} for {N} beams of {tuple(state.shape)}")
+    dev = _one_device("sv_beam_reorder", state, dst, parent, lens, workspace)
+    ws = workspace if workspace is not None else Workspace.get(
+        dev, draft_workspace_size(SV_DRAFT_REORDER, 0, 0, 0, 0, 0))
+    _call(dev, _lib.sv_beam_reorder, "sv_beam_reorder", _ptr(state), ss, _ptr(dst), ds, _ptr(parent), _ptr(lens), L, B,
+          W, N, H, S, pos, _ptr(ws), ws.numel())
+    _checked(dev, "sv_beam_reorder", workspace)
+    return dst

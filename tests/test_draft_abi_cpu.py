@@ -1,0 +1,183 @@
+"""The drafter-side C ABI without a GPU: exported names, workspace sizes, and refusals before any HIP call (pointers are
+fake addresses that are never read)."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+from lossless_draft_verification_04_amd import specverify as svx
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+L = svx._lib
+P = ctypes.c_void_p
+A, A2, A3, MIS, WS = P(0x10000), P(0x8000000), P(0x4000000), P(0x10002), P(0x40000)
+BIG = 1 << 30
+
+
+def test_every_declared_function_is_exported():
+    text = open(os.path.join(ROOT, "include", "specverify_draft.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = set(re.findall(r"\b(sv_[a-z_]+)\s*\(", text))
+    assert names == set(svx.DRAFT_EXPORTED)
+    for n in names:
+        assert hasattr(L, n)
+
+
+def size(op, dt=1, rows=8, W=2, V=1000, k=8):
+    n = ctypes.c_size_t(0)
+    return L.sv_draft_workspace_size(op, dt, rows, W, V, k, ctypes.byref(n)), n.value
+
+
+def test_workspace_sizes():
+    for op in range(4):
+        st, n = size(op)
+        assert st == svx.SV_OK and n % 256 == 0 and n >= 256 + 65536 * 4
+    assert size(4)[0] == svx.SV_EINVAL and size(-1)[0] == svx.SV_EINVAL
+    assert size(0, k=65)[0] == svx.SV_EUNSUPPORTED and size(0, k=0)[0] == svx.SV_EINVAL
+    assert size(1, k=256)[0] == svx.SV_OK and size(1, k=257)[0] == svx.SV_EUNSUPPORTED
+    assert size(2, W=65)[0] == svx.SV_EUNSUPPORTED and size(2, rows=1025, W=64)[0] == svx.SV_EUNSUPPORTED
+    assert size(0, rows=65537)[0] == svx.SV_EUNSUPPORTED and size(1, rows=-1)[0] == svx.SV_EINVAL
+    assert size(0, V=(1 << 24) + 1)[0] == svx.SV_EUNSUPPORTED and size(2, V=0)[0] == svx.SV_EINVAL
+    assert size(1, dt=9)[0] == svx.SV_EDTYPE
+    assert L.sv_draft_workspace_size(0, 1, 1, 1, 10, 1, None) == svx.SV_EINVAL
+    assert size(1, rows=65536, V=1 << 24, k=256)[0] == svx.SV_OK
+
+
+def rows_call(fn):
+    """Common refusals of an entry point over logit rows: fn(z=, dt=, s=, R=, V=, T=, ws=, wsb=)."""
+    assert fn(dt=7) == svx.SV_EDTYPE and fn(R=-1) == svx.SV_EINVAL and fn(V=0) == svx.SV_EINVAL
+    assert fn(R=65537) == svx.SV_EUNSUPPORTED and fn(V=(1 << 24) + 1) == svx.SV_EUNSUPPORTED
+    for T in (0.0, -1.0, float("inf"), float("nan"), 1e-45):
+        assert fn(T=T) == svx.SV_EINVAL, T
+    assert fn(z=None) == svx.SV_EINVAL and fn(z=MIS) == svx.SV_EALIGN
+    assert fn(s=999) == svx.SV_EINVAL and fn(s=1004) == svx.SV_EALIGN
+    assert fn(ws=None) == svx.SV_EWORKSPACE and fn(wsb=1024) == svx.SV_EWORKSPACE
+    assert fn(ws=P(0x40010)) == svx.SV_EALIGN
+    assert fn(R=0) == svx.SV_OK  # nothing enqueued
+
+
+def test_teacher_argument_checks():
+    def f(z=A, dt=1, s=1024, R=4, V=1000, k=8, T=1.0, ids=A, vals=A, rest=A, ws=WS, wsb=BIG):
+        return L.sv_teacher_topk(z, dt, s, R, V, k, T, ids, vals, rest, ws, wsb, None)
+
+    rows_call(f)
+    assert f(k=0) == svx.SV_EINVAL and f(k=65) == svx.SV_EUNSUPPORTED
+    assert f(ids=None) == svx.SV_EINVAL and f(vals=None) == svx.SV_EINVAL and f(rest=None) == svx.SV_EINVAL
+
+
+def test_distill_argument_checks():
+    def f(z=A, dt=1, s=1024, R=4, V=1000, ids=A, vals=A, k=8, T=1.0, loss=A, stat=A, grad=None, gs=0, ws=WS, wsb=BIG):
+        return L.sv_distill_topk(z, dt, s, R, V, ids, vals, None, k, T, None, loss, stat, grad, gs, ws, wsb, None)
+
+    rows_call(f)
+    assert f(k=0) == svx.SV_EINVAL and f(k=257) == svx.SV_EUNSUPPORTED
+    for name in ("ids", "vals", "loss", "stat"):
+        assert f(**{name: None}) == svx.SV_EINVAL, name
+    assert f(stat=P(0x10008)) == svx.SV_EALIGN
+
+    def b(z=A, dt=1, s=1024, R=4, V=1000, ids=A, vals=A, k=8, T=1.0, stat=A, grad=A2, gs=1024, ws=WS, wsb=BIG):
+        return L.sv_distill_topk_backward(z, dt, s, R, V, ids, vals, None, k, T, stat, None, grad, gs, ws, wsb, None)
+
+    rows_call(b)
+    for name in ("ids", "vals", "stat", "grad"):
+        assert b(**{name: None}) == svx.SV_EINVAL, name
+    assert b(stat=P(0x10004)) == svx.SV_EALIGN
+    for call in (lambda **kw: f(**{"gs": 1024, **kw}), b):
+        assert call(grad=MIS) == svx.SV_EALIGN
+        assert call(grad=A2, gs=999) == svx.SV_EINVAL and call(grad=A2, gs=1004) == svx.SV_EALIGN
+        # overlapping z: neither in place nor apart
+        assert call(grad=P(0x10000 + 2048)) == svx.SV_EINVAL
+        assert call(grad=P(0x10000 - 2048)) == svx.SV_EINVAL
+        assert call(grad=A, gs=2048) == svx.SV_EINVAL
+
+
+def test_beam_select_argument_checks():
+    def f(z=A, dt=1, s=1024, R=4, W=2, V=1000, T=1.0, N=4, sc=A, beam=A, tok=A, score=A, ws=WS, wsb=BIG):
+        return L.sv_beam_select(z, dt, s, sc, None, R, W, V, T, 0, N, beam, tok, score, ws, wsb, None)
+
+    rows_call(f)
+    assert f(W=0) == svx.SV_EINVAL and f(W=65) == svx.SV_EUNSUPPORTED and f(R=2000, W=64) == svx.SV_EUNSUPPORTED
+    assert f(N=0) == svx.SV_EINVAL and f(N=65) == svx.SV_EUNSUPPORTED
+    for name in ("sc", "beam", "tok", "score"):
+        assert f(**{name: None}) == svx.SV_EINVAL, name
+
+
+def strides(*v):
+    return (ctypes.c_int64 * 4)(*v)
+
+
+def test_beam_reorder_argument_checks():
+    # L=2, B=3, W=N=4, H=2, S=16 positions of 32 bytes
+    base = (12288, 4096, 1024, 512)
+
+    def f(src=A, ss=base, dst=A2, ds=base, parent=A3, L_=2, B=3, W=4, N=4, H=2, S=16, pos=32, ws=WS, wsb=BIG):
+        return L.sv_beam_reorder(src, strides(*ss), dst, strides(*ds), parent, None, L_, B, W, N, H, S, pos, ws, wsb,
+                                 None)
+
+    for name, v in (("L_", -1), ("B", -1), ("W", 0), ("N", 0), ("H", -1), ("S", -1), ("pos", 0)):
+        assert f(**{name: v}) == svx.SV_EINVAL, name
+    assert f(W=65) == svx.SV_EUNSUPPORTED and f(N=65) == svx.SV_EUNSUPPORTED and f(S=1 << 31) == svx.SV_EUNSUPPORTED
+    assert f(S=(1 << 31) - 1, pos=1 << 40) == svx.SV_EUNSUPPORTED
+    for name in ("src", "dst", "parent"):
+        assert f(**{name: None}) == svx.SV_EINVAL, name
+    assert L.sv_beam_reorder(A, None, A2, strides(*base), A3, None, 1, 1, 1, 1, 1, 1, 1, WS, BIG, None) == svx.SV_EINVAL
+    assert f(ss=(12288, 4096, -1024, 512)) == svx.SV_EINVAL
+    assert f(ds=(12288, 4096, 0, 512)) == svx.SV_EINVAL      # beams on top of each other
+    assert f(ds=(12288, 4096, 1024, 256)) == svx.SV_EINVAL   # segments that overlap
+    assert f(dst=P(0x10000 + 512)) == svx.SV_EINVAL          # over src, not in place
+    assert f(dst=A, ds=(16384, 4096, 1024, 512)) == svx.SV_EINVAL
+    assert f(dst=A, N=5) == svx.SV_EINVAL                    # in place with more beams than there are
+    assert f(ws=None) == svx.SV_EWORKSPACE and f(wsb=64) == svx.SV_EWORKSPACE and f(ws=P(0x40010)) == svx.SV_EALIGN
+    for name in ("L_", "B", "H", "S"):
+        assert f(**{name: 0}) == svx.SV_OK, name  # nothing enqueued
+    assert f(L_=1 << 20, B=1 << 20, H=1 << 20, ss=(0, 0, 0, 0), ds=(1 << 50, 1 << 30, 1 << 20, 512)) != svx.SV_OK
+
+
+def test_binding_refuses_layouts():
+    z = torch.zeros(4, 64)
+    ids, vals = torch.zeros(4, 8, dtype=torch.int32), torch.zeros(4, 8)
+    bad = [
+        lambda: svx.sv_teacher_topk(z, 8, 1.0),                                        # not on the GPU
+        lambda: svx.sv_teacher_topk(torch.zeros(4, 2, 64), 8, 1.0),
+        lambda: svx.sv_teacher_topk(z.double(), 8, 1.0),
+        lambda: svx.sv_distill_topk(z, ids.long(), vals, 1.0),
+        lambda: svx.sv_distill_topk(z, ids, vals[:, :4], 1.0),
+        lambda: svx.sv_distill_topk(z, ids[:2], vals, 1.0),
+        lambda: svx.sv_distill_topk(z, ids, vals, 1.0, rest=torch.zeros(3)),
+        lambda: svx.sv_distill_topk(z, ids, vals, 1.0, grad=torch.zeros(4, 60)),
+        lambda: svx.sv_distill_topk(z, ids, vals, 1.0, grad_loss=torch.zeros(4, dtype=torch.float64)),
+        lambda: svx.sv_beam_select(z, torch.zeros(4, 1), 2),
+        lambda: svx.sv_beam_select(z[None], torch.zeros(1, 3), 2),
+        lambda: svx.sv_beam_select(z[None], torch.zeros(1, 4), 2, pad_tok=1 << 31),
+        lambda: svx.sv_beam_reorder(torch.zeros(2, 3), torch.zeros(3, 2, dtype=torch.int32)),
+        lambda: svx.sv_beam_reorder(torch.zeros(1, 2, 3, 4), torch.zeros(2, 4, dtype=torch.int32)),  # in place, N > W
+        lambda: svx.sv_beam_reorder(torch.zeros(1, 2, 3, 4), torch.zeros(2, 3, dtype=torch.int32),
+                                    lens=torch.zeros(2, dtype=torch.int32)),
+        lambda: svx.sv_beam_reorder(torch.zeros(1, 2, 3, 4), torch.zeros(2, 3, dtype=torch.int32), pos_dim=2),
+        lambda: svx.sv_beam_reorder(torch.zeros(1, 2, 3, 4, 5).transpose(3, 4), torch.zeros(2, 3, dtype=torch.int32)),
+        lambda: svx.sv_beam_reorder(torch.zeros(1, 2, 3, 4), torch.zeros(2, 3, dtype=torch.int32),
+                                    out=torch.zeros(1, 2, 3, 4, dtype=torch.float16)),
+        lambda: svx.sv_beam_reorder(torch.zeros(1, 2, 3, 4), torch.zeros(2, 2, dtype=torch.int32),
+                                    out=torch.zeros(1, 2, 3, 4)),
+    ]
+    for i, f in enumerate(bad):
+        with pytest.raises(svx.SpecVerifyError):
+            f()
+            print("not refused:", i)
+
+
+def test_state_layouts():
+    t = torch.zeros(2, 3, 4, 5, 6, 8, dtype=torch.bfloat16)
+    (L_, B, W, H, S, pos), st = svx._state_layout(t, 4, "state")
+    assert (L_, B, W, H, S, pos) == (2, 3, 4, 5, 6, 16) and list(st) == [3 * 4 * 480, 4 * 480, 480, 96]
+    (L_, B, W, H, S, pos), st = svx._state_layout(t, None, "state")
+    assert (H, S, pos) == (1, 1, 480)
+    u = t.transpose(3, 4)  # positions before heads, in memory behind them
+    with pytest.raises(svx.SpecVerifyError):
+        svx._state_layout(u, 3, "state")
+    v = torch.zeros(2, 3, 4, 5, 7, 6, 8)[:, :, :, :, 2]  # heads evenly spaced, with a gap
+    assert svx._state_layout(v, 4, "state")[0] == (2, 3, 4, 5, 6, 32)
+    assert svx._state_layout(t[:, :, :, :, :3], 4, "state")[0] == (2, 3, 4, 5, 3, 16)
+    assert svx._state_layout(torch.zeros(1, 2, 3, dtype=torch.int32), None, "state")[0] == (1, 2, 3, 1, 1, 4)

@@ -1,0 +1,643 @@
+"""The drafter-side operators on the GPU against their plain 64-bit forms (tests/draft_ref.py, tolerances there)."""
+import math
+
+import pytest
+import torch
+
+from lossless_draft_verification_04_amd import specverify as svx
+from lossless_draft_verification_04_amd import workloads as W
+from tests import draft_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda", 0)
+F32, BF16 = torch.float32, torch.bfloat16
+INF = math.inf
+
+
+@pytest.fixture(autouse=True)
+def no_device_error():
+    svx.sv_get_device_error(DEV)
+    yield
+    assert svx.sv_get_device_error(DEV) == 0
+
+
+def rows(R, V, dtype, seed, spread=2.0):
+    """CPU logits: a normal bulk and some raised tokens, rounded to dtype."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(R, V, generator=g) * spread
+    n = min(V, 40)
+    at = torch.stack([torch.randperm(V, generator=g)[:n] for _ in range(R)])
+    x.scatter_(1, at, 14 - 1.5 * torch.arange(1, n + 1).float().log() + torch.randn(R, n, generator=g))
+    return x.to(dtype)
+
+
+def put(x):
+    """On the GPU with 16-byte aligned rows; what lies behind a row's end is large."""
+    V, per = x.shape[-1], 16 // x.element_size()
+    store = torch.full((*x.shape[:-1], -(-V // per) * per + per), 99.0, dtype=x.dtype, device=DEV)
+    view = store[..., :V]
+    view.copy_(x)
+    return view
+
+
+def near(got, want, tol, what):
+    got, want = got.double().cpu(), want.double()
+    fin = torch.isfinite(want)
+    assert torch.equal(fin, torch.isfinite(got)), what
+    assert torch.equal(got[~fin], want[~fin]), what
+    off = (got - want)[fin].abs()
+    tol = tol[fin] if isinstance(tol, torch.Tensor) else tol
+    assert bool((off <= tol).all()), (what, float(off.max()), float((off - tol).max()))
+
+
+# ---------------------------------------------------------------------------
+# the teacher's pass
+# ---------------------------------------------------------------------------
+def check_teacher(x, k, T):
+    got = svx.sv_teacher_topk(put(x), k, T)
+    ids, vals, rest = ref.teacher(x, k, T)
+    assert torch.equal(got["ids"].cpu().long(), ids)
+    assert torch.equal(got["vals"].cpu().double(), vals)
+    near(got["rest"], rest, ref.SUM + 2.0 ** -24 * rest.abs().nan_to_num(0, 0, 0), "rest")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R,V,k,T", [(1, 1, 1, 1.0), (3, 7, 9, 1.0), (2, 64, 64, 0.5), (5, 65, 64, 2.0), (1, 4099, 1, 1.0),
+                                     (4, 20011, 17, 0.7), (2, 152064, 64, 1.0), (600, 9001, 33, 1.0),
+                                     (520, 40961, 64, 1.3), (1, 300007, 64, 1.0)])
+def test_teacher(R, V, k, T, dtype):
+    check_teacher(rows(R, V, dtype, R + V), k, T)
+
+
+def teacher_rows(kind, R, V, dtype):
+    g = torch.Generator().manual_seed(7)
+    x = rows(R, V, dtype, 5)
+    if kind == "ties":
+        return torch.randint(-3, 3, (R, V), generator=g).to(dtype)
+    if kind == "equal":
+        return torch.zeros(R, V, dtype=dtype)
+    if kind == "masked":  # few tokens allowed, by -inf
+        return x.masked_fill(torch.rand(R, V, generator=g) < 0.998, -INF)
+    if kind == "lowest":  # the same by the type's lowest value
+        return x.masked_fill(torch.rand(R, V, generator=g) < 0.998, torch.finfo(dtype).min)
+    if kind == "one":  # a single token
+        y = torch.full((R, V), -INF, dtype=dtype)
+        y[:, V // 2] = 3.0
+        return y
+    if kind == "peak":  # nearly all mass in a few tokens of one thread's vectors
+        y = torch.randn(R, V, generator=g)
+        y[:, ::4096] += 60.0
+        return y.to(dtype)
+    if kind == "crowd":  # the top tokens side by side
+        x[:, 1000:1100] += 30.0
+        return x
+    if kind == "rising":  # every vector beats the one before
+        return torch.linspace(-20, 20, V).expand(R, V).to(dtype)
+    raise KeyError(kind)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R", [2, 530])
+@pytest.mark.parametrize("kind", ["ties", "equal", "masked", "lowest", "one", "peak", "crowd", "rising"])
+def test_teacher_hard_rows(kind, R, dtype):
+    check_teacher(teacher_rows(kind, R, 20011, dtype), 40, 1.0)
+
+
+def test_teacher_row_of_nothing():
+    x = torch.full((3, 5000), -INF, dtype=BF16)
+    got = svx.sv_teacher_topk(put(x), 5, 1.0)
+    assert bool((got["vals"] == -INF).all()) and bool((got["rest"] == -INF).all())
+    assert got["ids"].cpu().tolist() == [[0, 1, 2, 3, 4]] * 3
+
+
+def test_teacher_agrees_with_the_fan_out():
+    x = put(rows(70, 30011, BF16, 3))
+    got = svx.sv_teacher_topk(x, 24, 0.9)
+    ids, vals = svx.sv_fanout_topk(x, torch.full((70,), 24, dtype=torch.int32, device=DEV), 24)
+    assert torch.equal(ids, got["ids"]) and torch.equal(vals, got["vals"])
+
+
+# ---------------------------------------------------------------------------
+# distillation
+# ---------------------------------------------------------------------------
+def target(x, k, T, seed, noise=0.6):
+    """A teacher near the student's rows x [R, V]: ids, vals, rest (CPU)."""
+    g = torch.Generator().manual_seed(seed)
+    t = x.float().clamp(min=-50) + noise * torch.randn(x.shape, generator=g)
+    ids, vals, rest = ref.teacher(t, k, T)
+    return ids.int(), vals.float(), rest.float()
+
+
+def check_distill(x, ids, vals, rest, T, g=None, error=0, inplace=False):
+    dev = lambda t: None if t is None else t.to(DEV)
+    want_loss, want_stat, want_grad, size = ref.distill(x, ids, vals, rest, T, g)
+    a = (dev(ids), dev(vals))
+    kw = dict(rest=dev(rest), grad_loss=dev(g))
+    z = put(x)
+    fwd = svx.sv_distill_topk(z, *a, T, rest=kw["rest"])
+    assert fwd["grad"] is None
+    back = svx.sv_distill_topk_backward(z, *a, fwd["stat"], T, **kw)
+    both = svx.sv_distill_topk(z, *a, T, want_grad=True, **kw)
+    # the logarithms of the row's sum and of the sum outside I, each within SUM, enter with weights at most 1
+    loss_tol = 2 * ref.SUM + 2.0 ** -23 * want_loss.abs().nan_to_num(0, 0, 0)
+    for out in (fwd, both):
+        near(out["loss"], want_loss, loss_tol, "loss")
+        near(out["stat"], want_stat, ref.SUM * want_stat.abs().nan_to_num(0, 0, 0), "stat")
+    # an element q_v (1 - p_0 / q_0): the exponential (its argument up to |x| <= 80 in the far tail: 80 * 2 * 2^-24 * 0.7
+    # < 7e-6), s and s_0 (SUM each); p_v alike; all of it relative to q + p; then the rounding
+    tol = 3e-5 * size + ref.HALF[x.dtype] * want_grad.abs() + 1e-37
+    for out in (back, both["grad"]):
+        near(out, want_grad, tol, "grad")
+    if inplace:
+        for how in ("backward", "both"):
+            y = put(x)
+            edge = y.untyped_storage().size()
+            raw = torch.empty(0, dtype=y.dtype, device=DEV).set_(y.untyped_storage())
+            assert raw.numel() * raw.element_size() == edge
+            if how == "backward":
+                r = svx.sv_distill_topk_backward(y, *a, fwd["stat"], T, grad=y, **kw)
+            else:
+                r = svx.sv_distill_topk(y, *a, T, grad=y, **kw)["grad"]
+            assert r is y
+            near(y, want_grad, tol, how + " in place")
+            pad = raw.view(x.shape[0], -1)[:, x.shape[1]:]
+            assert bool((pad == 99.0).all())
+    torch.cuda.synchronize()
+    assert svx.sv_get_device_error(DEV) == error
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R,V,k,T", [(1, 1, 1, 1.0), (2, 5, 3, 1.0), (3, 9, 9, 0.5), (1, 4099, 1, 1.0), (7, 20011, 64, 2.0),
+                                     (2, 152064, 64, 1.0), (1, 300007, 256, 1.0), (90, 8195, 100, 0.8),
+                                     (1100, 1031, 16, 1.0), (600, 16391, 20, 1.4)])
+def test_distill(R, V, k, T, dtype):
+    x = rows(R, V, dtype, R + V)
+    g = torch.rand(R, generator=torch.Generator().manual_seed(1)) - 0.3
+    check_distill(x, *target(x, k, T, 2), T, g, inplace=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_distill_without_rest(dtype):
+    x = rows(9, 12007, dtype, 4)
+    ids, vals, _ = target(x, 32, 1.0, 5)
+    check_distill(x, ids, vals, None, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R", [6, 700])
+def test_distill_padded_rows_and_absent_ids(R, dtype):
+    x = rows(R, 5003, dtype, 6)
+    ids, vals, rest = target(x, 12, 1.0, 7)
+    ids[::3], vals[::3], rest[::3] = -1, -INF, -INF        # no target
+    x[0] = float("nan")                                    # such a row is not read
+    ids[1, 5:] = -1                                        # fewer tokens
+    vals[2, 4] = -INF                                      # a token of no mass
+    ids[4, 0::2] = -1                                      # holes
+    check_distill(x, ids, vals, rest, 1.0, inplace=True)
+
+
+def test_distill_every_row_empty():
+    x = torch.full((5, 1000), float("nan"), dtype=BF16)
+    ids = torch.full((5, 4), -1, dtype=torch.int32)
+    check_distill(x, ids, torch.zeros(5, 4), None, 1.0)
+    check_distill(x, ids, torch.zeros(5, 4), torch.full((5,), -INF), 1.0, inplace=True)
+
+
+def test_distill_only_the_rest():
+    """No token but mass outside: one class, loss 0, and q is its own."""
+    x = rows(4, 3001, F32, 8)
+    ids = torch.full((4, 3), -1, dtype=torch.int32)
+    check_distill(x, ids, torch.zeros(4, 3), torch.full((4,), 2.5), 1.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("low", ["-inf", "lowest"])
+def test_distill_masked_students(low, dtype):
+    v = -INF if low == "-inf" else torch.finfo(dtype).min
+    x = rows(8, 6007, dtype, 9)
+    ids, vals, rest = target(x, 16, 1.0, 10)
+    keep = torch.zeros(8, 6007, dtype=torch.bool).scatter_(1, ids.long(), True)
+    x[:2].masked_fill_(~keep[:2], v)              # everything outside I is masked
+    x[2, ids[2, 0].long()] = v                    # a teacher's token is
+    x[3].masked_fill_(keep[3], v)                 # all of them are
+    x[4].masked_fill_(torch.arange(6007) > 3000, v)
+    rest[0] = -INF                                # and nothing is asked of the others
+    check_distill(x, ids, vals, rest, 1.0, inplace=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_distill_row_of_nothing_sets_the_row_bit(dtype):
+    x = rows(3, 4001, dtype, 11)
+    ids, vals, rest = target(x, 8, 1.0, 12)
+    x[1] = -INF
+    check_distill(x, ids, vals, rest, 1.0, error=svx.DERR_ROW)
+
+
+def test_distill_bad_and_repeated_ids_are_flagged_and_absent():
+    x = rows(4, 4001, BF16, 13)
+    ids, vals, rest = target(x, 8, 1.0, 14)
+    ids[0, 3] = 4001
+    ids[1, 2] = -2
+    ids[2, 6] = ids[2, 1]
+    ids[3, 7] = 2 ** 31 - 1
+    check_distill(x, ids, vals, rest, 1.0, error=svx.DERR_TOKEN, inplace=True)
+
+
+def test_distill_peaked_rows_keep_the_digits_of_the_rest():
+    """Mass outside I near 1e-12 of the row: the sum outside is its own, not a difference."""
+    x = rows(6, 10007, F32, 15)
+    ids, vals, rest = target(x, 10, 1.0, 16)
+    x.scatter_add_(1, ids.long(), torch.full((6, 10), 25.0))
+    check_distill(x, ids, vals, rest, 1.0)
+    check_distill(x, ids, vals, rest - 25.0, 1.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [1e-3, 0.05, 30.0])
+def test_distill_temperatures(T, dtype):
+    """A large c = log2(e) / T: c z - c m loses digits with |c z| unless the shift is undone, so rows are small here:
+    |z| <= 0.02 at T = 1e-3."""
+    x = (rows(5, 3001, F32, 17).clamp(-20, 20) * min(1.0, T)).to(dtype)
+    check_distill(x, *target(x, 6, T, 18, noise=0.1 * min(1.0, T)), T)
+
+
+def test_distill_gradient_against_differences():
+    x = rows(3, 301, F32, 19).double()
+    ids, vals, rest = target(x.float(), 7, 1.5, 20)
+    z = x.float()
+    got = svx.sv_distill_topk(put(z), ids.to(DEV), vals.to(DEV), 1.5, rest=rest.to(DEV), want_grad=True)["grad"].cpu()
+    h = 1e-4
+    at = torch.cat([ids[0].long(), torch.arange(0, 301, 37)]).unique()
+    for v in at.tolist():
+        up, down = z.double(), z.double()
+        up[:, v] += h
+        down[:, v] -= h
+        d = (ref.distill(up, ids, vals, rest, 1.5)[0] - ref.distill(down, ids, vals, rest, 1.5)[0]) / (2 * h)
+        # third derivatives of the loss are below 2 / T^3: h^2 / 6 of that, and the kernel's own 3e-5 (q + p) / T
+        near(got[:, v], d, 1e-8 + 4e-5, v)
+
+
+def test_distill_gradient_buffer_of_its_own_and_strided_rows():
+    x = rows(12, 2003, BF16, 21)
+    ids, vals, rest = target(x, 5, 1.0, 22)
+    z = put(x)
+    store = torch.full((12, 2400), 5.0, dtype=BF16, device=DEV)
+    out = svx.sv_distill_topk(z, ids.to(DEV), vals.to(DEV), 1.0, rest=rest.to(DEV), grad=store[:, 8:2011])
+    assert out["grad"].data_ptr() == store.data_ptr() + 16
+    want = ref.distill(x, ids, vals, rest, 1.0)
+    near(out["grad"], want[2], 3e-5 * want[3] + ref.HALF[BF16] * want[2].abs() + 1e-37, "grad")
+    assert bool((store[:, :8] == 5).all()) and bool((store[:, 2011:] == 5).all())
+    with pytest.raises(svx.SpecVerifyError):  # overlaps z without being it
+        svx.sv_distill_topk(z[:-1], ids[:-1].to(DEV), vals[:-1].to(DEV), 1.0, grad=z[1:])
+
+
+# ---------------------------------------------------------------------------
+# beam search
+# ---------------------------------------------------------------------------
+def check_beams(x, scores, N, T=1.0, finished=None, pad=0, error=0):
+    fin = None if finished is None else finished.to(DEV)
+    got = svx.sv_beam_select(put(x), scores.to(DEV), N, T, finished=fin, pad_tok=pad)
+    beam, tok, score = ref.beams(x, scores, N, T, finished, pad)
+    s = score[:, :N]
+    # the row's logarithm within SUM; the rounding of the score
+    near(got["score"], s, ref.SUM + 2.0 ** -24 * s.abs().nan_to_num(0, 0, 0), "score")
+    # places that no error of the scores can exchange: a gap to both neighbours of more than both errors, or a tie of
+    # the inputs themselves (equal in 64 bits)
+    gap = (score[:, :-1] - score[:, 1:]).nan_to_num(INF, INF, INF)
+    clear = (gap > 4 * ref.SUM) | (gap == 0)
+    clear = clear & torch.cat([torch.ones_like(clear[:, :1]), clear[:, :-1]], 1)
+    assert float(clear.double().mean()) > 0.9
+    assert torch.equal(got["beam"].cpu().long()[clear], beam[:, :N][clear])
+    assert torch.equal(got["tok"].cpu().long()[clear], tok[:, :N][clear])
+    torch.cuda.synchronize()
+    assert svx.sv_get_device_error(DEV) == error
+
+
+def beam_scores(B, W_, seed):
+    return torch.randn(B, W_, generator=torch.Generator().manual_seed(seed)) * 2 - 9
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("B,Wd,V,N", [(1, 1, 1, 1), (1, 1, 3, 8), (2, 3, 11, 64), (1, 4, 32000, 8), (3, 64, 515, 64),
+                                      (5, 7, 20011, 14), (1, 2, 152064, 4), (70, 8, 4099, 16), (2, 5, 70001, 64)])
+def test_beam_select(B, Wd, V, N, dtype):
+    x = rows(B * Wd, V, dtype, B + V).view(B, Wd, V)
+    check_beams(x, beam_scores(B, Wd, 3), N, 0.9)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_beam_select_dead_and_finished(dtype):
+    B, Wd, V = 6, 5, 7001
+    x = rows(B * Wd, V, dtype, 31).view(B, Wd, V)
+    s = beam_scores(B, Wd, 4)
+    s[0, 1:] = -INF                # a first step
+    s[1] = -INF                    # nothing alive
+    fin = torch.zeros(B, Wd, dtype=torch.int32)
+    fin[2] = 1                     # all ended
+    fin[3, ::2] = 7
+    fin[4, 2] = 1
+    s[4, 2] = -INF                 # ended and dead
+    x[1], x[2] = float("nan"), float("nan")  # not read
+    x[4, 2] = float("nan")
+    check_beams(x, s, 9, 1.0, fin, pad=123)
+
+
+def test_beam_select_ties_go_to_the_lower_beam_and_token():
+    row = torch.randint(-4, 4, (4001,), generator=torch.Generator().manual_seed(5)).float()
+    x = row.expand(2, 6, 4001).contiguous()
+    s = torch.full((2, 6), -3.0)
+    s[1, 2] = -2.5
+    check_beams(x, s, 40)
+    check_beams(x.bfloat16(), s, 40)
+    fin = torch.zeros(2, 6, dtype=torch.int32)
+    fin[0, 1] = fin[0, 4] = 1
+    check_beams(x, s, 40, finished=fin, pad=-1)
+
+
+def test_beam_select_masked_rows():
+    x = rows(12, 5003, F32, 33).view(3, 4, 5003)
+    x[0, 1].masked_fill_(torch.arange(5003) > 1, -INF)
+    x[1, 2:].masked_fill_(torch.arange(5003) > 2, torch.finfo(F32).min)
+    x[2] = -INF
+    x[2, 3, 17] = 0.0
+    x[2, :3, 5] = 1.0
+    check_beams(x, beam_scores(3, 4, 6), 12)
+
+
+def test_beam_select_row_of_nothing_sets_the_row_bit():
+    x = rows(4, 3001, BF16, 34).view(1, 4, 3001)
+    x[0, 2] = -INF
+    check_beams(x, beam_scores(1, 4, 7), 6, error=svx.DERR_ROW)
+
+
+# ---------------------------------------------------------------------------
+# reordering
+# ---------------------------------------------------------------------------
+def state(shape, dtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    n = torch.empty((), dtype=dtype).element_size()
+    return torch.randint(0, 100, (*shape[:-1], shape[-1] * n), generator=g, dtype=torch.uint8).view(dtype)
+
+
+REORDER = [
+    # L, B, W, N, H, S, D, dtype
+    (1, 1, 1, 1, 1, 1, 1, torch.int32),
+    (1, 3, 4, 4, 1, 33, 1, torch.int32),
+    (2, 3, 5, 7, 2, 17, 8, torch.bfloat16),
+    (3, 2, 8, 8, 3, 70, 64, torch.bfloat16),
+    (1, 2, 16, 13, 2, 300, 20, torch.float32),
+    (2, 2, 24, 24, 1, 40, 24, torch.float16),
+    (1, 2, 64, 64, 2, 21, 16, torch.float32),
+    (1, 1, 33, 40, 1, 50, 3, torch.uint8),
+    (1, 2, 12, 12, 2, 19, 5, torch.int16),
+]
+
+
+@pytest.mark.parametrize("case", REORDER, ids=str)
+@pytest.mark.parametrize("inplace", [False, True])
+def test_beam_reorder(case, inplace):
+    L, B, Wd, N, H, S, D, dtype = case
+    N = min(N, Wd) if inplace else N
+    g = torch.Generator().manual_seed(S)
+    src = state((L, B, Wd, H, S, D), dtype, 1)
+    parent = torch.randint(-1, Wd, (B, N), generator=g, dtype=torch.int32)
+    lens = torch.randint(0, S + 1, (B,), generator=g, dtype=torch.int32)
+    lens[0] = S
+    x = src.to(DEV)
+    if inplace:
+        got = svx.sv_beam_reorder(x, parent.to(DEV), pos_dim=4, lens=lens.to(DEV))
+        assert got is x
+        want = ref.reorder(src, src[:, :, :N], parent, lens)
+        assert torch.equal(got.cpu()[:, :, :N], want) and torch.equal(got.cpu()[:, :, N:], src[:, :, N:])
+    else:
+        dst = state((L, B, N, H, S, D), dtype, 2)
+        y = dst.to(DEV)
+        got = svx.sv_beam_reorder(x, parent.to(DEV), pos_dim=4, lens=lens.to(DEV), out=y)
+        assert got is y and torch.equal(x.cpu(), src)
+        assert torch.equal(got.cpu(), ref.reorder(src, dst, parent, lens))
+        # no lengths: all of it, the inner part as one piece
+        y = dst.to(DEV)
+        svx.sv_beam_reorder(x, parent.to(DEV), out=y)
+        assert torch.equal(y.cpu(), ref.reorder(src, dst, parent, torch.full((B,), S)))
+
+
+def test_beam_reorder_strided_views():
+    """A layer's slice of a wider cache, heads with a gap, positions cut short, an odd first byte."""
+    src = state((2, 3, 6, 4, 40, 16), torch.bfloat16, 3)
+    big = src.to(DEV)
+    view = big[:, :, 1:5, ::2, :31]
+    want_all = src.clone()
+    parent = torch.tensor([[3, 0, 0, 2], [1, 1, 1, 1], [0, 1, 2, 3]], dtype=torch.int32)
+    lens = torch.tensor([31, 7, 20], dtype=torch.int32)
+    part = src[:, :, 1:5, ::2, :31]
+    want_all[:, :, 1:5, ::2, :31] = ref.reorder(part, part, parent, lens)
+    svx.sv_beam_reorder(view, parent.to(DEV), pos_dim=4, lens=lens.to(DEV))
+    assert torch.equal(big.cpu(), want_all)
+    raw = torch.arange(1 + 2 * 3 * 10, dtype=torch.uint8, device=DEV)
+    odd = raw[1:].view(1, 2, 3, 10)
+    p = torch.tensor([[2, 0, 1], [1, -1, 0]], dtype=torch.int32)
+    want = ref.reorder(odd.cpu()[:, :, :, None, :, None], odd.cpu()[:, :, :, None, :, None], p, [10, 10])
+    svx.sv_beam_reorder(odd, p.to(DEV))
+    assert torch.equal(odd.cpu(), want[:, :, :, 0, :, 0]) and int(raw[0]) == 0
+
+
+def test_beam_reorder_bad_parents_and_lengths():
+    src = state((1, 4, 3, 1, 9, 4), torch.float32, 4)
+    parent = torch.tensor([[3, 0, 1], [0, -2, 1], [2, 1, 0], [2 ** 31 - 1, 2, -1]], dtype=torch.int32)
+    for lens in ([9, 9, 9, 9], [9, 10, -1, 9]):
+        x = src.to(DEV)
+        ok = parent.clone()
+        ok[(ok < 0) | (ok >= 3)] = -1
+        for b, n in enumerate(lens):
+            if not 0 <= n <= 9:
+                ok[b] = -1
+        svx.sv_beam_reorder(x, parent.to(DEV), pos_dim=4, lens=torch.tensor(lens, dtype=torch.int32, device=DEV))
+        assert torch.equal(x.cpu(), ref.reorder(src, src, ok, [9] * 4))
+        assert svx.sv_get_device_error(DEV) == svx.DERR_RANGE
+
+
+def test_beam_reorder_offsets_past_32_bits():
+    """A state of more than 4 GiB: the last beams of the last sequence."""
+    x = torch.zeros(1, 2, 4, 1, (1 << 29) + 4096, 1, dtype=torch.int32, device=DEV)
+    x[0, 1, 3, 0, -5:] = torch.arange(5, dtype=torch.int32, device=DEV)[:, None] + 1
+    x[0, 1, 0, 0, -5:] = 9
+    p = torch.tensor([[0, 1, 2, 3], [3, 1, 2, 0]], dtype=torch.int32, device=DEV)
+    svx.sv_beam_reorder(x, p, pos_dim=4)
+    assert x[0, 1, 0, 0, -5:, 0].tolist() == [1, 2, 3, 4, 5] and x[0, 1, 3, 0, -5:, 0].tolist() == [9] * 5
+    assert int(x[0, 0].amax()) == 0
+
+
+# ---------------------------------------------------------------------------
+# graphs, streams, workspaces
+# ---------------------------------------------------------------------------
+def calls():
+    T = 1.0
+    x = rows(37, 20011, BF16, 41)
+    ids, vals, rest = (t.to(DEV) for t in target(x, 24, T, 42))
+    z = put(x)
+    few = rows(3, 50021, F32, 43)
+    fid, fval, frest = (t.to(DEV) for t in target(few, 24, T, 44))
+    fz = put(few)
+    stat = svx.sv_distill_topk(z, ids, vals, T, rest=rest)["stat"].clone()
+    bz, bs = put(rows(12, 20011, BF16, 45).view(3, 4, 20011)), beam_scores(3, 4, 8).to(DEV)
+    st = state((2, 3, 4, 2, 50, 16), torch.bfloat16, 5).to(DEV)
+    par = torch.randint(0, 4, (3, 4), generator=torch.Generator().manual_seed(9), dtype=torch.int32).to(DEV)
+    ln = torch.tensor([50, 3, 17], dtype=torch.int32, device=DEV)
+    zero = torch.zeros_like(st)
+    return {
+        "teacher": lambda **k: svx.sv_teacher_topk(z, 24, T, **k),
+        "teacher split": lambda **k: svx.sv_teacher_topk(fz, 24, T, **k),
+        "loss": lambda **k: svx.sv_distill_topk(z, ids, vals, T, rest=rest, **k),
+        "loss split": lambda **k: svx.sv_distill_topk(fz, fid, fval, T, rest=frest, **k),
+        "both": lambda **k: svx.sv_distill_topk(z, ids, vals, T, rest=rest, want_grad=True, **k),
+        "backward": lambda **k: {"g": svx.sv_distill_topk_backward(z, ids, vals, stat, T, rest=rest, **k)},
+        "select": lambda **k: svx.sv_beam_select(bz, bs, 8, **k),
+        "reorder": lambda **k: {"o": svx.sv_beam_reorder(st, par, pos_dim=4, lens=ln, out=zero.clone(), **k)},
+    }
+
+
+def bits(out):
+    return {k: v.clone().contiguous().view(torch.uint8) for k, v in out.items() if v is not None}
+
+
+def same(a, b):
+    return a.keys() == b.keys() and all(torch.equal(a[k], b[k]) for k in a)
+
+
+def test_captured_calls_replay():
+    """Every entry point captured and replayed, with eager calls of all of them on the same workspace between."""
+    every = calls()
+    eager = {n: bits(f()) for n, f in every.items()}
+    torch.cuda.synchronize()
+    graphs = {}
+    for n, f in every.items():
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = f()
+        graphs[n] = (g, out)
+    for rep in range(3):
+        for n, (g, out) in graphs.items():
+            for v in out.values():
+                if v is not None and n != "reorder":
+                    v.fill_(-7)
+            g.replay()
+            torch.cuda.synchronize()
+            assert same(bits(out), eager[n]), (rep, n)
+            assert same(bits(every[n]()), eager[n]), (rep, n)
+    assert svx.sv_get_device_error(DEV) == 0
+
+
+def test_two_streams_with_workspaces_of_their_own():
+    every = calls()
+    eager = {n: bits(f()) for n, f in every.items()}
+    ws = [torch.zeros(64 << 20, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    names = list(every)
+    got = [[], []]
+    for rep in range(6):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                for n in names if i == 0 else reversed(names):
+                    got[i].append((n, bits(every[n](workspace=ws[i]))))
+    torch.cuda.synchronize()
+    for lst in got:
+        for n, out in lst:
+            assert same(out, eager[n]), n
+    for w in ws:
+        assert int(w[:256 + 65536 * 4].max()) == 0  # error word and counters are left as a call finds them
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+def test_a_drafter_is_trained_towards_its_verifier():
+    """The verifier's rows -> target -> loss and gradient of a linear drafter's logits, handed to autograd; the weights'
+    gradient is the formula's, and the acceptance overlap is computed from the same rows."""
+    g = torch.Generator().manual_seed(50)
+    R, D, V, T = 48, 32, 4099, 1.0
+    h = torch.randn(R, D, generator=g)
+    verifier = put(rows(R, V, BF16, 51))
+    w = (torch.randn(V, D, generator=g) * 0.3).to(DEV).requires_grad_()
+    t = svx.sv_teacher_topk(verifier, 32, T)
+    live = torch.ones(R)
+    live[40:] = 0.0
+    t["ids"][40:] = -1           # padding
+    t["rest"][40:] = -INF
+    weight = (live / live.sum()).to(DEV)
+    z = torch.zeros(R, 4104, device=DEV)[:, :V].copy_((h.to(DEV) @ w.t()).detach())
+    out = svx.sv_distill_topk(z, t["ids"], t["vals"], T, rest=t["rest"], grad_loss=weight, want_grad=True)
+    zz = h.to(DEV) @ w.t()
+    zz.backward(out["grad"])
+    loss, _, grad, size = ref.distill(z.cpu(), t["ids"].cpu(), t["vals"].cpu(), t["rest"].cpu(), T, weight.cpu())
+    want = grad.t() @ h.double()
+    # the logits' gradient within 3e-5 (q + p) g / T; the product's sums of 48 terms in 32 bits
+    tol = (size * 3e-5 + grad.abs() * 48 * 2.0 ** -23).t() @ h.abs().double() + 1e-12
+    near(w.grad, want, tol, "weights")
+    near(out["loss"], loss, 2 * ref.SUM + 2.0 ** -23 * loss, "loss")
+
+
+def test_beams_draft_and_the_verifier_accepts():
+    """A drafter that is a table of next-token logits: beam search by select and reorder (histories and a state that
+    goes with them) finds the paths that enumeration finds; the best one, a deterministic draft, is verified."""
+    V, Wd, steps, B = 61, 4, 4, 3
+    g = torch.Generator().manual_seed(60)
+    table = torch.randn(V, V, generator=g) * 2.5
+    tab = torch.zeros(V, 64, device=DEV)[:, :V].copy_(table)
+    last = torch.tensor([5, 17, 40], dtype=torch.int32, device=DEV)[:, None].expand(B, Wd).contiguous()
+    scores = torch.full((B, Wd), -INF, device=DEV)
+    scores[:, 0] = 0.0
+    hist = torch.full((B, Wd, steps), -1, dtype=torch.int32, device=DEV)
+    mind = last[None, :, :, None].to(torch.float32).repeat(2, 1, 1, 5)  # a state per layer: the last token
+    for s in range(steps):
+        z = torch.zeros(B, Wd, 64, device=DEV)[..., :V].copy_(tab[last.long()])
+        r = svx.sv_beam_select(z, scores, Wd)
+        svx.sv_beam_reorder(hist[None], r["beam"])
+        svx.sv_beam_reorder(mind, r["beam"])
+        assert torch.equal(mind[0, :, :, 0].int(), torch.gather(last, 1, r["beam"].long()))
+        hist[:, :, s] = r["tok"]
+        last, scores = r["tok"].contiguous(), r["score"]
+        mind[:] = last[None, :, :, None].float()
+    lp = table.double().log_softmax(-1)
+    for b, start in enumerate([5, 17, 40]):
+        paths = {(): (0.0, start)}
+        for s in range(steps):
+            nxt = {}
+            for path, (sc, tok) in paths.items():
+                for v in range(V):
+                    nxt[path + (v,)] = (sc + float(lp[tok, v]), v)
+            paths = dict(sorted(nxt.items(), key=lambda kv: -kv[1][0])[:Wd])
+        want = list(paths.items())
+        assert [tuple(h) for h in hist[b].tolist()] == [p for p, _ in want]
+        near(scores[b], torch.tensor([s for _, (s, _) in want]).double(), steps * (ref.SUM + 1e-6), "score")
+    # verification against the same table: greedily, the accepted prefix is where the path follows the row maxima
+    draft = hist[:, 0].contiguous()
+    ctx = torch.cat([torch.tensor([[5], [17], [40]], dtype=torch.int32, device=DEV), draft], 1)
+    tgt = torch.zeros(B, steps + 1, 64, device=DEV)[..., :V].copy_(tab[ctx.long()])
+    out = svx.sv_verify_greedy(tgt, draft)
+    best = table.argmax(-1)
+    for b in range(B):
+        n = 0
+        while n < steps and int(best[ctx[b, n]]) == int(draft[b, n]):
+            n += 1
+        assert int(out["n"][b]) == n
+    pm = svx.sv_verify_chain_pm(tgt, draft, 1.0, seed=3)
+    want_p = torch.stack([lp[ctx[b, :steps].long().cpu()].gather(1, draft[b].long().cpu()[:, None])[:, 0].exp()
+                          for b in range(B)])
+    near(pm["p"], want_p, 1e-5, "p of the drafts")
+
+
+def test_large_vocabulary():
+    """A row of 2^24 logits (many parts of a row, the largest offsets)."""
+    V = 1 << 24
+    g = torch.Generator(device=DEV).manual_seed(70)
+    z = torch.randn(1, V, generator=g, device=DEV).mul_(2).bfloat16()
+    got = svx.sv_teacher_topk(z, 64, 1.0)
+    x = z.cpu()
+    ids, vals, rest = ref.teacher(x, 64, 1.0)
+    assert torch.equal(got["ids"].cpu().long(), ids)
+    near(got["rest"], rest, ref.SUM + 2.0 ** -24 * rest.abs(), "rest")
+    both = svx.sv_distill_topk(z, got["ids"], got["vals"] + 0.5, 1.0, rest=got["rest"], want_grad=True)
+    want = ref.distill(x, got["ids"].cpu(), got["vals"].cpu() + 0.5, got["rest"].cpu(), 1.0)
+    near(both["loss"], want[0], 2 * ref.SUM, "loss")
+    near(both["grad"], want[2], 3e-5 * want[3] + ref.HALF[BF16] * want[2].abs() + 1e-37, "grad")
