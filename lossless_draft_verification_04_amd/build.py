@@ -10,7 +10,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libspecverify.so")
 SOURCES = ["sv_api.hip", "sv_chain.hip", "sv_chain_small.hip", "sv_greedy.hip", "sv_tree.hip", "sv_fanout.hip", "sv_cache.hip", "sv_presto.hip", "sv_branch.hip", "sv_probe.hip",
-           "sv_draft_api.hip", "sv_teacher.hip", "sv_distill.hip", "sv_beam.hip"]
+           "sv_draft_api.hip", "sv_teacher.hip", "sv_distill.hip", "sv_distill_held.hip", "sv_beam.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

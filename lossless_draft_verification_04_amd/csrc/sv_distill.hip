@@ -18,23 +18,13 @@
 // digits where I holds nearly everything, and the error that the sum's
 // elements share (that of log2(e) / T in 32 bits) enters the loss only times
 // q_0 - p_0.
-#include "sv_draft.h"
-#include "sv_topmass.hpp"
+#include "sv_distill.hpp"
 
 namespace sv {
 
 constexpr int kDNT = 256;
 constexpr int kDU = 4;     // vectors in flight per thread
-constexpr int kTeach = SV_MAX_TEACHER / kWave;  // teacher tokens per lane of the finishing wave
 static_assert(SV_MAX_TEACHER <= kDNT, "a thread a teacher token");
-
-// A row's teacher tokens in LDS: id (-1: absent), value, the drafter's logit.
-struct Teacher {
-  int32_t id[SV_MAX_TEACHER];
-  float t[SV_MAX_TEACHER];
-  float z[SV_MAX_TEACHER];
-  int live;
-};
 
 // Loads them (every thread of a block of at least SV_MAX_TEACHER threads).
 // Out-of-range and repeated ids are flagged and become absent.  Returns
@@ -70,23 +60,6 @@ __device__ __forceinline__ bool load_teacher(const DistillParams& a, int r, cons
   return s.live != 0;
 }
 
-// The teacher's normaliser: its largest exponent m and Z relative to it.
-struct Norm {
-  double m, z;
-};
-__device__ __forceinline__ Norm wave_teacher_norm(const Teacher& s, int k, double rest, double invT, int lane) {
-  float tm = kNegInf;
-  for (int i = lane; i < k; i += kWave) tm = fmaxf(tm, s.t[i]);
-  tm = wave_fmax(tm);
-  Norm n;
-  n.m = fmax((double)tm * invT, rest);
-  double z = 0.0;
-  for (int i = lane; i < k; i += kWave)
-    if (s.t[i] > kNegInf) z += exp((double)s.t[i] * invT - n.m);
-  n.z = wave_sum(z) + exp(rest - n.m);
-  return n;
-}
-
 // The loss and the statistics of one row from the sum outside I, by one wave.
 __device__ __forceinline__ void finish_loss(const DistillParams& a, int r, const Teacher& s, const Partial& out,
                                             int lane) {
@@ -105,20 +78,20 @@ __device__ __forceinline__ void finish_loss(const DistillParams& a, int r, const
   }
   double sum = 0.0;
   for (int i = lane; i < a.k; i += kWave)
-    if (s.z[i] > kNegInf) sum += exp(((double)s.z[i] - (double)m) * a.invT);
+    if (s.z[i] > kNegInf) sum += exp_d(((double)s.z[i] - (double)m) * a.invT);
   sum = wave_sum(sum);
-  if (out.s > 0.0) sum += out.s * exp(((double)out.m - (double)m) * a.invT);
-  const double lt = n.m + log(n.z);
-  const double lq = (double)m * a.invT + log(sum);
+  if (out.s > 0.0) sum += out.s * exp_d(((double)out.m - (double)m) * a.invT);
+  const double lt = n.m + log_d(n.z);
+  const double lq = (double)m * a.invT + log_d(sum);
   double loss = 0.0;
   for (int i = lane; i < a.k; i += kWave) {
     const double lp = (double)s.t[i] * a.invT - lt;
-    const double p = s.t[i] > kNegInf ? exp(lp) : 0.0;
+    const double p = s.t[i] > kNegInf ? exp_d(lp) : 0.0;
     if (p > 0.0) loss += p * (lp - ((double)s.z[i] * a.invT - lq));
   }
   loss = wave_sum(loss);
-  const double p0 = exp(rest - lt);
-  if (p0 > 0.0) loss += p0 * ((rest - lt) - ((double)out.m * a.invT + log(out.s) - lq));
+  const double p0 = exp_d(rest - lt);
+  if (p0 > 0.0) loss += p0 * ((rest - lt) - ((double)out.m * a.invT + log_d(out.s) - lq));
   if (lane == 0) {
     a.out_loss[r] = (float)loss;
     reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(m, (float)sum, out.m, (float)out.s);
@@ -221,37 +194,6 @@ __global__ __launch_bounds__(kDNT) void distill_loss_kernel(DistillParams a) {
 // ---------------------------------------------------------------------------
 // Gradient.
 // ---------------------------------------------------------------------------
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-// E values as one vector of the row's type (bf16: round to nearest even).
-template <int DT>
-__device__ __forceinline__ u32x4 pack(const float* x) {
-  u32x4 d;
-  if constexpr (DT == SV_BF16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      d[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x[2 * i], x[2 * i + 1]}, bf16x2));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = __float_as_uint(x[i]);
-  }
-  return d;
-}
-template <int DT>
-__device__ __forceinline__ void store_elem(void* row, int64_t i, float x) {
-  if constexpr (DT == SV_BF16)
-    reinterpret_cast<__bf16*>(row)[i] = (__bf16)x;
-  else
-    reinterpret_cast<float*>(row)[i] = x;
-}
-
-// What the gradient of a row needs: dz_v = each * 2^(c z_v - cm) outside I
-// (each * 2^((z_v - m) c) where cm is not finite), top[i] at token i of I.
-struct GradRow {
-  float m, cm, each;
-};
-
 // One wave: the row's factors, and (q_i - p_i) g / T in place of s.z.
 __device__ __forceinline__ GradRow wave_grad_row(const DistillParams& a, int r, Teacher& s, const float4 st, int lane) {
   const double rest = a.rest ? (double)a.rest[r] : -__builtin_huge_val();
@@ -259,36 +201,13 @@ __device__ __forceinline__ GradRow wave_grad_row(const DistillParams& a, int r, 
   const double scale = (a.g ? (double)a.g[r] : 1.0) * a.invT;
   const double inv = 1.0 / (double)st.y;
   for (int i = lane; i < a.k; i += kWave) {
-    const double p = s.t[i] > kNegInf ? exp((double)s.t[i] * a.invT - n.m) / n.z : 0.0;
-    const double q = s.z[i] > kNegInf ? exp(((double)s.z[i] - (double)st.x) * a.invT) * inv : 0.0;
+    const double p = s.t[i] > kNegInf ? exp_d((double)s.t[i] * a.invT - n.m) / n.z : 0.0;
+    const double q = s.z[i] > kNegInf ? exp_d(((double)s.z[i] - (double)st.x) * a.invT) * inv : 0.0;
     s.z[i] = (float)((q - p) * scale);
   }
-  const double p0 = exp(rest - n.m) / n.z;
-  const double q0 = st.w > 0.f ? (double)st.w * exp(((double)st.z - (double)st.x) * a.invT) * inv : 0.0;
-  GradRow g;
-  g.m = st.x;
-  g.cm = a.c * st.x;
-  double each = p0 > 0.0 ? (q0 > 0.0 ? 1.0 - p0 / q0 : 0.0) : 1.0;
-  each *= scale * inv;
-  // 2^(c z - cm) has the shift cm, which is not quite c m
-  if (fabsf(g.cm) <= 3e38f) each *= exp2((double)g.cm - (double)a.c * (double)st.x);
-  g.each = (float)each;
-  return g;
-}
-
-template <int DT>
-__device__ __forceinline__ u32x4 grad_vec(const u32x4 d, const GradRow& g, float c) {
-  constexpr int E = Fmt<DT>::kPerVec;
-  float x[E];
-  unpack<DT>(d, x);
-  if (__builtin_expect(fabsf(g.cm) <= 3e38f, 1)) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = g.each * fast_exp2(__builtin_fmaf(x[e], c, -g.cm));
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) x[e] = g.each * fast_exp2((x[e] - g.m) * c);
-  }
-  return pack<DT>(x);
+  const double p0 = exp_d(rest - n.m) / n.z;
+  const double q0 = st.w > 0.f ? (double)st.w * exp_d(((double)st.z - (double)st.x) * a.invT) * inv : 0.0;
+  return grad_row(st.x, p0, q0, scale, inv);
 }
 
 // A block per (row part): the gradient outside I streams through, then the
@@ -333,11 +252,9 @@ __global__ __launch_bounds__(kDNT) void distill_grad_kernel(DistillParams a) {
       if (v + u * kDNT < vf) outv[v + u * kDNT] = grad_vec<DT>(d[u], g, a.c);
   }
   if (v1 > nfull && threadIdx.x < a.V - nfull * E) {
-    float x[E];
     const int e = threadIdx.x;
     const float z = load_elem<DT>(row, nfull * E + e);
-    const float arg = fabsf(g.cm) <= 3e38f ? __builtin_fmaf(z, a.c, -g.cm) : (z - g.m) * a.c;
-    store_elem<DT>(out, nfull * E + e, g.each * fast_exp2(arg));
+    store_elem<DT>(out, nfull * E + e, grad_elem(z, g, a.c));
   }
   __builtin_amdgcn_s_waitcnt(0);  // the stream's stores are done before any token's
   __syncthreads();

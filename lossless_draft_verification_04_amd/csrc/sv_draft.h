@@ -68,6 +68,7 @@ struct DistillParams {
   int64_t vpc, vpc2, nvec;
 };
 constexpr int64_t kDistillPartVecs = 32768;  // vectors of a loss part at most (a byte of LDS marks each)
+constexpr int64_t kHeldVecs = 1024 * 24;  // vectors of a row that a block can hold in registers
 
 struct ReorderParams {
   const char* src;
@@ -85,6 +86,7 @@ hipError_t launch_teacher(const TeacherParams& p, sv_dtype dt, hipStream_t s);
 hipError_t launch_beam(const BeamParams& p, sv_dtype dt, hipStream_t s);
 hipError_t launch_distill_loss(const DistillParams& p, sv_dtype dt, hipStream_t s);
 hipError_t launch_distill_grad(const DistillParams& p, sv_dtype dt, hipStream_t s);
+hipError_t launch_distill_held(const DistillParams& p, sv_dtype dt, hipStream_t s);
 hipError_t launch_reorder(const ReorderParams& p, int vec, hipStream_t s);
 
 }  // namespace sv

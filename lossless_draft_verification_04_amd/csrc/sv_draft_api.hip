@@ -211,6 +211,7 @@ sv_status sv_distill_topk(const void* z, sv_dtype dt, int64_t stride, int32_t R,
   p.out_stat = out_stat;
   p.stat = out_stat;
   const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (out_grad && pl.nvec <= kHeldVecs) return launch_distill_held(p, dt, s) == hipSuccess ? SV_OK : SV_EHIP;
   if (launch_distill_loss(p, dt, s) != hipSuccess) return SV_EHIP;
   if (out_grad && launch_distill_grad(p, dt, s) != hipSuccess) return SV_EHIP;
   return SV_OK;

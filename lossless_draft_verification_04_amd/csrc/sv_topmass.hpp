@@ -27,8 +27,8 @@ struct Mass {
 
 // a <- a + the E values x (-inf: nothing).  The shift is m, as fma(x, c, -c m);
 // where c m is not finite (rows masked with the type's lowest value), as
-// (x - m) c.
-template <int E>
+// (x - m) c; SUB: always so (no branch, an operation more a value).
+template <int E, bool SUB = false>
 __device__ __forceinline__ void fold_values(const float (&x)[E], float c, Mass& a) {
   float fm = x[0];
 #pragma unroll
@@ -37,7 +37,7 @@ __device__ __forceinline__ void fold_values(const float (&x)[E], float c, Mass& 
   const float ref = mn == kNegInf ? 0.f : mn;
   const float cm = c * ref;
   float t[E];
-  if (__builtin_expect(fabsf(cm) <= 3e38f, 1)) {
+  if (!SUB && __builtin_expect(fabsf(cm) <= 3e38f, 1)) {
 #pragma unroll
     for (int e = 0; e < E; ++e) t[e] = fast_exp2(__builtin_fmaf(x[e], c, -cm));
   } else {

@@ -483,11 +483,29 @@ def draft_workspace_size(op, dt, rows, W, V, k) -> int:
     return n.value
 
 
+def _draft_workspace(dev, *shape):
+    need = draft_workspace_size(*shape)
+    ws = Workspace._cache.get(dev.index)
+    return ws if ws is not None and ws.numel() >= need else Workspace.get(dev, need)
+
+
+# The small calls of decoding take about as long on the host as on the GPU, so
+# these bindings pass addresses as plain integers and ask for the stream's
+# handle without building a Stream object (1.8 us).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
 def _one_device(what, first, *others):
     if not first.is_cuda:
         raise SpecVerifyError(SV_EINVAL, f"{what}: want tensors on the GPU, got {first.device}")
+    index = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != index:
             raise SpecVerifyError(SV_EINVAL, f"{what}: tensors on {first.device} and {t.device}")
     return first.device
 
@@ -495,10 +513,12 @@ def _one_device(what, first, *others):
 def _call(dev, fn, what, *args):
     """One launch with `dev` current, on its current stream."""
     if dev.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(dev)), what)
+        status = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, _stream(dev)), what)
+            status = fn(*args, _raw_stream(dev.index))
+    if status != SV_OK:
+        raise SpecVerifyError(status, what)
 
 
 def _f32_tensor(t, shape, what):
@@ -519,13 +539,12 @@ def sv_teacher_topk(logits, k, T, workspace=None):
     R, V = _rows_2d(logits, "logits")
     dt, k = _dtype_code(logits), int(k)
     dev = _one_device("sv_teacher_topk", logits, workspace)
-    ws = workspace if workspace is not None else Workspace.get(
-        dev, draft_workspace_size(SV_DRAFT_TEACHER, dt, R, 1, V, k))
+    ws = workspace if workspace is not None else _draft_workspace(dev, SV_DRAFT_TEACHER, dt, R, 1, V, k)
     out = dict(ids=torch.empty(R, k, dtype=torch.int32, device=dev),
                vals=torch.empty(R, k, dtype=torch.float32, device=dev),
                rest=torch.empty(R, dtype=torch.float32, device=dev))
-    _call(dev, _lib.sv_teacher_topk, "sv_teacher_topk", _ptr(logits), dt, _row_stride(logits, "logits"), R, V, k,
-          float(T), _ptr(out["ids"]), _ptr(out["vals"]), _ptr(out["rest"]), _ptr(ws), ws.numel())
+    _call(dev, _lib.sv_teacher_topk, "sv_teacher_topk", _at(logits), dt, _row_stride(logits, "logits"), R, V, k,
+          float(T), _at(out["ids"]), _at(out["vals"]), _at(out["rest"]), _at(ws), ws.numel())
     _checked(dev, "sv_teacher_topk", workspace)
     return out
 
@@ -545,8 +564,7 @@ def _distill_args(what, z, ids, vals, rest, grad_loss, grad, workspace):
         raise SpecVerifyError(SV_EINVAL, f"grad: want {z.dtype} {(R, V)}, got {grad.dtype} {tuple(grad.shape)}")
     dt = _dtype_code(z)
     dev = _one_device(what, z, ids, vals, rest, grad_loss, grad, workspace)
-    ws = workspace if workspace is not None else Workspace.get(
-        dev, draft_workspace_size(SV_DRAFT_DISTILL, dt, R, 1, V, k))
+    ws = workspace if workspace is not None else _draft_workspace(dev, SV_DRAFT_DISTILL, dt, R, 1, V, k)
     return R, V, k, dt, dev, ws
 
 
@@ -566,9 +584,9 @@ def sv_distill_topk(z, ids, vals, T, rest=None, grad_loss=None, want_grad=False,
         grad = _grad_rows(z, R, V)
     out = dict(loss=torch.empty(R, dtype=torch.float32, device=dev),
                stat=torch.empty(R, 4, dtype=torch.float32, device=dev), grad=grad)
-    _call(dev, _lib.sv_distill_topk, "sv_distill_topk", _ptr(z), dt, _row_stride(z, "z"), R, V, _ptr(ids), _ptr(vals),
-          _ptr(rest), k, float(T), _ptr(grad_loss), _ptr(out["loss"]), _ptr(out["stat"]), _ptr(grad),
-          _row_stride(grad, "grad") if grad is not None else 0, _ptr(ws), ws.numel())
+    _call(dev, _lib.sv_distill_topk, "sv_distill_topk", _at(z), dt, _row_stride(z, "z"), R, V, _at(ids), _at(vals),
+          _at(rest), k, float(T), _at(grad_loss), _at(out["loss"]), _at(out["stat"]), _at(grad),
+          _row_stride(grad, "grad") if grad is not None else 0, _at(ws), ws.numel())
     _checked(dev, "sv_distill_topk", workspace)
     return out
 
@@ -580,9 +598,9 @@ def sv_distill_topk_backward(z, ids, vals, stat, T, rest=None, grad_loss=None, g
     _one_device("sv_distill_topk_backward", z, stat)
     if grad is None:
         grad = _grad_rows(z, R, V)
-    _call(dev, _lib.sv_distill_topk_backward, "sv_distill_topk_backward", _ptr(z), dt, _row_stride(z, "z"), R, V,
-          _ptr(ids), _ptr(vals), _ptr(rest), k, float(T), _ptr(stat), _ptr(grad_loss), _ptr(grad),
-          _row_stride(grad, "grad"), _ptr(ws), ws.numel())
+    _call(dev, _lib.sv_distill_topk_backward, "sv_distill_topk_backward", _at(z), dt, _row_stride(z, "z"), R, V,
+          _at(ids), _at(vals), _at(rest), k, float(T), _at(stat), _at(grad_loss), _at(grad),
+          _row_stride(grad, "grad"), _at(ws), ws.numel())
     _checked(dev, "sv_distill_topk_backward", workspace)
     return grad
 
@@ -600,29 +618,33 @@ def sv_beam_select(logits, scores, N, T=1.0, finished=None, pad_tok=0, workspace
     if not -(1 << 31) <= pad < 1 << 31:
         raise SpecVerifyError(SV_EINVAL, f"pad_tok {pad} outside int32")
     dev = _one_device("sv_beam_select", logits, scores, finished, workspace)
-    ws = workspace if workspace is not None else Workspace.get(
-        dev, draft_workspace_size(SV_DRAFT_BEAM, dt, B, W, V, N))
+    ws = workspace if workspace is not None else _draft_workspace(dev, SV_DRAFT_BEAM, dt, B, W, V, N)
     out = dict(beam=torch.empty(B, N, dtype=torch.int32, device=dev),
                tok=torch.empty(B, N, dtype=torch.int32, device=dev),
                score=torch.empty(B, N, dtype=torch.float32, device=dev))
-    _call(dev, _lib.sv_beam_select, "sv_beam_select", _ptr(logits), dt, _row_stride(logits, "logits"), _ptr(scores),
-          _ptr(finished), B, W, V, float(T), pad, N, _ptr(out["beam"]), _ptr(out["tok"]), _ptr(out["score"]), _ptr(ws),
+    _call(dev, _lib.sv_beam_select, "sv_beam_select", _at(logits), dt, _row_stride(logits, "logits"), _at(scores),
+          _at(finished), B, W, V, float(T), pad, N, _at(out["beam"]), _at(out["tok"]), _at(out["score"]), _at(ws),
           ws.numel())
     _checked(dev, "sv_beam_select", workspace)
     return out
 
 
 def _state_layout(t, pos_dim, what):
-    """(L, B, beams, H, S), position bytes and the strides in bytes of a state [L, B, beams, ...]."""
-    shape, st, es = t.shape, t.stride(), t.element_size()
-    if t.dim() < 3:
+    return _state_layout_of(t.shape, t.stride(), t.element_size(), pos_dim, what)
+
+
+@functools.lru_cache(maxsize=1024)
+def _state_layout_of(shape, st, es, pos_dim, what):
+    """(L, B, beams, H, S, position bytes) and the strides in bytes of a state [L, B, beams, ...]."""
+    dims = len(shape)
+    if dims < 3:
         raise SpecVerifyError(SV_EINVAL, f"{what}: want [L, B, beams, ...], got {tuple(shape)}")
-    p = t.dim() if pos_dim is None else int(pos_dim)
-    if pos_dim is not None and not 3 <= p < t.dim():
-        raise SpecVerifyError(SV_EINVAL, f"{what}: pos_dim {pos_dim} of a state of {t.dim()} dimensions")
+    p = dims if pos_dim is None else int(pos_dim)
+    if pos_dim is not None and not 3 <= p < dims:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: pos_dim {pos_dim} of a state of {dims} dimensions")
     first = 3 if pos_dim is None else p  # dimensions from here on are adjacent in memory
     run = 1
-    for ax in range(t.dim() - 1, first - 1, -1):
+    for ax in range(dims - 1, first - 1, -1):
         if shape[ax] > 1 and st[ax] != run:
             raise SpecVerifyError(SV_EINVAL, f"{what}: the values of a position and the positions must be adjacent")
         run *= shape[ax]
@@ -663,9 +685,8 @@ def sv_beam_reorder(state, parent, pos_dim=None, lens=None, out=None, workspace=
     elif Nd != N or dst.shape[:2] != state.shape[:2] or dst.shape[3:] != state.shape[3:]:
         raise SpecVerifyError(SV_EINVAL, f"out: shape {tuple(dst.shape)} for {N} beams of {tuple(state.shape)}")
     dev = _one_device("sv_beam_reorder", state, dst, parent, lens, workspace)
-    ws = workspace if workspace is not None else Workspace.get(
-        dev, draft_workspace_size(SV_DRAFT_REORDER, 0, 0, 0, 0, 0))
-    _call(dev, _lib.sv_beam_reorder, "sv_beam_reorder", _ptr(state), ss, _ptr(dst), ds, _ptr(parent), _ptr(lens), L, B,
-          W, N, H, S, pos, _ptr(ws), ws.numel())
+    ws = workspace if workspace is not None else _draft_workspace(dev, SV_DRAFT_REORDER, 0, 0, 0, 0, 0)
+    _call(dev, _lib.sv_beam_reorder, "sv_beam_reorder", _at(state), ss, _at(dst), ds, _at(parent), _at(lens), L, B,
+          W, N, H, S, pos, _at(ws), ws.numel())
     _checked(dev, "sv_beam_reorder", workspace)
     return dst
