@@ -24,40 +24,46 @@ namespace sv {
 
 constexpr int kDNT = 256;
 constexpr int kDU = 4;     // vectors in flight per thread
-static_assert(SV_MAX_TEACHER <= kDNT, "a thread a teacher token");
+static_assert(SV_MAX_TEACHER == kDNT, "a thread a teacher token");
 
-// Loads them (every thread of a block of at least SV_MAX_TEACHER threads).
-// Out-of-range and repeated ids are flagged and become absent.  Returns
-// whether the row has teacher mass, in every thread.
-template <int DT>
-__device__ __forceinline__ bool load_teacher(const DistillParams& a, int r, const void* row, Teacher& s, bool report) {
-  const int i = threadIdx.x;
-  int32_t id = -1;
-  float t = kNegInf;
-  if (i < a.k) {
-    id = a.ids[(int64_t)r * a.k + i];
-    t = a.vals[(int64_t)r * a.k + i];
+// A row's teacher on its way: thread i holds token i, its value, the rest.
+struct Fetched {
+  int32_t id;
+  float t, rest;
+};
+__device__ __forceinline__ Fetched fetch_teacher(const DistillParams& a, int r) {
+  Fetched f{-1, kNegInf, kNegInf};
+  if ((int)threadIdx.x < a.k) {
+    f.id = a.ids[(int64_t)r * a.k + threadIdx.x];
+    f.t = a.vals[(int64_t)r * a.k + threadIdx.x];
   }
-  const float rest = a.rest ? a.rest[r] : kNegInf;
-  bool bad = id < -1 || id >= a.V;
-  if (bad) id = -1;
-  if (i < SV_MAX_TEACHER) s.id[i] = id;
-  if (i == 0) s.live = rest > kNegInf;
+  if (a.rest) f.rest = a.rest[r];
+  return f;
+}
+
+// Into LDS (a block of at least SV_MAX_TEACHER threads).  Out-of-range and
+// repeated ids are flagged and become absent.  Returns whether the row has
+// teacher mass, in every thread; the drafter's logits are loaded if so.
+template <int DT>
+__device__ __forceinline__ bool place_teacher(const DistillParams& a, Fetched f, const void* row, Teacher& s,
+                                              bool report) {
+  const int i = threadIdx.x;
+  const bool bad = f.id < -1 || f.id >= a.V;
+  if (bad) f.id = -1;
+  s.id[i] = f.id;
+  if (i == 0) s.live = f.rest > kNegInf;
   lds_sync();
   bool twice = false;
-  if (id >= 0)
-    for (int j = 0; j < i; ++j) twice |= s.id[j] == id;
+  if (i < ((a.k + kWave - 1) & ~(kWave - 1))) twice = repeated(s.id, i, f.id, a.k);
   if (report && (bad || twice)) set_error(a.err, SV_DERR_TOKEN);
+  if (twice) f.id = -1;
+  s.t[i] = f.id >= 0 ? f.t : kNegInf;
+  if (f.id >= 0 && f.t > kNegInf) s.live = 1;
   lds_sync();
-  if (twice) id = -1;
-  if (i < SV_MAX_TEACHER) {
-    s.id[i] = id;
-    s.t[i] = id >= 0 ? t : kNegInf;
-    if (id >= 0 && t > kNegInf) s.live = 1;
-    s.z[i] = id >= 0 ? load_elem<DT>(row, id) : kNegInf;
-  }
-  lds_sync();
-  return s.live != 0;
+  const bool live = s.live != 0;
+  s.id[i] = f.id;
+  s.z[i] = live && f.id >= 0 ? load_elem<DT>(row, f.id) : kNegInf;
+  return live;
 }
 
 // The loss and the statistics of one row from the sum outside I, by one wave.
@@ -135,8 +141,15 @@ __global__ __launch_bounds__(kDNT) void distill_loss_kernel(DistillParams a) {
   const void* row = row_ptr(a.z, r, a.sb);
   const int64_t v0 = (int64_t)ch * a.vpc;
   const int64_t nv = (v0 + a.vpc < a.nvec ? v0 + a.vpc : a.nvec) - v0;
+  // the row's first vectors are on their way while its teacher is prepared
+  const Fetched f = fetch_teacher(a, r);
+  const __amdgpu_buffer_rsrc_t rs = range_rsrc(static_cast<const u32x4*>(row) + v0, (uint32_t)(nv * 16));
+  uint32_t off = threadIdx.x * 16u;
+  u32x4 cur[kDU];
+#pragma unroll
+  for (int u = 0; u < kDU; ++u) cur[u] = load_range(rs, off + (uint32_t)(u * kDNT * 16));
   for (int i = threadIdx.x; i < (int)(nv + 3) / 4; i += kDNT) s_mark[i] = 0u;
-  if (!load_teacher<DT>(a, r, row, s, ch == 0)) {  // block-uniform, the same for all of the row's blocks
+  if (!place_teacher<DT>(a, f, row, s, ch == 0)) {  // block-uniform, the same for all of the row's blocks
     if (ch == 0 && threadIdx.x == 0) {
       a.out_loss[r] = 0.f;
       reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -152,13 +165,8 @@ __global__ __launch_bounds__(kDNT) void distill_loss_kernel(DistillParams a) {
   const uint8_t* mark = reinterpret_cast<const uint8_t*>(s_mark);
   Mass acc;
   {
-    const __amdgpu_buffer_rsrc_t rs = range_rsrc(static_cast<const u32x4*>(row) + v0, (uint32_t)(nv * 16));
     // groups of kDU * kDNT vectors; the last one is masked (and may hold the row's end)
     const int64_t full = (nv - 1) / (kDU * kDNT);
-    uint32_t off = threadIdx.x * 16u;
-    u32x4 cur[kDU];
-#pragma unroll
-    for (int u = 0; u < kDU; ++u) cur[u] = load_range(rs, off + (uint32_t)(u * kDNT * 16));
     for (int64_t k = 0; k < full; ++k) {
       off += kDU * kDNT * 16;
       u32x4 nxt[kDU];
@@ -229,13 +237,23 @@ __global__ __launch_bounds__(kDNT) void distill_grad_kernel(DistillParams a) {
   const int64_t v1 = v0 + a.vpc2 < a.nvec ? v0 + a.vpc2 : a.nvec;
   const int64_t nfull = a.V / E;
   const int64_t vf = v1 < nfull ? v1 : nfull;  // whole vectors; the row's last one may be shorter
+  // the part's first vectors are on their way while the row's factors are formed
+  const Fetched f = fetch_teacher(a, r);
+  u32x4 d[kDU];
+#pragma unroll
+  for (int u = 0; u < kDU; ++u) {
+    const int64_t v = v0 + threadIdx.x + u * kDNT;
+    if (v < vf) d[u] = load_vec(row, v);
+  }
   const float4 st = reinterpret_cast<const float4*>(a.stat)[r];
   if (!(st.y > 0.f)) {  // no teacher mass, or no finite logit
-    for (int64_t v = v0 + threadIdx.x; v < vf; v += kDNT) outv[v] = u32x4{0u, 0u, 0u, 0u};
+    for (int64_t v = v0 + threadIdx.x; v < vf; v += kDNT)
+      __builtin_nontemporal_store(u32x4{0u, 0u, 0u, 0u}, outv + v);
     if (v1 > nfull && threadIdx.x < a.V - nfull * E) store_elem<DT>(out, nfull * E + threadIdx.x, 0.f);
     return;
   }
-  load_teacher<DT>(a, r, row, s, ch == 0);
+  place_teacher<DT>(a, f, row, s, ch == 0);
+  lds_sync();
   if (wave == 0) {
     const GradRow g = wave_grad_row(a, r, s, st, lane);
     if (lane == 0) s_g = g;
@@ -243,13 +261,12 @@ __global__ __launch_bounds__(kDNT) void distill_grad_kernel(DistillParams a) {
   lds_sync();
   const GradRow g = s_g;
   for (int64_t v = v0 + threadIdx.x; v < vf; v += kDU * kDNT) {
-    u32x4 d[kDU];
 #pragma unroll
     for (int u = 0; u < kDU; ++u)
-      if (v + u * kDNT < vf) d[u] = load_vec(row, v + u * kDNT);
+      if (v + u * kDNT < vf) __builtin_nontemporal_store(grad_vec<DT>(d[u], g, a.c), outv + v + u * kDNT);
 #pragma unroll
     for (int u = 0; u < kDU; ++u)
-      if (v + u * kDNT < vf) outv[v + u * kDNT] = grad_vec<DT>(d[u], g, a.c);
+      if (v + (kDU + u) * kDNT < vf) d[u] = load_vec(row, v + (kDU + u) * kDNT);
   }
   if (v1 > nfull && threadIdx.x < a.V - nfull * E) {
     const int e = threadIdx.x;

@@ -36,40 +36,42 @@ __device__ __forceinline__ void store_elem_alias(void* row, int64_t i, float x) 
     reinterpret_cast<f32_alias*>(row)[i] = x;
 }
 
-// A row's teacher on its way into LDS: thread i holds token i.
+// A row's teacher on its way into LDS.  Token i is held by the i-th thread
+// from the block's last SV_MAX_TEACHER on (wave 0 has the scalar work).
 struct Fetched {
   int32_t id;
   float t, rest;
 };
-__device__ __forceinline__ Fetched fetch_teacher(const DistillParams& a, int r) {
+__device__ __forceinline__ Fetched fetch_teacher(const DistillParams& a, int r, int i) {
   Fetched f{-1, kNegInf, kNegInf};
-  if ((int)threadIdx.x < a.k) {
-    f.id = a.ids[(int64_t)r * a.k + threadIdx.x];
-    f.t = a.vals[(int64_t)r * a.k + threadIdx.x];
+  if (i >= 0 && i < a.k) {
+    f.id = a.ids[(int64_t)r * a.k + i];
+    f.t = a.vals[(int64_t)r * a.k + i];
   }
   if (a.rest) f.rest = a.rest[r];
   return f;
 }
-// First half: the ids in range.  A barrier, then the second half: repeats
-// out, liveness.  (Visible after the next barrier.)
-__device__ __forceinline__ void teacher_ids(const DistillParams& a, Fetched& f, Teacher& s) {
+// The ids in range.  After a barrier, teacher_tokens.
+__device__ __forceinline__ void teacher_ids(const DistillParams& a, Fetched& f, Teacher& s, int i) {
   if (f.id < -1 || f.id >= a.V) {
     set_error(a.err, SV_DERR_TOKEN);
     f.id = -1;
   }
-  if (threadIdx.x < SV_MAX_TEACHER) s.id[threadIdx.x] = f.id;
-  if (threadIdx.x == 0) s.live = f.rest > kNegInf;
+  if (i >= 0) s.id[i] = f.id;
+  if (i == 0) s.live = f.rest > kNegInf;
 }
-// The repeats are found here and taken out of s.id by the caller after another barrier (drop_repeats).
-__device__ __forceinline__ bool teacher_live(const DistillParams& a, Fetched& f, Teacher& s) {
-  bool twice = false;
-  if (f.id >= 0)
-    for (int j = 0; j < (int)threadIdx.x; ++j) twice |= s.id[j] == f.id;
+// Repeats out, the values in, whether there is mass at all.  Final after a
+// barrier, but for s.id, from which the caller takes the repeats (-1: true)
+// behind that barrier.
+__device__ __forceinline__ bool teacher_tokens(const DistillParams& a, Fetched& f, Teacher& s, int i) {
+  if (i < 0) return false;
+  if (i >= ((a.k + kWave - 1) & ~(kWave - 1))) return false;  // a wave without tokens
+  const bool twice = repeated(s.id, i, f.id, a.k);
   if (twice) {
     set_error(a.err, SV_DERR_TOKEN);
     f.id = -1;
   }
-  if (threadIdx.x < SV_MAX_TEACHER) s.t[threadIdx.x] = f.id >= 0 ? f.t : kNegInf;
+  s.t[i] = f.id >= 0 ? f.t : kNegInf;
   if (f.id >= 0 && f.t > kNegInf) s.live = 1;
   return twice;
 }
@@ -95,32 +97,27 @@ template <int DT, int NT, int NV>
 __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
   constexpr int E = Fmt<DT>::kPerVec;
   constexpr int NW = NT / kWave;
-  constexpr int FU = 2;  // vectors folded at a time
-  static_assert(NV % FU == 0 && NT >= SV_MAX_TEACHER && NW <= kWave, "shape");
-  __shared__ uint32_t s_mark[NV * NT / 4];
+  constexpr int FU = 2;                   // vectors folded at a time
+  constexpr int LAG = NV < 4 ? NV : 4;    // loads ahead of the fold
+  constexpr int kMarks = NV * NT / 4;     // words of marks
+  static_assert(NV % FU == 0 && LAG % FU == 0 && NT >= SV_MAX_TEACHER && NW <= kWave, "shape");
+  __shared__ uint32_t s_mark[2][kMarks];
   __shared__ Teacher s_t[2];
   __shared__ double s_p[SV_MAX_TEACHER];  // the teacher's probabilities
   __shared__ float s_max[NW];
   __shared__ double s_sum[NW];
+  // wave 0's scalars wait here between the steps that use them: in registers
+  // they would push parts of the row out to memory
+  __shared__ volatile double s_c[8];
+  enum { kNm, kNz, kS0, kSum, kInv, kP0, kScale, kL0 };
   __shared__ GradRow s_g;
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int wave = tid / kWave;
+  const int ti = tid - (NT - SV_MAX_TEACHER);  // this thread's teacher token (negative: none)
   const int nvec = (int)a.nvec;
   const int nfull = a.V / E;
   const int tail = a.V - nfull * E;  // elements of the last, shorter vector
-  const uint8_t* mark = reinterpret_cast<const uint8_t*>(s_mark);
-  // marks: none, but for what lies past V
-  for (int i = tid; i < NV * NT / 4; i += NT) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int v = i * 4 + j;
-      const uint32_t b = v < nfull ? 0u : v == nfull && tail ? (0xffu << tail) & 0xffu : 0xffu;
-      m |= b << (8 * j);
-    }
-    s_mark[i] = m;
-  }
   int r = blockIdx.x;
   if (r >= a.R) return;
   u32x4 d[NV];
@@ -128,24 +125,79 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
   // a row that is not read is a range of no bytes, whose loads give zeros
   auto row_range = [&](int row, bool read) { return range_rsrc(row_of(row), read ? (uint32_t)nvec * 16u : 0u); };
   const uint32_t off0 = (uint32_t)tid * 16u;
-  // the first row's teacher
+  Mass acc;
+  // FU vectors from i on: the marked tokens leave the row for good (their
+  // gradients are stored apart), the others go into the mass
+  auto fold = [&](int i, const uint8_t* mark) {
+    uint32_t mk[FU], any = 0;
+    float x[FU * E];
+#pragma unroll
+    for (int u = 0; u < FU; ++u) any |= mk[u] = mark[(i + u) * NT + tid];
+    if (any) {
+#pragma unroll
+      for (int u = 0; u < FU; ++u) mask_vec<DT>(d[i + u], mk[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < FU; ++u) unpack<DT>(d[i + u], x + u * E);
+    fold_values<FU * E, true>(x, a.c, acc);
+  };
+  auto set_mark = [&](int b, int32_t id) { atomicOr(&s_mark[b][id / E / 4], 1u << ((id / E % 4) * 8 + id % E)); };
+  auto clear_mark = [&](int b, int32_t id) { atomicAnd(&s_mark[b][id / E / 4], ~(1u << ((id / E % 4) * 8 + id % E))); };
+  // wave 0: a row's teacher as probabilities
+  auto teacher_probs = [&](int row, const Teacher& s) {
+    const Norm n = wave_teacher_norm(s, a.k, a.rest ? (double)a.rest[row] : -__builtin_huge_val(), a.invT, lane);
+#pragma unroll 1
+    for (int i = lane; i < a.k; i += kWave)
+      s_p[i] = s.t[i] > kNegInf ? exp_d((double)s.t[i] * a.invT - n.m) / n.z : 0.0;
+    if (lane == 0) {
+      s_c[kNm] = n.m;
+      s_c[kNz] = n.z;
+    }
+  };
+  // the first row: its teacher, its vectors, its mass
   int b = 0;
-  float z = kNegInf, ztail = 0.f;
+  Fetched cur = fetch_teacher(a, r, ti);
   {
-    Fetched f = fetch_teacher(a, r);
-    teacher_ids(a, f, s_t[0]);
-    lds_sync();
-    const bool twice = teacher_live(a, f, s_t[0]);
-    lds_sync();
-    if (twice) s_t[0].id[tid] = -1;
-    lds_sync();
-    const bool live = s_t[0].live != 0;
-    const __amdgpu_buffer_rsrc_t rs = row_range(r, live);
-    if (live && f.id >= 0) z = load_elem<DT>(row_of(r), f.id);
-    if (live && tid < tail) ztail = load_elem<DT>(row_of(r), (int64_t)nfull * E + tid);
+    // its vectors are on their way while its teacher is prepared
+    const __amdgpu_buffer_rsrc_t rs = row_range(r, true);
 #pragma unroll
     for (int i = 0; i < NV; ++i) d[i] = load_range(rs, off0 + (uint32_t)(i * NT * 16));
   }
+  // marks: none, but for what lies past V
+  for (int i = tid; i < kMarks; i += NT) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int v = i * 4 + j;
+      const uint32_t w = v < nfull ? 0u : v == nfull && tail ? (0xffu << tail) & 0xffu : 0xffu;
+      m |= w << (8 * j);
+    }
+    s_mark[0][i] = s_mark[1][i] = m;
+  }
+  float z = kNegInf, ztail = 0.f;
+  {
+    teacher_ids(a, cur, s_t[0], ti);
+    lds_sync();
+    const bool twice = teacher_tokens(a, cur, s_t[0], ti);
+    if (cur.id >= 0) set_mark(0, cur.id);
+    lds_sync();
+    if (twice) s_t[0].id[ti] = -1;
+    const bool live = s_t[0].live != 0;
+    if (live && cur.id >= 0) z = load_elem<DT>(row_of(r), cur.id);
+    if (live && tid < tail) ztail = load_elem<DT>(row_of(r), (int64_t)nfull * E + tid);
+    if (!live) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) d[i] = u32x4{0u, 0u, 0u, 0u};
+    } else {
+      if (wave == 0) teacher_probs(r, s_t[0]);
+#pragma unroll
+      for (int i = 0; i < NV; i += FU) {
+        fold(i, reinterpret_cast<const uint8_t*>(s_mark[0]));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+  // a row a turn: its vectors are here and summed up thread by thread
   for (;;) {
     Teacher& s = s_t[b];
     Teacher& sn = s_t[b ^ 1];
@@ -153,120 +205,109 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
     const int rn = r + (int)gridDim.x;
     const bool next = rn < a.R;
     Fetched f{-1, kNegInf, kNegInf};
-    if (next) f = fetch_teacher(a, rn);
-    const int32_t id = tid < SV_MAX_TEACHER ? s.id[tid] : -1;
-    if (live && id >= 0) atomicOr(&s_mark[id / E / 4], 1u << ((id / E % 4) * 8 + id % E));
-    lds_sync();  // A: the marks
-    // the teacher's normaliser and probabilities (wave 0), while the row arrives
-    Norm n{0.0, 1.0};
-    const double rest = a.rest ? (double)a.rest[r] : -__builtin_huge_val();
-    if (live && wave == 0) {
-      n = wave_teacher_norm(s, a.k, rest, a.invT, lane);
-#pragma unroll 1
-      for (int i = lane; i < a.k; i += kWave)
-        s_p[i] = s.t[i] > kNegInf ? exp_d((double)s.t[i] * a.invT - n.m) / n.z : 0.0;
+    if (next) f = fetch_teacher(a, rn, ti);
+    const float wm = wave_fmax(acc.m);
+    const double ws = wave_sum(acc.m == kNegInf ? 0.0 : (double)acc.s * (double)fast_exp2((acc.m - wm) * a.c));
+    if (lane == 0) {
+      s_max[wave] = wm;
+      s_sum[wave] = ws;
     }
-    Mass acc;
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < NV; i += FU) {
-        // the marked tokens leave the row for good: their gradients are stored apart
-        uint32_t mk[FU], any = 0;
-        float x[FU * E];
-#pragma unroll
-        for (int u = 0; u < FU; ++u) any |= mk[u] = mark[(i + u) * NT + tid];
-        if (any) {
-#pragma unroll
-          for (int u = 0; u < FU; ++u) mask_vec<DT>(d[i + u], mk[u]);
-        }
-#pragma unroll
-        for (int u = 0; u < FU; ++u) unpack<DT>(d[i + u], x + u * E);
-        fold_values<FU * E, true>(x, a.c, acc);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (tid < SV_MAX_TEACHER) s.z[tid] = id >= 0 ? z : kNegInf;
-      const float wm = wave_fmax(acc.m);
-      const double ws = wave_sum(acc.m == kNegInf ? 0.0 : (double)acc.s * (double)fast_exp2((acc.m - wm) * a.c));
-      if (lane == 0) {
-        s_max[wave] = wm;
-        s_sum[wave] = ws;
-      }
-    }
-    if (next) teacher_ids(a, f, sn);
+    if (ti >= 0) s.z[ti] = live && cur.id >= 0 ? z : kNegInf;
+    if (next) teacher_ids(a, f, sn, ti);
     lds_sync();  // B: every wave's mass, the drafter's logits of I, the next row's ids
-    bool twice = false;
-    if (next) twice = teacher_live(a, f, sn);
-    if (live && id >= 0) atomicAnd(&s_mark[id / E / 4], ~(1u << ((id / E % 4) * 8 + id % E)));
-    float st_m = 0.f, st_s = 0.f, st_m0 = 0.f, st_s0 = 0.f, loss = 0.f;
-    if (live && wave == 0) {
+    if (wave == 0) {
       // the mass outside I, the whole row's, and the gradient's factors
-      const float wm = lane < NW ? s_max[lane] : kNegInf;
-      const double ws = lane < NW ? s_sum[lane] : 0.0;
-      const float m0 = wave_fmax(wm);
-      const double s0 = wave_sum(ws * rescale(wm, m0, a.c));
-      float m = kNegInf;
-#pragma unroll 1
-      for (int i = lane; i < a.k; i += kWave) m = fmaxf(m, s.z[i]);
-      m = fmaxf(wave_fmax(m), m0);
+      float4 stat = make_float4(0.f, 0.f, 0.f, 0.f);
       GradRow g{0.f, 0.f};
-      if (m > kNegInf) {
-        double sum = 0.0;
-  #pragma unroll 1
-      for (int i = lane; i < a.k; i += kWave)
-          if (s.z[i] > kNegInf) sum += exp_d(((double)s.z[i] - (double)m) * a.invT);
-        sum = wave_sum(sum);
-        const double out = s0 > 0.0 ? s0 * exp_d(((double)m0 - (double)m) * a.invT) : 0.0;
-        sum += out;
-        const double inv = 1.0 / sum;
-        const double p0 = exp_d(rest - n.m) / n.z;
-        const double scale = (a.g ? (double)a.g[r] : 1.0) * a.invT;
-        g = grad_row(m, p0, out * inv, scale, inv);
-        // the loss, and the gradient at the tokens of I in place of their logits
-        const double ln = log_d(lane == 0 ? n.z : lane == 1 ? sum : s0);
-        const double lt = n.m + readlane_d(ln, 0), lq = (double)m * a.invT + readlane_d(ln, 1);
-        double l = 0.0;
-  #pragma unroll 1
-      for (int i = lane; i < a.k; i += kWave) {
-          const double p = s_p[i], zi = (double)s.z[i] * a.invT;
-          if (p > 0.0) l += p * (((double)s.t[i] * a.invT - lt) - (zi - lq));
-          const double q = s.z[i] > kNegInf ? exp_d(zi - (double)m * a.invT) * inv : 0.0;
-          s.z[i] = (float)((q - p) * scale);
-        }
-        l = wave_sum(l);
-        if (p0 > 0.0) l += p0 * ((rest - lt) - ((double)m0 * a.invT + readlane_d(ln, 2) - lq));
-        loss = (float)l;
-        st_m = m;
-        st_s = (float)sum;
-        st_m0 = m0;
-        st_s0 = (float)s0;
-      } else {
-        if (lane == 0) set_error(a.err, SV_DERR_ROW);
-  #pragma unroll 1
-      for (int i = lane; i < a.k; i += kWave) s.z[i] = 0.f;
-      }
-      if (lane == 0) s_g = g;
-    } else if (wave == 0) {
-      if (lane == 0) s_g = GradRow{0.f, 0.f};
+      double loss = 0.0;
+      float m = kNegInf;
+      if (live) {
+        const float pm = lane < NW ? s_max[lane] : kNegInf;
+        const double ps = lane < NW ? s_sum[lane] : 0.0;
+        stat.z = wave_fmax(pm);
+        s_c[kS0] = wave_sum(ps * rescale(pm, stat.z, a.c));
 #pragma unroll 1
-      for (int i = lane; i < a.k; i += kWave) s.z[i] = 0.f;
+        for (int i = lane; i < a.k; i += kWave) m = fmaxf(m, s.z[i]);
+        m = fmaxf(wave_fmax(m), stat.z);
+        if (m == kNegInf && lane == 0) set_error(a.err, SV_DERR_ROW);
+      }
+      if (m > kNegInf) {
+        {
+          double sum = 0.0;
+#pragma unroll 1
+          for (int i = lane; i < a.k; i += kWave)
+            if (s.z[i] > kNegInf) sum += exp_d(((double)s.z[i] - (double)m) * a.invT);
+          sum = wave_sum(sum);
+          const double s0 = s_c[kS0];
+          const double out = s0 > 0.0 ? s0 * exp_d(((double)stat.z - (double)m) * a.invT) : 0.0;
+          sum += out;
+          const double inv = 1.0 / sum;
+          const double rest = a.rest ? (double)a.rest[r] : -__builtin_huge_val();
+          const double p0 = exp_d(rest - s_c[kNm]) / s_c[kNz];
+          const double scale = (a.g ? (double)a.g[r] : 1.0) * a.invT;
+          g = grad_row(m, p0, out * inv, scale, inv);
+          s_c[kSum] = sum;
+          s_c[kInv] = inv;
+          s_c[kP0] = p0;
+          s_c[kScale] = scale;
+          stat = make_float4(m, (float)sum, stat.z, (float)s0);
+        }
+        // the loss: log p_i - log q_i = t_i / T - z_i / T - (log of the
+        // normalisers), the last of which are the same for all i; and the
+        // gradient at the tokens of I in place of their logits
+        const double ln = log_d(lane == 0 ? s_c[kNz] : lane == 1 ? s_c[kSum] : s_c[kS0]);
+        const double lt = s_c[kNm] + readlane_d(ln, 0), lq = (double)m * a.invT + readlane_d(ln, 1);
+        s_c[kL0] = lt - lq + (double)stat.z * a.invT + readlane_d(ln, 2);  // of the others, but for rest
+#pragma unroll 1
+        for (int i = lane; i < a.k; i += kWave) {
+          const double zi = (double)s.z[i] * a.invT;
+          const double p = s_p[i];
+          if (p > 0.0) loss += p * (((double)s.t[i] * a.invT - zi) - (lt - lq));
+          const double q = s.z[i] > kNegInf ? exp_d(zi - (double)m * a.invT) * s_c[kInv] : 0.0;
+          s.z[i] = (float)((q - p) * s_c[kScale]);
+        }
+        loss = wave_sum(loss);
+        if (s_c[kP0] > 0.0) loss += s_c[kP0] * ((double)a.rest[r] - s_c[kL0]);
+      } else {
+        stat.z = 0.f;
+        for (int i = lane; i < a.k; i += kWave) s.z[i] = 0.f;
+      }
+      if (lane == 0) {
+        s_g = g;
+        a.out_loss[r] = (float)loss;
+        reinterpret_cast<float4*>(a.out_stat)[r] = stat;
+      }
     }
-    lds_sync();  // C: the factors, the gradients of I, the next row's liveness
-    if (twice) sn.id[tid] = -1;
+    // meanwhile: this row's marks go, the next row's tokens and marks come
+    if (cur.id >= 0) clear_mark(b, cur.id);
+    bool twice = false;
+    if (next) {
+      twice = teacher_tokens(a, f, sn, ti);
+      if (f.id >= 0) set_mark(b ^ 1, f.id);
+    }
+    lds_sync();  // C: the factors, the gradients of I, the next row's teacher and marks
+    if (twice) sn.id[ti] = -1;
     const bool nlive = next && sn.live != 0;
     const __amdgpu_buffer_rsrc_t rs = row_range(nlive ? rn : r, nlive);
     char* out = static_cast<char*>(a.grad) + (int64_t)r * a.gb;
     const __amdgpu_buffer_rsrc_t ro = range_rsrc(out, (uint32_t)nfull * 16u);
+    const GradRow g = s_g;
+    z = kNegInf;
     float zt = 0.f;
     if (nlive) {
       if (f.id >= 0) z = load_elem<DT>(row_of(rn), f.id);
       if (tid < tail) zt = load_elem<DT>(row_of(rn), (int64_t)nfull * E + tid);
     }
-    const GradRow g = s_g;
-    {
-      uint32_t off = off0;
-      asm volatile("" : "+v"(off));  // the NV offsets are formed as they are used, not kept
+    if (nlive && wave == 0) teacher_probs(rn, sn);
+    acc = Mass{};
+    // store this row's gradient, load the next row behind it, and fold that
+    // LAG vectors behind the loads
+    const uint8_t* mark = reinterpret_cast<const uint8_t*>(s_mark[b ^ 1]);
+    uint32_t off = off0;
+    asm volatile("" : "+v"(off));  // the NV offsets are formed as they are used, not kept
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NV + LAG; ++i) {
+      if (i < NV) {
         // the row stays packed: without this the compiler keeps the fold's
         // unpacked values alive beside it, twice the registers there are
         asm volatile("" : "+v"(d[i]));
@@ -275,34 +316,35 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
         off += NT * 16;
         __builtin_amdgcn_sched_barrier(0);
       }
+      if (i >= LAG && (i - LAG) % FU == FU - 1) {
+        if (nlive) fold(i - LAG - (FU - 1), mark);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
     if (tid < tail) store_elem_alias<DT>(out, (int64_t)nfull * E + tid, grad_elem(ztail, g, a.c));
     // the tokens of I whose vectors this wave's threads stored
     for (int i0 = 0; i0 < a.k; i0 += kWave) {
       const int i = i0 + lane;
-      const int32_t ti = i < a.k ? s.id[i] : -1;
-      const float tv = i < a.k ? s.z[i] : 0.f;
+      const int32_t id = i < a.k ? s.id[i] : -1;
+      const float gv = i < a.k ? s.z[i] : 0.f;
       // in the shorter last vector thread e stored element e
-      const int owner = ti / E < nfull ? ti / E % NT : ti - nfull * E;
-      uint64_t mine = __ballot(ti >= 0 && owner / kWave == wave);
+      const int owner = id / E < nfull ? id / E % NT : id - nfull * E;
+      uint64_t mine = __ballot(id >= 0 && owner / kWave == wave);
       while (mine) {
         const int q = __builtin_ctzll(mine);
         mine &= mine - 1;
-        const int oid = __builtin_amdgcn_readlane(ti, q);
-        const float ov = readlane_f(tv, q);
+        const int oid = __builtin_amdgcn_readlane(id, q);
+        const float ov = readlane_f(gv, q);
         const int ol = __builtin_amdgcn_readlane(owner, q) & (kWave - 1);
         if (lane == ol) store_elem_alias<DT>(out, oid, ov);
       }
     }
-    if (tid == 0) {
-      a.out_loss[r] = loss;
-      reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(st_m, st_s, st_m0, st_s0);
-    }
     if (!next) return;
     ztail = zt;
+    cur.id = f.id;
     r = rn;
     b ^= 1;
-    lds_sync();  // the next row's ids are final; this row's teacher may be overwritten
+    lds_sync();  // the tokens of I are stored: their row in LDS may be written again
   }
 }
 
