@@ -41,12 +41,12 @@ __device__ __forceinline__ Fetched fetch_teacher(const DistillParams& a, int r) 
   return f;
 }
 
-// Into LDS (a block of at least SV_MAX_TEACHER threads).  Out-of-range and
-// repeated ids are flagged and become absent.  Returns whether the row has
-// teacher mass, in every thread; the drafter's logits are loaded if so.
+// Into LDS: thread i has token i.  Out-of-range and repeated ids are flagged
+// and become absent.  Returns whether the row has teacher mass, in every
+// thread; if so *z is on its way, the drafter's logit of the thread's token.
 template <int DT>
-__device__ __forceinline__ bool place_teacher(const DistillParams& a, Fetched f, const void* row, Teacher& s,
-                                              bool report) {
+__device__ __forceinline__ bool place_teacher(const DistillParams& a, Fetched& f, const void* row, Teacher& s,
+                                              bool report, float* z) {
   const int i = threadIdx.x;
   const bool bad = f.id < -1 || f.id >= a.V;
   if (bad) f.id = -1;
@@ -57,51 +57,14 @@ __device__ __forceinline__ bool place_teacher(const DistillParams& a, Fetched f,
   if (i < ((a.k + kWave - 1) & ~(kWave - 1))) twice = repeated(s.id, i, f.id, a.k);
   if (report && (bad || twice)) set_error(a.err, SV_DERR_TOKEN);
   if (twice) f.id = -1;
-  s.t[i] = f.id >= 0 ? f.t : kNegInf;
   if (f.id >= 0 && f.t > kNegInf) s.live = 1;
   lds_sync();
   const bool live = s.live != 0;
+  *z = kNegInf;
+  if (live && f.id >= 0) *z = load_elem<DT>(row, f.id);
   s.id[i] = f.id;
-  s.z[i] = live && f.id >= 0 ? load_elem<DT>(row, f.id) : kNegInf;
+  token_teacher(s, i, f.id >= 0 ? f.t : kNegInf, a.k, a.invT);
   return live;
-}
-
-// The loss and the statistics of one row from the sum outside I, by one wave.
-__device__ __forceinline__ void finish_loss(const DistillParams& a, int r, const Teacher& s, const Partial& out,
-                                            int lane) {
-  const double rest = a.rest ? (double)a.rest[r] : -__builtin_huge_val();
-  const Norm n = wave_teacher_norm(s, a.k, rest, a.invT, lane);
-  float m = kNegInf;
-  for (int i = lane; i < a.k; i += kWave) m = fmaxf(m, s.z[i]);
-  m = fmaxf(wave_fmax(m), out.m);
-  if (m == kNegInf) {
-    if (lane == 0) {
-      set_error(a.err, SV_DERR_ROW);
-      a.out_loss[r] = 0.f;
-      reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    return;
-  }
-  double sum = 0.0;
-  for (int i = lane; i < a.k; i += kWave)
-    if (s.z[i] > kNegInf) sum += exp_d(((double)s.z[i] - (double)m) * a.invT);
-  sum = wave_sum(sum);
-  if (out.s > 0.0) sum += out.s * exp_d(((double)out.m - (double)m) * a.invT);
-  const double lt = n.m + log_d(n.z);
-  const double lq = (double)m * a.invT + log_d(sum);
-  double loss = 0.0;
-  for (int i = lane; i < a.k; i += kWave) {
-    const double lp = (double)s.t[i] * a.invT - lt;
-    const double p = s.t[i] > kNegInf ? exp_d(lp) : 0.0;
-    if (p > 0.0) loss += p * (lp - ((double)s.z[i] * a.invT - lq));
-  }
-  loss = wave_sum(loss);
-  const double p0 = exp_d(rest - lt);
-  if (p0 > 0.0) loss += p0 * ((rest - lt) - ((double)out.m * a.invT + log_d(out.s) - lq));
-  if (lane == 0) {
-    a.out_loss[r] = (float)loss;
-    reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(m, (float)sum, out.m, (float)out.s);
-  }
 }
 
 // kDU vectors of a row; tokens of I and elements past V become -inf.
@@ -134,6 +97,9 @@ __global__ __launch_bounds__(kDNT) void distill_loss_kernel(DistillParams a) {
   constexpr int E = Fmt<DT>::kPerVec;
   extern __shared__ uint32_t s_mark[];  // a byte per vector of the part: its tokens in I
   __shared__ Teacher s;
+  __shared__ Drafter q;
+  __shared__ float s_max[kDNT / kWave];
+  __shared__ double s_sum[kDNT / kWave];
   const int r = blockIdx.x / a.nch;
   const int ch = blockIdx.x - r * a.nch;
   const int lane = threadIdx.x & (kWave - 1);
@@ -142,24 +108,24 @@ __global__ __launch_bounds__(kDNT) void distill_loss_kernel(DistillParams a) {
   const int64_t v0 = (int64_t)ch * a.vpc;
   const int64_t nv = (v0 + a.vpc < a.nvec ? v0 + a.vpc : a.nvec) - v0;
   // the row's first vectors are on their way while its teacher is prepared
-  const Fetched f = fetch_teacher(a, r);
+  Fetched f = fetch_teacher(a, r);
   const __amdgpu_buffer_rsrc_t rs = range_rsrc(static_cast<const u32x4*>(row) + v0, (uint32_t)(nv * 16));
   uint32_t off = threadIdx.x * 16u;
   u32x4 cur[kDU];
 #pragma unroll
   for (int u = 0; u < kDU; ++u) cur[u] = load_range(rs, off + (uint32_t)(u * kDNT * 16));
   for (int i = threadIdx.x; i < (int)(nv + 3) / 4; i += kDNT) s_mark[i] = 0u;
-  if (!place_teacher<DT>(a, f, row, s, ch == 0)) {  // block-uniform, the same for all of the row's blocks
+  float z;
+  if (!place_teacher<DT>(a, f, row, s, ch == 0, &z)) {  // block-uniform, the same for all of the row's blocks
     if (ch == 0 && threadIdx.x == 0) {
       a.out_loss[r] = 0.f;
       reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     return;
   }
-  if (threadIdx.x < a.k) {
-    const int32_t id = s.id[threadIdx.x];
-    const int64_t i = (int64_t)id / E - v0;
-    if (id >= 0 && i >= 0 && i < nv) atomicOr(&s_mark[i >> 2], 1u << ((i & 3) * 8 + id % E));
+  if (f.id >= 0) {
+    const int64_t i = (int64_t)f.id / E - v0;
+    if (i >= 0 && i < nv) atomicOr(&s_mark[i >> 2], 1u << ((i & 3) * 8 + f.id % E));
   }
   lds_sync();
   const uint8_t* mark = reinterpret_cast<const uint8_t*>(s_mark);
@@ -178,46 +144,66 @@ __global__ __launch_bounds__(kDNT) void distill_loss_kernel(DistillParams a) {
     }
     fold_group<DT, true>(cur, mark, full * (kDU * kDNT) + threadIdx.x, nv, v0, a.V, a.c, acc);
   }
-  Partial out = block_mass<kDNT>(acc, a.c);
+  token_drafter(q, threadIdx.x, z, a.k, a.invT);
+  const float wm = wave_fmax(acc.m);
+  const double ws = wave_sum(acc.m == kNegInf ? 0.0 : (double)acc.s * (double)fast_exp2((acc.m - wm) * a.c));
+  if (lane == 0) {
+    s_max[wave] = wm;
+    s_sum[wave] = ws;
+  }
+  lds_sync();
+  // wave 0: its lanes' partial sums outside I, then the row's
+  float pm = kNegInf;
+  double ps = 0.0;
+  if (wave == 0 && lane < kDNT / kWave) {
+    pm = s_max[lane];
+    ps = s_sum[lane];
+  }
   if (a.nch > 1) {
     Partial* parts = static_cast<Partial*>(a.parts) + (int64_t)r * a.nch;
-    if (threadIdx.x == 0) put_partial(parts + ch, out);
+    if (wave == 0) {
+      Partial out;
+      out.pad = 0.f;
+      out.m = wave_fmax(pm);
+      out.s = wave_sum(ps * rescale(pm, out.m, a.c));
+      if (lane == 0) put_partial(parts + ch, out);
+    }
     if (!arrive_last<kDNT>(&a.cnt[r], (uint32_t)a.nch)) return;
     if (wave == 0) {
-      float m = kNegInf;
-      for (int i = lane; i < a.nch; i += kWave) m = fmaxf(m, get_partial(parts + i).m);
-      out.m = wave_fmax(m);
-      double t = 0.0;
-      for (int i = lane; i < a.nch; i += kWave) {
-        const Partial p = get_partial(parts + i);
-        t += p.s * rescale(p.m, out.m, a.c);
-      }
-      out.s = wave_sum(t);
+      pm = kNegInf;
+      ps = 0.0;
+      if (lane < kPL)
+        for (int i = lane; i < a.nch; i += kPL) {
+          const Partial p = get_partial(parts + i);
+          const float m = fmaxf(pm, p.m);
+          ps = ps * rescale(pm, m, a.c) + p.s * rescale(p.m, m, a.c);
+          pm = m;
+        }
       if (lane == 0) __hip_atomic_store(&a.cnt[r], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
-  if (wave == 0) finish_loss(a, r, s, out, lane);
+  if (wave != 0) return;
+  const double rest = (double)f.rest;
+  const Norm n = wave_teacher(s, a.k, rest, a.invT, lane);
+  const RowSums w = wave_row_sums(q, pm, ps, a.invT, lane);
+  if (w.m == kNegInf) {
+    if (lane == 0) {
+      set_error(a.err, SV_DERR_ROW);
+      a.out_loss[r] = 0.f;
+      reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    return;
+  }
+  const double loss = wave_loss(s, q, a.k, rest, n, w, a.invT, lane);
+  if (lane == 0) {
+    a.out_loss[r] = (float)loss;
+    reinterpret_cast<float4*>(a.out_stat)[r] = make_float4(w.m, (float)w.sum, w.m0, (float)w.s0);
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Gradient.
 // ---------------------------------------------------------------------------
-// One wave: the row's factors, and (q_i - p_i) g / T in place of s.z.
-__device__ __forceinline__ GradRow wave_grad_row(const DistillParams& a, int r, Teacher& s, const float4 st, int lane) {
-  const double rest = a.rest ? (double)a.rest[r] : -__builtin_huge_val();
-  const Norm n = wave_teacher_norm(s, a.k, rest, a.invT, lane);
-  const double scale = (a.g ? (double)a.g[r] : 1.0) * a.invT;
-  const double inv = 1.0 / (double)st.y;
-  for (int i = lane; i < a.k; i += kWave) {
-    const double p = s.t[i] > kNegInf ? exp_d((double)s.t[i] * a.invT - n.m) / n.z : 0.0;
-    const double q = s.z[i] > kNegInf ? exp_d(((double)s.z[i] - (double)st.x) * a.invT) * inv : 0.0;
-    s.z[i] = (float)((q - p) * scale);
-  }
-  const double p0 = exp_d(rest - n.m) / n.z;
-  const double q0 = st.w > 0.f ? (double)st.w * exp_d(((double)st.z - (double)st.x) * a.invT) * inv : 0.0;
-  return grad_row(st.x, p0, q0, scale, inv);
-}
-
 // A block per (row part): the gradient outside I streams through, then the
 // part's tokens of I are written over it.  In place this holds: the block
 // reads its tokens' logits before it writes, and no other block's.
@@ -226,6 +212,7 @@ __global__ __launch_bounds__(kDNT) void distill_grad_kernel(DistillParams a) {
   constexpr int E = Fmt<DT>::kPerVec;
   __shared__ Teacher s;
   __shared__ GradRow s_g;
+  __shared__ double s_scale;
   const int r = blockIdx.x / a.nch2;
   const int ch = blockIdx.x - r * a.nch2;
   const int lane = threadIdx.x & (kWave - 1);
@@ -238,7 +225,7 @@ __global__ __launch_bounds__(kDNT) void distill_grad_kernel(DistillParams a) {
   const int64_t nfull = a.V / E;
   const int64_t vf = v1 < nfull ? v1 : nfull;  // whole vectors; the row's last one may be shorter
   // the part's first vectors are on their way while the row's factors are formed
-  const Fetched f = fetch_teacher(a, r);
+  Fetched f = fetch_teacher(a, r);
   u32x4 d[kDU];
 #pragma unroll
   for (int u = 0; u < kDU; ++u) {
@@ -252,11 +239,21 @@ __global__ __launch_bounds__(kDNT) void distill_grad_kernel(DistillParams a) {
     if (v1 > nfull && threadIdx.x < a.V - nfull * E) store_elem<DT>(out, nfull * E + threadIdx.x, 0.f);
     return;
   }
-  place_teacher<DT>(a, f, row, s, ch == 0);
+  float z;
+  place_teacher<DT>(a, f, row, s, ch == 0, &z);
+  // q at the thread's token, before any thread stores over it
+  const double inv = 1.0 / (double)st.y;
+  double q = z > kNegInf ? exp_d(((double)z - (double)st.x) * a.invT) * inv : 0.0;
+  asm volatile("" : "+v"(q));  // read before the barrier: the barrier orders LDS only
   lds_sync();
   if (wave == 0) {
-    const GradRow g = wave_grad_row(a, r, s, st, lane);
-    if (lane == 0) s_g = g;
+    const Norm n = wave_teacher(s, a.k, (double)f.rest, a.invT, lane);
+    const double scale = (a.g ? (double)a.g[r] : 1.0) * a.invT;
+    const double q0 = st.w > 0.f ? (double)st.w * exp_d(((double)st.z - (double)st.x) * a.invT) * inv : 0.0;
+    if (lane == 0) {
+      s_g = grad_row(st.x, n.p0, q0, scale, inv);
+      s_scale = scale;
+    }
   }
   lds_sync();
   const GradRow g = s_g;
@@ -275,10 +272,8 @@ __global__ __launch_bounds__(kDNT) void distill_grad_kernel(DistillParams a) {
   }
   __builtin_amdgcn_s_waitcnt(0);  // the stream's stores are done before any token's
   __syncthreads();
-  if (threadIdx.x < a.k) {
-    const int32_t id = s.id[threadIdx.x];
-    if (id >= 0 && id / E >= v0 && id / E < v1) store_elem<DT>(out, id, s.z[threadIdx.x]);
-  }
+  if (f.id >= 0 && f.id / E >= v0 && f.id / E < v1)
+    store_elem<DT>(out, f.id, (float)((q - s.p[threadIdx.x]) * s_scale));
 }
 
 hipError_t launch_distill_loss(const DistillParams& p, sv_dtype dt, hipStream_t s) {

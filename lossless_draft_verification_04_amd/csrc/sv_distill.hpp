@@ -42,12 +42,26 @@ __device__ __forceinline__ double log_d(double x) {
   return y >= 0.0 ? y + (x * exp_d(-y) - 1.0) : y + (x - exp_d(y)) / x;
 }
 
-// A row's teacher tokens in LDS: id (-1: absent), value, the drafter's logit.
+// A row's teacher in LDS.  Token i belongs to the i-th of the block's token
+// threads (whole waves): each wave sums its own tokens' exponentials, against
+// its own largest value, and one wave then joins the waves' sums (lane by
+// lane, so that no step takes longer for more tokens than one pass over them).
+constexpr int kTW = SV_MAX_TEACHER / kWave;  // token waves
 struct alignas(16) Teacher {
-  int32_t id[SV_MAX_TEACHER];
-  float t[SV_MAX_TEACHER];
+  int32_t id[SV_MAX_TEACHER];  // -1: absent
+  float t[SV_MAX_TEACHER];     // value (-inf: no mass)
+  double p[SV_MAX_TEACHER];    // exp((t - tm) / T), then the probability
+  double ts[kTW];              // its wave's sum
+  float tm[kTW];               // its wave's largest value
+  int live;                    // the row has teacher mass
+};
+// The drafter's logits at these tokens.
+struct Drafter {
   float z[SV_MAX_TEACHER];
-  int live;
+  double e[SV_MAX_TEACHER];  // exp((z - zm) / T)
+  float g[SV_MAX_TEACHER];   // the loss's gradient there
+  double zs[kTW];
+  float zm[kTW];
 };
 
 // Whether token i's id stands among those before it (ids in LDS).  Every token
@@ -64,22 +78,113 @@ __device__ __forceinline__ bool repeated(const int32_t* ids, int i, int32_t id, 
   return twice && id >= 0;
 }
 
-// The teacher's normaliser: its largest exponent m and Z relative to it.
+// Token i's exponential and its wave's sum (every token wave whole).
+__device__ __forceinline__ double wave_exponentials(float x, double invT, float* m, double* e) {
+  *m = wave_fmax(x);
+  *e = x > kNegInf ? exp_d(((double)x - (double)*m) * invT) : 0.0;
+  return wave_sum(*e);
+}
+__device__ __forceinline__ void token_teacher(Teacher& s, int i, float t, int k, double invT) {
+  const int w = i / kWave;
+  float m = kNegInf;
+  double e = 0.0, sum = 0.0;
+  if (w * kWave < k) sum = wave_exponentials(t, invT, &m, &e);
+  s.t[i] = t;
+  s.p[i] = e;
+  if (i % kWave == 0) {
+    s.tm[w] = m;
+    s.ts[w] = sum;
+  }
+}
+__device__ __forceinline__ void token_drafter(Drafter& s, int i, float z, int k, double invT) {
+  const int w = i / kWave;
+  float m = kNegInf;
+  double e = 0.0, sum = 0.0;
+  if (w * kWave < k) sum = wave_exponentials(z, invT, &m, &e);
+  s.z[i] = z;
+  s.e[i] = e;
+  if (i % kWave == 0) {
+    s.zm[w] = m;
+    s.zs[w] = sum;
+  }
+}
+
+// One wave: the teacher's probabilities in s.p; p_0 and the normaliser
+// Z = zs e^zm.
 struct Norm {
-  double m, z;
+  double zm, zs, p0;
 };
-__device__ __forceinline__ Norm wave_teacher_norm(const Teacher& s, int k, double rest, double invT, int lane) {
-  float tm = kNegInf;
-  for (int i = lane; i < k; i += kWave) tm = fmaxf(tm, s.t[i]);
-  tm = wave_fmax(tm);
+__device__ __forceinline__ Norm wave_teacher(Teacher& s, int k, double rest, double invT, int lane) {
+  double a = -__builtin_huge_val(), w = 0.0;
+  if (lane < kTW && s.tm[lane] > kNegInf) {
+    a = (double)s.tm[lane] * invT;
+    w = s.ts[lane];
+  }
+  if (lane == kTW && rest > -__builtin_huge_val()) {
+    a = rest;
+    w = 1.0;
+  }
   Norm n;
-  n.m = fmax((double)tm * invT, rest);
-  double z = 0.0;
+  n.zm = readlane_d(a, 0);
+#pragma unroll
+  for (int l = 1; l <= kTW; ++l) n.zm = fmax(n.zm, readlane_d(a, l));
+  const double f = w > 0.0 ? exp_d(a - n.zm) : 0.0;
+  w *= f;
+  n.zs = readlane_d(w, 0);
+#pragma unroll
+  for (int l = 1; l <= kTW; ++l) n.zs += readlane_d(w, l);
+  const double inv = 1.0 / n.zs;
+  n.p0 = readlane_d(w, kTW) * inv;
 #pragma unroll 1
-  for (int i = lane; i < k; i += kWave)
-    if (s.t[i] > kNegInf) z += exp_d((double)s.t[i] * invT - n.m);
-  n.z = wave_sum(z) + exp_d(rest - n.m);
+  for (int i = lane; i < k; i += kWave) s.p[i] *= readlane_d(f, i / kWave) * inv;
   return n;
+}
+
+// One wave: the row's sums from the partial sums outside I, a lane each
+// (lanes below kPL: pm, ps), and the tokens'.  m is the row's largest logit
+// (-inf: it has none), sum = sum_v exp((z_v - m) / T); m0, s0 the same outside
+// I; out = the sum outside I relative to m; fac (lane kPL + w) = the factor
+// that brings token wave w's exponentials to m.
+constexpr int kPL = kWave - kTW - 1;
+struct RowSums {
+  float m, m0;
+  double sum, s0, out, fac;
+};
+__device__ __forceinline__ RowSums wave_row_sums(const Drafter& s, float pm, double ps, double invT, int lane) {
+  RowSums r;
+  if (lane >= kPL) {
+    pm = lane < kPL + kTW ? s.zm[lane - kPL] : kNegInf;
+    ps = lane < kPL + kTW ? s.zs[lane - kPL] : 0.0;
+  }
+  r.m0 = wave_fmax(lane < kPL ? pm : kNegInf);
+  r.m = wave_fmax(pm);
+  // lane by lane: a partial sum outside I to m0, a token wave's to m, m0 to m
+  const float x = lane == kPL + kTW ? r.m0 : pm;
+  r.fac = x > kNegInf ? exp_d(((double)x - (double)(lane < kPL ? r.m0 : r.m)) * invT) : 0.0;
+  ps *= r.fac;
+  r.s0 = wave_sum(lane < kPL ? ps : 0.0);
+  r.out = r.s0 * readlane_d(r.fac, kPL + kTW);
+  r.sum = r.out;
+#pragma unroll
+  for (int w = 0; w < kTW; ++w) r.sum += readlane_d(ps, kPL + w);
+  return r;
+}
+
+// One wave: the loss from the joined sums.  log p_i - log q_i is
+// (t_i - z_i) / T less the difference of the normalisers' logarithms.
+__device__ __forceinline__ double wave_loss(const Teacher& s, const Drafter& q, int k, double rest, const Norm& n,
+                                            const RowSums& r, double invT, int lane) {
+  const double ln = log_d(lane == 0 ? n.zs : lane == 1 ? r.sum : r.s0);
+  const double lt = n.zm + readlane_d(ln, 0), lq = (double)r.m * invT + readlane_d(ln, 1);
+  double loss = 0.0;
+#pragma unroll 1
+  for (int i = lane; i < k; i += kWave) {
+    const double p = s.p[i];
+    if (p > 0.0) loss += p * (((double)s.t[i] * invT - (double)q.z[i] * invT) - (lt - lq));
+  }
+  loss = wave_sum(loss);
+  if (n.p0 > 0.0) loss += n.p0 * ((rest - lt) - ((double)r.m0 * invT + readlane_d(ln, 2) - lq));
+  return loss;
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

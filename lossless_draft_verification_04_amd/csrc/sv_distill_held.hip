@@ -60,19 +60,19 @@ __device__ __forceinline__ void teacher_ids(const DistillParams& a, Fetched& f, 
   if (i >= 0) s.id[i] = f.id;
   if (i == 0) s.live = f.rest > kNegInf;
 }
-// Repeats out, the values in, whether there is mass at all.  Final after a
-// barrier, but for s.id, from which the caller takes the repeats (-1: true)
+// Repeats out, the exponentials in, whether there is mass at all.  Final after
+// a barrier, but for s.id, from which the caller takes the repeats (true)
 // behind that barrier.
 __device__ __forceinline__ bool teacher_tokens(const DistillParams& a, Fetched& f, Teacher& s, int i) {
-  if (i < 0) return false;
-  if (i >= ((a.k + kWave - 1) & ~(kWave - 1))) return false;  // a wave without tokens
-  const bool twice = repeated(s.id, i, f.id, a.k);
+  if (i < 0) return false;  // whole waves
+  bool twice = false;
+  if (i < ((a.k + kWave - 1) & ~(kWave - 1))) twice = repeated(s.id, i, f.id, a.k);
   if (twice) {
     set_error(a.err, SV_DERR_TOKEN);
     f.id = -1;
   }
-  s.t[i] = f.id >= 0 ? f.t : kNegInf;
   if (f.id >= 0 && f.t > kNegInf) s.live = 1;
+  token_teacher(s, i, f.id >= 0 ? f.t : kNegInf, a.k, a.invT);
   return twice;
 }
 
@@ -100,16 +100,16 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
   constexpr int FU = 2;                   // vectors folded at a time
   constexpr int LAG = NV < 4 ? NV : 4;    // loads ahead of the fold
   constexpr int kMarks = NV * NT / 4;     // words of marks
-  static_assert(NV % FU == 0 && LAG % FU == 0 && NT >= SV_MAX_TEACHER && NW <= kWave, "shape");
+  constexpr int kLossWave = NW > 2 ? 1 : 0, kNextWave = NW > 2 ? 2 : 0;
+  static_assert(NV % FU == 0 && LAG % FU == 0 && NT >= SV_MAX_TEACHER && NW <= kPL, "shape");
   __shared__ uint32_t s_mark[2][kMarks];
   __shared__ Teacher s_t[2];
-  __shared__ double s_p[SV_MAX_TEACHER];  // the teacher's probabilities
+  __shared__ Drafter s_q;
   __shared__ float s_max[NW];
   __shared__ double s_sum[NW];
-  // wave 0's scalars wait here between the steps that use them: in registers
-  // they would push parts of the row out to memory
-  __shared__ volatile double s_c[8];
-  enum { kNm, kNz, kS0, kSum, kInv, kP0, kScale, kL0 };
+  __shared__ Norm s_n[2];       // of the teachers in s_t
+  __shared__ double s_scale[2];  // g / T of those rows
+  __shared__ RowSums s_r;
   __shared__ GradRow s_g;
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
@@ -143,15 +143,13 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
   };
   auto set_mark = [&](int b, int32_t id) { atomicOr(&s_mark[b][id / E / 4], 1u << ((id / E % 4) * 8 + id % E)); };
   auto clear_mark = [&](int b, int32_t id) { atomicAnd(&s_mark[b][id / E / 4], ~(1u << ((id / E % 4) * 8 + id % E))); };
-  // wave 0: a row's teacher as probabilities
-  auto teacher_probs = [&](int row, const Teacher& s) {
-    const Norm n = wave_teacher_norm(s, a.k, a.rest ? (double)a.rest[row] : -__builtin_huge_val(), a.invT, lane);
-#pragma unroll 1
-    for (int i = lane; i < a.k; i += kWave)
-      s_p[i] = s.t[i] > kNegInf ? exp_d((double)s.t[i] * a.invT - n.m) / n.z : 0.0;
+  // one wave: a row's teacher as probabilities
+  auto teacher_probs = [&](int row, int b) {
+    const double scale = (a.g ? (double)a.g[row] : 1.0) * a.invT;
+    const Norm n = wave_teacher(s_t[b], a.k, a.rest ? (double)a.rest[row] : -__builtin_huge_val(), a.invT, lane);
     if (lane == 0) {
-      s_c[kNm] = n.m;
-      s_c[kNz] = n.z;
+      s_n[b] = n;
+      s_scale[b] = scale;
     }
   };
   // the first row: its teacher, its vectors, its mass
@@ -189,7 +187,7 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) d[i] = u32x4{0u, 0u, 0u, 0u};
     } else {
-      if (wave == 0) teacher_probs(r, s_t[0]);
+      if (wave == kNextWave) teacher_probs(r, 0);
 #pragma unroll
       for (int i = 0; i < NV; i += FU) {
         fold(i, reinterpret_cast<const uint8_t*>(s_mark[0]));
@@ -212,70 +210,26 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
       s_max[wave] = wm;
       s_sum[wave] = ws;
     }
-    if (ti >= 0) s.z[ti] = live && cur.id >= 0 ? z : kNegInf;
+    if (ti >= 0) token_drafter(s_q, ti, live && cur.id >= 0 ? z : kNegInf, a.k, a.invT);
     if (next) teacher_ids(a, f, sn, ti);
     lds_sync();  // B: every wave's mass, the drafter's logits of I, the next row's ids
     if (wave == 0) {
-      // the mass outside I, the whole row's, and the gradient's factors
-      float4 stat = make_float4(0.f, 0.f, 0.f, 0.f);
+      // the row's sums, the gradient's factors, and the gradient at the tokens of I
       GradRow g{0.f, 0.f};
-      double loss = 0.0;
-      float m = kNegInf;
+      RowSums w{kNegInf, kNegInf, 0.0, 0.0, 0.0, 0.0};
       if (live) {
-        const float pm = lane < NW ? s_max[lane] : kNegInf;
-        const double ps = lane < NW ? s_sum[lane] : 0.0;
-        stat.z = wave_fmax(pm);
-        s_c[kS0] = wave_sum(ps * rescale(pm, stat.z, a.c));
-#pragma unroll 1
-        for (int i = lane; i < a.k; i += kWave) m = fmaxf(m, s.z[i]);
-        m = fmaxf(wave_fmax(m), stat.z);
-        if (m == kNegInf && lane == 0) set_error(a.err, SV_DERR_ROW);
+        w = wave_row_sums(s_q, lane < NW ? s_max[lane] : kNegInf, lane < NW ? s_sum[lane] : 0.0, a.invT, lane);
+        if (w.m == kNegInf && lane == 0) set_error(a.err, SV_DERR_ROW);
       }
-      if (m > kNegInf) {
-        {
-          double sum = 0.0;
+      const bool some = w.m > kNegInf;
+      const double inv = some ? 1.0 / w.sum : 0.0, scale = some ? s_scale[b] : 0.0;
+      if (some) g = grad_row(w.m, s_n[b].p0, w.out * inv, scale, inv);
 #pragma unroll 1
-          for (int i = lane; i < a.k; i += kWave)
-            if (s.z[i] > kNegInf) sum += exp_d(((double)s.z[i] - (double)m) * a.invT);
-          sum = wave_sum(sum);
-          const double s0 = s_c[kS0];
-          const double out = s0 > 0.0 ? s0 * exp_d(((double)stat.z - (double)m) * a.invT) : 0.0;
-          sum += out;
-          const double inv = 1.0 / sum;
-          const double rest = a.rest ? (double)a.rest[r] : -__builtin_huge_val();
-          const double p0 = exp_d(rest - s_c[kNm]) / s_c[kNz];
-          const double scale = (a.g ? (double)a.g[r] : 1.0) * a.invT;
-          g = grad_row(m, p0, out * inv, scale, inv);
-          s_c[kSum] = sum;
-          s_c[kInv] = inv;
-          s_c[kP0] = p0;
-          s_c[kScale] = scale;
-          stat = make_float4(m, (float)sum, stat.z, (float)s0);
-        }
-        // the loss: log p_i - log q_i = t_i / T - z_i / T - (log of the
-        // normalisers), the last of which are the same for all i; and the
-        // gradient at the tokens of I in place of their logits
-        const double ln = log_d(lane == 0 ? s_c[kNz] : lane == 1 ? s_c[kSum] : s_c[kS0]);
-        const double lt = s_c[kNm] + readlane_d(ln, 0), lq = (double)m * a.invT + readlane_d(ln, 1);
-        s_c[kL0] = lt - lq + (double)stat.z * a.invT + readlane_d(ln, 2);  // of the others, but for rest
-#pragma unroll 1
-        for (int i = lane; i < a.k; i += kWave) {
-          const double zi = (double)s.z[i] * a.invT;
-          const double p = s_p[i];
-          if (p > 0.0) loss += p * (((double)s.t[i] * a.invT - zi) - (lt - lq));
-          const double q = s.z[i] > kNegInf ? exp_d(zi - (double)m * a.invT) * s_c[kInv] : 0.0;
-          s.z[i] = (float)((q - p) * s_c[kScale]);
-        }
-        loss = wave_sum(loss);
-        if (s_c[kP0] > 0.0) loss += s_c[kP0] * ((double)a.rest[r] - s_c[kL0]);
-      } else {
-        stat.z = 0.f;
-        for (int i = lane; i < a.k; i += kWave) s.z[i] = 0.f;
-      }
+      for (int i = lane; i < a.k; i += kWave)
+        s_q.g[i] = some ? (float)((s_q.e[i] * readlane_d(w.fac, kPL + i / kWave) * inv - s.p[i]) * scale) : 0.f;
       if (lane == 0) {
         s_g = g;
-        a.out_loss[r] = (float)loss;
-        reinterpret_cast<float4*>(a.out_stat)[r] = stat;
+        s_r = w;
       }
     }
     // meanwhile: this row's marks go, the next row's tokens and marks come
@@ -292,13 +246,25 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
     char* out = static_cast<char*>(a.grad) + (int64_t)r * a.gb;
     const __amdgpu_buffer_rsrc_t ro = range_rsrc(out, (uint32_t)nfull * 16u);
     const GradRow g = s_g;
+    if (wave == kLossWave) {
+      const RowSums w = s_r;
+      const bool some = w.m > kNegInf;
+      double loss = 0.0;
+      if (some)
+        loss = wave_loss(s, s_q, a.k, a.rest ? (double)a.rest[r] : -__builtin_huge_val(), s_n[b], w, a.invT, lane);
+      if (lane == 0) {
+        a.out_loss[r] = (float)loss;
+        reinterpret_cast<float4*>(a.out_stat)[r] =
+            some ? make_float4(w.m, (float)w.sum, w.m0, (float)w.s0) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
     z = kNegInf;
     float zt = 0.f;
     if (nlive) {
       if (f.id >= 0) z = load_elem<DT>(row_of(rn), f.id);
       if (tid < tail) zt = load_elem<DT>(row_of(rn), (int64_t)nfull * E + tid);
     }
-    if (nlive && wave == 0) teacher_probs(rn, sn);
+    if (nlive && wave == kNextWave) teacher_probs(rn, b ^ 1);
     acc = Mass{};
     // store this row's gradient, load the next row behind it, and fold that
     // LAG vectors behind the loads
@@ -326,7 +292,7 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
     for (int i0 = 0; i0 < a.k; i0 += kWave) {
       const int i = i0 + lane;
       const int32_t id = i < a.k ? s.id[i] : -1;
-      const float gv = i < a.k ? s.z[i] : 0.f;
+      const float gv = i < a.k ? s_q.g[i] : 0.f;
       // in the shorter last vector thread e stored element e
       const int owner = id / E < nfull ? id / E % NT : id - nfull * E;
       uint64_t mine = __ballot(id >= 0 && owner / kWave == wave);
