@@ -13,9 +13,10 @@ namespace sv {
 // One launch: a block per (row part) finds the part's N best and the mass
 // outside them (sv_topmass.hpp), in one read of the row; dead and finished
 // beams' blocks read nothing.  The sequence's last block merges each beam's
-// parts (a wave per beam) and then the beams: their lists are sorted, so one
-// wave holds the head of every list, a lane a beam, and takes the best head N
-// times.  Scores are formed and compared in 64 bits: differences between
+// parts (a wave per beam) and then the beams: up to 512 candidates by a
+// thread each, which counts the better ones; more by one wave that holds the
+// head of every sorted list, a lane a beam, and takes the best head N times
+// (64 beams of 64: 64 steps where counting would compare 4096 x 4096).  Scores are formed and compared in 64 bits: differences between
 // beams near 1e-7 of a score decide as the inputs have it.
 // ---------------------------------------------------------------------------
 constexpr int kBNT = 512;
@@ -23,6 +24,7 @@ constexpr int kBNT = 512;
 struct BeamLds {
   TopEntry list[SV_MAX_BEAMS * SV_MAX_FANOUT];
   double shift[SV_MAX_BEAMS];  // s_w - lse_w; -inf: no continuation
+  uint64_t merge[kBNT / kWave][kPartEntries];
 };
 
 // The order of doubles as unsigned integers (larger = better; -inf lowest of
@@ -43,7 +45,7 @@ __device__ __forceinline__ uint64_t wave_key_max(uint64_t k) {
 }
 
 template <int DT>
-__global__ __launch_bounds__(kBNT) void beam_select_kernel(BeamParams a) {
+__global__ __launch_bounds__(kBNT, 4) void beam_select_kernel(BeamParams a) {
   constexpr int E = Fmt<DT>::kPerVec;
   __shared__ BeamLds lds;
   const int r = blockIdx.x / a.nch;  // row (b, w)
@@ -59,10 +61,9 @@ __global__ __launch_bounds__(kBNT) void beam_select_kernel(BeamParams a) {
   if (live) {
     const int64_t v0 = (int64_t)ch * a.vpc;
     const int64_t v1 = v0 + a.vpc < a.nvec ? v0 + a.vpc : a.nvec;
-    Mass own;
+    Partial rest;
     const TopPair t =
-        block_topk_mass<kBNT, E>(RowValues<DT>{row_ptr(a.logits, r, a.sb), a.V}, v0, v1, a.V, N, a.c, &own);
-    const Partial rest = block_mass<kBNT>(own, a.c);
+        block_topk_mass<kBNT, E>(MassRow<DT>{row_ptr(a.logits, r, a.sb), a.V}, v0, v1, a.V, N, a.c, &rest);
     if (wave == 0) {
       const int64_t part = (int64_t)r * a.nch + ch;
       if (lane < N) put_entry(lists + part * N + lane, t.v, t.i);
@@ -86,54 +87,91 @@ __global__ __launch_bounds__(kBNT) void beam_select_kernel(BeamParams a) {
         }
         shift = (double)sc;
       } else {
-        const Partial rest = wave_merge_parts(lists + row * a.nch * N, parts + row * a.nch, a.nch, N, a.c, lane, lv, li);
+        const Partial rest = wave_merge_parts(lists + row * a.nch * N, parts + row * a.nch, a.nch, N, a.c, lane,
+                                              lds.merge[wave], lv, li);
         // all of the row's mass: what its list holds and the rest
         const float m = fmaxf(rest.m, readlane_f(lv, 0));
         if (m > kNegInf) {
           const double s = wave_sum(lane < N ? rescale(lv, m, a.c) : 0.0) + rest.s * rescale(rest.m, m, a.c);
-          shift = (double)sc - ((double)m * a.invT + log(s));
+          shift = (double)sc - ((double)m * a.invT + log_d(s));
         } else if (lane == 0) {
           set_error(a.err, SV_DERR_ROW);
         }
       }
     }
-    if (lane < N) lds.list[w * SV_MAX_FANOUT + lane] = TopEntry{lv, fin && lane > 0 ? kNoIdx : li};
+    if (lane < N) lds.list[w * SV_MAX_FANOUT + lane] = TopEntry{lv, li};
     if (lane == 0) lds.shift[w] = shift;
   }
   lds_sync();
-  if (wave != 0) return;
-  const int w = lane < a.W ? lane : 0;
-  const double shift = lane < a.W ? lds.shift[w] : -__builtin_huge_val();
-  const bool fin = lane < a.W && a.finished && a.finished[(int64_t)b * a.W + w] != 0;
-  int pos = 0;
-  auto head = [&](int i) -> double {
-    if (!(shift > -__builtin_huge_val()) || i >= N) return -__builtin_huge_val();
-    if (fin) return i == 0 ? shift : -__builtin_huge_val();
-    return shift + (double)lds.list[w * SV_MAX_FANOUT + i].val * a.invT;
+  constexpr double kNone = -__builtin_huge_val();
+  // score of beam w's p-th candidate (-inf: none)
+  auto score_of = [&](int w, int p) -> double {
+    const double shift = lds.shift[w];
+    const TopEntry t = lds.list[w * SV_MAX_FANOUT + p];
+    if (!(shift > kNone) || t.val == kNegInf) return kNone;
+    return shift + (double)t.val * a.invT;
   };
-  double cur = head(0);
-  int32_t ob = -1, ot = -1;
-  float os = kNegInf;
-  for (int n = 0; n < N; ++n) {
-    const uint64_t k = cur > -__builtin_huge_val() ? double_key(cur) : 0ull;
-    const uint64_t best = wave_key_max(k);
-    if (best == 0ull) break;
-    const int win = __builtin_ctzll(__ballot(k == best));  // ties: the lowest beam
-    const int p = __builtin_amdgcn_readlane(pos, win);
-    if (lane == n) {
-      ob = win;
-      ot = lds.list[win * SV_MAX_FANOUT + p].idx;
+  const int n = a.W * N;
+  if (n <= kBNT) {
+    // a thread a candidate: its place is the number of better ones, earlier
+    // ones first where scores tie
+    uint64_t* keys = lds.merge[0];
+    int* slot = reinterpret_cast<int*>(lds.merge[kBNT / kPartEntries]);
+    const int i = threadIdx.x;
+    const int w = i / N;
+    const double sc = i < n ? score_of(w, i - w * N) : kNone;
+    const uint64_t k = sc > kNone ? double_key(sc) : 0ull;
+    keys[i] = k;
+    if (i < N) slot[i] = -1;
+    lds_sync();
+    int above = 0;
+    if ((i & ~(kWave - 1)) < n)
+#pragma unroll 4
+      for (int j = 0; j < n; ++j) {
+        const uint64_t o = keys[j];
+        above += (o > k) | ((o == k) & (j < i)) ? 1 : 0;
+      }
+    if (k != 0ull && above < N) {
+      slot[above] = i;
+      a.out_score[(int64_t)b * N + above] = (float)sc;
     }
-    const double sc = readlane_d(cur, win);
-    if (lane == n) os = (float)sc;
-    if (lane == win) cur = head(++pos);
+    lds_sync();
+    if (i < N) {
+      const int at = slot[i];
+      a.out_beam[(int64_t)b * N + i] = at >= 0 ? at / N : -1;
+      a.out_tok[(int64_t)b * N + i] = at >= 0 ? lds.list[at / N * SV_MAX_FANOUT + at % N].idx : -1;
+      if (at < 0) a.out_score[(int64_t)b * N + i] = kNegInf;
+    }
+  } else if (wave == 0) {
+    // a lane a beam: the best head of the sorted lists, N times
+    int pos = 0;
+    double cur = lane < a.W ? score_of(lane, 0) : kNone;
+    int32_t ob = -1, ot = -1;
+    float os = kNegInf;
+    for (int m = 0; m < N; ++m) {
+      const uint64_t k = cur > kNone ? double_key(cur) : 0ull;
+      const uint64_t best = wave_key_max(k);
+      if (best == 0ull) break;
+      const int win = __builtin_ctzll(__ballot(k == best));  // ties: the lowest beam
+      const int p = __builtin_amdgcn_readlane(pos, win);
+      const double sc = readlane_d(cur, win);
+      if (lane == m) {
+        ob = win;
+        ot = lds.list[win * SV_MAX_FANOUT + p].idx;
+        os = (float)sc;
+      }
+      if (lane == win) {
+        ++pos;
+        cur = pos < N ? score_of(lane, pos) : kNone;
+      }
+    }
+    if (lane < N) {
+      a.out_beam[(int64_t)b * N + lane] = ob;
+      a.out_tok[(int64_t)b * N + lane] = ot;
+      a.out_score[(int64_t)b * N + lane] = os;
+    }
   }
-  if (lane < N) {
-    a.out_beam[(int64_t)b * N + lane] = ob;
-    a.out_tok[(int64_t)b * N + lane] = ot;
-    a.out_score[(int64_t)b * N + lane] = os;
-  }
-  if (lane == 0) __hip_atomic_store(&a.cnt[b], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (threadIdx.x == 0) __hip_atomic_store(&a.cnt[b], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 hipError_t launch_beam(const BeamParams& p, sv_dtype dt, hipStream_t s) {

@@ -7,41 +7,6 @@
 
 namespace sv {
 
-// A 64-bit constant, formed in scalar registers where it stands: left alone
-// the compiler lifts such constants out of the loop over rows into vector
-// registers, which there hold a row.
-__device__ __forceinline__ double here(double c) {
-  asm volatile("" : "+s"(c));
-  return c;
-}
-// e^x for x <= 0 in 64 bits to about 1e-11: x = n log 2 + r with |r| <= log(2) / 2
-// (log 2 in two parts, the first short enough that n times it is exact), and
-// the series of e^r to r^9 / 9!; 0 below the range.
-__device__ __forceinline__ double exp_d(double x) {
-  x = fmax(x, here(-800.0));
-  const double n = rint(x * here(1.4426950408889634));
-  double r = fma(n, here(-0.693147180369123816490), x);
-  r = fma(n, here(-1.90821492927058770002e-10), r);
-  double p = fma(here(1.0 / 362880.0), r, here(1.0 / 40320.0));
-  p = fma(p, r, here(1.0 / 5040.0));
-  p = fma(p, r, here(1.0 / 720.0));
-  p = fma(p, r, here(1.0 / 120.0));
-  p = fma(p, r, here(1.0 / 24.0));
-  p = fma(p, r, here(1.0 / 6.0));
-  p = fma(p, r, 0.5);
-  p = fma(p, r, 1.0);
-  p = fma(p, r, 1.0);
-  return ldexp(p, (int)n);
-}
-// log x of an x in the range of fp32 by one step of Newton's method on
-// e^y = x from a 32-bit logarithm (1e-7 before, 1e-13 after); -inf of 0.
-__device__ __forceinline__ double log_d(double x) {
-  if (!(x > 0.0)) return -__builtin_huge_val();
-  const double y = (double)__builtin_amdgcn_logf((float)x) * here(0.6931471805599453);
-  // e^-y with a non-positive argument
-  return y >= 0.0 ? y + (x * exp_d(-y) - 1.0) : y + (x - exp_d(y)) / x;
-}
-
 // A row's teacher in LDS.  Token i belongs to the i-th of the block's token
 // threads (whole waves): each wave sums its own tokens' exponentials, against
 // its own largest value, and one wave then joins the waves' sums (lane by

@@ -76,21 +76,6 @@ __device__ __forceinline__ bool teacher_tokens(const DistillParams& a, Fetched& 
   return twice;
 }
 
-// -inf in place of vector d's marked elements (a bit each).
-template <int DT>
-__device__ __forceinline__ void mask_vec(u32x4& d, uint32_t mk) {
-  if constexpr (DT == SV_BF16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t m = ((mk >> (2 * i)) & 1u ? 0xffffu : 0u) | ((mk >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
-      d[i] = (d[i] & ~m) | (0xff80ff80u & m);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = (mk >> i) & 1u ? 0xff800000u : d[i];
-  }
-}
-
 }  // namespace
 
 template <int DT, int NT, int NV>

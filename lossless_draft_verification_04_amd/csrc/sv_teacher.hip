@@ -27,7 +27,7 @@ __device__ __forceinline__ void put_target(const TeacherParams& a, int r, int la
 }
 
 template <int DT>
-__global__ __launch_bounds__(kTNT) void teacher_kernel(TeacherParams a) {
+__global__ __launch_bounds__(kTNT, 4) void teacher_kernel(TeacherParams a) {
   constexpr int E = Fmt<DT>::kPerVec;
   const int r = blockIdx.x / a.nch;
   const int ch = blockIdx.x - r * a.nch;
@@ -35,10 +35,10 @@ __global__ __launch_bounds__(kTNT) void teacher_kernel(TeacherParams a) {
   const int wave = threadIdx.x / kWave;
   const int64_t v0 = (int64_t)ch * a.vpc;
   const int64_t v1 = v0 + a.vpc < a.nvec ? v0 + a.vpc : a.nvec;
-  Mass own;
+  __shared__ uint64_t s_merge[kPartEntries];
+  Partial rest;
   const TopPair t =
-      block_topk_mass<kTNT, E>(RowValues<DT>{row_ptr(a.logits, r, a.sb), a.V}, v0, v1, a.V, a.k, a.c, &own);
-  const Partial rest = block_mass<kTNT>(own, a.c);
+      block_topk_mass<kTNT, E>(MassRow<DT>{row_ptr(a.logits, r, a.sb), a.V}, v0, v1, a.V, a.k, a.c, &rest);
   if (a.nch == 1) {
     if (wave == 0) put_target(a, r, lane, t.v, t.i, rest);
     return;
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(kTNT) void teacher_kernel(TeacherParams a) {
   if (wave == 0) {
     float lv;
     int32_t li;
-    const Partial whole = wave_merge_parts(lists, parts, a.nch, a.k, a.c, lane, lv, li);
+    const Partial whole = wave_merge_parts(lists, parts, a.nch, a.k, a.c, lane, s_merge, lv, li);
     put_target(a, r, lane, lv, li, whole);
     if (lane == 0) __hip_atomic_store(&a.cnt[r], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }

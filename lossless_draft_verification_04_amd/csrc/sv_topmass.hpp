@@ -3,20 +3,59 @@
 // Shared by the teacher's pass and beam search.
 //
 // The selection is that of sv_topk.hpp: each thread keeps its best vector, a
-// bound from groups of threads, candidates in LDS.  The mass is summed beside
-// it so that no listed value ever enters a sum: a thread folds every vector
-// but its best one (a new best vector sends the old one into the sum), and
-// once the F-th best key is known adds what its best vector holds below it.
-// Only a thread that owns a listed value outside its best vector has its sum
-// dropped and its vectors read again, spread over its wave.  So the mass
-// keeps full relative precision however little of it there is, where a
-// difference "all minus the top" would keep none.
+// bound from groups of threads, candidates in LDS.  The mass must keep its
+// digits where the list holds nearly everything, so it is no difference of
+// rounded sums: beside the selection each thread adds up 64-bit sums of its
+// vectors' 32-bit sums, against a reference that its wave takes from its first
+// vectors.  Once the list is known, every vector that holds a listed value is
+// taken out again whole -- the same instructions on the same bits give the
+// same 32-bit sum, so it leaves nothing behind -- and its other values are put
+// back.  Which vectors those are the thread knows of its best one, and looks
+// up for the others, spread over the wave, where its second largest value
+// reaches the list.  A wave whose reference turns out useless (values 2^100
+// above it, or a mass near underflow below it) reads its vectors once more and
+// sums them against their largest value.
 #pragma once
 
 #include "sv_device.hpp"
 #include "sv_topk.hpp"
 
 namespace sv {
+
+// A 64-bit constant, formed in scalar registers where it stands: left alone
+// the compiler lifts such constants out of the loop over rows into vector
+// registers, which there hold a row.
+__device__ __forceinline__ double here(double c) {
+  asm volatile("" : "+s"(c));
+  return c;
+}
+// e^x for x <= 0 in 64 bits to about 1e-11: x = n log 2 + r with |r| <= log(2) / 2
+// (log 2 in two parts, the first short enough that n times it is exact), and
+// the series of e^r to r^9 / 9!; 0 below the range.
+__device__ __forceinline__ double exp_d(double x) {
+  x = fmax(x, here(-800.0));
+  const double n = rint(x * here(1.4426950408889634));
+  double r = fma(n, here(-0.693147180369123816490), x);
+  r = fma(n, here(-1.90821492927058770002e-10), r);
+  double p = fma(here(1.0 / 362880.0), r, here(1.0 / 40320.0));
+  p = fma(p, r, here(1.0 / 5040.0));
+  p = fma(p, r, here(1.0 / 720.0));
+  p = fma(p, r, here(1.0 / 120.0));
+  p = fma(p, r, here(1.0 / 24.0));
+  p = fma(p, r, here(1.0 / 6.0));
+  p = fma(p, r, 0.5);
+  p = fma(p, r, 1.0);
+  p = fma(p, r, 1.0);
+  return ldexp(p, (int)n);
+}
+// log x of an x in the range of fp32 by one step of Newton's method on
+// e^y = x from a 32-bit logarithm (1e-7 before, 1e-13 after); -inf of 0.
+__device__ __forceinline__ double log_d(double x) {
+  if (!(x > 0.0)) return -__builtin_huge_val();
+  const double y = (double)__builtin_amdgcn_logf((float)x) * here(0.6931471805599453);
+  // e^-y with a non-positive argument
+  return y >= 0.0 ? y + (x * exp_d(-y) - 1.0) : y + (x - exp_d(y)) / x;
+}
 
 // A sum of exponentials: sum of 2^(c (x - m)), m the largest x (-inf, 0: of
 // nothing).
@@ -57,15 +96,46 @@ __device__ __forceinline__ double rescale(float a, float b, float c) {
   return a == kNegInf ? 0.0 : exp2_d((double)c * ((double)a - (double)b));
 }
 
-// The block's sum of its threads' masses, in every thread.
-template <int NT>
-__device__ Partial block_mass(const Mass& a, float c) {
-  Partial p;
-  p.pad = 0.f;
-  p.m = block_fmax<NT>(a.m);
-  p.s = block_sum<NT>(a.m == kNegInf ? 0.0 : (double)a.s * (double)fast_exp2((a.m - p.m) * c));
-  return p;
+// -inf in place of the elements of vector d that mk marks (a bit each).
+template <int DT>
+__device__ __forceinline__ void mask_vec(u32x4& d, uint32_t mk) {
+  if constexpr (DT == SV_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t m = ((mk >> (2 * i)) & 1u ? 0xffffu : 0u) | ((mk >> (2 * i + 1)) & 1u ? 0xffff0000u : 0u);
+      d[i] = (d[i] & ~m) | (0xff80ff80u & m);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = (mk >> i) & 1u ? 0xff800000u : d[i];
+  }
 }
+
+// One logit row as a value source for block_topk_mass: what lies past V is
+// masked as its vector is loaded, so no other step looks at V.
+template <int DT>
+struct MassRow {
+  static constexpr int E = Fmt<DT>::kPerVec;
+  const void* row;
+  int V;
+  __device__ __forceinline__ u32x4 load(int64_t v) const {
+    u32x4 d = load_vec(row, v);
+    if ((int)v == V / E) mask_vec<DT>(d, 0xffu << (V % E));  // the row's last vector, if it is a shorter one
+    return d;
+  }
+  using Data = u32x4;
+  static constexpr bool kSkipNegInf = false;
+  __device__ __forceinline__ void values(const u32x4& d, int64_t, float* x) const { unpack<DT>(d, x); }
+  __device__ __forceinline__ static u32x4 none() {
+    u32x4 d{0u, 0u, 0u, 0u};
+    mask_vec<DT>(d, 0xffu);
+    return d;
+  }
+};
+
+// Keeps a vector packed across a phase: without it the compiler holds the
+// unpacked values of one use for the next, twice the registers.
+__device__ __forceinline__ void stay_packed(u32x4& d) { asm volatile("" : "+v"(d)); }
 
 // Values of vector v below the key kth, the others -inf.
 template <int E, class Src>
@@ -78,12 +148,27 @@ __device__ __forceinline__ void values_below(const Src& src, const typename Src:
     if (top_key(x[e], i0 + e) >= kth) x[e] = kNegInf;
 }
 
+// The 32-bit sum of 2^(c x - r) over a vector's values: the same instructions
+// wherever a vector is added or taken out.
+template <int E>
+__device__ __forceinline__ float vec_sum(const float (&x)[E], float c, float r) {
+  float t[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) t[e] = fast_exp2(__builtin_fmaf(x[e], c, -r));
+#pragma unroll
+  for (int w = E / 2; w > 0; w >>= 1)
+#pragma unroll
+    for (int e = 0; e < w; ++e) t[e] += t[e + w];
+  return t[0];
+}
+
 // As block_topk (wave 0 returns the list of the range's F best), and mass =
-// this thread's share of the sum over the range's other values.  F >= 1.
+// the sum over the range's other values, in every thread.  F >= 1.
 template <int NT, int E, class Src>
 __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, int64_t v1, int V, int F, float c,
-                                                   Mass* mass) {
+                                                   Partial* mass) {
   constexpr int kWin = 4;  // vectors in flight per thread
+  constexpr int NW = NT / kWave;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = threadIdx.x / kWave;
   const int tid = threadIdx.x;
@@ -93,77 +178,89 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   __shared__ uint64_t s_sel[kWave];
   __shared__ uint64_t s_tau;
   __shared__ int s_nc;
+  __shared__ float s_wm[NW];
+  __shared__ double s_ws[NW];
   float lv = kNegInf;
   int32_t li = kNoIdx;
-  const int64_t span = v1 - v0;
-  const int64_t nk = span > 0 ? (span + NT - 1) / NT : 0;  // vectors per thread at most
-  const bool held = nk <= kWin;                            // block-uniform: every vector stays in registers
+  const int span = (int)(v1 - v0);
+  const int nk = span > 0 ? (span + NT - 1) / NT : 0;  // vectors per thread at most
+  const bool held = nk <= kWin;                        // block-uniform: every vector stays in registers
   float bm = kNegInf;    // the best vector's largest value, offset and data
   int32_t bo = kNoIdx;
-  typename Src::Data bd{};
-  bool more = false;     // the thread owns vectors besides its best one
-  Mass rest;             // their mass; rest.m is their largest value
+  typename Src::Data bd = Src::none();
+  const bool more = tid + NT < span;  // the thread owns vectors besides its best one
+  float om = kNegInf;                 // their largest value
+  double sum = 0.0;                   // of all its vectors
+  float ref = kNegInf, r = 0.f;       // the wave's reference and c times it
   typename Src::Data d[kWin];
 #pragma unroll
-  for (int u = 0; u < kWin; ++u) {
-    const int64_t a = v0 + tid + (int64_t)u * NT;
-    if (a < v1) d[u] = src.load(a);
-  }
+  for (int u = 0; u < kWin; ++u)
+    if (tid + u * NT < span) d[u] = src.load(v0 + tid + u * NT);
+  auto largest = [&](const typename Src::Data& dd) {
+    float x[E];
+    src.values(dd, 0, x);
+    float vm = x[0];
+#pragma unroll
+    for (int e = 1; e < E; ++e) vm = fmaxf(vm, x[e]);
+    return vm;
+  };
   if (held) {
 #pragma unroll
     for (int u = 0; u < kWin; ++u) {
-      const int64_t vu = v0 + tid + (int64_t)u * NT;
-      if (vu < v1) {
-        float x[E];
-        src.values(d[u], vu, x);
-        float vm = x[0];
-#pragma unroll
-        for (int e = 1; e < E; ++e) vm = fmaxf(vm, x[e]);
-        const int32_t o = (int32_t)(vu - v0);
-        const bool t = (bo == kNoIdx) | top_better(vm, o, bm, bo);
+      const int32_t o = tid + u * NT;
+      if (o < span) {
+        const float vm = largest(d[u]);
+        const bool t = top_better(vm, o, bm, bo);  // an empty best (-inf, kNoIdx) loses to any vector
         bm = t ? vm : bm;
         bo = t ? o : bo;
       }
+      stay_packed(d[u]);
     }
   } else {
-    for (int64_t v = v0 + tid; v < v1; v += (int64_t)kWin * NT) {
+    // the wave's reference: the largest value of its first whole window
+    {
+      float m = kNegInf;
+#pragma unroll
+      for (int u = 0; u < kWin; ++u) {
+        m = fmaxf(m, tid + u * NT < span ? largest(d[u]) : kNegInf);
+        stay_packed(d[u]);
+      }
+      ref = wave_fmax(m);
+      r = ref == kNegInf ? 0.f : c * ref;
+    }
+    auto take = [&](const typename Src::Data& dd, int32_t o) {
+      float x[E];
+      src.values(dd, 0, x);
+      float vm = x[0];
+#pragma unroll
+      for (int e = 1; e < E; ++e) vm = fmaxf(vm, x[e]);
+      const bool t = top_better(vm, o, bm, bo);
+      om = __builtin_amdgcn_fmed3f(om, bm, vm);  // the second largest: om <= bm
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bd[i] = t ? dd[i] : bd[i];
+      bm = t ? vm : bm;
+      bo = t ? o : bo;
+      sum += (double)vec_sum<E>(x, c, r);
+    };
+    int32_t o = tid;
+    for (; o + (2 * kWin - 1) * NT < span; o += kWin * NT) {
+      // this window and the next are whole
       typename Src::Data nx[kWin];
 #pragma unroll
-      for (int u = 0; u < kWin; ++u) {
-        const int64_t a = v + (int64_t)(kWin + u) * NT;
-        if (a < v1) nx[u] = src.load(a);
-      }
+      for (int u = 0; u < kWin; ++u) nx[u] = src.load(v0 + o + (kWin + u) * NT);
 #pragma unroll
-      for (int u = 0; u < kWin; ++u) {
-        const int64_t vu = v + (int64_t)u * NT;
-        if (vu < v1) {
-          float x[E];
-          src.values(d[u], vu, x);
-          float vm = x[0];
+      for (int u = 0; u < kWin; ++u) take(d[u], o + u * NT);
 #pragma unroll
-          for (int e = 1; e < E; ++e) vm = fmaxf(vm, x[e]);
-          const int32_t o = (int32_t)(vu - v0);
-          if (bo == kNoIdx) {
-            bm = vm;
-            bo = o;
-            bd = d[u];
-          } else {
-            const bool t = top_better(vm, o, bm, bo);
-            typename Src::Data f = d[u];
-            int32_t fo = o;
-            if (t) {
-              f = bd;
-              fo = bo;
-              bm = vm;
-              bo = o;
-              bd = d[u];
-            }
-            src.values(f, v0 + fo, x);
-            fold_values<E>(x, c, rest);
-            more = true;
-          }
-        }
-      }
+      for (int u = 0; u < kWin; ++u) d[u] = nx[u];
+    }
+    for (; o < span; o += kWin * NT) {  // twice at most
+      typename Src::Data nx[kWin];
+#pragma unroll
+      for (int u = 0; u < kWin; ++u)
+        if (o + (kWin + u) * NT < span) nx[u] = src.load(v0 + o + (kWin + u) * NT);
+#pragma unroll
+      for (int u = 0; u < kWin; ++u)
+        if (o + u * NT < span) take(d[u], o + u * NT);
 #pragma unroll
       for (int u = 0; u < kWin; ++u) d[u] = nx[u];
     }
@@ -187,32 +284,40 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   lds_sync();
   if (wave == 0) {
     uint32_t p = 0;
-    uint32_t gh[kMaxH];
+    if (H == 1) {  // one group per lane (F <= 8)
+      const uint32_t gh = s_gm[lane];
 #pragma unroll
-    for (int h = 0; h < kMaxH; ++h) gh[h] = h < H ? s_gm[h * kWave + lane] : 0u;
-    for (int bit = 31; bit >= 16; --bit) {
-      const uint32_t q = p | (1u << bit);
-      int cnt = 0;
+      for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t q = p | (1u << bit);
+        if (__builtin_popcountll(__ballot(gh >= q)) >= F) p = q;
+      }
+    } else {
+      uint32_t gh[kMaxH];
 #pragma unroll
-      for (int h = 0; h < kMaxH; ++h) cnt += __builtin_popcountll(__ballot(gh[h] >= q));
-      if (cnt >= F) p = q;
+      for (int h = 0; h < kMaxH; ++h) gh[h] = h < H ? s_gm[h * kWave + lane] : 0u;
+      for (int bit = 31; bit >= 16; --bit) {
+        const uint32_t q = p | (1u << bit);
+        int cnt = 0;
+#pragma unroll
+        for (int h = 0; h < kMaxH; ++h) cnt += __builtin_popcountll(__ballot(gh[h] >= q));  // empty groups are 0
+        if (cnt >= F) p = q;
+      }
     }
     if (lane == 0) s_tau = (uint64_t)p << 32;
   }
   lds_sync();
   uint64_t tau = s_tau;
   // the thread's vectors besides its best may hold a key of at least t
-  auto others_reach = [&](uint64_t t) { return more && top_key(rest.m, (int32_t)((v0 + tid) * E)) >= t; };
+  auto others_reach = [&](uint64_t t) { return more && top_key(om, (int32_t)((v0 + tid) * E)) >= t; };
   // f(vs, d) for every vector of the wave's lanes with `pick`, one per lane at
   // a time (vs < 0: none); bo of its owner is passed on
   auto spread = [&](bool pick, auto&& f) {
     const uint64_t fm = __ballot(pick);
     if (!fm) return;  // wave-uniform
-    const int nkk = (int)nk;
-    const int items = __builtin_popcountll(fm) * nkk;
+    const int items = __builtin_popcountll(fm) * nk;
     for (int base = 0; base < items; base += kWave) {
       const int t = base + lane;
-      const int j = t < items ? t / nkk : -1;
+      const int j = t < items ? t / nk : -1;
       int sl = 0;  // the j-th such lane of the wave
       uint64_t m = fm;
       for (int q = 0; m; ++q) {
@@ -223,8 +328,8 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
       const int32_t sbo = __shfl(bo, sl, kWave);
       int64_t vs = -1;
       if (j >= 0) {
-        const int64_t r = (int64_t)(wave * kWave + sl) + (int64_t)(t - j * nkk) * NT;
-        if (r < span) vs = v0 + r;
+        const int at = wave * kWave + sl + (t - j * nk) * NT;
+        if (at < span) vs = v0 + at;
       }
       typename Src::Data dd{};
       if (vs >= 0) dd = src.load(vs);
@@ -239,10 +344,12 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
       for (int u = 0; u < kWin; ++u) {
         const int64_t vu = v0 + tid + (int64_t)u * NT;
         flag_candidates<E>(src, d[u], sel && vu < v1 ? vu : -1, V, tau, s_cand, &s_nc);
+        stay_packed(d[u]);
       }
     } else {
       const bool full = sel && others_reach(tau);
       flag_candidates<E>(src, bd, sel && !full ? v0 + bo : -1, V, tau, s_cand, &s_nc);
+      stay_packed(bd);
       spread(full, [&](int64_t vs, int32_t, const typename Src::Data& dd) {
         flag_candidates<E>(src, dd, vs, V, tau, s_cand, &s_nc);
       });
@@ -269,67 +376,148 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   }
   // the F-th best key; 0 where fewer are listed, which then are all there are
   const uint64_t kth = s_tau;
-  float x[E];
-  if (held) {
-    Mass a;
+  // the wave's mass outside the list: ws relative to wm
+  double ws = 0.0;
+  float wm = kNegInf;
+  bool again = held;  // wave-uniform
+  if (!held) {
+    float gone = 0.f;
+    // a vector with listed values: out whole, its other values back
+    auto strip = [&](int64_t v, const typename Src::Data& dd) {
+      float y[E];
+      src.values(dd, v, y);
+      const float s = vec_sum<E>(y, c, r);
+      values_below<E>(src, dd, v, kth, y);
+      gone += s;
+      sum -= (double)s;
+      sum += (double)vec_sum<E>(y, c, r);
+    };
+    if (tkey >= kth && bo != kNoIdx) strip(v0 + bo, bd);
+    spread(others_reach(kth), [&](int64_t vs, int32_t sbo, const typename Src::Data& dd) {
+      if (vs >= 0 && vs != v0 + sbo && top_key(largest(dd), (int32_t)(vs * E)) >= kth) strip(vs, dd);
+    });
+    ws = wave_sum(sum);
+    wm = wave_fmax(bm);
+    // what went leaves 2^-53 of itself behind, some sixty times over: no more
+    // than 2^-25 of what stays.  Values 2^-126 of the reference are lost.
+    again = !(ws > 0x1p-70) | !(ws > 0x1p-22 * (double)wave_fmax(gone)) | !(fabsf(r) <= 3e38f) | ((wm - ref) * c > 100.f);
+    if (!again) {
+      wm = ref;
+      ws *= 1.0 + 0.6931471805599453 * ((double)r - (double)c * (double)ref);  // r is not quite c ref
+    }
+  }
+  if (again) {
+    Mass own;
+    float x[E];
+    if (held) {
 #pragma unroll
-    for (int u = 0; u < kWin; ++u) {
-      const int64_t vu = v0 + tid + (int64_t)u * NT;
-      if (vu < v1) {
-        values_below<E>(src, d[u], vu, kth, x);
-        fold_values<E>(x, c, a);
+      for (int u = 0; u < kWin; ++u) {
+        const int o = tid + u * NT;
+        if (o < span) {
+          values_below<E>(src, d[u], v0 + o, kth, x);
+          fold_values<E>(x, c, own);
+        }
+      }
+    } else {
+      for (int o = tid; o < span; o += NT) {
+        values_below<E>(src, src.load(v0 + o), v0 + o, kth, x);
+        fold_values<E>(x, c, own);
       }
     }
-    *mass = a;
-  } else {
-    const bool redo = others_reach(kth);
-    if (redo) rest = Mass{};
-    if (bo != kNoIdx) {
-      values_below<E>(src, bd, v0 + bo, kth, x);
-      fold_values<E>(x, c, rest);
-    }
-    spread(redo, [&](int64_t vs, int32_t sbo, const typename Src::Data& dd) {
-      if (vs < 0 || vs == v0 + sbo) return;
-      float y[E];
-      values_below<E>(src, dd, vs, kth, y);
-      fold_values<E>(y, c, rest);
-    });
-    *mass = rest;
+    wm = wave_fmax(own.m);
+    ws = wave_sum(own.m == kNegInf ? 0.0 : (double)own.s * (double)fast_exp2((own.m - wm) * c));
   }
+  if (lane == 0) {
+    s_wm[wave] = ws > 0.0 ? wm : kNegInf;
+    s_ws[wave] = ws;
+  }
+  lds_sync();
+  const float pm = lane < NW ? s_wm[lane] : kNegInf;
+  mass->pad = 0.f;
+  mass->m = wave_fmax(pm);
+  mass->s = wave_sum(pm == kNegInf ? 0.0 : s_ws[lane] * rescale(pm, mass->m, c));
   return TopPair{lv, li};
 }
 
-// The lists and masses of a row's nch parts as the row's: (lv, li) is the
-// merged list (lane l = l-th best); the return value is the mass outside it,
-// in every lane.  Called by one wave.
+// Entries of all parts of a row, at most (a row's parts times F).
+constexpr int kPartEntries = 256;
+constexpr int kPerLane = kPartEntries / kWave;
+
+// The lists and masses of a row's nch parts (nch * F <= kPartEntries, nch <=
+// 64) as the row's: (lv, li) is the merged list (lane l = l-th best); the
+// return value is the mass outside it, in every lane.  Called by one wave,
+// with kPartEntries words of LDS of its own.  All is loaded in one round; an
+// entry's rank is the number of better ones, counted over LDS.
 __device__ __forceinline__ Partial wave_merge_parts(const TopEntry* lists, const Partial* parts, int nch, int F,
-                                                    float c, int lane, float& lv, int32_t& li) {
+                                                    float c, int lane, uint64_t* keys, float& lv, int32_t& li) {
   lv = kNegInf;
   li = kNoIdx;
-  wave_merge_entries(lists, nch * F, F, lv, li, lane);
-  const float kv = readlane_f(lv, F - 1);
-  const int32_t ki = __builtin_amdgcn_readlane(li, F - 1);
-  const uint64_t kth = ki == kNoIdx ? 0ull : top_key(kv, ki);
-  // the parts' masses and the listed values that did not make the row's list
-  float m = kNegInf;
-  for (int i = lane; i < nch; i += kWave) m = fmaxf(m, get_partial(parts + i).m);
-  for (int i = lane; i < nch * F; i += kWave) {
-    const TopEntry t = get_entry(lists + i);
-    if (t.idx != kNoIdx && top_key(t.val, t.idx) < kth) m = fmaxf(m, t.val);
-  }
   Partial r;
   r.pad = 0.f;
+  if (nch == 1) {
+    TopEntry t{kNegInf, kNoIdx};
+    if (lane < F) t = get_entry(lists + lane);
+    r = get_partial(parts);
+    lv = t.val;
+    li = t.idx;
+    return r;
+  }
+  const int n = nch * F;
+  float v[kPerLane];
+  uint64_t key[kPerLane];
+  int above[kPerLane];
+  Partial p{kNegInf, 0.f, 0.0};
+  TopEntry t[kPerLane];
+#pragma unroll
+  for (int q = 0; q < kPerLane; ++q) {
+    t[q] = TopEntry{kNegInf, kNoIdx};
+    if (q * kWave + lane < n) t[q] = get_entry(lists + q * kWave + lane);
+  }
+  if (lane < nch) p = get_partial(parts + lane);
+#pragma unroll
+  for (int q = 0; q < kPerLane; ++q) {
+    v[q] = t[q].val;
+    key[q] = t[q].idx == kNoIdx ? 0ull : top_key(v[q], t[q].idx);
+    above[q] = 0;
+    keys[q * kWave + lane] = key[q];
+  }
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll 4
+  for (int j = 0; j < n; ++j) {
+    const uint64_t k = keys[j];
+#pragma unroll
+    for (int q = 0; q < kPerLane; ++q) above[q] += k > key[q] ? 1 : 0;
+  }
+  float m = p.m;
+#pragma unroll
+  for (int q = 0; q < kPerLane; ++q)
+    if (key[q] && above[q] >= F) m = fmaxf(m, v[q]);
   r.m = wave_fmax(m);
-  double s = 0.0;
-  for (int i = lane; i < nch; i += kWave) {
-    const Partial p = get_partial(parts + i);
-    s += p.s * rescale(p.m, r.m, c);
-  }
-  for (int i = lane; i < nch * F; i += kWave) {
-    const TopEntry t = get_entry(lists + i);
-    if (t.idx != kNoIdx && top_key(t.val, t.idx) < kth) s += rescale(t.val, r.m, c);
-  }
+  double s = p.s * rescale(p.m, r.m, c);
+#pragma unroll
+  for (int q = 0; q < kPerLane; ++q)
+    if (key[q] && above[q] >= F) s += rescale(v[q], r.m, c);
   r.s = wave_sum(s);
+  // the list, through the same words: entry of rank l to lane l
+  __builtin_amdgcn_wave_barrier();
+  keys[lane] = 0ull;
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int q = 0; q < kPerLane; ++q)
+    if (key[q] && above[q] < F) keys[above[q]] = pack_cand(v[q], t[q].idx);
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  const uint64_t mine = keys[lane];
+  const int found = __builtin_popcountll(__ballot(key[0] != 0)) + __builtin_popcountll(__ballot(key[1] != 0)) +
+                    __builtin_popcountll(__ballot(key[2] != 0)) + __builtin_popcountll(__ballot(key[3] != 0));
+  static_assert(kPerLane == 4, "entries a lane");
+  if (lane < F && lane < found) {
+    lv = cand_value(mine);
+    li = (int32_t)(mine >> 32);
+  }
+  __builtin_amdgcn_wave_barrier();
   return r;
 }
 
