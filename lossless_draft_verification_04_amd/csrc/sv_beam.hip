@@ -12,42 +12,61 @@ namespace sv {
 //
 // One launch: a block per (row part) finds the part's N best and the mass
 // outside them (sv_topmass.hpp), in one read of the row; dead and finished
-// beams' blocks read nothing.  The sequence's last block merges each beam's
-// parts (a wave per beam) and then the beams: up to 512 candidates by a
-// thread each, which counts the better ones; more by one wave that holds the
-// head of every sorted list, a lane a beam, and takes the best head N times
-// (64 beams of 64: 64 steps where counting would compare 4096 x 4096).  Scores are formed and compared in 64 bits: differences between
-// beams near 1e-7 of a score decide as the inputs have it.
+// beams' blocks read nothing.  The sequence's last block joins: a wave a beam
+// merges the beam's parts, scores its list and merges that into the wave's
+// running list; the waves' lists then merge pairwise.  A merge of two sorted
+// lists, a lane an entry, is one exchange with the other list reversed and
+// log2(N) compare-exchange steps (a bitonic merge), so the join takes a few
+// steps more where there are more beams, not more rounds of a selection.
+// Scores are formed and compared in 64 bits: differences between beams near
+// 1e-7 of a score decide as the inputs have it.
 // ---------------------------------------------------------------------------
-constexpr int kBNT = 512;
+constexpr double kNoScore = -__builtin_huge_val();
 
+// A continuation: lane l of a sorted list holds the l-th best.
+struct Cont {
+  double s;  // score (kNoScore: none)
+  int32_t beam, tok;
+};
+__device__ __forceinline__ bool cont_better(const Cont& a, const Cont& b) {
+  return (a.s > b.s) | ((a.s == b.s) & ((a.beam < b.beam) | ((a.beam == b.beam) & (a.tok < b.tok))));
+}
+__device__ __forceinline__ Cont cont_from(const Cont& c, int lane) {
+  const uint64_t b = (uint64_t)__double_as_longlong(c.s);
+  const int at = lane * 4;
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)(uint32_t)b);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)(uint32_t)(b >> 32));
+  Cont r;
+  r.s = __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+  r.beam = __builtin_amdgcn_ds_bpermute(at, c.beam);
+  r.tok = __builtin_amdgcn_ds_bpermute(at, c.tok);
+  return r;
+}
+// The P best of two sorted lists of P (a power of two <= 64; empty entries
+// last), sorted.  y comes reversed: lane l holds entry P - 1 - l.
+__device__ __forceinline__ Cont cont_merge(Cont x, const Cont& y, int P, int lane) {
+  if (cont_better(y, x)) x = y;  // the P best, falling then rising
+  for (int h = P / 2; h > 0; h /= 2) {
+    const Cont o = cont_from(x, lane ^ h);
+    const bool low = (lane & h) == 0;  // keeps the better of the two
+    if (cont_better(o, x) == low) x = o;
+  }
+  return x;
+}
+
+template <int NW>
 struct BeamLds {
-  TopEntry list[SV_MAX_BEAMS * SV_MAX_FANOUT];
-  double shift[SV_MAX_BEAMS];  // s_w - lse_w; -inf: no continuation
-  uint64_t merge[kBNT / kWave][kPartEntries];
+  Cont list[NW][kWave];
+  alignas(16) double merge[NW][kPartEntries];
+  float scores[SV_MAX_BEAMS];
+  int32_t finished[SV_MAX_BEAMS];
 };
 
-// The order of doubles as unsigned integers (larger = better; -inf lowest of
-// the values, 0 below all).
-__device__ __forceinline__ uint64_t double_key(double v) {
-  const uint64_t b = (uint64_t)__double_as_longlong(v == 0.0 ? 0.0 : v);
-  return (b >> 63) ? ~b : (b | 0x8000000000000000ull);
-}
-
-__device__ __forceinline__ uint64_t wave_key_max(uint64_t k) {
-  key_max_step<kRowShr + 1, 0xF>(k);
-  key_max_step<kRowShr + 2, 0xF>(k);
-  key_max_step<kRowShr + 4, 0xF>(k);
-  key_max_step<kRowShr + 8, 0xF>(k);
-  key_max_step<kRowBcast15, 0xA>(k);
-  key_max_step<kRowBcast31, 0xC>(k);
-  return readlane_u64(k, kWave - 1);
-}
-
-template <int DT>
-__global__ __launch_bounds__(kBNT, 4) void beam_select_kernel(BeamParams a) {
+template <int DT, int NT>
+__global__ __launch_bounds__(NT, 4) void beam_select_kernel(BeamParams a) {
   constexpr int E = Fmt<DT>::kPerVec;
-  __shared__ BeamLds lds;
+  constexpr int NW = NT / kWave;
+  __shared__ BeamLds<NW> lds;
   const int r = blockIdx.x / a.nch;  // row (b, w)
   const int ch = blockIdx.x - r * a.nch;
   const int b = r / a.W;
@@ -56,6 +75,10 @@ __global__ __launch_bounds__(kBNT, 4) void beam_select_kernel(BeamParams a) {
   const int N = a.N;
   const bool done = a.finished && a.finished[r] != 0;
   const bool live = !done && a.scores[r] > kNegInf;  // block-uniform
+  if (threadIdx.x < (unsigned)a.W) {  // for the join, if it falls to this block
+    lds.scores[threadIdx.x] = a.scores[(int64_t)b * a.W + threadIdx.x];
+    lds.finished[threadIdx.x] = a.finished ? a.finished[(int64_t)b * a.W + threadIdx.x] : 0;
+  }
   TopEntry* lists = static_cast<TopEntry*>(a.lists);
   Partial* parts = static_cast<Partial*>(a.parts);
   if (live) {
@@ -63,123 +86,72 @@ __global__ __launch_bounds__(kBNT, 4) void beam_select_kernel(BeamParams a) {
     const int64_t v1 = v0 + a.vpc < a.nvec ? v0 + a.vpc : a.nvec;
     Partial rest;
     const TopPair t =
-        block_topk_mass<kBNT, E>(MassRow<DT>{row_ptr(a.logits, r, a.sb), a.V}, v0, v1, a.V, N, a.c, &rest);
+        block_topk_mass<NT, E>(MassRow<DT>{row_ptr(a.logits, r, a.sb), a.V}, v0, v1, a.V, N, a.c, &rest);
     if (wave == 0) {
       const int64_t part = (int64_t)r * a.nch + ch;
       if (lane < N) put_entry(lists + part * N + lane, t.v, t.i);
       if (lane == 0) put_partial(parts + part, rest);
     }
   }
-  if (!arrive_last<kBNT>(&a.cnt[b], (uint32_t)(a.W * a.nch))) return;
-  // every beam's list and normaliser, a wave a beam
-  for (int w = wave; w < a.W; w += kBNT / kWave) {
+  if (!arrive_last<NT>(&a.cnt[b], (uint32_t)(a.W * a.nch))) return;
+  int P = 1;
+  while (P < N) P *= 2;
+  const Cont none{kNoScore, -1, -1};
+  Cont best = none;
+  for (int w = wave; w < a.W; w += NW) {
     const int64_t row = (int64_t)b * a.W + w;
-    const bool fin = a.finished && a.finished[row] != 0;
-    const float sc = a.scores[row];
-    float lv = kNegInf;
-    int32_t li = kNoIdx;
-    double shift = -__builtin_huge_val();
-    if (sc > kNegInf) {
-      if (fin) {
-        if (lane == 0) {
-          lv = 0.f;
-          li = a.pad;
-        }
-        shift = (double)sc;
-      } else {
-        const Partial rest = wave_merge_parts(lists + row * a.nch * N, parts + row * a.nch, a.nch, N, a.c, lane,
-                                              lds.merge[wave], lv, li);
-        // all of the row's mass: what its list holds and the rest
-        const float m = fmaxf(rest.m, readlane_f(lv, 0));
-        if (m > kNegInf) {
-          const double s = wave_sum(lane < N ? rescale(lv, m, a.c) : 0.0) + rest.s * rescale(rest.m, m, a.c);
-          shift = (double)sc - ((double)m * a.invT + log_d(s));
-        } else if (lane == 0) {
-          set_error(a.err, SV_DERR_ROW);
-        }
+    const float sc = lds.scores[w];
+    Cont own = none;
+    if (!(sc > kNegInf)) continue;  // wave-uniform
+    if (lds.finished[w] != 0) {
+      if (lane == 0) own = Cont{(double)sc, w, a.pad};
+    } else {
+      float lv;
+      int32_t li;
+      const Partial rest = wave_merge_parts(lists + row * a.nch * N, parts + row * a.nch, a.nch, N, a.c, lane,
+                                            lds.merge[wave], lv, li);
+      // all of the row's mass: what its list holds and the rest
+      const float m = fmaxf(rest.m, readlane_f(lv, 0));
+      if (m > kNegInf) {
+        const double s = wave_sum(lane < N ? rescale(lv, m, a.c) : 0.0) + rest.s * rescale(rest.m, m, a.c);
+        const double shift = (double)sc - ((double)m * a.invT + log_d(s));
+        if (lane < N && lv > kNegInf) own = Cont{shift + (double)lv * a.invT, w, li};
+      } else if (lane == 0) {
+        set_error(a.err, SV_DERR_ROW);
       }
     }
-    if (lane < N) lds.list[w * SV_MAX_FANOUT + lane] = TopEntry{lv, li};
-    if (lane == 0) lds.shift[w] = shift;
+    best = w == wave ? own : cont_merge(best, cont_from(own, lane ^ (P - 1)), P, lane);
   }
-  lds_sync();
-  constexpr double kNone = -__builtin_huge_val();
-  // score of beam w's p-th candidate (-inf: none)
-  auto score_of = [&](int w, int p) -> double {
-    const double shift = lds.shift[w];
-    const TopEntry t = lds.list[w * SV_MAX_FANOUT + p];
-    if (!(shift > kNone) || t.val == kNegInf) return kNone;
-    return shift + (double)t.val * a.invT;
-  };
-  const int n = a.W * N;
-  if (n <= kBNT) {
-    // a thread a candidate: its place is the number of better ones, earlier
-    // ones first where scores tie
-    uint64_t* keys = lds.merge[0];
-    int* slot = reinterpret_cast<int*>(lds.merge[kBNT / kPartEntries]);
-    const int i = threadIdx.x;
-    const int w = i / N;
-    const double sc = i < n ? score_of(w, i - w * N) : kNone;
-    const uint64_t k = sc > kNone ? double_key(sc) : 0ull;
-    keys[i] = k;
-    if (i < N) slot[i] = -1;
+  // the waves' lists, in pairs; a wave past the beams has an empty one
+  for (int d = 1; d < NW && d < a.W; d *= 2) {
+    if ((wave & (2 * d - 1)) == d) lds.list[wave][lane] = best;
     lds_sync();
-    int above = 0;
-    if ((i & ~(kWave - 1)) < n)
-#pragma unroll 4
-      for (int j = 0; j < n; ++j) {
-        const uint64_t o = keys[j];
-        above += (o > k) | ((o == k) & (j < i)) ? 1 : 0;
-      }
-    if (k != 0ull && above < N) {
-      slot[above] = i;
-      a.out_score[(int64_t)b * N + above] = (float)sc;
-    }
-    lds_sync();
-    if (i < N) {
-      const int at = slot[i];
-      a.out_beam[(int64_t)b * N + i] = at >= 0 ? at / N : -1;
-      a.out_tok[(int64_t)b * N + i] = at >= 0 ? lds.list[at / N * SV_MAX_FANOUT + at % N].idx : -1;
-      if (at < 0) a.out_score[(int64_t)b * N + i] = kNegInf;
-    }
-  } else if (wave == 0) {
-    // a lane a beam: the best head of the sorted lists, N times
-    int pos = 0;
-    double cur = lane < a.W ? score_of(lane, 0) : kNone;
-    int32_t ob = -1, ot = -1;
-    float os = kNegInf;
-    for (int m = 0; m < N; ++m) {
-      const uint64_t k = cur > kNone ? double_key(cur) : 0ull;
-      const uint64_t best = wave_key_max(k);
-      if (best == 0ull) break;
-      const int win = __builtin_ctzll(__ballot(k == best));  // ties: the lowest beam
-      const int p = __builtin_amdgcn_readlane(pos, win);
-      const double sc = readlane_d(cur, win);
-      if (lane == m) {
-        ob = win;
-        ot = lds.list[win * SV_MAX_FANOUT + p].idx;
-        os = (float)sc;
-      }
-      if (lane == win) {
-        ++pos;
-        cur = pos < N ? score_of(lane, pos) : kNone;
-      }
-    }
-    if (lane < N) {
-      a.out_beam[(int64_t)b * N + lane] = ob;
-      a.out_tok[(int64_t)b * N + lane] = ot;
-      a.out_score[(int64_t)b * N + lane] = os;
-    }
+    if ((wave & (2 * d - 1)) == 0 && wave + d < a.W)
+      best = cont_merge(best, lds.list[wave + d][lane ^ (P - 1)], P, lane);
   }
-  if (threadIdx.x == 0) __hip_atomic_store(&a.cnt[b], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (wave != 0) return;
+  if (lane < N) {
+    a.out_beam[(int64_t)b * N + lane] = best.s > kNoScore ? best.beam : -1;
+    a.out_tok[(int64_t)b * N + lane] = best.s > kNoScore ? best.tok : -1;
+    a.out_score[(int64_t)b * N + lane] = (float)best.s;
+  }
+  if (lane == 0) __hip_atomic_store(&a.cnt[b], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+template <int DT>
+static void launch_beam_dt(const BeamParams& p, hipStream_t s) {
+  const int64_t grid = (int64_t)p.B * p.W * p.nch;
+  if (grid >= kTopFill)
+    beam_select_kernel<DT, 256><<<dim3((unsigned)grid), dim3(256), 0, s>>>(p);
+  else
+    beam_select_kernel<DT, 512><<<dim3((unsigned)grid), dim3(512), 0, s>>>(p);
 }
 
 hipError_t launch_beam(const BeamParams& p, sv_dtype dt, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.B * p.W * p.nch));
   if (dt == SV_BF16)
-    beam_select_kernel<SV_BF16><<<grid, dim3(kBNT), 0, s>>>(p);
+    launch_beam_dt<SV_BF16>(p, s);
   else
-    beam_select_kernel<SV_F32><<<grid, dim3(kBNT), 0, s>>>(p);
+    launch_beam_dt<SV_F32>(p, s);
   return hipGetLastError();
 }
 

@@ -16,8 +16,13 @@ namespace sv {
 
 namespace {
 
-constexpr int kDraftBlocks = 512;  // 512-thread blocks that fill the device
-constexpr int kTopPartVecs = 2048;  // smallest part of a row that is split for its top values
+// Blocks of the top-value passes, and the smallest part of a row split for
+// them: joining parts costs about as much as a block takes for 8192 vectors
+// (17 x 32000 fp32 rows, 64 values: 13.1 us whole, 18.4 in parts of 2667;
+// 17 x 152064 bf16 rows: 21.6 us in 2 parts, 22.8 in 4).  Beams are joined
+// anyway (8 beams of 152064: 17.8 us in 4 parts each, 19.4 in 2).
+constexpr int kTopBlocks = 256;
+constexpr int kTopPartVecs = 8192, kBeamPartVecs = 4096;
 
 // Blocks of the distillation passes.  A part of a loss costs a hand-off, so
 // rows are split only until every compute unit has a block: 64 x 152064 bf16
@@ -33,10 +38,10 @@ constexpr int kGradFew = 1024;
 // T and its log2(e) / T usable in 32 bits.
 bool bad_scale(float T) { return bad_temperature(T) || !std::isfinite(log2e_over(T)) || !(log2e_over(T) > 0.f); }
 
-sv_status plan_topmass(sv_dtype dt, int64_t rows, int32_t V, int32_t k, Plan* pl) {
+sv_status plan_topmass(sv_dtype dt, int64_t rows, int32_t V, int32_t k, int64_t part, Plan* pl) {
   pl->nvec = (V + per_vec(dt) - 1) / per_vec(dt);
-  split(rows, pl->nvec, kDraftBlocks, &pl->nch1, &pl->vpc1, kTopPartVecs);
-  const int32_t most = std::min(kPartEntries / k, kWave);
+  split(rows, pl->nvec, kTopBlocks, &pl->nch1, &pl->vpc1, part);
+  const int32_t most = std::min(kPartEntries / k, kMostParts);
   if (pl->nch1 > most) {
     pl->vpc1 = (pl->nvec + most - 1) / most;
     pl->nch1 = (int32_t)((pl->nvec + pl->vpc1 - 1) / pl->vpc1);
@@ -56,14 +61,14 @@ sv_status plan_teacher(sv_dtype dt, int32_t R, int32_t V, int32_t k, Plan* pl) {
   if (bad_dtype(dt)) return SV_EDTYPE;
   if (R < 0 || V < 1 || k < 1) return SV_EINVAL;
   if (R > SV_MAX_ROWS || V > SV_MAX_V || k > SV_MAX_FANOUT) return SV_EUNSUPPORTED;
-  return plan_topmass(dt, R, V, k, pl);
+  return plan_topmass(dt, R, V, k, kTopPartVecs, pl);
 }
 
 sv_status plan_beam(sv_dtype dt, int32_t B, int32_t W, int32_t V, int32_t N, Plan* pl) {
   if (bad_dtype(dt)) return SV_EDTYPE;
   if (B < 0 || W < 1 || V < 1 || N < 1) return SV_EINVAL;
   if (W > SV_MAX_BEAMS || (int64_t)B * W > SV_MAX_ROWS || V > SV_MAX_V || N > SV_MAX_FANOUT) return SV_EUNSUPPORTED;
-  return plan_topmass(dt, (int64_t)B * W, V, N, pl);
+  return plan_topmass(dt, (int64_t)B * W, V, N, kBeamPartVecs, pl);
 }
 
 sv_status plan_distill(sv_dtype dt, int32_t R, int32_t V, int32_t k, Plan* pl) {

@@ -15,8 +15,6 @@
 
 namespace sv {
 
-constexpr int kTNT = 512;
-
 __device__ __forceinline__ void put_target(const TeacherParams& a, int r, int lane, float lv, int32_t li,
                                            const Partial& rest) {
   if (lane < a.k) {
@@ -26,8 +24,8 @@ __device__ __forceinline__ void put_target(const TeacherParams& a, int r, int la
   if (lane == 0) a.out_rest[r] = rest.s > 0.0 ? (float)((double)rest.m * a.invT + log(rest.s)) : kNegInf;
 }
 
-template <int DT>
-__global__ __launch_bounds__(kTNT, 4) void teacher_kernel(TeacherParams a) {
+template <int DT, int NT>
+__global__ __launch_bounds__(NT, 4) void teacher_kernel(TeacherParams a) {
   constexpr int E = Fmt<DT>::kPerVec;
   const int r = blockIdx.x / a.nch;
   const int ch = blockIdx.x - r * a.nch;
@@ -35,10 +33,10 @@ __global__ __launch_bounds__(kTNT, 4) void teacher_kernel(TeacherParams a) {
   const int wave = threadIdx.x / kWave;
   const int64_t v0 = (int64_t)ch * a.vpc;
   const int64_t v1 = v0 + a.vpc < a.nvec ? v0 + a.vpc : a.nvec;
-  __shared__ uint64_t s_merge[kPartEntries];
+  __shared__ alignas(16) double s_merge[kPartEntries];
   Partial rest;
   const TopPair t =
-      block_topk_mass<kTNT, E>(MassRow<DT>{row_ptr(a.logits, r, a.sb), a.V}, v0, v1, a.V, a.k, a.c, &rest);
+      block_topk_mass<NT, E>(MassRow<DT>{row_ptr(a.logits, r, a.sb), a.V}, v0, v1, a.V, a.k, a.c, &rest);
   if (a.nch == 1) {
     if (wave == 0) put_target(a, r, lane, t.v, t.i, rest);
     return;
@@ -49,7 +47,7 @@ __global__ __launch_bounds__(kTNT, 4) void teacher_kernel(TeacherParams a) {
     if (lane < a.k) put_entry(lists + (int64_t)ch * a.k + lane, t.v, t.i);
     if (lane == 0) put_partial(parts + ch, rest);
   }
-  if (!arrive_last<kTNT>(&a.cnt[r], (uint32_t)a.nch)) return;
+  if (!arrive_last<NT>(&a.cnt[r], (uint32_t)a.nch)) return;
   if (wave == 0) {
     float lv;
     int32_t li;
@@ -59,12 +57,20 @@ __global__ __launch_bounds__(kTNT, 4) void teacher_kernel(TeacherParams a) {
   }
 }
 
-hipError_t launch_teacher(const TeacherParams& p, sv_dtype dt, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)p.R * p.nch));
-  if (dt == SV_BF16)
-    teacher_kernel<SV_BF16><<<grid, dim3(kTNT), 0, s>>>(p);
+template <int DT>
+static void launch_teacher_dt(const TeacherParams& p, hipStream_t s) {
+  const int64_t grid = (int64_t)p.R * p.nch;
+  if (grid >= kTopFill)
+    teacher_kernel<DT, 256><<<dim3((unsigned)grid), dim3(256), 0, s>>>(p);
   else
-    teacher_kernel<SV_F32><<<grid, dim3(kTNT), 0, s>>>(p);
+    teacher_kernel<DT, 512><<<dim3((unsigned)grid), dim3(512), 0, s>>>(p);
+}
+
+hipError_t launch_teacher(const TeacherParams& p, sv_dtype dt, hipStream_t s) {
+  if (dt == SV_BF16)
+    launch_teacher_dt<SV_BF16>(p, s);
+  else
+    launch_teacher_dt<SV_F32>(p, s);
   return hipGetLastError();
 }
 

@@ -17,10 +17,18 @@
 // sums them against their largest value.
 #pragma once
 
+#include <type_traits>
+
 #include "sv_device.hpp"
 #include "sv_topk.hpp"
 
 namespace sv {
+
+// Blocks from which the device is full with blocks of 256 threads; fewer get
+// 512 threads each.  Teacher's pass: 2048 x 151936 bf16 rows take 116 us with
+// 256 threads, 127 with 512; 2000 x 4000 rows 21 and 33; 17 x 152064 rows 27
+// and 22; 256 x 128256 rows 25 and 22.
+constexpr int64_t kTopFill = 512;
 
 // A 64-bit constant, formed in scalar registers where it stands: left alone
 // the compiler lifts such constants out of the loop over rows into vector
@@ -118,6 +126,7 @@ struct MassRow {
   static constexpr int E = Fmt<DT>::kPerVec;
   const void* row;
   int V;
+  __device__ __forceinline__ u32x4 load_whole(int64_t v) const { return load_vec(row, v); }  // not the row's last
   __device__ __forceinline__ u32x4 load(int64_t v) const {
     u32x4 d = load_vec(row, v);
     if ((int)v == V / E) mask_vec<DT>(d, 0xffu << (V % E));  // the row's last vector, if it is a shorter one
@@ -243,11 +252,11 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
       sum += (double)vec_sum<E>(x, c, r);
     };
     int32_t o = tid;
-    for (; o + (2 * kWin - 1) * NT < span; o += kWin * NT) {
-      // this window and the next are whole
+    for (; o + (2 * kWin - 1) * NT < span - 1; o += kWin * NT) {
+      // this window and the next are whole, without the last vector
       typename Src::Data nx[kWin];
 #pragma unroll
-      for (int u = 0; u < kWin; ++u) nx[u] = src.load(v0 + o + (kWin + u) * NT);
+      for (int u = 0; u < kWin; ++u) nx[u] = src.load_whole(v0 + o + (kWin + u) * NT);
 #pragma unroll
       for (int u = 0; u < kWin; ++u) take(d[u], o + u * NT);
 #pragma unroll
@@ -439,17 +448,26 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   return TopPair{lv, li};
 }
 
-// Entries of all parts of a row, at most (a row's parts times F).
+// Entries of all parts of a row, at most (a row's parts times F), and parts.
 constexpr int kPartEntries = 256;
+constexpr int kMostParts = 16;
 constexpr int kPerLane = kPartEntries / kWave;
 
-// The lists and masses of a row's nch parts (nch * F <= kPartEntries, nch <=
-// 64) as the row's: (lv, li) is the merged list (lane l = l-th best); the
-// return value is the mass outside it, in every lane.  Called by one wave,
-// with kPartEntries words of LDS of its own.  All is loaded in one round; an
-// entry's rank is the number of better ones, counted over LDS.
+// An entry's order as a positive double (larger = better; 0: none): the value's
+// order bits over 24 bits of complemented index, 56 bits in all, read as the
+// bits of a double, whose comparison is one full-rate instruction.
+__device__ __forceinline__ double order_of(float v, int32_t i) {
+  const uint64_t k = top_key(v, i);
+  return i == kNoIdx ? 0.0 : __longlong_as_double((long long)(((k >> 32) << 24) | (k & 0xffffffull)));
+}
+
+// The lists and masses of a row's nch parts (nch * F <= kPartEntries) as the
+// row's: (lv, li) is the merged list (lane l = l-th best); the return value is
+// the mass outside it, in every lane.  Called by one wave, with kPartEntries
+// words of LDS of its own.  All is loaded in one round; an entry's rank is the
+// number of better ones, counted over LDS.
 __device__ __forceinline__ Partial wave_merge_parts(const TopEntry* lists, const Partial* parts, int nch, int F,
-                                                    float c, int lane, uint64_t* keys, float& lv, int32_t& li) {
+                                                    float c, int lane, double* keys, float& lv, int32_t& li) {
   lv = kNegInf;
   li = kNoIdx;
   Partial r;
@@ -463,8 +481,7 @@ __device__ __forceinline__ Partial wave_merge_parts(const TopEntry* lists, const
     return r;
   }
   const int n = nch * F;
-  float v[kPerLane];
-  uint64_t key[kPerLane];
+  double key[kPerLane];
   int above[kPerLane];
   Partial p{kNegInf, 0.f, 0.0};
   TopEntry t[kPerLane];
@@ -476,47 +493,48 @@ __device__ __forceinline__ Partial wave_merge_parts(const TopEntry* lists, const
   if (lane < nch) p = get_partial(parts + lane);
 #pragma unroll
   for (int q = 0; q < kPerLane; ++q) {
-    v[q] = t[q].val;
-    key[q] = t[q].idx == kNoIdx ? 0ull : top_key(v[q], t[q].idx);
+    key[q] = order_of(t[q].val, t[q].idx);
     above[q] = 0;
     keys[q * kWave + lane] = key[q];
   }
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
   __builtin_amdgcn_wave_barrier();
+  const double2* pairs = reinterpret_cast<const double2*>(keys);
+  auto count = [&](auto nq) {
 #pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const uint64_t k = keys[j];
+    for (int j = 0; j < n; j += 2) {
+      const double2 k = pairs[j >> 1];  // past the n-th: 0, above none
 #pragma unroll
-    for (int q = 0; q < kPerLane; ++q) above[q] += k > key[q] ? 1 : 0;
-  }
+      for (int q = 0; q < decltype(nq)::value; ++q) above[q] += (k.x > key[q] ? 1 : 0) + (k.y > key[q] ? 1 : 0);
+    }
+  };
+  if (n <= 2 * kWave)
+    count(std::integral_constant<int, 2>{});
+  else
+    count(std::integral_constant<int, kPerLane>{});
   float m = p.m;
 #pragma unroll
   for (int q = 0; q < kPerLane; ++q)
-    if (key[q] && above[q] >= F) m = fmaxf(m, v[q]);
+    if (key[q] > 0.0 && above[q] >= F) m = fmaxf(m, t[q].val);
   r.m = wave_fmax(m);
   double s = p.s * rescale(p.m, r.m, c);
 #pragma unroll
   for (int q = 0; q < kPerLane; ++q)
-    if (key[q] && above[q] >= F) s += rescale(v[q], r.m, c);
+    if (key[q] > 0.0 && above[q] >= F) s += rescale(t[q].val, r.m, c);
   r.s = wave_sum(s);
-  // the list, through the same words: entry of rank l to lane l
+  // the list, through the same words: the entry of rank l to lane l
+  uint64_t* out = reinterpret_cast<uint64_t*>(keys);
   __builtin_amdgcn_wave_barrier();
-  keys[lane] = 0ull;
+  out[lane] = pack_cand(kNegInf, kNoIdx);
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
   __builtin_amdgcn_wave_barrier();
 #pragma unroll
   for (int q = 0; q < kPerLane; ++q)
-    if (key[q] && above[q] < F) keys[above[q]] = pack_cand(v[q], t[q].idx);
+    if (key[q] > 0.0 && above[q] < F) out[above[q]] = pack_cand(t[q].val, t[q].idx);
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
   __builtin_amdgcn_wave_barrier();
-  const uint64_t mine = keys[lane];
-  const int found = __builtin_popcountll(__ballot(key[0] != 0)) + __builtin_popcountll(__ballot(key[1] != 0)) +
-                    __builtin_popcountll(__ballot(key[2] != 0)) + __builtin_popcountll(__ballot(key[3] != 0));
-  static_assert(kPerLane == 4, "entries a lane");
-  if (lane < F && lane < found) {
-    lv = cand_value(mine);
-    li = (int32_t)(mine >> 32);
-  }
+  lv = cand_value(out[lane]);
+  li = (int32_t)(out[lane] >> 32);
   __builtin_amdgcn_wave_barrier();
   return r;
 }
