@@ -521,57 +521,61 @@ def _call(dev, fn, what, *args):
         raise SpecVerifyError(status, what)
 
 
-def _f32_tensor(t, shape, what):
-    if t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-        raise SpecVerifyError(SV_EINVAL, f"{what}: want contiguous float32 {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    return t
+def _want(t, dtype, shape, what):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise SpecVerifyError(SV_EINVAL, f"{what}: want contiguous {dtype} {shape}, got {t.dtype} {tuple(t.shape)}")
 
 
 def _rows_2d(t, what):
+    """R, V and the row stride of a [R, V] tensor."""
     if t.dim() != 2:
         raise SpecVerifyError(SV_EINVAL, f"{what}: want [rows, V], got {tuple(t.shape)}")
-    return t.shape
+    stride, unit = t.stride()
+    if unit != 1:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: vocabulary axis must have unit stride")
+    return *t.shape, stride
 
 
 def sv_teacher_topk(logits, k, T, workspace=None):
     """The k largest logits of each row and the logarithm of the mass outside them at temperature T.
     logits [R, V] -> dict(ids [R, k] int32, vals [R, k], rest [R])."""
-    R, V = _rows_2d(logits, "logits")
+    R, V, stride = _rows_2d(logits, "logits")
     dt, k = _dtype_code(logits), int(k)
     dev = _one_device("sv_teacher_topk", logits, workspace)
     ws = workspace if workspace is not None else _draft_workspace(dev, SV_DRAFT_TEACHER, dt, R, 1, V, k)
     out = dict(ids=torch.empty(R, k, dtype=torch.int32, device=dev),
                vals=torch.empty(R, k, dtype=torch.float32, device=dev),
                rest=torch.empty(R, dtype=torch.float32, device=dev))
-    _call(dev, _lib.sv_teacher_topk, "sv_teacher_topk", _at(logits), dt, _row_stride(logits, "logits"), R, V, k,
-          float(T), _at(out["ids"]), _at(out["vals"]), _at(out["rest"]), _at(ws), ws.numel())
+    _call(dev, _lib.sv_teacher_topk, "sv_teacher_topk", logits.data_ptr(), dt, stride, R, V, k,
+          float(T), out["ids"].data_ptr(), out["vals"].data_ptr(), out["rest"].data_ptr(), ws.data_ptr(), ws.numel())
     _checked(dev, "sv_teacher_topk", workspace)
     return out
 
 
 def _distill_args(what, z, ids, vals, rest, grad_loss, grad, workspace):
-    R, V = _rows_2d(z, "z")
+    R, V, stride = _rows_2d(z, "z")
     if ids.dim() != 2 or ids.shape[0] != R:
         raise SpecVerifyError(SV_EINVAL, f"ids: want [{R}, k], got {tuple(ids.shape)}")
     k = ids.shape[1]
-    _i32_tensor(ids, (R, k), "ids")
-    _f32_tensor(vals, (R, k), "vals")
+    _want(ids, torch.int32, (R, k), "ids")
+    _want(vals, torch.float32, (R, k), "vals")
     if rest is not None:
-        _f32_tensor(rest, (R,), "rest")
+        _want(rest, torch.float32, (R,), "rest")
     if grad_loss is not None:
-        _f32_tensor(grad_loss, (R,), "grad_loss")
-    if grad is not None and (tuple(grad.shape) != (R, V) or grad.dtype != z.dtype):
+        _want(grad_loss, torch.float32, (R,), "grad_loss")
+    if grad is not None and (grad.shape != (R, V) or grad.dtype is not z.dtype):
         raise SpecVerifyError(SV_EINVAL, f"grad: want {z.dtype} {(R, V)}, got {grad.dtype} {tuple(grad.shape)}")
     dt = _dtype_code(z)
     dev = _one_device(what, z, ids, vals, rest, grad_loss, grad, workspace)
     ws = workspace if workspace is not None else _draft_workspace(dev, SV_DRAFT_DISTILL, dt, R, 1, V, k)
-    return R, V, k, dt, dev, ws
+    return R, V, stride, k, dt, dev, ws
 
 
 def _grad_rows(z, R, V):
     """Gradient rows beside z, 16-byte aligned (a view of padded rows where V needs it)."""
-    per = 16 // z.element_size()
-    return torch.empty(R, -(-V // per) * per, dtype=z.dtype, device=z.device)[:, :V]
+    pad = -V % (16 // z.element_size())
+    rows = torch.empty(R, V + pad, dtype=z.dtype, device=z.device)
+    return rows[:, :V] if pad else rows
 
 
 def sv_distill_topk(z, ids, vals, T, rest=None, grad_loss=None, want_grad=False, grad=None, workspace=None):
@@ -579,28 +583,28 @@ def sv_distill_topk(z, ids, vals, T, rest=None, grad_loss=None, want_grad=False,
     renormalised over the ids), and with want_grad its gradient, times grad_loss [R] (None: 1).
     z [R, V], ids, vals [R, k] -> dict(loss [R], stat [R, 4] for the backward pass, grad [R, V] or None).
     grad: where to write the gradient (z itself: in place); hand it on with z.backward(out["grad"])."""
-    R, V, k, dt, dev, ws = _distill_args("sv_distill_topk", z, ids, vals, rest, grad_loss, grad, workspace)
+    R, V, stride, k, dt, dev, ws = _distill_args("sv_distill_topk", z, ids, vals, rest, grad_loss, grad, workspace)
     if grad is None and want_grad:
         grad = _grad_rows(z, R, V)
     out = dict(loss=torch.empty(R, dtype=torch.float32, device=dev),
                stat=torch.empty(R, 4, dtype=torch.float32, device=dev), grad=grad)
-    _call(dev, _lib.sv_distill_topk, "sv_distill_topk", _at(z), dt, _row_stride(z, "z"), R, V, _at(ids), _at(vals),
-          _at(rest), k, float(T), _at(grad_loss), _at(out["loss"]), _at(out["stat"]), _at(grad),
-          _row_stride(grad, "grad") if grad is not None else 0, _at(ws), ws.numel())
+    _call(dev, _lib.sv_distill_topk, "sv_distill_topk", z.data_ptr(), dt, stride, R, V, ids.data_ptr(), vals.data_ptr(),
+          _at(rest), k, float(T), _at(grad_loss), out["loss"].data_ptr(), out["stat"].data_ptr(), _at(grad),
+          _rows_2d(grad, "grad")[2] if grad is not None else 0, ws.data_ptr(), ws.numel())
     _checked(dev, "sv_distill_topk", workspace)
     return out
 
 
 def sv_distill_topk_backward(z, ids, vals, stat, T, rest=None, grad_loss=None, grad=None, workspace=None):
     """The gradient of sv_distill_topk from its stat: [R, V] of z's type (grad: where to write it; z itself: in place)."""
-    R, V, k, dt, dev, ws = _distill_args("sv_distill_topk_backward", z, ids, vals, rest, grad_loss, grad, workspace)
-    _f32_tensor(stat, (R, 4), "stat")
+    R, V, stride, k, dt, dev, ws = _distill_args("sv_distill_topk_backward", z, ids, vals, rest, grad_loss, grad, workspace)
+    _want(stat, torch.float32, (R, 4), "stat")
     _one_device("sv_distill_topk_backward", z, stat)
     if grad is None:
         grad = _grad_rows(z, R, V)
-    _call(dev, _lib.sv_distill_topk_backward, "sv_distill_topk_backward", _at(z), dt, _row_stride(z, "z"), R, V,
-          _at(ids), _at(vals), _at(rest), k, float(T), _at(stat), _at(grad_loss), _at(grad),
-          _row_stride(grad, "grad"), _at(ws), ws.numel())
+    _call(dev, _lib.sv_distill_topk_backward, "sv_distill_topk_backward", z.data_ptr(), dt, stride, R, V,
+          ids.data_ptr(), vals.data_ptr(), _at(rest), k, float(T), stat.data_ptr(), _at(grad_loss), _at(grad),
+          _rows_2d(grad, "grad")[2], ws.data_ptr(), ws.numel())
     _checked(dev, "sv_distill_topk_backward", workspace)
     return grad
 
@@ -611,9 +615,9 @@ def sv_beam_select(logits, scores, N, T=1.0, finished=None, pad_tok=0, workspace
     if logits.dim() != 3:
         raise SpecVerifyError(SV_EINVAL, f"logits: want [B, W, V], got {tuple(logits.shape)}")
     B, W, V = logits.shape
-    _f32_tensor(scores, (B, W), "scores")
+    _want(scores, torch.float32, (B, W), "scores")
     if finished is not None:
-        _i32_tensor(finished, (B, W), "finished")
+        _want(finished, torch.int32, (B, W), "finished")
     dt, N, pad = _dtype_code(logits), int(N), int(pad_tok)
     if not -(1 << 31) <= pad < 1 << 31:
         raise SpecVerifyError(SV_EINVAL, f"pad_tok {pad} outside int32")
@@ -622,8 +626,8 @@ def sv_beam_select(logits, scores, N, T=1.0, finished=None, pad_tok=0, workspace
     out = dict(beam=torch.empty(B, N, dtype=torch.int32, device=dev),
                tok=torch.empty(B, N, dtype=torch.int32, device=dev),
                score=torch.empty(B, N, dtype=torch.float32, device=dev))
-    _call(dev, _lib.sv_beam_select, "sv_beam_select", _at(logits), dt, _row_stride(logits, "logits"), _at(scores),
-          _at(finished), B, W, V, float(T), pad, N, _at(out["beam"]), _at(out["tok"]), _at(out["score"]), _at(ws),
+    _call(dev, _lib.sv_beam_select, "sv_beam_select", logits.data_ptr(), dt, _row_stride(logits, "logits"), scores.data_ptr(),
+          _at(finished), B, W, V, float(T), pad, N, out["beam"].data_ptr(), out["tok"].data_ptr(), out["score"].data_ptr(), ws.data_ptr(),
           ws.numel())
     _checked(dev, "sv_beam_select", workspace)
     return out
@@ -676,9 +680,9 @@ def sv_beam_reorder(state, parent, pos_dim=None, lens=None, out=None, workspace=
     if parent.dim() != 2:
         raise SpecVerifyError(SV_EINVAL, f"parent: want [B, N], got {tuple(parent.shape)}")
     N = parent.shape[1]
-    _i32_tensor(parent, (B, N), "parent")
+    _want(parent, torch.int32, (B, N), "parent")
     if lens is not None:
-        _i32_tensor(lens, (B,), "lens")
+        _want(lens, torch.int32, (B,), "lens")
     if out is None:
         if N > W:
             raise SpecVerifyError(SV_EINVAL, f"parent: {N} beams in place of {W}")
@@ -686,7 +690,7 @@ def sv_beam_reorder(state, parent, pos_dim=None, lens=None, out=None, workspace=
         raise SpecVerifyError(SV_EINVAL, f"out: shape {tuple(dst.shape)} for {N} beams of {tuple(state.shape)}")
     dev = _one_device("sv_beam_reorder", state, dst, parent, lens, workspace)
     ws = workspace if workspace is not None else _draft_workspace(dev, SV_DRAFT_REORDER, 0, 0, 0, 0, 0)
-    _call(dev, _lib.sv_beam_reorder, "sv_beam_reorder", _at(state), ss, _at(dst), ds, _at(parent), _at(lens), L, B,
-          W, N, H, S, pos, _at(ws), ws.numel())
+    _call(dev, _lib.sv_beam_reorder, "sv_beam_reorder", state.data_ptr(), ss, dst.data_ptr(), ds, parent.data_ptr(), _at(lens), L, B,
+          W, N, H, S, pos, ws.data_ptr(), ws.numel())
     _checked(dev, "sv_beam_reorder", workspace)
     return dst
