@@ -165,8 +165,7 @@ sv_status sv_beam_select(const void* logits, sv_dtype dt, int64_t stride, const 
  * in place, and a beam that follows itself costs nothing.  Otherwise they must
  * not overlap, and dst's rows must not overlap each other (SV_EINVAL).
  * A parent outside [-1, W) or a length outside [0, S] sets SV_DERR_RANGE; that
- * beam, or that whole sequence, is left as it was.  Any alignment is taken;
- * bases, strides and pos_bytes that are multiples of 16 are fastest.
+ * beam, or that whole sequence, is left as it was.  Any alignment is taken.
  */
 sv_status sv_beam_reorder(const void* src, const int64_t* src_stride, void* dst, const int64_t* dst_stride,
                           const int32_t* parent, const int32_t* lens, int32_t L, int32_t B, int32_t W, int32_t N,

@@ -156,42 +156,72 @@ hipError_t launch_beam(const BeamParams& p, sv_dtype dt, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Reordering.  A thread owns one vector of U bytes at one place of a segment,
-// for all N beams of a sequence: it loads the N vectors from their parents,
-// then stores them.  No other thread touches that place, so the same kernel
-// works in place (all loads of a thread come before its stores).  A source
-// that several beams follow is loaded by the same thread, from the cache
-// after the first time.  Memory-bound: every source once, every moved beam
-// once.
+// Reordering.  A thread owns one place of a segment for all N beams of a
+// sequence: it loads the N pieces from their parents, then stores them.  No
+// other thread touches that place, so the same kernel works in place (all
+// loads of a thread come before its stores).  A source that several beams
+// follow is loaded by the same thread, from the cache after the first time.
+// Memory-bound: every source once, every moved beam once.
+//
+// Places are of U bytes, at any alignment (unaligned vector accesses are
+// native; beams of a ragged cache rarely share one), and the last bytes of a
+// segment are places of 4 bytes and of one, each a thread's.  U is 16 unless
+// more than 16 beams in place would have to be held at once.
+//
+// A state larger than the last-level cache is stored past it (NTS: 2.1 GB in
+// place 506 -> 484 us, 4.9 TB/s of reads and writes; 439 MB 99 -> 78 us); a
+// smaller one stays there for its next reader (275 MB: 50 us, 55 past it).
 // ---------------------------------------------------------------------------
 template <int U>
 struct Bytes;
 template <>
 struct Bytes<16> {
-  using T = u32x4;
+  typedef u32x4 T __attribute__((aligned(1), may_alias));
 };
 template <>
 struct Bytes<8> {
-  using T = uint64_t;
+  typedef uint64_t T __attribute__((aligned(1), may_alias));
 };
 template <>
 struct Bytes<4> {
-  using T = uint32_t;
-};
-template <>
-struct Bytes<2> {
-  using T = uint16_t;
+  typedef uint32_t T __attribute__((aligned(1), may_alias));
 };
 template <>
 struct Bytes<1> {
-  using T = uint8_t;
+  typedef uint8_t T __attribute__((may_alias));
 };
 
 constexpr int kRNT = 256;
 
-template <int U, int MAXN>
-__global__ __launch_bounds__(kRNT) void reorder_kernel(ReorderParams a, int64_t nblk) {
+// One place of U bytes for all beams.
+template <int U, int MAXN, bool NTS>
+__device__ __forceinline__ void reorder_place(const ReorderParams& a, const char* src, char* dst, const int32_t* parent) {
   using T = typename Bytes<U>::T;
+  for (int n0 = 0; n0 < a.N; n0 += MAXN) {  // in place: one round (N <= MAXN)
+    T v[MAXN];
+#pragma unroll
+    for (int i = 0; i < MAXN; ++i) {
+      const int n = n0 + i;
+      const int32_t p = n < a.N ? parent[n] : -1;
+      if (p >= 0 && p < a.W && !(a.inplace && p == n)) v[i] = *reinterpret_cast<const T*>(src + (int64_t)p * a.ss[2]);
+    }
+#pragma unroll
+    for (int i = 0; i < MAXN; ++i) {
+      const int n = n0 + i;
+      const int32_t p = n < a.N ? parent[n] : -1;
+      if (p >= 0 && p < a.W && !(a.inplace && p == n)) {
+        T* to = reinterpret_cast<T*>(dst + (int64_t)n * a.ds[2]);
+        if constexpr (NTS)
+          __builtin_nontemporal_store(v[i], to);
+        else
+          *to = v[i];
+      }
+    }
+  }
+}
+
+template <int U, int MAXN, bool NTS>
+__global__ __launch_bounds__(kRNT) void reorder_kernel(ReorderParams a, int64_t nblk) {
   // block -> (layer, sequence, segment, chunk)
   int64_t q = blockIdx.x;
   const int64_t chunk = q % nblk;
@@ -201,98 +231,50 @@ __global__ __launch_bounds__(kRNT) void reorder_kernel(ReorderParams a, int64_t 
   const int b = (int)(q % a.B);
   const int64_t l = q / a.B;
   int64_t len = a.lens ? (int64_t)a.lens[b] : a.S;
-  if (len < 0 || len > a.S) {
-    if (threadIdx.x == 0 && chunk == 0 && h == 0 && l == 0) set_error(a.err, SV_DERR_RANGE);
-    len = 0;
-  }
-  const int64_t bytes = len * a.pos;
-  const int64_t off = (chunk * kRNT + threadIdx.x) * U;
-  const char* src = a.src + l * a.ss[0] + (int64_t)b * a.ss[1] + (int64_t)h * a.ss[3] + off;
-  char* dst = a.dst + l * a.ds[0] + (int64_t)b * a.ds[1] + (int64_t)h * a.ds[3] + off;
   const int32_t* parent = a.parent + (int64_t)b * a.N;
-  if (chunk == 0 && h == 0 && l == 0 && threadIdx.x < a.N) {
-    const int32_t p = parent[threadIdx.x];
-    if (p < -1 || p >= a.W) set_error(a.err, SV_DERR_RANGE);
-  }
-  if (off >= bytes) return;
-  const bool whole = off + U <= bytes;
-  for (int n0 = 0; n0 < a.N; n0 += MAXN) {  // in place: one round (N <= MAXN)
-    T v[MAXN];
-#pragma unroll
-    for (int i = 0; i < MAXN; ++i) {
-      const int n = n0 + i;
-      if (n < a.N) {
-        const int32_t p = parent[n];
-        if (p >= 0 && p < a.W && !(a.inplace && p == n) && whole)
-          v[i] = *reinterpret_cast<const T*>(src + (int64_t)p * a.ss[2]);
-      }
+  if (chunk == 0 && h == 0 && l == 0) {
+    if (threadIdx.x < a.N) {
+      const int32_t p = parent[threadIdx.x];
+      if (p < -1 || p >= a.W) set_error(a.err, SV_DERR_RANGE);
     }
-#pragma unroll
-    for (int i = 0; i < MAXN; ++i) {
-      const int n = n0 + i;
-      if (n < a.N) {
-        const int32_t p = parent[n];
-        if (p >= 0 && p < a.W && !(a.inplace && p == n) && whole)
-          *reinterpret_cast<T*>(dst + (int64_t)n * a.ds[2]) = v[i];
-      }
-    }
+    if (threadIdx.x == 0 && (len < 0 || len > a.S)) set_error(a.err, SV_DERR_RANGE);
   }
-  if (!whole) {
-    // the last bytes of a segment whose length is no multiple of U, a byte
-    // of all beams at a time
-    for (int64_t j = 0; off + j < bytes; ++j) {
-      for (int n0 = 0; n0 < a.N; n0 += MAXN) {
-        uint8_t v[MAXN];
-#pragma unroll
-        for (int i = 0; i < MAXN; ++i) {
-          const int n = n0 + i;
-          const int32_t p = n < a.N ? parent[n] : -1;
-          if (p >= 0 && p < a.W) v[i] = *reinterpret_cast<const uint8_t*>(src + (int64_t)p * a.ss[2] + j);
-        }
-#pragma unroll
-        for (int i = 0; i < MAXN; ++i) {
-          const int n = n0 + i;
-          const int32_t p = n < a.N ? parent[n] : -1;
-          if (p >= 0 && p < a.W) *reinterpret_cast<uint8_t*>(dst + (int64_t)n * a.ds[2] + j) = v[i];
-        }
-      }
-    }
-  }
+  if (len < 0 || len > a.S) return;
+  const int64_t bytes = len * a.pos;
+  const char* src = a.src + l * a.ss[0] + (int64_t)b * a.ss[1] + (int64_t)h * a.ss[3];
+  char* dst = a.dst + l * a.ds[0] + (int64_t)b * a.ds[1] + (int64_t)h * a.ds[3];
+  const int64_t j = chunk * kRNT + threadIdx.x;
+  const int64_t nu = bytes / U;
+  const int64_t n4 = bytes % U / 4;
+  if (j < nu)
+    reorder_place<U, MAXN, NTS>(a, src + j * U, dst + j * U, parent);
+  else if (j < nu + n4)
+    reorder_place<4, MAXN, false>(a, src + nu * U + (j - nu) * 4, dst + nu * U + (j - nu) * 4, parent);
+  else if (j < nu + n4 + bytes % 4)
+    reorder_place<1, MAXN, false>(a, src + bytes / 4 * 4 + (j - nu - n4), dst + bytes / 4 * 4 + (j - nu - n4), parent);
 }
 
-template <int U>
+constexpr double kPastCache = 320.0 * (1 << 20);  // bytes of a state that the 256 MB cache no longer serves
+
+template <int U, int MAXN>
 static hipError_t launch_reorder_u(const ReorderParams& p, hipStream_t s) {
-  const int64_t bytes = p.S * p.pos;
-  const int64_t nblk = (bytes + (int64_t)U * kRNT - 1) / ((int64_t)U * kRNT);
+  const int64_t places = p.S * p.pos / U + kReorderOdd;
+  const int64_t nblk = (places + kRNT - 1) / kRNT;
   const int64_t grid = nblk * p.L * p.B * p.H;
   if (grid > INT32_MAX) return hipErrorInvalidValue;
-  const dim3 g((unsigned)grid);
-  // in place every beam's vector is held at once
-  if (p.N <= 8)
-    reorder_kernel<U, 8><<<g, dim3(kRNT), 0, s>>>(p, nblk);
-  else if (p.N <= 16 || !p.inplace)
-    reorder_kernel<U, 16><<<g, dim3(kRNT), 0, s>>>(p, nblk);
-  else if constexpr (U <= 8) {
-    if (p.N <= 32)
-      reorder_kernel<U, 32><<<g, dim3(kRNT), 0, s>>>(p, nblk);
-    else if constexpr (U <= 4)
-      reorder_kernel<U, 64><<<g, dim3(kRNT), 0, s>>>(p, nblk);
-    else
-      return launch_reorder_u<4>(p, s);
-  } else {
-    return launch_reorder_u<8>(p, s);
-  }
+  if ((double)p.L * p.B * p.N * p.H * p.S * p.pos > kPastCache)
+    reorder_kernel<U, MAXN, true><<<dim3((unsigned)grid), dim3(kRNT), 0, s>>>(p, nblk);
+  else
+    reorder_kernel<U, MAXN, false><<<dim3((unsigned)grid), dim3(kRNT), 0, s>>>(p, nblk);
   return hipGetLastError();
 }
 
-hipError_t launch_reorder(const ReorderParams& p, int vec, hipStream_t s) {
-  switch (vec) {
-    case 16: return launch_reorder_u<16>(p, s);
-    case 8: return launch_reorder_u<8>(p, s);
-    case 4: return launch_reorder_u<4>(p, s);
-    case 2: return launch_reorder_u<2>(p, s);
-    default: return launch_reorder_u<1>(p, s);
-  }
+hipError_t launch_reorder(const ReorderParams& p, hipStream_t s) {
+  // in place every beam's piece is held at once; apart, 16 beams at a time
+  if (p.N <= 8) return launch_reorder_u<16, 8>(p, s);
+  if (p.N <= 16 || !p.inplace) return launch_reorder_u<16, 16>(p, s);
+  if (p.N <= 32) return launch_reorder_u<8, 32>(p, s);
+  return launch_reorder_u<4, 64>(p, s);
 }
 
 }  // namespace sv

@@ -87,6 +87,7 @@ hipError_t launch_beam(const BeamParams& p, sv_dtype dt, hipStream_t s);
 hipError_t launch_distill_loss(const DistillParams& p, sv_dtype dt, hipStream_t s);
 hipError_t launch_distill_grad(const DistillParams& p, sv_dtype dt, hipStream_t s);
 hipError_t launch_distill_held(const DistillParams& p, sv_dtype dt, hipStream_t s);
-hipError_t launch_reorder(const ReorderParams& p, int vec, hipStream_t s);
+hipError_t launch_reorder(const ReorderParams& p, hipStream_t s);
+constexpr int kReorderOdd = 6;  // places at a segment's end: of 4 bytes (3 at most) and of one (3)
 
 }  // namespace sv

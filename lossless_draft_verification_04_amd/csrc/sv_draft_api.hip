@@ -319,17 +319,8 @@ sv_status sv_beam_reorder(const void* src, const int64_t* src_stride, void* dst,
   plan_reorder(&pl);
   sv_status st;
   if ((st = check_ws(ws, ws_bytes, pl)) != SV_OK) return st;
-  // the widest vector that every address allows
-  uint64_t bits = a | b;
-  for (int i = 0; i < 4; ++i) {
-    if (ns[i] > 1) bits |= (uint64_t)src_stride[i];
-    if (nd[i] > 1) bits |= (uint64_t)dst_stride[i];
-  }
-  int vec = 16;
-  while (vec > 1 && bits % (uint64_t)vec != 0) vec /= 2;
-  // 256-thread blocks over a segment's bytes, the narrowest vector a launch may fall back to
-  const int64_t least = std::min<int64_t>(vec, 4) * 256;
-  if ((run + least - 1) / least > INT32_MAX / ((int64_t)L * B) / H) return SV_EUNSUPPORTED;
+  // blocks of 256 places of 4 bytes, the smallest that a launch takes
+  if ((run / 4 + kReorderOdd + 255) / 256 > INT32_MAX / ((int64_t)L * B) / H) return SV_EUNSUPPORTED;
   ReorderParams p;
   p.src = static_cast<const char*>(src);
   p.dst = static_cast<char*>(dst);
@@ -348,7 +339,7 @@ sv_status sv_beam_reorder(const void* src, const int64_t* src_stride, void* dst,
   p.pos = pos_bytes;
   p.inplace = inplace;
   p.err = reinterpret_cast<int32_t*>(static_cast<char*>(ws));
-  return launch_reorder(p, vec, static_cast<hipStream_t>(stream)) == hipSuccess ? SV_OK : SV_EHIP;
+  return launch_reorder(p, static_cast<hipStream_t>(stream)) == hipSuccess ? SV_OK : SV_EHIP;
 }
 
 }  // extern "C"
