@@ -19,6 +19,7 @@ struct alignas(16) Teacher {
   double ts[kTW];              // its wave's sum
   float tm[kTW];               // its wave's largest value
   int live;                    // the row has teacher mass
+  int dup;                     // an id comes twice
 };
 // The drafter's logits at these tokens.
 struct Drafter {

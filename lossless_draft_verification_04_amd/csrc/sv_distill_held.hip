@@ -14,8 +14,8 @@
 //
 // A byte of LDS per vector marks the tokens of I; bits past V stay set for
 // good.  The gradients at the tokens of I are stored, after the row's vectors,
-// by the thread that stored the vector they lie in: a thread's stores to one
-// place stay in order, and no wait for the next row's loads comes between.
+// by the wave that stored the vector they lie in: a wave's stores to one place
+// stay in order, and no wait for the next row's loads comes between.
 #include "sv_distill.hpp"
 #include "sv_internal.h"
 
@@ -58,22 +58,41 @@ __device__ __forceinline__ void teacher_ids(const DistillParams& a, Fetched& f, 
     f.id = -1;
   }
   if (i >= 0) s.id[i] = f.id;
-  if (i == 0) s.live = f.rest > kNegInf;
+  if (i == 0) {
+    s.live = f.rest > kNegInf;
+    s.dup = 0;
+  }
 }
-// Repeats out, the exponentials in, whether there is mass at all.  Final after
-// a barrier, but for s.id, from which the caller takes the repeats (true)
-// behind that barrier.
-__device__ __forceinline__ bool teacher_tokens(const DistillParams& a, Fetched& f, Teacher& s, int i) {
-  if (i < 0) return false;  // whole waves
-  bool twice = false;
-  if (i < ((a.k + kWave - 1) & ~(kWave - 1))) twice = repeated(s.id, i, f.id, a.k);
+// The marks and exponentials in, whether there is mass at all; final after a
+// barrier, behind which teacher_repeats looks after an id that comes twice (its
+// mark was set already).
+template <int E>
+__device__ __forceinline__ void teacher_tokens(const DistillParams& a, const Fetched& f, Teacher& s, uint32_t* mark,
+                                               int i) {
+  if (i < 0) return;  // whole waves
+  if (f.id >= 0) {
+    const uint32_t bit = 1u << ((f.id / E % 4) * 8 + f.id % E);
+    if (atomicOr(&mark[f.id / E / 4], bit) & bit) s.dup = 1;
+    if (f.t > kNegInf) s.live = 1;
+  }
+  token_teacher(s, i, f.id >= 0 ? f.t : kNegInf, a.k, a.invT);
+}
+// The block's threads, for a row with repeats (s.dup): they become absent.
+__device__ __forceinline__ void teacher_repeats(const DistillParams& a, Fetched& f, Teacher& s, int i) {
+  const bool twice = i >= 0 && repeated(s.id, i, f.id, a.k);
+  lds_sync();
   if (twice) {
     set_error(a.err, SV_DERR_TOKEN);
     f.id = -1;
+    s.id[i] = -1;
   }
-  if (f.id >= 0 && f.t > kNegInf) s.live = 1;
-  token_teacher(s, i, f.id >= 0 ? f.t : kNegInf, a.k, a.invT);
-  return twice;
+  if (i == 0) s.live = f.rest > kNegInf;
+  lds_sync();
+  if (i >= 0) {
+    if (f.id >= 0 && f.t > kNegInf) s.live = 1;
+    token_teacher(s, i, f.id >= 0 ? f.t : kNegInf, a.k, a.invT);
+  }
+  lds_sync();
 }
 
 }  // namespace
@@ -126,7 +145,6 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
     for (int u = 0; u < FU; ++u) unpack<DT>(d[i + u], x + u * E);
     fold_values<FU * E, true>(x, a.c, acc);
   };
-  auto set_mark = [&](int b, int32_t id) { atomicOr(&s_mark[b][id / E / 4], 1u << ((id / E % 4) * 8 + id % E)); };
   auto clear_mark = [&](int b, int32_t id) { atomicAnd(&s_mark[b][id / E / 4], ~(1u << ((id / E % 4) * 8 + id % E))); };
   // one wave: a row's teacher as probabilities
   auto teacher_probs = [&](int row, int b) {
@@ -161,10 +179,9 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
   {
     teacher_ids(a, cur, s_t[0], ti);
     lds_sync();
-    const bool twice = teacher_tokens(a, cur, s_t[0], ti);
-    if (cur.id >= 0) set_mark(0, cur.id);
+    teacher_tokens<E>(a, cur, s_t[0], s_mark[0], ti);
     lds_sync();
-    if (twice) s_t[0].id[ti] = -1;
+    if (s_t[0].dup) teacher_repeats(a, cur, s_t[0], ti);
     const bool live = s_t[0].live != 0;
     if (live && cur.id >= 0) z = load_elem<DT>(row_of(r), cur.id);
     if (live && tid < tail) ztail = load_elem<DT>(row_of(r), (int64_t)nfull * E + tid);
@@ -219,13 +236,9 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
     }
     // meanwhile: this row's marks go, the next row's tokens and marks come
     if (cur.id >= 0) clear_mark(b, cur.id);
-    bool twice = false;
-    if (next) {
-      twice = teacher_tokens(a, f, sn, ti);
-      if (f.id >= 0) set_mark(b ^ 1, f.id);
-    }
+    if (next) teacher_tokens<E>(a, f, sn, s_mark[b ^ 1], ti);
     lds_sync();  // C: the factors, the gradients of I, the next row's teacher and marks
-    if (twice) sn.id[ti] = -1;
+    if (next && sn.dup) teacher_repeats(a, f, sn, ti);  // block-uniform
     const bool nlive = next && sn.live != 0;
     const __amdgpu_buffer_rsrc_t rs = row_range(nlive ? rn : r, nlive);
     char* out = static_cast<char*>(a.grad) + (int64_t)r * a.gb;
@@ -273,22 +286,14 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
       }
     }
     if (tid < tail) store_elem_alias<DT>(out, (int64_t)nfull * E + tid, grad_elem(ztail, g, a.c));
-    // the tokens of I whose vectors this wave's threads stored
-    for (int i0 = 0; i0 < a.k; i0 += kWave) {
-      const int i = i0 + lane;
-      const int32_t id = i < a.k ? s.id[i] : -1;
-      const float gv = i < a.k ? s_q.g[i] : 0.f;
+    // the tokens of I whose vectors this wave stored: a wave's stores to one
+    // place stay in order
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    for (int i = lane; i < a.k; i += kWave) {
+      const int32_t id = s.id[i];
       // in the shorter last vector thread e stored element e
       const int owner = id / E < nfull ? id / E % NT : id - nfull * E;
-      uint64_t mine = __ballot(id >= 0 && owner / kWave == wave);
-      while (mine) {
-        const int q = __builtin_ctzll(mine);
-        mine &= mine - 1;
-        const int oid = __builtin_amdgcn_readlane(id, q);
-        const float ov = readlane_f(gv, q);
-        const int ol = __builtin_amdgcn_readlane(owner, q) & (kWave - 1);
-        if (lane == ol) store_elem_alias<DT>(out, oid, ov);
-      }
+      if (id >= 0 && owner / kWave == wave) store_elem_alias<DT>(out, id, s_q.g[i]);
     }
     if (!next) return;
     ztail = zt;
