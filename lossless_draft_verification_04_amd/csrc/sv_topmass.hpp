@@ -157,6 +157,14 @@ __device__ __forceinline__ void values_below(const Src& src, const typename Src:
     if (top_key(x[e], i0 + e) >= kth) x[e] = kNegInf;
 }
 
+// An entry's order as a positive double (larger = better; 0: none): the value's
+// order bits over 24 bits of complemented index, 56 bits in all, read as the
+// bits of a double, whose comparison is one full-rate instruction.
+__device__ __forceinline__ double order_of(float v, int32_t i) {
+  const uint64_t k = top_key(v, i);
+  return i == kNoIdx ? 0.0 : __longlong_as_double((long long)(((k >> 32) << 24) | (k & 0xffffffull)));
+}
+
 // The 32-bit sum of 2^(c x - r) over a vector's values: the same instructions
 // wherever a vector is added or taken out.
 template <int E>
@@ -183,7 +191,7 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   const int tid = threadIdx.x;
   __shared__ uint64_t s_cand[kCand];
   __shared__ uint32_t s_gm[NT];
-  __shared__ uint64_t s_key[kCand];
+  __shared__ alignas(16) uint64_t s_key[kCand];
   __shared__ uint64_t s_sel[kWave];
   __shared__ uint64_t s_tau;
   __shared__ int s_nc;
@@ -278,8 +286,12 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   const uint64_t tkey = bo == kNoIdx ? 0ull : top_key(bm, (int32_t)((v0 + bo) * E));
   constexpr int kMaxH = NT / kWave;
   static_assert(kMaxH >= 1 && kMaxH <= 16 && kMaxH * kWave == NT, "whole waves, at most 16");
+  // four times as many groups as listed values: more of them lengthen the
+  // search, fewer loosen the bound, so that more threads' other vectors are
+  // read again (2048 x 151936 bf16 rows, 64 values: 133 us at twice as many,
+  // 112 at four and eight times; 128 x 32000, 16 values: 11.5 and 12.6 us)
   int H = 1;
-  while (H < kMaxH && 8 * F > kWave * H) H *= 2;  // block-uniform
+  while (H < kMaxH && 4 * F > kWave * H) H *= 2;  // block-uniform
   const int GS = NT / (kWave * H);
   {
     uint64_t k = tkey;
@@ -293,7 +305,7 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   lds_sync();
   if (wave == 0) {
     uint32_t p = 0;
-    if (H == 1) {  // one group per lane (F <= 8)
+    if (H == 1) {  // one group per lane (F <= 16)
       const uint32_t gh = s_gm[lane];
 #pragma unroll
       for (int bit = 31; bit >= 16; --bit) {
@@ -318,31 +330,32 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   uint64_t tau = s_tau;
   // the thread's vectors besides its best may hold a key of at least t
   auto others_reach = [&](uint64_t t) { return more && top_key(om, (int32_t)((v0 + tid) * E)) >= t; };
-  // f(vs, d) for every vector of the wave's lanes with `pick`, one per lane at
-  // a time (vs < 0: none); bo of its owner is passed on
+  // f(vs, o, d) for every vector of the wave's lanes with `pick`: two such
+  // lanes' vectors at a time, one each per lane (vs < 0: none), o the owner's
+  // best vector
   auto spread = [&](bool pick, auto&& f) {
-    const uint64_t fm = __ballot(pick);
-    if (!fm) return;  // wave-uniform
-    const int items = __builtin_popcountll(fm) * nk;
-    for (int base = 0; base < items; base += kWave) {
-      const int t = base + lane;
-      const int j = t < items ? t / nk : -1;
-      int sl = 0;  // the j-th such lane of the wave
-      uint64_t m = fm;
-      for (int q = 0; m; ++q) {
-        const int bl = __builtin_ctzll(m);
+    constexpr int kOwners = 2;
+    uint64_t m = __ballot(pick);
+    while (m) {  // wave-uniform
+      int own[kOwners];
+#pragma unroll
+      for (int q = 0; q < kOwners; ++q) {
+        own[q] = m ? __builtin_ctzll(m) : -1;
         m &= m - 1;
-        sl = j == q ? bl : sl;
       }
-      const int32_t sbo = __shfl(bo, sl, kWave);
-      int64_t vs = -1;
-      if (j >= 0) {
-        const int at = wave * kWave + sl + (t - j * nk) * NT;
-        if (at < span) vs = v0 + at;
+      for (int k = lane; k - lane < nk; k += kWave) {
+        typename Src::Data dd[kOwners];
+        int64_t vs[kOwners];
+#pragma unroll
+        for (int q = 0; q < kOwners; ++q) {
+          const int at = wave * kWave + own[q] + k * NT;
+          vs[q] = own[q] >= 0 && at < span ? v0 + at : -1;
+          if (vs[q] >= 0) dd[q] = src.load(vs[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < kOwners; ++q)
+          f(vs[q], __builtin_amdgcn_readlane(bo, own[q] >= 0 ? own[q] : 0), dd[q]);
       }
-      typename Src::Data dd{};
-      if (vs >= 0) dd = src.load(vs);
-      f(vs, sbo, dd);
     }
   };
   int nc;
@@ -370,15 +383,29 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
     if (tid == 0) s_nc = 0;
     lds_sync();
   }
-  if (nc <= kWave) {  // block-uniform
-    if (wave == 0) {
-      wave_rank(s_cand, nc, F, lane, lv, li);
-      if (lane == F - 1) s_tau = li == kNoIdx ? 0ull : top_key(lv, li);
+  // a candidate's place is the number of better ones, counted over LDS
+  {
+    double* keys = reinterpret_cast<double*>(s_key);
+    const double2* pairs = reinterpret_cast<const double2*>(s_key);
+    if (tid == 0) s_tau = 0ull;
+    for (int i = tid; i < kCand; i += NT) {  // past the last one 0, above none
+      const uint64_t cd = i < nc ? s_cand[i] : 0ull;
+      keys[i] = i < nc ? order_of(cand_value(cd), (int32_t)(cd >> 32)) : 0.0;
     }
     lds_sync();
-  } else {
-    block_select<NT>(s_cand, s_key, s_sel, nc, F, &s_tau);
-    if (wave == 0 && lane < F) {
+    for (int i = tid; i < nc; i += NT) {
+      const double k = keys[i];
+      int above = 0;
+#pragma unroll 4
+      for (int j = 0; j < nc; j += 2) {
+        const double2 o = pairs[j >> 1];
+        above += (o.x > k ? 1 : 0) + (o.y > k ? 1 : 0);
+      }
+      if (above < F) s_sel[above] = s_cand[i];
+      if (above == F - 1) s_tau = cand_key(s_cand[i]);
+    }
+    lds_sync();
+    if (wave == 0 && lane < F && lane < nc) {
       lv = cand_value(s_sel[lane]);
       li = (int32_t)(s_sel[lane] >> 32);
     }
@@ -452,14 +479,6 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
 constexpr int kPartEntries = 256;
 constexpr int kMostParts = 16;
 constexpr int kPerLane = kPartEntries / kWave;
-
-// An entry's order as a positive double (larger = better; 0: none): the value's
-// order bits over 24 bits of complemented index, 56 bits in all, read as the
-// bits of a double, whose comparison is one full-rate instruction.
-__device__ __forceinline__ double order_of(float v, int32_t i) {
-  const uint64_t k = top_key(v, i);
-  return i == kNoIdx ? 0.0 : __longlong_as_double((long long)(((k >> 32) << 24) | (k & 0xffffffull)));
-}
 
 // The lists and masses of a row's nch parts (nch * F <= kPartEntries) as the
 // row's: (lv, li) is the merged list (lane l = l-th best); the return value is

@@ -530,10 +530,29 @@ def _rows_2d(t, what):
     """R, V and the row stride of a [R, V] tensor."""
     if t.dim() != 2:
         raise SpecVerifyError(SV_EINVAL, f"{what}: want [rows, V], got {tuple(t.shape)}")
+    R, V = t.shape
     stride, unit = t.stride()
-    if unit != 1:
+    if unit != 1 and V > 1:
         raise SpecVerifyError(SV_EINVAL, f"{what}: vocabulary axis must have unit stride")
-    return *t.shape, stride
+    return R, V, stride if R > 1 else _one_row(V, t)
+
+
+def _one_row(V, t):
+    """A stride for a single row, whatever the tensor says of it."""
+    return V + -V % (16 // t.element_size())
+
+
+def _rows_3d(t, what):
+    """B, W, V and the row stride of a [B, W, V] tensor of evenly spaced rows."""
+    if t.dim() != 3:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: want [B, W, V], got {tuple(t.shape)}")
+    B, W, V = t.shape
+    outer, stride, unit = t.stride()
+    if unit != 1 and V > 1:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: vocabulary axis must have unit stride")
+    if B > 1 and W > 1 and outer != W * stride:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: rows must be evenly spaced")
+    return B, W, V, stride if W > 1 else outer if B > 1 else _one_row(V, t)
 
 
 def sv_teacher_topk(logits, k, T, workspace=None):
@@ -612,9 +631,7 @@ def sv_distill_topk_backward(z, ids, vals, stat, T, rest=None, grad_loss=None, g
 def sv_beam_select(logits, scores, N, T=1.0, finished=None, pad_tok=0, workspace=None):
     """One step of beam search.  logits [B, W, V], scores [B, W] float32, finished [B, W] int32 or None
     -> dict(beam, tok [B, N] int32, score [B, N])."""
-    if logits.dim() != 3:
-        raise SpecVerifyError(SV_EINVAL, f"logits: want [B, W, V], got {tuple(logits.shape)}")
-    B, W, V = logits.shape
+    B, W, V, stride = _rows_3d(logits, "logits")
     _want(scores, torch.float32, (B, W), "scores")
     if finished is not None:
         _want(finished, torch.int32, (B, W), "finished")
@@ -626,7 +643,7 @@ def sv_beam_select(logits, scores, N, T=1.0, finished=None, pad_tok=0, workspace
     out = dict(beam=torch.empty(B, N, dtype=torch.int32, device=dev),
                tok=torch.empty(B, N, dtype=torch.int32, device=dev),
                score=torch.empty(B, N, dtype=torch.float32, device=dev))
-    _call(dev, _lib.sv_beam_select, "sv_beam_select", logits.data_ptr(), dt, _row_stride(logits, "logits"), scores.data_ptr(),
+    _call(dev, _lib.sv_beam_select, "sv_beam_select", logits.data_ptr(), dt, stride, scores.data_ptr(),
           _at(finished), B, W, V, float(T), pad, N, out["beam"].data_ptr(), out["tok"].data_ptr(), out["score"].data_ptr(), ws.data_ptr(),
           ws.numel())
     _checked(dev, "sv_beam_select", workspace)

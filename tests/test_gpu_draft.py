@@ -91,6 +91,16 @@ def teacher_rows(kind, R, V, dtype):
     if kind == "crowd":  # the top tokens side by side
         x[:, 1000:1100] += 30.0
         return x
+    if kind == "cliff":  # the last values lie far above all others (2^200 and more of them)
+        y = torch.randn(R, V, generator=g) - 100.0
+        y[:, -500:] += 150.0
+        return y.to(dtype)
+    if kind == "late":  # nothing in the first three quarters
+        return x.masked_fill(torch.arange(V) < 3 * V // 4, -INF)
+    if kind == "low rest":  # the list holds all but 2^-150 of the mass
+        y = torch.randn(R, V, generator=g)
+        y[:, 7000:7040] += 105.0
+        return y.to(dtype)
     if kind == "rising":  # every vector beats the one before
         return torch.linspace(-20, 20, V).expand(R, V).to(dtype)
     raise KeyError(kind)
@@ -98,7 +108,8 @@ def teacher_rows(kind, R, V, dtype):
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("R", [2, 530])
-@pytest.mark.parametrize("kind", ["ties", "equal", "masked", "lowest", "one", "peak", "crowd", "rising"])
+@pytest.mark.parametrize("kind", ["ties", "equal", "masked", "lowest", "one", "peak", "crowd", "rising", "cliff", "late",
+                                  "low rest"])
 def test_teacher_hard_rows(kind, R, dtype):
     check_teacher(teacher_rows(kind, R, 20011, dtype), 40, 1.0)
 
@@ -174,6 +185,47 @@ def test_distill(R, V, k, T, dtype):
     x = rows(R, V, dtype, R + V)
     g = torch.rand(R, generator=torch.Generator().manual_seed(1)) - 0.3
     check_distill(x, *target(x, k, T, 2), T, g, inplace=True)
+
+
+@pytest.mark.parametrize("dtype,R,V", [
+    (BF16, 3000, 1031), (F32, 2700, 3001), (BF16, 2900, 9001), (F32, 1700, 12007), (BF16, 1700, 30011), (F32, 1300, 30011),
+    (BF16, 1300, 60013), (F32, 530, 40013), (BF16, 530, 90001), (F32, 530, 60001), (BF16, 530, 128256), (F32, 530, 80001),
+    (BF16, 520, 160003), (F32, 520, 98304), (BF16, 520, 196608)])
+def test_distill_more_rows_than_blocks(dtype, R, V):
+    """Blocks that walk several rows, at every size of row that a block can hold; rows without a target, repeated and
+    bad ids among them; some rows are compared."""
+    g = torch.Generator().manual_seed(R + V)
+    k = 20
+    x = (torch.randn(R, V, generator=g) * 2).to(dtype)
+    ids = torch.randint(0, V, (R, 3 * k), generator=g, dtype=torch.int32)
+    for r in range(R):  # distinct
+        ids[r, :k] = ids[r].unique()[torch.randperm(len(ids[r].unique()), generator=g)[:k]]
+    ids = ids[:, :k].contiguous()
+    ids[:, 1] = torch.where((ids == V - 1).any(1), ids[:, 1], torch.full((R,), V - 1, dtype=torch.int32))
+    x.scatter_add_(1, ids.long(), torch.full((R, k), 9.0, dtype=dtype))
+    vals = x.gather(1, ids.long()).float() + 0.5 * torch.randn(R, k, generator=g)
+    rest = torch.rand(R, generator=g) * 4 + math.log(V)
+    ids[4::5], rest[4::5] = -1, -INF
+    ids[3::50, 7] = ids[3::50, 2]
+    ids[8::50, 5] = V
+    weight = torch.rand(R, generator=g)
+    dev = [t.to(DEV) for t in (ids, vals, rest, weight)]
+    got = svx.sv_distill_topk(put(x), dev[0], dev[1], 1.0, rest=dev[2], grad_loss=dev[3], want_grad=True)
+    torch.cuda.synchronize()
+    assert svx.sv_get_device_error(DEV) == svx.DERR_TOKEN
+    pick = torch.cat([torch.arange(10), torch.randperm(R, generator=g)[:14], torch.arange(R - 6, R),
+                      torch.tensor([253, 258, 303, 508])]).unique()
+    loss, stat, grad, size = ref.distill(x[pick], ids[pick], vals[pick], rest[pick], 1.0, weight[pick])
+    at = pick.to(DEV)
+    near(got["loss"][at], loss, 2 * ref.SUM + 2.0 ** -23 * loss.abs(), "loss")
+    near(got["stat"][at], stat, ref.SUM * stat.abs(), "stat")
+    near(got["grad"][at], grad, 3e-5 * size + ref.HALF[dtype] * grad.abs() + 1e-37, "grad")
+    # the other rows: the same call on each in place, alone, gives the same bits
+    y = put(x[:40])
+    svx.sv_distill_topk(y, dev[0][:40], dev[1][:40], 1.0, rest=dev[2][:40], grad_loss=dev[3][:40], grad=y)
+    torch.cuda.synchronize()
+    assert svx.sv_get_device_error(DEV) == svx.DERR_TOKEN
+    assert torch.equal(y, got["grad"][:40])
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -352,6 +404,41 @@ def test_beam_select_ties_go_to_the_lower_beam_and_token():
     fin = torch.zeros(2, 6, dtype=torch.int32)
     fin[0, 1] = fin[0, 4] = 1
     check_beams(x, s, 40, finished=fin, pad=-1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_layouts_of_few_rows(dtype):
+    """Dimensions of one: their strides say nothing, and a single row needs no padded end."""
+    V = 20011
+    x = rows(6, V, dtype, 35)
+    big = put(x)
+    s = beam_scores(6, 1, 9)
+    for view, sc in ((big.view(6, 1, V), s), (big.unflatten(0, (1, 6)), s.view(1, 6)), (big[::2].unflatten(0, (3, 1)), s[::2])):
+        got = svx.sv_beam_select(view, sc.contiguous().to(DEV), 5)
+        want = ref.beams(view.cpu(), sc.reshape(view.shape[:2]), 5, 1.0)
+        assert torch.equal(got["tok"].cpu().long(), want[1][:, :5])
+    one = x[2].to(DEV)  # V elements exactly
+    for z in (one[None], one.view(1, V).expand(1, V), one.as_strided((1, V), (1, 1))):
+        got = svx.sv_teacher_topk(z, 6, 1.0)
+        ids, vals, rest = ref.teacher(x[2:3], 6, 1.0)
+        assert torch.equal(got["ids"].cpu().long(), ids)
+        out = svx.sv_distill_topk(z, got["ids"], got["vals"], 1.0, rest=got["rest"], want_grad=True)
+        near(out["loss"], torch.zeros(1), 2 * ref.SUM, "loss of a teacher against itself")
+    assert svx.sv_beam_select(one[None, None], torch.zeros(1, 1, device=DEV), 3)["tok"].cpu().tolist()[0] == ids[0, :3].tolist()
+    with pytest.raises(svx.SpecVerifyError):
+        svx.sv_beam_select(big.unflatten(0, (2, 3))[:, :2], s.view(2, 3)[:, :2].contiguous().to(DEV), 2)
+
+
+def test_empty_batches():
+    z = torch.empty(0, 1000, dtype=BF16, device=DEV)
+    r = svx.sv_teacher_topk(z, 4, 1.0)
+    assert r["ids"].shape == (0, 4)
+    out = svx.sv_distill_topk(z, r["ids"], r["vals"], 1.0, rest=r["rest"], want_grad=True)
+    assert out["grad"].shape == (0, 1000) and out["loss"].shape == (0,)
+    b = svx.sv_beam_select(torch.empty(0, 3, 1000, dtype=BF16, device=DEV), torch.empty(0, 3, device=DEV), 2)
+    assert b["beam"].shape == (0, 2)
+    st = torch.empty(2, 0, 3, 5, device=DEV)
+    assert svx.sv_beam_reorder(st, torch.empty(0, 3, dtype=torch.int32, device=DEV)) is st
 
 
 def test_beam_select_masked_rows():
