@@ -93,6 +93,13 @@ sv_status plan_distill(sv_dtype dt, int32_t R, int32_t V, int32_t k, Plan* pl) {
   return SV_OK;
 }
 
+// Whether loss and gradient together hold rows in registers, a block a row:
+// wherever a row fits, but for a few long ones, which many blocks finish
+// sooner in two launches (128256 bf16 logits, 1 row: 20 us held, 17 in two
+// launches; 40 rows 22 and 19; 96 rows 22 and 26; 2000 rows 208 and 275;
+// 64000 logits, any number of rows: held 14-111, two launches 17-150).
+bool hold_rows(int32_t R, int64_t nvec) { return nvec <= kHeldVecs && !(R <= 48 && nvec > 14000); }
+
 void plan_reorder(Plan* pl) { pl->bytes = kWsFixed; }
 
 // The gradient's rows: z itself, or apart from it.
@@ -235,7 +242,7 @@ sv_status sv_distill_topk(const void* z, sv_dtype dt, int64_t stride, int32_t R,
   p.out_stat = out_stat;
   p.stat = out_stat;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (out_grad && pl.nvec <= kHeldVecs) return launch_distill_held(p, dt, s) == hipSuccess ? SV_OK : SV_EHIP;
+  if (out_grad && hold_rows(R, pl.nvec)) return launch_distill_held(p, dt, s) == hipSuccess ? SV_OK : SV_EHIP;
   if (launch_distill_loss(p, dt, s) != hipSuccess) return SV_EHIP;
   if (out_grad && launch_distill_grad(p, dt, s) != hipSuccess) return SV_EHIP;
   return SV_OK;
