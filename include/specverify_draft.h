@@ -164,7 +164,9 @@ sv_status sv_beam_select(const void* logits, sv_dtype dt, int64_t stride, const 
  *   parent [B, N]: -1 leaves a beam's state as it is
  * dst may be src (the same pointer and strides, N <= W): the call then works
  * in place, and a beam that follows itself costs nothing.  Otherwise they must
- * not overlap, and dst's rows must not overlap each other (SV_EINVAL).
+ * not overlap, first byte to last.  What is written (in place: all W beams'
+ * states) must not overlap itself, and its strides must nest: each at least
+ * what the smaller ones span.  SV_EINVAL otherwise.
  * A parent outside [-1, W) or a length outside [0, S] sets SV_DERR_RANGE; that
  * beam, or that whole sequence, is left as it was.  Any alignment is taken.
  */

@@ -320,6 +320,7 @@ sv_status sv_beam_reorder(const void* src, const int64_t* src_stride, void* dst,
   if (es < 0 || ed < 0 || !apart_d) return SV_EINVAL;
   bool inplace = src == dst && N <= W;
   for (int i = 0; i < 4; ++i) inplace = inplace && (src_stride[i] == dst_stride[i] || (ns[i] == 1 && nd[i] == 1));
+  if (inplace && !apart_s) return SV_EINVAL;  // a beam that no beam takes the place of could lie under one that moves
   const uintptr_t a = reinterpret_cast<uintptr_t>(src), b = reinterpret_cast<uintptr_t>(dst);
   if (!inplace && a < b + (uintptr_t)ed && b < a + (uintptr_t)es) return SV_EINVAL;
   Plan pl;

@@ -129,6 +129,10 @@ def test_beam_reorder_argument_checks():
     assert f(dst=P(0x10000 + 512)) == svx.SV_EINVAL          # over src, not in place
     assert f(dst=A, ds=(16384, 4096, 1024, 512)) == svx.SV_EINVAL
     assert f(dst=A, N=5) == svx.SV_EINVAL                    # in place with more beams than there are
+    over = (12288, 4096, 512, 512)                           # in place, beam 1 lies over beam 0's second segment
+    assert f(dst=A, ss=over, ds=over, W=2, N=1) == svx.SV_EINVAL
+    next_ = (8192, 2048, 1024, 512)                          # and beams 2, 3 over the next sequence's
+    assert f(dst=A, ss=next_, ds=next_, N=2) == svx.SV_EINVAL
     assert f(ws=None) == svx.SV_EWORKSPACE and f(wsb=64) == svx.SV_EWORKSPACE and f(ws=P(0x40010)) == svx.SV_EALIGN
     for name in ("L_", "B", "H", "S"):
         assert f(**{name: 0}) == svx.SV_OK, name  # nothing enqueued
