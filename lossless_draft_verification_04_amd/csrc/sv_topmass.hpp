@@ -72,9 +72,10 @@ struct Mass {
   float s = 0.f;
 };
 
-// a <- a + the E values x (-inf: nothing).  The shift is m, as fma(x, c, -c m);
-// where c m is not finite (rows masked with the type's lowest value), as
-// (x - m) c; SUB: always so (no branch, an operation more a value).
+// a <- a + the E values x (-inf: nothing).  The shift is m, as fma(x, c, -c m),
+// whose -c m carries a rounding of 2^-25 |c m| into every term; past 2^6 (values
+// far from 0, a low temperature, rows masked with the type's lowest value) it
+// is (x - m) c; SUB: always so (no branch, an operation more a value).
 template <int E, bool SUB = false>
 __device__ __forceinline__ void fold_values(const float (&x)[E], float c, Mass& a) {
   float fm = x[0];
@@ -84,7 +85,7 @@ __device__ __forceinline__ void fold_values(const float (&x)[E], float c, Mass& 
   const float ref = mn == kNegInf ? 0.f : mn;
   const float cm = c * ref;
   float t[E];
-  if (!SUB && __builtin_expect(fabsf(cm) <= 3e38f, 1)) {
+  if (!SUB && __builtin_expect(fabsf(cm) <= 64.f, 1)) {
 #pragma unroll
     for (int e = 0; e < E; ++e) t[e] = fast_exp2(__builtin_fmaf(x[e], c, -cm));
   } else {
@@ -436,10 +437,10 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
     wm = wave_fmax(bm);
     // what went leaves 2^-53 of itself behind, some sixty times over: no more
     // than 2^-25 of what stays.  Values 2^-126 of the reference are lost.
-    again = !(ws > 0x1p-70) | !(ws > 0x1p-22 * (double)wave_fmax(gone)) | !(fabsf(r) <= 3e38f) | ((wm - ref) * c > 100.f);
+    again = !(ws > 0x1p-70) | !(ws > 0x1p-22 * (double)wave_fmax(gone)) | !(fabsf(r) <= 0x1p30f) | ((wm - ref) * c > 100.f);
     if (!again) {
       wm = ref;
-      ws *= 1.0 + 0.6931471805599453 * ((double)r - (double)c * (double)ref);  // r is not quite c ref
+      ws *= exp2_d((double)r - (double)c * (double)ref);  // r is not quite c ref: 2^-25 of it, 2^5 at most
     }
   }
   if (again) {

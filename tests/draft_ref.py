@@ -4,6 +4,7 @@ Tolerances.  A kernel's sum of exponentials has terms 2^x, x = c (z - m): the ha
 (2^-23 relative), x carries the roundings of c and of one fused multiply-add (2^-24 |x| each, times ln 2 in the result).
 Terms that matter have |x| <= 25, so a term is within 25 * 2 * 2^-24 * 0.7 + 2^-23 < 2.3e-6.  A thread adds at most
 about 100 terms in sequence after trees of five levels (2^-24 each: < 6.3e-6 in the worst case, one sign throughout).
+A shift c m that is rounded before it is taken off is below 64 then: 2^-25 * 64 * 0.7 < 1.4e-6, whatever the logits' size.
 So a sum is within SUM = 1e-5 of itself, and its logarithm within 1e-5.
 """
 import math
@@ -14,8 +15,14 @@ SUM = 1e-5
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}  # half a step, relative
 
 
+def in_32_bits(T):
+    """The temperature as the entry points take it: at |z / T| = 1e7 its rounding shows."""
+    return float(torch.tensor(T, dtype=torch.float32))
+
+
 def teacher(z, k, T):
     """ids, vals, rest of [R, V] rows (any device) in 64 bits."""
+    T = in_32_bits(T)
     z = z.double()
     R, V = z.shape
     n = min(k, V)
@@ -29,6 +36,7 @@ def teacher(z, k, T):
 
 def distill(z, ids, vals, rest, T, g=None):
     """loss, stat, gradient, and |gradient|'s scale (g / T) (q + p) per element, from the formulas."""
+    T = in_32_bits(T)
     z = z.double()
     R, V = z.shape
     ids, vals = ids.long(), vals.double()
@@ -82,6 +90,7 @@ def distill(z, ids, vals, rest, T, g=None):
 
 def beams(z, scores, N, T, finished=None, pad=0):
     """beam, tok, score [B, N + 1] (one more than asked: the next score) in 64 bits."""
+    T = in_32_bits(T)
     B, W, V = z.shape
     beam = torch.full((B, N + 1), -1, dtype=torch.int64)
     tok, score = beam.clone(), torch.full((B, N + 1), -math.inf, dtype=torch.float64)

@@ -306,6 +306,17 @@ def test_distill_peaked_rows_keep_the_digits_of_the_rest():
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("T", [1.0, 0.01])
+@pytest.mark.parametrize("V", [4099, 40009, 210011])
+def test_rows_far_from_zero(V, T, dtype):
+    """An offset that all of a row's logits share changes nothing, whatever it is in units of T."""
+    x = (rows(5, V, F32, 23) + torch.tensor([0.0, 70, -3000, 20000, -5e5])[:, None]).to(dtype)
+    check_teacher(x, 20, T)
+    ids, vals, rest = ref.teacher(x.float() + 0.6 * torch.randn(x.shape, generator=torch.Generator().manual_seed(24)), 20, T)
+    check_distill(x, ids.int(), vals.float(), rest.float(), T)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T", [1e-3, 0.05, 30.0])
 def test_distill_temperatures(T, dtype):
     """A large c = log2(e) / T: c z - c m loses digits with |c z| unless the shift is undone, so rows are small here:
