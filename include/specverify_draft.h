@@ -98,11 +98,12 @@ sv_status sv_teacher_topk(const void* logits, sv_dtype dt, int64_t stride, int32
  *     that stands in its row already sets SV_DERR_TOKEN and counts as absent.
  *   grad_loss [R] the loss's upstream gradient g, or NULL (all 1)
  * A row without teacher mass (no id with a value above -inf, rest NULL or
- * -inf), as padding has it, is not read: loss, stat and gradient are 0.  A row
+ * -inf), as padding has it, may hold anything: loss, stat and gradient are 0.  A row
  * with teacher mass and no finite logit sets SV_DERR_ROW and gives the same
  * zeros.  A token with p_i > 0 and q_i = 0 makes the loss +inf; its gradient
- * is finite (q_i - p_i), and so is that of the others (p_0 > 0 and q_0 = 0
- * gives the other tokens the gradient 0).
+ * is finite (q_i - p_i), and so is that of the others (q_v / q_0 is formed
+ * without q_0, which may underflow; where every logit outside I is -inf their
+ * gradient is 0).
  * Outputs:
  *   out_loss [R]
  *   out_stat [R, 4] what the backward pass needs: m, the row's largest logit;

@@ -249,9 +249,9 @@ __global__ __launch_bounds__(kDNT) void distill_grad_kernel(DistillParams a) {
   if (wave == 0) {
     const Norm n = wave_teacher(s, a.k, (double)f.rest, a.invT, lane);
     const double scale = (a.g ? (double)a.g[r] : 1.0) * a.invT;
-    const double q0 = st.w > 0.f ? (double)st.w * exp_d(((double)st.z - (double)st.x) * a.invT) * inv : 0.0;
+    const double ratio = st.w > 0.f ? exp_d(((double)st.z - (double)st.x) * a.invT) * inv : 0.0;
     if (lane == 0) {
-      s_g = grad_row(st.x, n.p0, q0, scale, inv);
+      s_g = grad_row(st.z, (double)st.w, n.p0, ratio, scale);
       s_scale = scale;
     }
   }

@@ -109,12 +109,12 @@ __device__ __forceinline__ Norm wave_teacher(Teacher& s, int k, double rest, dou
 // One wave: the row's sums from the partial sums outside I, a lane each
 // (lanes below kPL: pm, ps), and the tokens'.  m is the row's largest logit
 // (-inf: it has none), sum = sum_v exp((z_v - m) / T); m0, s0 the same outside
-// I; out = the sum outside I relative to m; fac (lane kPL + w) = the factor
-// that brings token wave w's exponentials to m.
+// I; fac: the factor that brings token wave w's exponentials to m (lane kPL + w)
+// and that of s0 (lane kPL + kTW).
 constexpr int kPL = kWave - kTW - 1;
 struct RowSums {
   float m, m0;
-  double sum, s0, out, fac;
+  double sum, s0, fac;
 };
 __device__ __forceinline__ RowSums wave_row_sums(const Drafter& s, float pm, double ps, double invT, int lane) {
   RowSums r;
@@ -129,8 +129,7 @@ __device__ __forceinline__ RowSums wave_row_sums(const Drafter& s, float pm, dou
   r.fac = x > kNegInf ? exp_d(((double)x - (double)(lane < kPL ? r.m0 : r.m)) * invT) : 0.0;
   ps *= r.fac;
   r.s0 = wave_sum(lane < kPL ? ps : 0.0);
-  r.out = r.s0 * readlane_d(r.fac, kPL + kTW);
-  r.sum = r.out;
+  r.sum = r.s0 * readlane_d(r.fac, kPL + kTW);
 #pragma unroll
   for (int w = 0; w < kTW; ++w) r.sum += readlane_d(ps, kPL + w);
   return r;
@@ -178,14 +177,17 @@ __device__ __forceinline__ void store_elem(void* row, int64_t i, float x) {
     reinterpret_cast<float*>(row)[i] = x;
 }
 
-// What the gradient of a row needs outside I: dz_v = each * 2^((z_v - m) c).
+// What the gradient of a row needs outside I: dz_v = each * 2^((z_v - m) c), m
+// the largest logit outside I.  There it is
+//   (g / T) (q_v - p_0 q_v / q_0) = (g / T) e^((z_v - m_0) / T) (e^((m_0 - m) / T) / s - p_0 / s_0),
+// of which nothing overflows however little of q is outside I.
 struct GradRow {
   float m, each;
 };
-// Of a row whose largest logit is m, inv = 1 / sum exp((z - m) / T).
-__device__ __forceinline__ GradRow grad_row(float m, double p0, double q0, double scale, double inv) {
-  const double other = p0 > 0.0 ? (q0 > 0.0 ? 1.0 - p0 / q0 : 0.0) : 1.0;
-  return GradRow{m, (float)(other * scale * inv)};
+// m0, s0 of the row; ratio = e^((m_0 - m) / T) / s; scale = g / T.
+__device__ __forceinline__ GradRow grad_row(float m0, double s0, double p0, double ratio, double scale) {
+  if (!(s0 > 0.0)) return GradRow{0.f, 0.f};  // every logit outside I is -inf
+  return GradRow{m0, (float)(scale * (ratio - p0 / s0))};
 }
 
 __device__ __forceinline__ float grad_elem(float z, const GradRow& g, float c) {

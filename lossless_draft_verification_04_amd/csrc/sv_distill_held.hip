@@ -218,14 +218,14 @@ __global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
     if (wave == 0) {
       // the row's sums, the gradient's factors, and the gradient at the tokens of I
       GradRow g{0.f, 0.f};
-      RowSums w{kNegInf, kNegInf, 0.0, 0.0, 0.0, 0.0};
+      RowSums w{kNegInf, kNegInf, 0.0, 0.0, 0.0};
       if (live) {
         w = wave_row_sums(s_q, lane < NW ? s_max[lane] : kNegInf, lane < NW ? s_sum[lane] : 0.0, a.invT, lane);
         if (w.m == kNegInf && lane == 0) set_error(a.err, SV_DERR_ROW);
       }
       const bool some = w.m > kNegInf;
       const double inv = some ? 1.0 / w.sum : 0.0, scale = some ? s_scale[b] : 0.0;
-      if (some) g = grad_row(w.m, s_n[b].p0, w.out * inv, scale, inv);
+      if (some) g = grad_row(w.m0, w.s0, s_n[b].p0, readlane_d(w.fac, kPL + kTW) * inv, scale);
 #pragma unroll 1
       for (int i = lane; i < a.k; i += kWave)
         s_q.g[i] = some ? (float)((s_q.e[i] * readlane_d(w.fac, kPL + i / kWave) * inv - s.p[i]) * scale) : 0.f;

@@ -75,14 +75,12 @@ def distill(z, ids, vals, rest, T, g=None):
             x = x + p0 * (math.log(p0) - lq0)
         loss[r] = x
         stat[r] = torch.stack([m, s, m0, s0])
-        d = q.clone()
-        if p0 > 0:
-            q0 = lq0.exp()
-            d[out] = q[out] * (1 - p0 / q0) if float(q0) > 0 else 0.0
+        d, w = q.clone(), q.clone()
+        if p0 > 0 and float(m0) > -math.inf:  # p_0 q_v / q_0 without q_0, which may underflow
+            e = p0 * ((zo - m0) / T).exp() / s0
+            d[out] = q[out] - e
+            w[out] = q[out] + e
         d[at] = q[at] - p
-        w = q.clone()
-        if p0 > 0 and float(lq0.exp()) > 0:
-            w[out] = q[out] * (1 + p0 / lq0.exp())
         w[at] = q[at] + p
         grad[r], size[r] = d * g[r] / T, w * abs(float(g[r])) / T
     return loss, stat, grad, size

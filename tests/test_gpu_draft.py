@@ -317,6 +317,17 @@ def test_rows_far_from_zero(V, T, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R,V", [(4, 4099), (5, 130003)])
+def test_distill_next_to_nothing_outside(R, V, dtype):
+    """The others' part of q far below the smallest 32-bit number, then the smallest of 64: p_0 q_v / q_0 stays."""
+    x = torch.randn(R, V, generator=torch.Generator().manual_seed(51)) - torch.tensor([110.0, 200, 800, 5000, 1e30])[:R, None]
+    ids = torch.arange(3, 3 + 7 * 50, 50).expand(R, 7).contiguous().int()
+    x.scatter_(1, ids.long(), torch.linspace(0, 3, 7).expand(R, 7))
+    check_distill(x.to(dtype), ids, torch.linspace(2, 0, 7).expand(R, 7).contiguous(), torch.full((R,), 1.5), 1.0,
+                  g=torch.linspace(-1, 1, R), inplace=True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T", [1e-3, 0.05, 30.0])
 def test_distill_temperatures(T, dtype):
     """A large c = log2(e) / T: c z - c m loses digits with |c z| unless the shift is undone, so rows are small here:
