@@ -435,9 +435,10 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
     });
     ws = wave_sum(sum);
     wm = wave_fmax(bm);
-    // what went leaves 2^-53 of itself behind, some sixty times over: no more
-    // than 2^-25 of what stays.  Values 2^-126 of the reference are lost.
-    again = !(ws > 0x1p-70) | !(ws > 0x1p-22 * (double)wave_fmax(gone)) | !(fabsf(r) <= 0x1p30f) | ((wm - ref) * c > 100.f);
+    // what went leaves up to 2^-53 of itself behind at each of its lane's nk
+    // additions: 2^-25 of what stays (2^-19 if all 64 lanes agreed in size and
+    // sign).  Values 2^-126 of the reference are lost.
+    again = !(ws > 0x1p-70) | !(ws > 0x1p-28 * nk * (double)wave_fmax(gone)) | !(fabsf(r) <= 0x1p30f) | ((wm - ref) * c > 100.f);
     if (!again) {
       wm = ref;
       ws *= exp2_d((double)r - (double)c * (double)ref);  // r is not quite c ref: 2^-25 of it, 2^5 at most

@@ -330,8 +330,7 @@ def test_distill_next_to_nothing_outside(R, V, dtype):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("T", [1e-3, 0.05, 30.0])
 def test_distill_temperatures(T, dtype):
-    """A large c = log2(e) / T: c z - c m loses digits with |c z| unless the shift is undone, so rows are small here:
-    |z| <= 0.02 at T = 1e-3."""
+    """A large c = log2(e) / T, with rows of the size that such a T goes with: |z| <= 0.02 at T = 1e-3."""
     x = (rows(5, 3001, F32, 17).clamp(-20, 20) * min(1.0, T)).to(dtype)
     check_distill(x, *target(x, 6, T, 18, noise=0.1 * min(1.0, T)), T)
 
