@@ -97,8 +97,12 @@ __device__ __forceinline__ void teacher_repeats(const DistillParams& a, Fetched&
 
 }  // namespace
 
+// 128 registers a thread at most, so that two blocks of 512 threads share a
+// compute unit: one stores while the other waits for its row's sums (2000 x
+// 34480 bf16 rows 94 us in one block of 138 registers, 81 in two; 600 rows 38
+// and 30).
 template <int DT, int NT, int NV>
-__global__ __launch_bounds__(NT) void distill_held_kernel(DistillParams a) {
+__global__ __launch_bounds__(NT, 4) void distill_held_kernel(DistillParams a) {
   constexpr int E = Fmt<DT>::kPerVec;
   constexpr int NW = NT / kWave;
   constexpr int FU = 2;                   // vectors folded at a time
@@ -323,17 +327,23 @@ hipError_t launch_held(const DistillParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
+// The fewest vectors a thread, in steps of two, that hold the row: a place that
+// holds nothing costs nearly as much as one that does (2000 bf16 rows of 34480
+// logits, 4310 vectors: 81 us in 512 threads of 16, 67 of 10; of 20000: 50 us
+// of 8, 44 of 6; 600 of 140000: 91 us in 1024 threads of 20, 88 of 18).
+template <int DT, int NT, int NV, int MOST>
+hipError_t launch_held_nv(const DistillParams& p, hipStream_t s) {
+  if constexpr (NV < MOST)
+    if (p.nvec > NT * NV) return launch_held_nv<DT, NT, NV + 2, MOST>(p, s);
+  return launch_held<DT, NT, NV>(p, s);
+}
+
 template <int DT>
 hipError_t launch_held_dt(const DistillParams& p, hipStream_t s) {
-  const int64_t n = p.nvec;
-  if (n <= 256 * 4) return launch_held<DT, 256, 4>(p, s);
-  if (n <= 256 * 8) return launch_held<DT, 256, 8>(p, s);
-  if (n <= 512 * 8) return launch_held<DT, 512, 8>(p, s);
-  if (n <= 512 * 16) return launch_held<DT, 512, 16>(p, s);
-  if (n <= 1024 * 12) return launch_held<DT, 1024, 12>(p, s);
-  if (n <= 1024 * 16) return launch_held<DT, 1024, 16>(p, s);
-  if (n <= 1024 * 20) return launch_held<DT, 1024, 20>(p, s);
-  return launch_held<DT, 1024, 24>(p, s);
+  if (p.nvec <= 256 * 8) return launch_held_nv<DT, 256, 4, 8>(p, s);
+  if (p.nvec <= 512 * 16) return launch_held_nv<DT, 512, 6, 16>(p, s);
+  static_assert(kHeldVecs == 1024 * 24, "the longest row");
+  return launch_held_nv<DT, 1024, 10, 24>(p, s);
 }
 
 }  // namespace

@@ -95,10 +95,11 @@ sv_status plan_distill(sv_dtype dt, int32_t R, int32_t V, int32_t k, Plan* pl) {
 
 // Whether loss and gradient together hold rows in registers, a block a row:
 // wherever a row fits, but for a few long ones, which many blocks finish
-// sooner in two launches (128256 bf16 logits, 1 row: 20 us held, 17 in two
-// launches; 40 rows 22 and 19; 96 rows 22 and 26; 2000 rows 208 and 275;
-// 64000 logits, any number of rows: held 14-111, two launches 17-150).
-bool hold_rows(int32_t R, int64_t nvec) { return nvec <= kHeldVecs && !(R <= 48 && nvec > 14000); }
+// sooner in two launches.  bf16 rows held / in two launches, us: 65000 logits
+// 15.0 / 16.9 (16 rows), 119 / 154 (2000); 110000: 21 / 17 (16), 22.5 / 20.7
+// (72), 22.5 / 24.0 (96), 204 / 255 (2000); 152064: 25.6 / 17.6 (16), 26.6 /
+// 24.0 (72), 26.9 / 28.3 (96), 38 / 52 (256).
+bool hold_rows(int32_t R, int64_t nvec) { return nvec <= kHeldVecs && !(nvec > 10000 && R <= nvec / 200); }
 
 void plan_reorder(Plan* pl) { pl->bytes = kWsFixed; }
 

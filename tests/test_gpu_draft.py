@@ -190,7 +190,11 @@ def test_distill(R, V, k, T, dtype):
 @pytest.mark.parametrize("dtype,R,V", [
     (BF16, 3000, 1031), (F32, 2700, 3001), (BF16, 2900, 9001), (F32, 1700, 12007), (BF16, 1700, 30011), (F32, 1300, 30011),
     (BF16, 1300, 60013), (F32, 530, 40013), (BF16, 530, 90001), (F32, 530, 60001), (BF16, 530, 128256), (F32, 530, 80001),
-    (BF16, 520, 160003), (F32, 520, 98304), (BF16, 520, 196608)])
+    (BF16, 520, 160003), (F32, 520, 98304), (BF16, 520, 196608),
+    (BF16, 1300, 11003), (BF16, 1100, 15003), (BF16, 1100, 22003), (BF16, 530, 38003), (BF16, 530, 46003), (BF16, 530, 55003),
+    (BF16, 520, 78003), (BF16, 520, 110003), (BF16, 520, 140003), (BF16, 520, 178003),
+    (F32, 1300, 6001), (F32, 1100, 7501), (F32, 1100, 11003), (F32, 530, 19003), (F32, 530, 23003), (F32, 530, 27003),
+    (F32, 520, 39003), (F32, 520, 55003), (F32, 520, 70001), (F32, 520, 89003)])
 def test_distill_more_rows_than_blocks(dtype, R, V):
     """Blocks that walk several rows, at every size of row that a block can hold; rows without a target, repeated and
     bad ids among them; some rows are compared."""
