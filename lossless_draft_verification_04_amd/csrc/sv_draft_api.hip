@@ -40,7 +40,10 @@ bool bad_scale(float T) { return bad_temperature(T) || !std::isfinite(log2e_over
 
 sv_status plan_topmass(sv_dtype dt, int64_t rows, int32_t V, int32_t k, int64_t part, Plan* pl) {
   pl->nvec = (V + per_vec(dt) - 1) / per_vec(dt);
-  split(rows, pl->nvec, kTopBlocks, &pl->nch1, &pl->vpc1, part);
+  // no more blocks than kTopBlocks, rows in equal numbers of parts: the few of a
+  // second round take as long as the first (200 x 152064 bf16 rows: 24.2 us in
+  // 400 blocks, 19.4 whole; 11 x 8 beams of 128256: 21.5 in 264, 19.4 in 176)
+  split(rows, pl->nvec, rows > 0 ? (int)std::max(rows, kTopBlocks / rows * rows) : 1, &pl->nch1, &pl->vpc1, part);
   const int32_t most = std::min(kPartEntries / k, kMostParts);
   if (pl->nch1 > most) {
     pl->vpc1 = (pl->nvec + most - 1) / most;

@@ -24,11 +24,11 @@
 
 namespace sv {
 
-// Blocks from which the device is full with blocks of 256 threads; fewer get
-// 512 threads each.  Teacher's pass: 2048 x 151936 bf16 rows take 116 us with
-// 256 threads, 127 with 512; 2000 x 4000 rows 21 and 33; 17 x 152064 rows 27
-// and 22; 256 x 128256 rows 25 and 22.
-constexpr int64_t kTopFill = 512;
+// Up to this many blocks, one to a compute unit, have 512 threads each, more
+// 256.  Teacher's pass, bf16, 256 threads / 512: 2048 x 151936 rows 116 us /
+// 127; 2000 x 4000 21 / 33; 300 x 128256 24.4 / 26.1; 480 x 32000 14.4 / 16.2;
+// 256 x 128256 21.5 / 19.2; 17 x 152064 27 / 22.
+constexpr int64_t kTopWide = 256;
 
 // A 64-bit constant, formed in scalar registers where it stands: left alone
 // the compiler lifts such constants out of the loop over rows into vector
