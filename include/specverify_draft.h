@@ -28,7 +28,8 @@
  * timing: the same call gives the same bits.
  *
  * Calls that overlap in time (two streams, two captured graphs that may be
- * replayed together) need a workspace each.
+ * replayed together) need a workspace each; a captured graph needs the one of
+ * its capture for as long as it is replayed.
  */
 #ifndef SPECVERIFY_DRAFT_H
 #define SPECVERIFY_DRAFT_H

@@ -472,7 +472,8 @@ def sv_geometric_fanout(F0, a_p, r, K, capped_last=False):
 # current stream.  The default workspace is the device's: calls that overlap
 # in time on several streams, and graphs that may be replayed together, take a
 # zero-filled one each (workspace=, a uint8 tensor of draft_workspace_size
-# bytes).
+# bytes).  A captured graph keeps the workspace of its capture, which has to
+# live as long: the default one is replaced when a larger call comes.
 # ---------------------------------------------------------------------------
 
 
