@@ -5,16 +5,17 @@
 // The selection is that of sv_topk.hpp: each thread keeps its best vector, a
 // bound from groups of threads, candidates in LDS.  The mass must keep its
 // digits where the list holds nearly everything, so it is no difference of
-// rounded sums: beside the selection each thread adds up 64-bit sums of its
-// vectors' 32-bit sums, against a reference that its wave takes from its first
-// vectors.  Once the list is known, every vector that holds a listed value is
-// taken out again whole -- the same instructions on the same bits give the
-// same 32-bit sum, so it leaves nothing behind -- and its other values are put
-// back.  Which vectors those are the thread knows of its best one, and looks
-// up for the others, spread over the wave, where its second largest value
-// reaches the list.  A wave whose reference turns out useless (values 2^100
-// above it, or a mass near underflow below it) reads its vectors once more and
-// sums them against their largest value.
+// rounded sums: beside the selection each thread adds up, in 64 bits, the
+// 32-bit sums of its vectors but its best one, against a reference that its
+// wave takes from its first vectors.  Once the list is known the best vector's
+// unlisted values are added; another vector that holds a listed value (looked
+// up, spread over the wave, where a thread's second largest value reaches the
+// list) is taken out again whole -- the same instructions on the same bits
+// give the same 32-bit sum, so it leaves nothing behind but roundings -- and
+// its other values are put back.  A wave whose sum turns out useless (values
+// 2^100 above the reference, a mass near underflow below it, or one that is
+// small against a value taken out) reads its vectors once more and sums the
+// unlisted values against their largest.
 #pragma once
 
 #include <type_traits>
@@ -208,7 +209,8 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   typename Src::Data bd = Src::none();
   const bool more = tid + NT < span;  // the thread owns vectors besides its best one
   float om = kNegInf;                 // their largest value
-  double sum = 0.0;                   // of all its vectors
+  double sum = 0.0;                   // of all its vectors but the best one
+  float bs = 0.f;                     // and of that one
   float ref = kNegInf, r = 0.f;       // the wave's reference and c times it
   typename Src::Data d[kWin];
 #pragma unroll
@@ -235,15 +237,20 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
       stay_packed(d[u]);
     }
   } else {
-    // the wave's reference: the largest value of its first whole window
+    // the wave's reference, near the largest values that are no outliers: the
+    // largest over its threads of the smallest of the first window's vectors'
+    // largest values (all kWin are there: nk > kWin)
     {
-      float m = kNegInf;
+      float m = __builtin_huge_valf(), top = kNegInf;
 #pragma unroll
       for (int u = 0; u < kWin; ++u) {
-        m = fmaxf(m, tid + u * NT < span ? largest(d[u]) : kNegInf);
+        const float vm = largest(d[u]);
+        m = fminf(m, vm);
+        top = fmaxf(top, vm);
         stay_packed(d[u]);
       }
       ref = wave_fmax(m);
+      if (ref == kNegInf) ref = wave_fmax(top);
       r = ref == kNegInf ? 0.f : c * ref;
     }
     auto take = [&](const typename Src::Data& dd, int32_t o) {
@@ -258,7 +265,9 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
       for (int i = 0; i < 4; ++i) bd[i] = t ? dd[i] : bd[i];
       bm = t ? vm : bm;
       bo = t ? o : bo;
-      sum += (double)vec_sum<E>(x, c, r);
+      const float s = vec_sum<E>(x, c, r);
+      sum += (double)(t ? bs : s);
+      bs = t ? s : bs;
     };
     int32_t o = tid;
     for (; o + (2 * kWin - 1) * NT < span - 1; o += kWin * NT) {
@@ -429,16 +438,21 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
       sum -= (double)s;
       sum += (double)vec_sum<E>(y, c, r);
     };
-    if (tkey >= kth && bo != kNoIdx) strip(v0 + bo, bd);
+    if (tkey >= kth && bo != kNoIdx) {
+      float y[E];
+      values_below<E>(src, bd, v0 + bo, kth, y);
+      bs = vec_sum<E>(y, c, r);
+    }
+    sum += (double)bs;
     spread(others_reach(kth), [&](int64_t vs, int32_t sbo, const typename Src::Data& dd) {
       if (vs >= 0 && vs != v0 + sbo && top_key(largest(dd), (int32_t)(vs * E)) >= kth) strip(vs, dd);
     });
     ws = wave_sum(sum);
-    wm = wave_fmax(bm);
     // what went leaves up to 2^-53 of itself behind at each of its lane's nk
     // additions: 2^-25 of what stays (2^-19 if all 64 lanes agreed in size and
-    // sign).  Values 2^-126 of the reference are lost.
-    again = !(ws > 0x1p-70) | !(ws > 0x1p-28 * nk * (double)wave_fmax(gone)) | !(fabsf(r) <= 0x1p30f) | ((wm - ref) * c > 100.f);
+    // sign).  Values 2^-126 of the reference are lost; a NaN fails every test.
+    again = !(ws > 0x1p-70) | !(ws < 0x1p100) | !(ws > 0x1p-28 * nk * (double)wave_fmax(gone)) | !(fabsf(r) <= 0x1p30f) |
+            (ref == kNegInf);
     if (!again) {
       wm = ref;
       ws *= exp2_d((double)r - (double)c * (double)ref);  // r is not quite c ref: 2^-25 of it, 2^5 at most
@@ -457,9 +471,20 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
         }
       }
     } else {
-      for (int o = tid; o < span; o += NT) {
-        values_below<E>(src, src.load(v0 + o), v0 + o, kth, x);
-        fold_values<E>(x, c, own);
+      for (int o = tid; o < span; o += kWin * NT) {
+#pragma unroll
+        for (int u = 0; u < kWin; ++u)
+          if (o + u * NT < span) d[u] = src.load(v0 + o + u * NT);
+#pragma unroll
+        for (int u = 0; u < kWin; ++u)
+          if (o + u * NT < span) {
+            const int64_t v = v0 + o + u * NT;
+            if (top_key(largest(d[u]), (int32_t)(v * E)) >= kth)
+              values_below<E>(src, d[u], v, kth, x);
+            else
+              src.values(d[u], v, x);
+            fold_values<E>(x, c, own);
+          }
       }
     }
     wm = wave_fmax(own.m);

@@ -4,7 +4,9 @@ Tolerances.  A kernel's sum of exponentials has terms 2^x, x = c (z - m): the ha
 (2^-23 relative), x carries the roundings of c and of one fused multiply-add (2^-24 |x| each, times ln 2 in the result).
 Terms that matter have |x| <= 25, so a term is within 25 * 2 * 2^-24 * 0.7 + 2^-23 < 2.3e-6.  A thread adds at most
 about 100 terms in sequence after trees of five levels (2^-24 each: < 6.3e-6 in the worst case, one sign throughout).
-A shift c m that is rounded before it is taken off is below 64 then: 2^-25 * 64 * 0.7 < 1.4e-6, whatever the logits' size.
+The top-value pass takes terms up to 2^100 of its reference (100 * 1.5 * 2^-24 * 0.7 + 2^-23 < 6.4e-6) and no 32-bit sum of
+more than a vector.  A shift c m that is rounded before it is taken off is below 64 then: 2^-25 * 64 * 0.7 < 1.4e-6,
+whatever the logits' size.
 So a sum is within SUM = 1e-5 of itself, and its logarithm within 1e-5.
 """
 import math

@@ -114,6 +114,16 @@ def test_teacher_hard_rows(kind, R, dtype):
     check_teacher(teacher_rows(kind, R, 20011, dtype), 40, 1.0)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R,V", [(2, 40009), (530, 20011), (3, 152064)])
+@pytest.mark.parametrize("T", [0.02, 0.1, 0.3, 0.67])
+def test_teacher_low_temperatures(T, R, V, dtype):
+    """The listed values hold up to all but e^-700 of a row; values that are not listed stand far above the bulk."""
+    x = rows(R, V, dtype, 25)
+    for k in (2, 20, 64):
+        check_teacher(x, k, T)
+
+
 def test_teacher_row_of_nothing():
     x = torch.full((3, 5000), -INF, dtype=BF16)
     got = svx.sv_teacher_topk(put(x), 5, 1.0)
