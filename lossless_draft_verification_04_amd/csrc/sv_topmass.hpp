@@ -18,8 +18,6 @@
 // unlisted values against their largest.
 #pragma once
 
-#include <type_traits>
-
 #include "sv_device.hpp"
 #include "sv_topk.hpp"
 
@@ -507,15 +505,40 @@ constexpr int kPartEntries = 256;
 constexpr int kMostParts = 16;
 constexpr int kPerLane = kPartEntries / kWave;
 
+// An order's value and index (a value of -0 comes back as 0).
+__device__ __forceinline__ float order_value(double k) {
+  const uint32_t o = (uint32_t)((uint64_t)__double_as_longlong(k) >> 24);
+  return __uint_as_float((o & 0x80000000u) ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ int32_t order_index(double k) {
+  return (int32_t)(~(uint32_t)(uint64_t)__double_as_longlong(k) & 0xffffffu);
+}
+__device__ __forceinline__ double order_from(double k, int lane) {
+  const uint64_t b = (uint64_t)__double_as_longlong(k);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_ds_bpermute(lane * 4, (int)(uint32_t)b);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(lane * 4, (int)(uint32_t)(b >> 32));
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+// Runs of P lanes that fall and then rise, sorted: log2 P compare-exchange steps.
+__device__ __forceinline__ double order_clean(double x, int P, int lane) {
+  for (int h = P / 2; h > 0; h /= 2) {
+    const double o = order_from(x, lane ^ h);
+    x = (o > x) == ((lane & h) == 0) ? o : x;  // the lower lane keeps the larger
+  }
+  return x;
+}
+
 // The lists and masses of a row's nch parts (nch * F <= kPartEntries) as the
 // row's: (lv, li) is the merged list (lane l = l-th best); the return value is
 // the mass outside it, in every lane.  Called by one wave, with kPartEntries
-// words of LDS of its own.  All is loaded in one round; an entry's rank is the
-// number of better ones, counted over LDS.
+// words of LDS of its own.  All is loaded in one round; the lists, a run of P
+// lanes each (P the power of two from F on), merge as sorted ones do: the
+// better of one and the other reversed, then order_clean.  Its steps grow with
+// the logarithm of F and the lists, where counting every entry's place grows
+// with their product (8 beams of 152064 in 4 parts, 64 kept: 24.1 and 31.4 us;
+// 8 kept: 15.2 and 15.0).  The code is kept short: it runs once, from cold.
 __device__ __forceinline__ Partial wave_merge_parts(const TopEntry* lists, const Partial* parts, int nch, int F,
                                                     float c, int lane, double* keys, float& lv, int32_t& li) {
-  lv = kNegInf;
-  li = kNoIdx;
   Partial r;
   r.pad = 0.f;
   if (nch == 1) {
@@ -527,10 +550,9 @@ __device__ __forceinline__ Partial wave_merge_parts(const TopEntry* lists, const
     return r;
   }
   const int n = nch * F;
-  double key[kPerLane];
-  int above[kPerLane];
-  Partial p{kNegInf, 0.f, 0.0};
   TopEntry t[kPerLane];
+  double key[kPerLane];
+  Partial p{kNegInf, 0.f, 0.0};
 #pragma unroll
   for (int q = 0; q < kPerLane; ++q) {
     t[q] = TopEntry{kNegInf, kNoIdx};
@@ -540,48 +562,41 @@ __device__ __forceinline__ Partial wave_merge_parts(const TopEntry* lists, const
 #pragma unroll
   for (int q = 0; q < kPerLane; ++q) {
     key[q] = order_of(t[q].val, t[q].idx);
-    above[q] = 0;
     keys[q * kWave + lane] = key[q];
   }
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
   __builtin_amdgcn_wave_barrier();
-  const double2* pairs = reinterpret_cast<const double2*>(keys);
-  auto count = [&](auto nq) {
-#pragma unroll 4
-    for (int j = 0; j < n; j += 2) {
-      const double2 k = pairs[j >> 1];  // past the n-th: 0, above none
-#pragma unroll
-      for (int q = 0; q < decltype(nq)::value; ++q) above[q] += (k.x > key[q] ? 1 : 0) + (k.y > key[q] ? 1 : 0);
-    }
-  };
-  if (n <= 2 * kWave)
-    count(std::integral_constant<int, 2>{});
-  else
-    count(std::integral_constant<int, kPerLane>{});
+  int P = 1;
+  while (P < F) P *= 2;
+  const int e = lane & (P - 1), list = lane / P;
+  auto entry = [&](int l, int at) { return l < nch && at < F ? keys[l * F + at] : 0.0; };
+  double best = entry(list, e);
+#pragma unroll 1
+  for (int l = kWave / P; l < nch; l += kWave / P) {  // the runs of the next lists
+    const double o = entry(l + list, P - 1 - e);
+    best = order_clean(o > best ? o : best, P, lane);
+  }
+#pragma unroll 1
+  for (int g = P; g < kWave && g < P * nch; g *= 2) {  // the runs among themselves
+    const double o = order_from(best, lane ^ (g + P - 1));
+    best = order_clean(o > best ? o : best, P, lane);
+  }
+  __builtin_amdgcn_wave_barrier();
+  // what is listed no longer goes back into the mass
+  const double kth = readlane_d(best, F - 1);  // 0: fewer than F entries, all of them listed
   float m = p.m;
 #pragma unroll
   for (int q = 0; q < kPerLane; ++q)
-    if (key[q] > 0.0 && above[q] >= F) m = fmaxf(m, t[q].val);
+    if (key[q] > 0.0 && key[q] < kth) m = fmaxf(m, t[q].val);
   r.m = wave_fmax(m);
   double s = p.s * rescale(p.m, r.m, c);
 #pragma unroll
   for (int q = 0; q < kPerLane; ++q)
-    if (key[q] > 0.0 && above[q] >= F) s += rescale(t[q].val, r.m, c);
+    if (key[q] > 0.0 && key[q] < kth && t[q].val > kNegInf) s += (double)fast_exp2((t[q].val - r.m) * c);
   r.s = wave_sum(s);
-  // the list, through the same words: the entry of rank l to lane l
-  uint64_t* out = reinterpret_cast<uint64_t*>(keys);
-  __builtin_amdgcn_wave_barrier();
-  out[lane] = pack_cand(kNegInf, kNoIdx);
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-  __builtin_amdgcn_wave_barrier();
-#pragma unroll
-  for (int q = 0; q < kPerLane; ++q)
-    if (key[q] > 0.0 && above[q] < F) out[above[q]] = pack_cand(t[q].val, t[q].idx);
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-  __builtin_amdgcn_wave_barrier();
-  lv = cand_value(out[lane]);
-  li = (int32_t)(out[lane] >> 32);
-  __builtin_amdgcn_wave_barrier();
+  const bool in = lane < F && best > 0.0;
+  lv = in ? order_value(best) : kNegInf;
+  li = in ? order_index(best) : kNoIdx;
   return r;
 }
 
