@@ -190,7 +190,7 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   const int wave = threadIdx.x / kWave;
   const int tid = threadIdx.x;
   __shared__ uint64_t s_cand[kCand];
-  __shared__ uint32_t s_gm[NT];
+  __shared__ uint64_t s_gk[NT];
   __shared__ alignas(16) uint64_t s_key[kCand];
   __shared__ uint64_t s_sel[kWave];
   __shared__ uint64_t s_tau;
@@ -307,37 +307,70 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
     if (GS >= 4) key_max_step<kRowShr + 2, 0xF>(k);
     if (GS >= 8) key_max_step<kRowShr + 4, 0xF>(k);
     if (GS >= 16) key_max_step<kRowShr + 8, 0xF>(k);
-    if ((lane & (GS - 1)) == GS - 1) s_gm[tid / GS] = (uint32_t)(k >> 32);  // 0: the group holds nothing
+    // as a key that the vector's best element has at least; 0: the group holds nothing
+    if ((lane & (GS - 1)) == GS - 1) s_gk[tid / GS] = k ? k - (E - 1) : 0ull;
   }
   if (tid == 0) s_nc = 0;
   lds_sync();
   if (wave == 0) {
-    uint32_t p = 0;
+    uint64_t gk[kMaxH];
+    uint32_t hi = 0;  // the bound's upper 32 bits, of which the upper 16 are sought
+    int n = 0;
     if (H == 1) {  // one group per lane (F <= 16)
-      const uint32_t gh = s_gm[lane];
+      gk[0] = s_gk[lane];
+      const uint32_t gh = (uint32_t)(gk[0] >> 32);
 #pragma unroll
       for (int bit = 31; bit >= 16; --bit) {
-        const uint32_t q = p | (1u << bit);
-        if (__builtin_popcountll(__ballot(gh >= q)) >= F) p = q;
+        const uint32_t q = hi | (1u << bit);
+        if (__builtin_popcountll(__ballot(gh >= q)) >= F) hi = q;
       }
-    } else {
-      uint32_t gh[kMaxH];
+      n = __builtin_popcountll(__ballot(gh >= hi));
 #pragma unroll
-      for (int h = 0; h < kMaxH; ++h) gh[h] = h < H ? s_gm[h * kWave + lane] : 0u;
+      for (int h = 1; h < kMaxH; ++h) gk[h] = 0ull;
+    } else {
+#pragma unroll
+      for (int h = 0; h < kMaxH; ++h) gk[h] = h < H ? s_gk[h * kWave + lane] : 0ull;
       for (int bit = 31; bit >= 16; --bit) {
-        const uint32_t q = p | (1u << bit);
+        const uint32_t q = hi | (1u << bit);
         int cnt = 0;
 #pragma unroll
-        for (int h = 0; h < kMaxH; ++h) cnt += __builtin_popcountll(__ballot(gh[h] >= q));  // empty groups are 0
-        if (cnt >= F) p = q;
+        for (int h = 0; h < kMaxH; ++h) cnt += __builtin_popcountll(__ballot((uint32_t)(gk[h] >> 32) >= q));
+        if (cnt >= F) hi = q;
       }
+#pragma unroll
+      for (int h = 0; h < kMaxH; ++h) n += __builtin_popcountll(__ballot((uint32_t)(gk[h] >> 32) >= hi));
     }
-    if (lane == 0) s_tau = (uint64_t)p << 32;
+    uint64_t p = (uint64_t)hi << 32;
+    // many groups tie in the upper 16 bits of the value (bf16: all of it): the
+    // bound goes on to the whole value and the index, without which rows of
+    // few values list far too many (512 x 128256 bf16 zeros: 349 us, 28 so)
+    if (hi != 0u && n > 2 * F + 16) {
+      auto take = [&](int bit) {
+        const uint64_t q = p | (1ull << bit);
+        int cnt = 0;
+#pragma unroll
+        for (int h = 0; h < kMaxH; ++h) cnt += __builtin_popcountll(__ballot(gk[h] >= q));
+        if (cnt >= F) p = q;
+      };
+      if constexpr (E == 4) {
+#pragma unroll 1
+        for (int bit = 47; bit >= 32; --bit) take(bit);
+      } else {
+        p |= (p >> 63) ? 0ull : 0xffffull << 32;  // of negative values these bits are set
+      }
+      p |= 0xffull << 24;  // as in every key: indices have 24 bits
+#pragma unroll 1
+      for (int bit = 23; bit >= 0; --bit) take(bit);
+    }
+    if (lane == 0) s_tau = p;
   }
   lds_sync();
   uint64_t tau = s_tau;
-  // the thread's vectors besides its best may hold a key of at least t
-  auto others_reach = [&](uint64_t t) { return more && top_key(om, (int32_t)((v0 + tid) * E)) >= t; };
+  // the thread's vectors besides its best may hold a key of at least t: they
+  // come after it where they tie with it, and in any case not before the first
+  const int32_t oo = om == bm ? bo + NT : bo == tid ? tid + NT : tid;
+  const uint64_t okey = more ? top_key(om, (int32_t)((v0 + oo) * E)) : 0ull;
+  auto others_reach = [&](uint64_t t) { return okey != 0ull && okey >= t; };
   // f(vs, o, d) for every vector of the wave's lanes with `pick`: two such
   // lanes' vectors at a time, one each per lane (vs < 0: none), o the owner's
   // best vector

@@ -124,6 +124,20 @@ def test_teacher_low_temperatures(T, R, V, dtype):
         check_teacher(x, k, T)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("R,V", [(2, 20011), (530, 20011), (5, 152064)])
+@pytest.mark.parametrize("kind", ["few values", "near ties", "negative", "few left"])
+def test_teacher_many_ties(kind, R, V, dtype):
+    """The bound's index part: rows of a few values, values that differ in their last bits only, fewer finite values than
+    are asked for."""
+    g = torch.Generator().manual_seed(26)
+    n = torch.randint(0, 7, (R, V), generator=g).float()
+    x = {"few values": n - 3, "near ties": 1 + n * 2.0 ** -22, "negative": -5 - n,
+         "few left": torch.where(torch.rand(R, V, generator=g) < 30 / V, n, torch.tensor(-INF))}[kind]
+    for k in (1, 9, 64):
+        check_teacher(x.to(dtype), k, 1.0)
+
+
 def test_teacher_row_of_nothing():
     x = torch.full((3, 5000), -INF, dtype=BF16)
     got = svx.sv_teacher_topk(put(x), 5, 1.0)
