@@ -8,9 +8,9 @@
 // rounded sums: beside the selection each thread adds up, in 64 bits, the
 // 32-bit sums of its vectors but its best one, against a reference that its
 // wave takes from its first vectors.  Once the list is known the best vector's
-// unlisted values are added; another vector that holds a listed value (looked
-// up, spread over the wave, where a thread's second largest value reaches the
-// list) is taken out again whole -- the same instructions on the same bits
+// unlisted values are added; another vector that holds a listed value (found
+// with the candidates, where a thread's second largest value reaches the
+// bound) is taken out again whole -- the same instructions on the same bits
 // give the same 32-bit sum, so it leaves nothing behind but roundings -- and
 // its other values are put back.  A wave whose sum turns out useless (values
 // 2^100 above the reference, a mass near underflow below it, or one that is
@@ -197,6 +197,7 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   __shared__ int s_nc;
   __shared__ float s_wm[NW];
   __shared__ double s_ws[NW];
+  __shared__ int32_t s_hit[NW][kWave];
   float lv = kNegInf;
   int32_t li = kNoIdx;
   const int span = (int)(v1 - v0);
@@ -400,7 +401,9 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
     }
   };
   int nc;
+  int hits = 0;  // the wave's vectors, none a thread's best one, that reach tau: their offsets in s_hit, the first kWave
   for (;;) {  // block-uniform; tau rises on every repetition
+    hits = 0;
     const bool sel = tkey != 0ull && tkey >= tau;
     if (held) {
 #pragma unroll
@@ -413,8 +416,14 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
       const bool full = sel && others_reach(tau);
       flag_candidates<E>(src, bd, sel && !full ? v0 + bo : -1, V, tau, s_cand, &s_nc);
       stay_packed(bd);
-      spread(full, [&](int64_t vs, int32_t, const typename Src::Data& dd) {
-        flag_candidates<E>(src, dd, vs, V, tau, s_cand, &s_nc);
+      spread(full, [&](int64_t vs, int32_t sbo, const typename Src::Data& dd) {
+        const bool hit = vs >= 0 && top_key(largest(dd), (int32_t)(vs * E)) >= tau;
+        if (__ballot(hit) == 0ull) return;
+        flag_candidates<E>(src, dd, hit ? vs : -1, V, tau, s_cand, &s_nc);
+        const uint64_t rest = __ballot(hit && vs != v0 + sbo);
+        const int at = hits + __builtin_popcountll(rest & ((1ull << lane) - 1));
+        if (((rest >> lane) & 1u) && at < kWave) s_hit[wave][at] = (int32_t)(vs - v0);
+        hits += __builtin_popcountll(rest);
       });
     }
     lds_sync();
@@ -475,9 +484,19 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
       bs = vec_sum<E>(y, c, r);
     }
     sum += (double)bs;
-    spread(others_reach(kth), [&](int64_t vs, int32_t sbo, const typename Src::Data& dd) {
-      if (vs >= 0 && vs != v0 + sbo && top_key(largest(dd), (int32_t)(vs * E)) >= kth) strip(vs, dd);
-    });
+    auto strip_listed = [&](int64_t v, const typename Src::Data& dd) {
+      if (top_key(largest(dd), (int32_t)(v * E)) >= kth) strip(v, dd);
+    };
+    if (hits <= kWave) {  // wave-uniform
+      if (lane < hits) {
+        const int64_t v = v0 + s_hit[wave][lane];
+        strip_listed(v, src.load(v));
+      }
+    } else {
+      spread(others_reach(kth), [&](int64_t vs, int32_t sbo, const typename Src::Data& dd) {
+        if (vs >= 0 && vs != v0 + sbo) strip_listed(vs, dd);
+      });
+    }
     ws = wave_sum(sum);
     // what went leaves up to 2^-53 of itself behind at each of its lane's nk
     // additions: 2^-25 of what stays (2^-19 if all 64 lanes agreed in size and
