@@ -15,7 +15,7 @@
 // 2048 x 151936 bf16 rows, 64 values: 105 us, 5.9 TB/s (a plain read reaches
 // 7.1); what is missing is the selection at a block's end, which only the
 // other blocks of a compute unit cover.  17 x 32000 fp32 rows, 8 values:
-// 9.8 us, a chain of latencies (load, bound, candidates, ranks, stores).
+// 9.9 us, a chain of latencies (load, bound, candidates, ranks, stores).
 #include "sv_draft.h"
 #include "sv_topmass.hpp"
 

@@ -238,7 +238,7 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   } else {
     // the wave's reference, near the largest values that are no outliers: the
     // largest over its threads of the smallest of the first window's vectors'
-    // largest values (all kWin are there: nk > kWin)
+    // largest values (all kWin are there: nk > kWin); of masked ones 0
     {
       float m = __builtin_huge_valf(), top = kNegInf;
 #pragma unroll
@@ -250,7 +250,8 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
       }
       ref = wave_fmax(m);
       if (ref == kNegInf) ref = wave_fmax(top);
-      r = ref == kNegInf ? 0.f : c * ref;
+      if (ref == kNegInf) ref = 0.f;
+      r = c * ref;
     }
     auto take = [&](const typename Src::Data& dd, int32_t o) {
       float x[E];
@@ -501,8 +502,8 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
     // what went leaves up to 2^-53 of itself behind at each of its lane's nk
     // additions: 2^-25 of what stays (2^-19 if all 64 lanes agreed in size and
     // sign).  Values 2^-126 of the reference are lost; a NaN fails every test.
-    again = !(ws > 0x1p-70) | !(ws < 0x1p100) | !(ws > 0x1p-28 * nk * (double)wave_fmax(gone)) | !(fabsf(r) <= 0x1p30f) |
-            (ref == kNegInf);
+    again = (wave_fmax(bm) > kNegInf) &
+            (!(ws > 0x1p-70) | !(ws < 0x1p100) | !(ws > 0x1p-28 * nk * (double)wave_fmax(gone)) | !(fabsf(r) <= 0x1p30f));
     if (!again) {
       wm = ref;
       ws *= exp2_d((double)r - (double)c * (double)ref);  // r is not quite c ref: 2^-25 of it, 2^5 at most

@@ -138,6 +138,18 @@ def test_teacher_many_ties(kind, R, V, dtype):
         check_teacher(x.to(dtype), k, 1.0)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("offset", [0.0, 300.0, -300.0])
+def test_teacher_few_left_far_from_zero(offset, dtype):
+    """Rows masked but for 1 in 500: many waves see nothing finite in their first vectors, or nothing at all."""
+    g = torch.Generator().manual_seed(27)
+    x = torch.randn(530, 40009, generator=g) * 2 + offset
+    x[torch.rand(530, 40009, generator=g) > 1 / 500] = -INF
+    for k in (1, 16, 64):
+        check_teacher(x[:4].to(dtype), k, 1.0)
+        check_teacher(x.to(dtype), k, 0.7)
+
+
 def test_teacher_row_of_nothing():
     x = torch.full((3, 5000), -INF, dtype=BF16)
     got = svx.sv_teacher_topk(put(x), 5, 1.0)
