@@ -76,7 +76,8 @@ sv_status sv_draft_workspace_size(sv_draft_op op, sv_dtype dt, int32_t rows, int
  * The teacher's probabilities at temperature T follow from these alone:
  * p_i = exp(vals_i / T) / Z with Z = sum_i exp(vals_i / T) + exp(rest).  The
  * mass outside is summed by itself, never as a difference, so it keeps its
- * digits where the top tokens hold nearly everything.  Reads each row once.
+ * digits where the top tokens hold nearly everything.  Reads each row once, parts
+ * of it again where their values lie too far apart (2^100 in exp(z / T)).
  */
 sv_status sv_teacher_topk(const void* logits, sv_dtype dt, int64_t stride, int32_t R, int32_t V, int32_t k, float T,
                           int32_t* out_ids, float* out_vals, float* out_rest, void* ws, size_t ws_bytes, void* stream);
