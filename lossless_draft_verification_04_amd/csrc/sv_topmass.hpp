@@ -403,6 +403,7 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   };
   int nc;
   int hits = 0;  // the wave's vectors, none a thread's best one, that reach tau: their offsets in s_hit, the first kWave
+  bool first = true;
   for (;;) {  // block-uniform; tau rises on every repetition
     hits = 0;
     const bool sel = tkey != 0ull && tkey >= tau;
@@ -431,6 +432,7 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
     nc = s_nc;
     if (nc <= kCand) break;
     tau = block_select<NT>(s_cand, s_key, s_sel, kCand, F, &s_tau);
+    first = false;
     if (tid == 0) s_nc = 0;
     lds_sync();
   }
@@ -488,7 +490,9 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
     auto strip_listed = [&](int64_t v, const typename Src::Data& dd) {
       if (top_key(largest(dd), (int32_t)(v * E)) >= kth) strip(v, dd);
     };
-    if (hits <= kWave) {  // wave-uniform
+    // a bound from a repetition depends on the order of arrivals, and with it
+    // which lane would take which of the noted vectors out
+    if (first && hits <= kWave) {  // wave-uniform
       if (lane < hits) {
         const int64_t v = v0 + s_hit[wave][lane];
         strip_listed(v, src.load(v));

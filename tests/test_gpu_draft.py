@@ -138,6 +138,15 @@ def test_teacher_many_ties(kind, R, V, dtype):
         check_teacher(x.to(dtype), k, 1.0)
 
 
+@pytest.mark.parametrize("kind", ["ties", "crowd", "rising", "peak"])
+def test_teacher_gives_the_same_bits(kind):
+    """Also where more candidates arrive, in any order, than there is room for."""
+    z = put(teacher_rows(kind, 530, 20011, BF16))
+    first = svx.sv_teacher_topk(z, 64, 0.4)
+    for _ in range(20):
+        assert same(bits(svx.sv_teacher_topk(z, 64, 0.4)), bits(first))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("offset", [0.0, 300.0, -300.0])
 def test_teacher_few_left_far_from_zero(offset, dtype):
