@@ -172,24 +172,59 @@ def _i32_tensor(t: torch.Tensor, shape, what):
     return t
 
 
+def _capturing(index) -> bool:
+    """Whether the device's current stream is being captured into a graph."""
+    if index == torch.cuda.current_device():
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.device(index):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class Workspace:
-    """Per-device scratch for the kernels (zero-filled on creation, grown on demand)."""
+    """Per-device scratch for the kernels (zero-filled on creation, grown on demand).
+
+    A buffer that a larger one replaces is kept: graphs captured with it go on using it, and calls of other streams may
+    still be running in it.  Sizes double, so that the replaced ones together take less than the one in use.  A buffer
+    made while a graph is being captured lies in the graph's memory and its zero fill runs with the graph, so it serves
+    that one call and is never handed to another."""
 
     _lock = threading.Lock()
     _cache = {}
+    _replaced = {}  # by device: buffers replaced, and those of captured calls
 
     @classmethod
-    def get(cls, device, nbytes: int) -> torch.Tensor:
+    def get(cls, device, nbytes: int, in_capture=True) -> torch.Tensor:
+        """The device's buffer, of nbytes at least.  in_capture: what to do where that takes a new one while a graph is
+        being captured: give the call one of its own, or (False) raise."""
         dev = torch.device(device)
         key = dev.index if dev.index is not None else torch.cuda.current_device()
         with cls._lock:
             ws = cls._cache.get(key)
             if ws is None or ws.numel() < nbytes:
-                ws = torch.zeros(max(nbytes, 1 << 20), dtype=torch.uint8, device=dev)
-                if ws.data_ptr() % 256:
+                capturing = _capturing(key)
+                if capturing and not in_capture:
+                    raise SpecVerifyError(SV_EWORKSPACE, f"default workspace of {nbytes} bytes while a graph is being "
+                                          "captured: make a call of this size before the capture, or hand over workspace=")
+                least = 2 * ws.numel() if ws is not None and not capturing else 1 << 20
+                new = torch.zeros(max(nbytes, least), dtype=torch.uint8, device=dev)
+                if new.data_ptr() % 256:
                     raise SpecVerifyError(SV_EALIGN, "workspace allocation not 256-byte aligned")
-                cls._cache[key] = ws
+                other = new if capturing else ws
+                if other is not None:
+                    cls._replaced.setdefault(key, []).append(other)
+                if not capturing:
+                    cls._cache[key] = new
+                return new
             return ws
+
+    @classmethod
+    def every(cls, device):
+        """All of the device's buffers (at least the one in use)."""
+        first = cls.get(device, 0)
+        dev = torch.device(device)
+        key = dev.index if dev.index is not None else torch.cuda.current_device()
+        with cls._lock:
+            return [first, *cls._replaced.get(key, ())]
 
 
 def workspace_size(op, dt, B, K, gamma_or_N, V, F_max=1) -> int:
@@ -199,12 +234,15 @@ def workspace_size(op, dt, B, K, gamma_or_N, V, F_max=1) -> int:
 
 
 def sv_get_device_error(device=None) -> int:
-    """Synchronise and read (and clear) the device error word of this device's workspace."""
+    """Synchronise and read (and clear) the device error word of this device's workspace; graphs that keep an earlier
+    one report there."""
     device = device if device is not None else torch.device("cuda", torch.cuda.current_device())
-    ws = Workspace.get(device, 0)
-    flags = _i32(0)
-    _check(_lib.sv_get_device_error(_ptr(ws), ctypes.byref(flags), _stream(device)), "sv_get_device_error")
-    return flags.value
+    found = 0
+    for ws in Workspace.every(device):
+        flags = _i32(0)
+        _check(_lib.sv_get_device_error(_ptr(ws), ctypes.byref(flags), _stream(device)), "sv_get_device_error")
+        found |= flags.value
+    return found
 
 
 def sv_verify_chain(tgt, drf, tok, T, seed=0, round_=0, want_pq=True, workspace=None):
@@ -472,8 +510,9 @@ def sv_geometric_fanout(F0, a_p, r, K, capped_last=False):
 # current stream.  The default workspace is the device's: calls that overlap
 # in time on several streams, and graphs that may be replayed together, take a
 # zero-filled one each (workspace=, a uint8 tensor of draft_workspace_size
-# bytes).  A captured graph keeps the workspace of its capture, which has to
-# live as long: the default one is replaced when a larger call comes.
+# bytes).  A captured graph keeps the workspace of its capture.  The default
+# one lives as long as the process, but is not made or grown in a capture:
+# call once with the same sizes before, or hand over a workspace.
 # ---------------------------------------------------------------------------
 
 
@@ -487,7 +526,7 @@ def draft_workspace_size(op, dt, rows, W, V, k) -> int:
 def _draft_workspace(dev, *shape):
     need = draft_workspace_size(*shape)
     ws = Workspace._cache.get(dev.index)
-    return ws if ws is not None and ws.numel() >= need else Workspace.get(dev, need)
+    return ws if ws is not None and ws.numel() >= need else Workspace.get(dev, need, in_capture=False)
 
 
 # The small calls of decoding take about as long on the host as on the GPU, so
