@@ -139,7 +139,9 @@ sv_status sv_distill_topk_backward(const void* z, sv_dtype dt, int64_t stride, i
  * One step of beam search: of all continuations (w, v) of a sequence's beams,
  * the N with the largest score
  *   scores[b, w] + z_{w,v} / T - log sum_u exp(z_{w,u} / T),
- * ordered by score descending, then w, then v ascending.
+ * ordered by score descending, then w ascending; within a beam by logit
+ * descending, then v ascending (so also where the scores' rounding makes
+ * different logits equal: a beam at -1e30 continues with its best tokens).
  *   logits [B, W, V], row (b, w) at b*W + w; 1 <= W <= SV_MAX_BEAMS
  *   scores [B, W] the beams' log-probabilities; a beam at -inf has no
  *     continuation (at the first step all but one)

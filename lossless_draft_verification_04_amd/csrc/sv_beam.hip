@@ -22,18 +22,21 @@ namespace sv {
 // (17 us of it the read): 512 blocks start at once, two to a compute unit, so
 // their selections and joins come at the same time and nothing covers them.
 // 1 x 4 beams of 32000: 12.5 us, latencies of the pass, the hand-off and join.
-// Scores are formed and compared in 64 bits: differences between beams near
-// 1e-7 of a score decide as the inputs have it.
+// Scores are formed and compared in 64 bits.  Within a beam the order is that
+// of the list, by logit and then token, and the comparison goes by the place
+// there: a score of large magnitude (-1e30 for a beam that is to lose) rounds
+// every logit away, and the merges need lists that are sorted as they compare.
 // ---------------------------------------------------------------------------
 constexpr double kNoScore = -__builtin_huge_val();
 
 // A continuation: lane l of a sorted list holds the l-th best.
 struct Cont {
-  double s;  // score (kNoScore: none)
-  int32_t beam, tok;
+  double s;    // score (kNoScore: none)
+  int32_t at;  // beam * kWave + place in the beam's list
+  int32_t tok;
 };
 __device__ __forceinline__ bool cont_better(const Cont& a, const Cont& b) {
-  return (a.s > b.s) | ((a.s == b.s) & ((a.beam < b.beam) | ((a.beam == b.beam) & (a.tok < b.tok))));
+  return (a.s > b.s) | ((a.s == b.s) & (a.at < b.at));
 }
 __device__ __forceinline__ Cont cont_from(const Cont& c, int lane) {
   const uint64_t b = (uint64_t)__double_as_longlong(c.s);
@@ -42,7 +45,7 @@ __device__ __forceinline__ Cont cont_from(const Cont& c, int lane) {
   const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_bpermute(at, (int)(uint32_t)(b >> 32));
   Cont r;
   r.s = __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
-  r.beam = __builtin_amdgcn_ds_bpermute(at, c.beam);
+  r.at = __builtin_amdgcn_ds_bpermute(at, c.at);
   r.tok = __builtin_amdgcn_ds_bpermute(at, c.tok);
   return r;
 }
@@ -108,7 +111,7 @@ __global__ __launch_bounds__(NT, 4) void beam_select_kernel(BeamParams a) {
     Cont own = none;
     if (!(sc > kNegInf)) continue;  // wave-uniform
     if (lds.finished[w] != 0) {
-      if (lane == 0) own = Cont{(double)sc, w, a.pad};
+      if (lane == 0) own = Cont{(double)sc, w * kWave, a.pad};
     } else {
       float lv;
       int32_t li;
@@ -119,7 +122,7 @@ __global__ __launch_bounds__(NT, 4) void beam_select_kernel(BeamParams a) {
       if (m > kNegInf) {
         const double s = wave_sum(lane < N ? rescale(lv, m, a.c) : 0.0) + rest.s * rescale(rest.m, m, a.c);
         const double shift = (double)sc - ((double)m * a.invT + log_d(s));
-        if (lane < N && lv > kNegInf) own = Cont{shift + (double)lv * a.invT, w, li};
+        if (lane < N && lv > kNegInf) own = Cont{shift + (double)lv * a.invT, w * kWave + lane, li};
       } else if (lane == 0) {
         set_error(a.err, SV_DERR_ROW);
       }
@@ -135,7 +138,7 @@ __global__ __launch_bounds__(NT, 4) void beam_select_kernel(BeamParams a) {
   }
   if (wave != 0) return;
   if (lane < N) {
-    a.out_beam[(int64_t)b * N + lane] = best.s > kNoScore ? best.beam : -1;
+    a.out_beam[(int64_t)b * N + lane] = best.s > kNoScore ? best.at / kWave : -1;
     a.out_tok[(int64_t)b * N + lane] = best.s > kNoScore ? best.tok : -1;
     a.out_score[(int64_t)b * N + lane] = (float)best.s;
   }
