@@ -15,7 +15,7 @@
 // its other values are put back.  A wave whose sum turns out useless (values
 // 2^100 above the reference, a mass near underflow below it, or one that is
 // small against a value taken out) reads its vectors once more and sums the
-// unlisted values against their largest.
+// unlisted values, in 64 bits again, against one near their largest.
 #pragma once
 
 #include "sv_device.hpp"
@@ -97,6 +97,34 @@ __device__ __forceinline__ void fold_values(const float (&x)[E], float c, Mass& 
     for (int e = 0; e < w; ++e) t[e] += t[e + w];
   a.s = __builtin_fmaf(a.s, fast_exp2((a.m - ref) * c), t[0]);
   a.m = mn;
+}
+
+// The same over any number of vectors (a row of 2^24 logits gives a thread
+// thousands): added up in 64 bits, each vector's values in 32.  m is a value
+// that the largest passes by 2^32 at most, so that it seldom moves: a factor
+// for every new largest value would bring its own rounding thousands of times.
+struct LongMass {
+  float m = kNegInf;
+  double s = 0.0;
+};
+template <int E>
+__device__ __forceinline__ void fold_long(const float (&x)[E], float c, LongMass& a) {
+  float fm = x[0];
+#pragma unroll
+  for (int e = 1; e < E; ++e) fm = fmaxf(fm, x[e]);
+  if ((fm - a.m) * c > 32.f) {  // the first finite value too: a.m = -inf
+    a.s *= (double)fast_exp2((a.m - fm) * c);
+    a.m = fm;
+  }
+  const float ref = a.m == kNegInf ? 0.f : a.m;
+  float t[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) t[e] = fast_exp2((x[e] - ref) * c);
+#pragma unroll
+  for (int w = E / 2; w > 0; w >>= 1)
+#pragma unroll
+    for (int e = 0; e < w; ++e) t[e] += t[e + w];
+  a.s += (double)t[0];
 }
 
 // 2^(c (a - b)) for a merge of sums, a <= b; 0 for a = -inf.
@@ -514,9 +542,9 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
     }
   }
   if (again) {
-    Mass own;
     float x[E];
     if (held) {
+      Mass own;  // of kWin vectors at most
 #pragma unroll
       for (int u = 0; u < kWin; ++u) {
         const int o = tid + u * NT;
@@ -525,7 +553,10 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
           fold_values<E>(x, c, own);
         }
       }
+      wm = wave_fmax(own.m);
+      ws = wave_sum(own.m == kNegInf ? 0.0 : (double)own.s * (double)fast_exp2((own.m - wm) * c));
     } else {
+      LongMass own;
       for (int o = tid; o < span; o += kWin * NT) {
 #pragma unroll
         for (int u = 0; u < kWin; ++u)
@@ -538,12 +569,12 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
               values_below<E>(src, d[u], v, kth, x);
             else
               src.values(d[u], v, x);
-            fold_values<E>(x, c, own);
+            fold_long<E>(x, c, own);
           }
       }
+      wm = wave_fmax(own.m);
+      ws = wave_sum(own.s * rescale(own.m, wm, c));
     }
-    wm = wave_fmax(own.m);
-    ws = wave_sum(own.m == kNegInf ? 0.0 : (double)own.s * (double)fast_exp2((own.m - wm) * c));
   }
   if (lane == 0) {
     s_wm[wave] = ws > 0.0 ? wm : kNegInf;

@@ -78,3 +78,74 @@ def test_beams_whose_scores_tie_in_part(far, dtype):
         for w in range(Wd):
             mine = got["tok"][b][got["beam"][b] == w].tolist()
             assert mine == x[b, w].double().sort(descending=True, stable=True)[1][: len(mine)].tolist(), (b, w)
+
+
+# ---------------------------------------------------------------------------
+# rows whose parts are read a second time, thousands of vectors a thread
+# ---------------------------------------------------------------------------
+def second_read(V, threads, parts, bulk):
+    """fp32 logits whose mass outside the listed values has to be summed again: a thread of every wave owns two listed
+    values, in different vectors, that outweigh all the rest by e^40.  Returns the row and the number of listed values."""
+    x = bulk.clone()
+    per = V // 4 // parts  # vectors of a part
+    n = 0
+    for p in range(parts):
+        for w in range(threads // 64):
+            for j in (100, 900):
+                v = p * per + w * 64 + 5 + j * threads
+                x[4 * v + j % 4] = 60.0 + 0.25 * (n % 4)
+                n += 1
+    return x, n
+
+
+def one_above(V, threads, parts, above):
+    """Zeros, and one value above them in every thread's first vector, against which the thread's sum is formed."""
+    x = torch.zeros(V)
+    per = V // 4 // parts
+    for p in range(parts):
+        x[4 * p * per: 4 * (p * per + threads): 4] = above
+    return x
+
+
+BULKS = [2.8, 4.95, 3.31, 1.4, "rising", "falling", "normal", "steps"]
+
+
+def bulk_of(kind, V, threads, parts):
+    if kind == "rising":
+        return torch.linspace(0, 3, V)
+    if kind == "falling":
+        return torch.linspace(3, 0, V)
+    if kind == "normal":
+        return torch.randn(V, generator=torch.Generator().manual_seed(3))
+    if kind == "steps":  # from 2^-170 to the largest in jumps of 2^1 to 2^80
+        at = torch.tensor([-118.0, -80.0, -79.0, -40.0, -38.0, -16.0, 0.0, 5.0])
+        return at[torch.arange(V) // (V // 4) % 4 * 2 + torch.arange(V) // (V // 8) % 2]
+    return one_above(V, threads, parts, kind)
+
+
+@pytest.mark.parametrize("kind", BULKS)
+def test_long_row_read_twice(kind):
+    """2^24 logits in 4 parts of 512 threads: 2048 vectors a thread."""
+    V, k = 1 << 24, 64
+    x, n = second_read(V, 512, 4, bulk_of(kind, V, 512, 4))
+    assert n == k
+    got = svx.sv_teacher_topk(x[None].to(DEV), k, 1.0)
+    ids, vals, rest = ref.teacher(x[None], k, 1.0)
+    assert torch.equal(got["ids"].cpu().long(), ids)
+    near(got["rest"], rest, ref.SUM + 2.0 ** -24 * rest.abs(), "rest")
+
+
+@pytest.mark.parametrize("kind", BULKS)
+def test_long_rows_read_twice(kind):
+    """257 rows of 2^21 logits, a block of 256 threads each: 2048 vectors a thread; and beams of such rows."""
+    V, R = 1 << 21, 257
+    x, k = second_read(V, 256, 1, bulk_of(kind, V, 256, 1))
+    z = x.to(DEV).expand(R, V).contiguous()
+    got = svx.sv_teacher_topk(z, k, 1.0)
+    ids, vals, rest = ref.teacher(x[None], k, 1.0)
+    assert torch.equal(got["ids"].cpu().long(), ids.expand(R, k))
+    near(got["rest"], rest.expand(R), ref.SUM + 2.0 ** -24 * rest.abs().expand(R), "rest")
+    out = svx.sv_beam_select(z[:, None], torch.zeros(R, 1, device=DEV), k)
+    assert torch.equal(out["tok"].cpu().long(), ids.expand(R, k))
+    score = vals - x.double().logsumexp(-1)
+    near(out["score"], score.expand(R, k), ref.SUM + 2.0 ** -24 * score.abs().expand(R, k), "score")
