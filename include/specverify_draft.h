@@ -117,7 +117,7 @@ sv_status sv_teacher_topk(const void* logits, sv_dtype dt, int64_t stride, int32
  *     overlap z otherwise.  What lies between the rows is not written.
  * Reads each row once for the loss; with the gradient, rows of up to 196608
  * bf16 or 98304 fp32 logits once in all, longer ones (and up to some 100 rows
- * of more than 80000 or 40000) twice.  The gradient of a row may therefore
+ * of more than 80000 or 52000) twice.  The gradient of a row may therefore
  * differ in its last bits between calls with different numbers of rows.
  */
 sv_status sv_distill_topk(const void* z, sv_dtype dt, int64_t stride, int32_t R, int32_t V, const int32_t* t_ids,

@@ -98,11 +98,25 @@ sv_status plan_distill(sv_dtype dt, int32_t R, int32_t V, int32_t k, Plan* pl) {
 
 // Whether loss and gradient together hold rows in registers, a block a row:
 // wherever a row fits, but for a few long ones, which many blocks finish
-// sooner in two launches.  bf16 rows held / in two launches, us: 65000 logits
-// 15.0 / 16.9 (16 rows), 119 / 154 (2000); 110000: 21 / 17 (16), 22.5 / 20.7
-// (72), 22.5 / 24.0 (96), 204 / 255 (2000); 152064: 25.6 / 17.6 (16), 26.6 /
-// 24.0 (72), 26.9 / 28.3 (96), 38 / 52 (256).
-bool hold_rows(int32_t R, int64_t nvec) { return nvec <= kHeldVecs && !(nvec > 10000 && R <= nvec / 200); }
+// sooner in two launches.  The fewer values a vector has, the sooner a block
+// is through with a row, so fp32 rows are held from longer ones and fewer on.
+// Held / in two launches, us:
+//   bf16  82000 logits  17.7 / 16.9 (16 rows), 18.2 / 18.7 (48)
+//        110000         20.0 / 17.4 (16), 20.7 / 20.8 (56), 20.9 / 23.2 (72)
+//        152064         25.9 / 18.4 (16), 27.0 / 25.9 (72), 27.2 / 27.8 (80), 27.5 / 31.3 (96)
+//        196608         32.7 / 18.4 (16), 35.8 / 35.5 (104), 36.1 / 39.8 (128)
+//   fp32  48000         13.3 / 14.5 (4)
+//         64128         15.9 / 14.6 (4), 16.5 / 16.9 (32), 16.7 / 18.5 (40)
+//         76032         19.1 / 17.3 (16), 19.7 / 18.7 (40), 19.8 / 20.4 (48)
+//         98304         25.0 / 17.4 (16), 27.2 / 25.5 (80), 27.6 / 30.3 (88)
+// and many rows: 2000 bf16 of 128256 210 / 278, of 152064 254 / 330, of 196608
+// 340 / 423; a little more than a block a compute unit at the greatest lengths
+// is the worst of it (300 of 196608: 81 / 76).
+bool hold_rows(sv_dtype dt, int32_t R, int64_t nvec) {
+  if (nvec > kHeldVecs) return false;
+  if (dt == SV_F32) return R > (nvec - 13000) / 140;
+  return nvec <= 10000 || R > nvec / 240;
+}
 
 void plan_reorder(Plan* pl) { pl->bytes = kWsFixed; }
 
@@ -246,7 +260,7 @@ sv_status sv_distill_topk(const void* z, sv_dtype dt, int64_t stride, int32_t R,
   p.out_stat = out_stat;
   p.stat = out_stat;
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  if (out_grad && hold_rows(R, pl.nvec)) return launch_distill_held(p, dt, s) == hipSuccess ? SV_OK : SV_EHIP;
+  if (out_grad && hold_rows(dt, R, pl.nvec)) return launch_distill_held(p, dt, s) == hipSuccess ? SV_OK : SV_EHIP;
   if (launch_distill_loss(p, dt, s) != hipSuccess) return SV_EHIP;
   if (out_grad && launch_distill_grad(p, dt, s) != hipSuccess) return SV_EHIP;
   return SV_OK;
