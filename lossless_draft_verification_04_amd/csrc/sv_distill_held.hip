@@ -19,6 +19,8 @@
 // good.  The gradients at the tokens of I are stored, after the row's vectors,
 // by the wave that stored the vector they lie in: a wave's stores to one place
 // stay in order, and no wait for the next row's loads comes between.
+#include <atomic>
+
 #include "sv_distill.hpp"
 #include "sv_internal.h"
 
@@ -315,15 +317,15 @@ namespace {
 
 template <int DT, int NT, int NV>
 hipError_t launch_held(const DistillParams& p, hipStream_t s) {
-  static int cache[64];
+  static std::atomic<int> cache[64];  // of any host thread
   int dev = 0;
   const hipError_t e = hipGetDevice(&dev);
   if (e != hipSuccess) return e;
-  int cap = dev >= 0 && dev < 64 ? cache[dev] : 0;
+  int cap = dev >= 0 && dev < 64 ? cache[dev].load(std::memory_order_relaxed) : 0;
   if (cap == 0) {
     cap = device_capacity(reinterpret_cast<const void*>(&distill_held_kernel<DT, NT, NV>), NT, dev);
     if (cap <= 0) return hipErrorInvalidConfiguration;
-    if (dev >= 0 && dev < 64) cache[dev] = cap;
+    if (dev >= 0 && dev < 64) cache[dev].store(cap, std::memory_order_relaxed);
   }
   const unsigned grid = (unsigned)(p.R < cap ? p.R : cap);
   distill_held_kernel<DT, NT, NV><<<dim3(grid), dim3(NT), 0, s>>>(p);
