@@ -175,6 +175,9 @@ sv_status sv_beam_select(const void* logits, sv_dtype dt, int64_t stride, const 
  * what the smaller ones span.  SV_EINVAL otherwise.
  * A parent outside [-1, W) or a length outside [0, S] sets SV_DERR_RANGE; that
  * beam, or that whole sequence, is left as it was.  Any alignment is taken.
+ * One beam's states hold fewer than 2^32 places of 16 bytes (8 or 4 where more than
+ * 16 or 32 beams move in place; every segment takes multiples of 256 places);
+ * SV_EUNSUPPORTED beyond.
  */
 sv_status sv_beam_reorder(const void* src, const int64_t* src_stride, void* dst, const int64_t* dst_stride,
                           const int32_t* parent, const int32_t* lens, int32_t L, int32_t B, int32_t W, int32_t N,

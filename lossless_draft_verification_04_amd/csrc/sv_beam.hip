@@ -198,7 +198,7 @@ struct Bytes<1> {
   typedef uint8_t T __attribute__((may_alias));
 };
 
-constexpr int kRNT = 256;
+constexpr int kRNT = kReorderThreads;
 
 // One place of U bytes for all beams.
 template <int U, int MAXN, bool NTS>
@@ -265,10 +265,9 @@ constexpr double kPastCache = 320.0 * (1 << 20);  // bytes of a state that the 2
 
 template <int U, int MAXN>
 static hipError_t launch_reorder_u(const ReorderParams& p, hipStream_t s) {
-  const int64_t places = p.S * p.pos / U + kReorderOdd;
-  const int64_t nblk = (places + kRNT - 1) / kRNT;
+  const int64_t nblk = reorder_blocks(p.S * p.pos, U);
   const int64_t grid = nblk * p.L * p.B * p.H;
-  if (grid > INT32_MAX) return hipErrorInvalidValue;
+  if (grid > kReorderMostBlocks) return hipErrorInvalidValue;
   if ((double)p.L * p.B * p.N * p.H * p.S * p.pos > kPastCache)
     reorder_kernel<U, MAXN, true><<<dim3((unsigned)grid), dim3(kRNT), 0, s>>>(p, nblk);
   else
@@ -277,11 +276,11 @@ static hipError_t launch_reorder_u(const ReorderParams& p, hipStream_t s) {
 }
 
 hipError_t launch_reorder(const ReorderParams& p, hipStream_t s) {
-  // in place every beam's piece is held at once; apart, 16 beams at a time
-  if (p.N <= 8) return launch_reorder_u<16, 8>(p, s);
-  if (p.N <= 16 || !p.inplace) return launch_reorder_u<16, 16>(p, s);
-  if (p.N <= 32) return launch_reorder_u<8, 32>(p, s);
-  return launch_reorder_u<4, 64>(p, s);
+  switch (reorder_unit(p.N, p.inplace)) {
+    case 16: return p.N <= 8 ? launch_reorder_u<16, 8>(p, s) : launch_reorder_u<16, 16>(p, s);
+    case 8: return launch_reorder_u<8, 32>(p, s);
+    default: return launch_reorder_u<4, 64>(p, s);
+  }
 }
 
 }  // namespace sv

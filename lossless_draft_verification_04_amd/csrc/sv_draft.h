@@ -89,5 +89,13 @@ hipError_t launch_distill_grad(const DistillParams& p, sv_dtype dt, hipStream_t 
 hipError_t launch_distill_held(const DistillParams& p, sv_dtype dt, hipStream_t s);
 hipError_t launch_reorder(const ReorderParams& p, hipStream_t s);
 constexpr int kReorderOdd = 6;  // places at a segment's end: of 4 bytes (3 at most) and of one (3)
+constexpr int kReorderThreads = 256;
+// Bytes of a place: in place every beam's piece is held at once; apart, 16 beams at a time.
+inline int reorder_unit(int32_t N, bool inplace) { return N <= 16 || !inplace ? 16 : N <= 32 ? 8 : 4; }
+// Blocks of a segment of `run` bytes, and of a launch at most (fewer than 2^32 threads).
+inline int64_t reorder_blocks(int64_t run, int unit) {
+  return (run / unit + kReorderOdd + kReorderThreads - 1) / kReorderThreads;
+}
+constexpr int64_t kReorderMostBlocks = UINT32_MAX / kReorderThreads;
 
 }  // namespace sv

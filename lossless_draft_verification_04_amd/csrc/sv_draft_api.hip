@@ -345,8 +345,7 @@ sv_status sv_beam_reorder(const void* src, const int64_t* src_stride, void* dst,
   plan_reorder(&pl);
   sv_status st;
   if ((st = check_ws(ws, ws_bytes, pl)) != SV_OK) return st;
-  // blocks of 256 places of 4 bytes, the smallest that a launch takes
-  if ((run / 4 + kReorderOdd + 255) / 256 > INT32_MAX / ((int64_t)L * B) / H) return SV_EUNSUPPORTED;
+  if (reorder_blocks(run, reorder_unit(N, inplace)) > kReorderMostBlocks / ((int64_t)L * B) / H) return SV_EUNSUPPORTED;
   ReorderParams p;
   p.src = static_cast<const char*>(src);
   p.dst = static_cast<char*>(dst);

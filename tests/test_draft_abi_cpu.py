@@ -185,3 +185,17 @@ def test_state_layouts():
     assert svx._state_layout(v, 4, "state")[0] == (2, 3, 4, 5, 6, 32)
     assert svx._state_layout(t[:, :, :, :, :3], 4, "state")[0] == (2, 3, 4, 5, 3, 16)
     assert svx._state_layout(torch.zeros(1, 2, 3, dtype=torch.int32), None, "state")[0] == (1, 2, 3, 1, 1, 4)
+
+
+def test_beam_reorder_refuses_more_places_than_a_launch_has_threads():
+    """A launch takes fewer than 2^32 threads, each a place of 16 bytes (4 where more than 32 beams move in place)."""
+    def f(S, pos, B=1, H=1, beams=1, inplace=False):
+        run = S * pos
+        st = (run * beams * H * B, run * beams * H, run * H, run)
+        return L.sv_beam_reorder(P(1 << 12), strides(*st), P(1 << (12 if inplace else 60)), strides(*st), A3, None, 1, B, beams,
+                                 beams, H, S, pos, WS, BIG, None)
+
+    assert f((1 << 31) - 1, 64) == svx.SV_EUNSUPPORTED
+    assert f(1 << 30, 8, H=8, B=2) == svx.SV_EUNSUPPORTED
+    assert f(1 << 20, 16, B=1 << 12, beams=33, inplace=True) == svx.SV_EUNSUPPORTED
+    assert f(1, 4, B=1 << 12, H=1 << 12) == svx.SV_EUNSUPPORTED
