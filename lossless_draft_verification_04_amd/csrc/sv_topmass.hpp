@@ -37,13 +37,13 @@ __device__ __forceinline__ double here(double c) {
   return c;
 }
 // e^x for x <= 0 in 64 bits to about 1e-11: x = n log 2 + r with |r| <= log(2) / 2
-// (log 2 in two parts, the first short enough that n times it is exact), and
+// (log 2 as its first 40 bits, which n times are exact, and the next 53), and
 // the series of e^r to r^9 / 9!; 0 below the range.
 __device__ __forceinline__ double exp_d(double x) {
   x = fmax(x, here(-800.0));
   const double n = rint(x * here(1.4426950408889634));
-  double r = fma(n, here(-0.693147180369123816490), x);
-  r = fma(n, here(-1.90821492927058770002e-10), r);
+  double r = fma(n, here(-0x1.62e42fefa2p-1), x);
+  r = fma(n, here(-0x1.9ef35793c7673p-41), r);
   double p = fma(here(1.0 / 362880.0), r, here(1.0 / 40320.0));
   p = fma(p, r, here(1.0 / 5040.0));
   p = fma(p, r, here(1.0 / 720.0));
