@@ -3,11 +3,17 @@
 //
 // The formulas and their arithmetic are those of sv_distill.hip.  A row's
 // gradient needs the row's sums, so two passes read every logit twice; a
-// compute unit's registers (512 KB) hold a row of up to about 190 thousand
-// bf16 logits, so here each is read once and its gradient written once: 4096 x
-// 128256 bf16 rows, a tenth of them empty, 409 us at 4.9 TB/s (a copy's rate);
-// 2000 rows 206 us, 274 in two launches.  96 x 32000 fp32 rows: 12.6 us, the
-// latencies of one row's turn.
+// compute unit's registers (512 KB) hold a row of up to about 130 thousand
+// bf16 logits beside what the work takes, so here each is read once and its
+// gradient written once: 4096 x 128256 bf16 rows, a tenth of them empty, 407 us
+// at 4.9 TB/s (a copy's rate); 2000 rows 210 us, 278 in two launches.  96 x
+// 32000 fp32 rows: 12.6 us, the latencies of one row's turn.
+//
+// Longer rows spill some registers to memory: 12, 40, 68 and 160 bytes a thread
+// at 18, 20, 22 and 24 vectors (rows of up to 147456, 163840, 180224 and 196608
+// bf16 logits; 12, 36, 76 and 112 in fp32).  Counted, 2000 rows of 152064 read
+// 584 MiB of 580 and write 595, in 252 us; of 196608, 779 of 750 and 814, in
+// 341 us.  Two launches take 330 and 423.
 //
 // Blocks are persistent and walk rows r, r + grid, ...; while a row's gradient
 // is stored, the next row's vectors are loaded into the registers that fall
@@ -168,7 +174,9 @@ __global__ __launch_bounds__(NT, 4) void distill_held_kernel(DistillParams a) {
   int b = 0;
   Fetched cur = fetch_teacher(a, r, ti);
   {
-    // its vectors are on their way while its teacher is prepared
+    // its vectors are asked for once rest is here, ahead of the rest of its
+    // teacher's preparation; the row number counts as divergent here, so that
+    // each load stands in a loop over lanes (later rows' do not)
     const __amdgpu_buffer_rsrc_t rs = row_range(r, true);
 #pragma unroll
     for (int i = 0; i < NV; ++i) d[i] = load_range(rs, off0 + (uint32_t)(i * NT * 16));

@@ -18,9 +18,9 @@ namespace {
 
 // Blocks of the top-value passes, and the smallest part of a row split for
 // them: joining parts costs about as much as a block takes for 8192 vectors
-// (17 x 32000 fp32 rows, 64 values: 13.1 us whole, 18.4 in parts of 2667;
-// 17 x 152064 bf16 rows: 21.6 us in 2 parts, 22.8 in 4).  Beams are joined
-// anyway (8 beams of 152064: 17.8 us in 4 parts each, 19.4 in 2).
+// (17 x 32000 fp32 rows, 64 values: 12.4 us whole, 16.5 in parts of 2667;
+// 17 x 152064 bf16 rows: 20.7 us in 2 parts, 21.4 in 4).  Beams are joined
+// anyway (8 beams of 152064, 16 kept: 15.9 us in 4 parts each, 18.7 in 2).
 constexpr int kTopBlocks = 256;
 constexpr int kTopPartVecs = 8192, kBeamPartVecs = 4096;
 
@@ -41,8 +41,8 @@ bool bad_scale(float T) { return bad_temperature(T) || !std::isfinite(log2e_over
 sv_status plan_topmass(sv_dtype dt, int64_t rows, int32_t V, int32_t k, int64_t part, Plan* pl) {
   pl->nvec = (V + per_vec(dt) - 1) / per_vec(dt);
   // no more blocks than kTopBlocks, rows in equal numbers of parts: the few of a
-  // second round take as long as the first (200 x 152064 bf16 rows: 24.2 us in
-  // 400 blocks, 19.4 whole; 11 x 8 beams of 128256: 21.5 in 264, 19.4 in 176)
+  // second round take as long as the first (200 x 152064 bf16 rows: 32 us in
+  // 400 blocks, 21.7 whole; 11 x 8 beams of 128256: 22.1 in 264, 19.7 in 176)
   split(rows, pl->nvec, rows > 0 ? (int)std::max(rows, kTopBlocks / rows * rows) : 1, &pl->nch1, &pl->vpc1, part);
   const int32_t most = std::min(kPartEntries / k, kMostParts);
   if (pl->nch1 > most) {

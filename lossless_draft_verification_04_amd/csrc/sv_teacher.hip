@@ -2,8 +2,8 @@
 // distillation target per row, on gfx950.
 //
 // Per row: the k largest logits (value descending, index ascending) and
-// rest = log sum over the others of exp(z / T), natural logarithm.  One read
-// of each row bounds it from below; the work beside it is one exponential (a
+// rest = log sum over the others of exp(z / T), natural logarithm.  A read of
+// each row bounds it from below; the work beside it is one exponential (a
 // quarter-rate instruction), its argument, a maximum and an addition a logit,
 // more than half of the vector unit's time at the memory's rate.
 //
@@ -12,10 +12,13 @@
 // block, otherwise the row's last block merges the parts: what a part listed
 // and the row does not is counted back into the mass.
 //
-// 2048 x 151936 bf16 rows, 64 values: 105 us, 5.9 TB/s (a plain read reaches
-// 7.1); what is missing is the selection at a block's end, which only the
-// other blocks of a compute unit cover.  17 x 32000 fp32 rows, 8 values:
-// 9.9 us, a chain of latencies (load, bound, candidates, ranks, stores).
+// 2048 x 151936 bf16 rows, 64 values that no two stand in one thread's share:
+// 106 us, 5.85 TB/s (a plain read reaches 7.1); what is missing is a block's
+// start (a window whose loads wait for each other) and the selection at its
+// end, which only the other blocks of a compute unit cover.  Unordered rows
+// have some 7 threads with two of the 64, whose vectors are read again: 137 us.
+// 17 x 32000 fp32 rows, 8 values: 10 us, a chain of latencies (four loads,
+// bound, candidates, ranks, stores).
 #include "sv_draft.h"
 #include "sv_topmass.hpp"
 

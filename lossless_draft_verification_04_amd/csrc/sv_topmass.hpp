@@ -24,9 +24,10 @@
 namespace sv {
 
 // Up to this many blocks, one to a compute unit, have 512 threads each, more
-// 256.  Teacher's pass, bf16, 256 threads / 512: 2048 x 151936 rows 116 us /
-// 127; 2000 x 4000 21 / 33; 300 x 128256 24.4 / 26.1; 480 x 32000 14.4 / 16.2;
-// 256 x 128256 21.5 / 19.2; 17 x 152064 27 / 22.
+// 256.  Teacher's pass, bf16, 64 values, 256 threads / 512: 2048 x 151936 rows
+// 109 us / 122; 2000 x 4000 24.5 / 36.8; 1536 x 32000 33.6 / 47.0; 480 x 32000
+// 16.6 / 18.3; 300 x 128256 27.9 / 28.1; 256 x 128256 25.5 / 21.5; 17 x 152064
+// 25.4 / 20.9.  Beams, 16 kept: 64 x 8 of 128256 32.6 / 33.1; 72 x 8 38.4 / 44.4.
 constexpr int64_t kTopWide = 256;
 
 // A 64-bit constant, formed in scalar registers where it stands: left alone
@@ -212,7 +213,10 @@ __device__ __forceinline__ float vec_sum(const float (&x)[E], float c, float r) 
 template <int NT, int E, class Src>
 __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, int64_t v1, int V, int F, float c,
                                                    Partial* mass) {
-  constexpr int kWin = 4;  // vectors in flight per thread
+  // vectors of a thread's window: the loop over whole windows has the next one
+  // in flight; the first window (in fp32 the last ones too) waits for each load
+  // in turn, as each stands under a condition and is masked where it is made
+  constexpr int kWin = 4;
   constexpr int NW = NT / kWave;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = threadIdx.x / kWave;
@@ -326,8 +330,8 @@ __device__ __forceinline__ TopPair block_topk_mass(const Src src, int64_t v0, in
   static_assert(kMaxH >= 1 && kMaxH <= 16 && kMaxH * kWave == NT, "whole waves, at most 16");
   // four times as many groups as listed values: more of them lengthen the
   // search, fewer loosen the bound, so that more threads' other vectors are
-  // read again (2048 x 151936 bf16 rows, 64 values: 133 us at twice as many,
-  // 112 at four and eight times; 128 x 32000, 16 values: 11.5 and 12.6 us)
+  // read again (2048 x 151936 bf16 rows, 64 values: 131 us at twice as many,
+  // 108 at four and eight times; 128 x 32000, 16 values: 11.3, 11.4, 12.6 us)
   int H = 1;
   while (H < kMaxH && 4 * F > kWave * H) H *= 2;  // block-uniform
   const int GS = NT / (kWave * H);
