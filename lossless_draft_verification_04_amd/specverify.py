@@ -186,7 +186,7 @@ class Workspace:
     A buffer that a larger one replaces is kept: graphs captured with it go on using it, and calls of other streams may
     still be running in it.  Sizes double, so that the replaced ones together take less than the one in use.  A buffer
     made while a graph is being captured lies in the graph's memory and its zero fill runs with the graph, so it serves
-    that one call and is never handed to another."""
+    that one call and is never handed to another; its error word means something once the graph has run."""
 
     _lock = threading.Lock()
     _cache = {}

@@ -1,5 +1,5 @@
-"""Drafter-side operators where 64-bit scores no longer tell logits apart, and where a thread adds up thousands of
-terms."""
+"""Drafter-side operators where 64-bit scores no longer tell logits apart, where a thread adds up thousands of terms,
+in place where a block walks several rows, and past 4 GiB of rows."""
 import math
 
 import pytest
@@ -149,3 +149,57 @@ def test_long_rows_read_twice(kind):
     assert torch.equal(out["tok"].cpu().long(), ids.expand(R, k))
     score = vals - x.double().logsumexp(-1)
     near(out["score"], score.expand(R, k), ref.SUM + 2.0 ** -24 * score.abs().expand(R, k), "score")
+
+
+# ---------------------------------------------------------------------------
+# loss and gradient in place where a block walks several rows, and rows past 4 GiB
+# ---------------------------------------------------------------------------
+def teacher_of(z, k, seed):
+    """k distinct tokens of every row, some rows without a target."""
+    R, V = z.shape
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    ids = ((torch.randint(0, V, (R, 1), generator=g, device=DEV) + torch.arange(k, device=DEV) * (V // k)) % V).int()
+    vals = torch.randn(R, k, generator=g, device=DEV) + 9
+    rest = torch.rand(R, generator=g, device=DEV) * 4 + math.log(V)
+    ids[5::7], rest[5::7] = -1, -INF
+    return ids, vals, rest, torch.rand(R, generator=g, device=DEV)
+
+
+@pytest.mark.parametrize("dtype,R,V", [(BF16, 3000, 1031), (F32, 1700, 8003), (BF16, 1300, 30011), (BF16, 600, 128256),
+                                       (F32, 600, 60001), (BF16, 600, 147456), (BF16, 600, 160003), (BF16, 600, 180003),
+                                       (BF16, 600, 196608), (F32, 600, 98304)])
+def test_in_place_gives_the_bits_of_apart(dtype, R, V):
+    g = torch.Generator(device=DEV).manual_seed(V)
+    z = put(torch.randn(R, V, generator=g, device=DEV).mul_(2).to(dtype))
+    ids, vals, rest, w = teacher_of(z, 24, R)
+    apart = svx.sv_distill_topk(z, ids, vals, 1.0, rest=rest, grad_loss=w, want_grad=True)
+    want = apart["grad"].clone()
+    got = svx.sv_distill_topk(z, ids, vals, 1.0, rest=rest, grad_loss=w, grad=z)
+    assert got["grad"] is z and torch.equal(z, want)
+    assert torch.equal(got["loss"], apart["loss"]) and torch.equal(got["stat"], apart["stat"])
+    assert float(want.abs().amax()) > 0
+
+
+@pytest.mark.parametrize("dtype,R,V", [(BF16, 18001, 128256), (F32, 600, 1 << 21)])
+def test_rows_past_4_gib(dtype, R, V):
+    """The last rows, in every entry point over rows; by a block a row that holds it, and in two launches."""
+    z = torch.zeros(R, V, dtype=dtype, device=DEV)
+    assert z.numel() * z.element_size() > 1 << 32
+    last = rows(3, V, dtype, 5)
+    z[-3:] = last.to(DEV)
+    k, T = 16, 1.0
+    got = svx.sv_teacher_topk(z, k, T)
+    ids, vals, rest = ref.teacher(last, k, T)
+    assert torch.equal(got["ids"][-3:].cpu().long(), ids)
+    near(got["rest"][-3:], rest, ref.SUM + 2.0 ** -24 * rest.abs(), "rest")
+    out = svx.sv_beam_select(z[:, None], torch.zeros(R, 1, device=DEV), k)
+    assert torch.equal(out["tok"][-3:].cpu().long(), ids)
+    target = got["ids"], got["vals"] + 0.25 * torch.arange(k, device=DEV), got["rest"]
+    loss, stat, grad, size = ref.distill(last, *(t[-3:].cpu() for t in target), T)
+    tol = 3e-5 * size + ref.HALF[dtype] * grad.abs() + 1e-37
+    fwd = svx.sv_distill_topk(z, *target[:2], T, rest=target[2])
+    near(fwd["loss"][-3:], loss, 2 * ref.SUM + 2.0 ** -23 * loss.abs(), "loss")
+    near(svx.sv_distill_topk_backward(z, *target[:2], fwd["stat"], T, rest=target[2])[-3:], grad, tol, "backward")
+    both = svx.sv_distill_topk(z, *target[:2], T, rest=target[2], grad=z)
+    near(both["loss"][-3:], loss, 2 * ref.SUM + 2.0 ** -23 * loss.abs(), "loss")
+    near(z[-3:], grad, tol, "in place")

@@ -91,3 +91,18 @@ def test_replaced_after_a_capture(fresh):
         assert same(bits(svx.sv_teacher_topk(z, 24, 1.0)), want)
         assert svx.sv_get_device_error(DEV) == svx.DERR_TOKEN
     assert all(int(t.min()) == 3 and int(t.max()) == 3 for t in kept)
+
+
+def test_captured_before_any_call_in_a_workspace_of_its_own(fresh):
+    z = rows(3, 150011, 7)
+    own = torch.zeros(8 << 20, dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = svx.sv_teacher_topk(z, 24, 1.0, workspace=own)
+    want = bits(svx.sv_teacher_topk(z, 24, 1.0))
+    for _ in range(3):
+        for v in out.values():
+            v.fill_(-7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(bits(out), want)
