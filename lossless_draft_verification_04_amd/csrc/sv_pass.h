@@ -1,0 +1,98 @@
+// sv_pass.h -- launch parameters of the verifier's pass (not part of the
+// public C ABI).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "specverify_pass.h"
+
+namespace sv {
+
+// A cache as the kernels see it; offsets in bytes within a head's part of a page.
+struct Kv {
+  char* pool;
+  const int32_t* pages;
+  int64_t page_stride, layer_stride;
+  int64_t head;          // bytes of a head in a page
+  int64_t ks, vc, vs;    // where the keys' scales, the values, their scales begin
+  int32_t num_pages, max_pages, pshift, H, layers;
+  int64_t room;          // tokens that a sequence's table holds
+};
+
+struct RopeParams {
+  const char* in[2];
+  char* out[2];
+  int64_t is[2][3], os[2][3];  // bytes: sequence, node, head
+  int32_t B, N, heads[2], D, R;
+  const double* freq;
+  float factor;
+  bool interleaved, inverse;
+  const int32_t* positions;
+  const int32_t* lens;
+  const int32_t* parent;
+  int32_t* err;
+};
+
+struct KvMoveParams {  // write, read
+  Kv c;
+  char* k;  // read by the write, written by the read
+  char* v;
+  int64_t st[2][3];  // bytes: sequence, token, head
+  const int32_t* lens;
+  const int32_t* news;
+  int32_t B, N;
+  int32_t* err;
+};
+
+struct KvCommitParams {
+  Kv c;
+  const int32_t* lens;
+  const int32_t* n;
+  const int32_t* path;
+  int32_t B, M;
+  int32_t* out_lens;
+  int32_t* err;
+};
+
+struct AttentionParams {
+  Kv c;
+  const char* q;
+  char* out;
+  int64_t qs[3], os[3];  // bytes: sequence, node, head
+  float* lse;
+  const int32_t* lens;
+  const int32_t* news;
+  const int32_t* parent;
+  int32_t B, N, Hq, G;  // G query heads of a key head
+  float scale, cap;
+  const float* slopes;
+  int32_t reach;
+  int32_t* err;
+  int32_t tiles, groups;  // tiles of 16 rows in a group of rows, groups
+  int32_t blocks;
+  float* part_o;  // [2 * blocks][tiles * 16][D]
+  float* part_ml; // [2 * blocks][tiles * 16][2]
+  void* desc;     // [blocks] of AttentionItem
+};
+
+// An item (a sequence's key head and group of rows) that several blocks share.
+struct AttentionItem {
+  int32_t b, h, group;      // b = -1: none
+  int32_t first, last;      // blocks
+  int32_t slot;             // of the first block's part
+  int32_t pad[2];
+};
+
+hipError_t launch_rope(const RopeParams& p, sv_dtype dt, hipStream_t s);
+hipError_t launch_kv_write(const KvMoveParams& p, sv_dtype dt, int D, hipStream_t s);
+hipError_t launch_kv_read(const KvMoveParams& p, sv_dtype dt, int D, hipStream_t s);
+hipError_t launch_kv_commit(const KvCommitParams& p, int D, hipStream_t s);
+hipError_t launch_kv_attention(const AttentionParams& p, sv_dtype dt, int D, hipStream_t s);
+
+// Rows of nodes x heads are taken in groups of up to this many tiles of 16.
+inline int attention_tiles(int D) { return D == 256 ? 2 : 4; }
+constexpr int kAttentionBlocks = 512;
+constexpr int kAttentionUnit = 128;  // tokens of a step: 32 for each of a block's 4 waves
+
+}  // namespace sv

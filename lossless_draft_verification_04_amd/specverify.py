@@ -38,6 +38,10 @@ DERR_TOKEN, DERR_TREE, DERR_FANOUT, DERR_ROW, DERR_TIMEOUT = 1, 2, 4, 8, 16
 # the drafter's side (specverify_draft.h)
 SV_DRAFT_TEACHER, SV_DRAFT_DISTILL, SV_DRAFT_BEAM, SV_DRAFT_REORDER = range(4)
 DERR_RANGE = 32
+# the verifier's pass (specverify_pass.h)
+SV_F16 = 2
+SV_PASS_ROPE, SV_PASS_WRITE, SV_PASS_READ, SV_PASS_ATTENTION, SV_PASS_COMMIT = range(5)
+SV_ROPE_KINDS = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
 
 _P = ctypes.c_void_p
 _i32, _i64, _u32, _u64, _f32, _f64, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_uint32, ctypes.c_uint64,
@@ -83,13 +87,36 @@ _DRAFT_SIGS = {
     "sv_beam_reorder": ([_P, ctypes.POINTER(_i64), _P, ctypes.POINTER(_i64), _P, _P, _i32, _i32, _i32, _i32, _i32,
                          _i64, _i64, _P, _sz, _P], _i32),
 }
-for _name, (_args, _res) in (*_SIGS.items(), *_DRAFT_SIGS.items()):
+
+
+class _CCache(ctypes.Structure):
+    """sv_kv_cache"""
+    _fields_ = [("pool", _P), ("pages", _P), ("page_stride", _i64), ("layer_stride", _i64), ("num_pages", _i32),
+                ("max_pages", _i32), ("page_tokens", _i32), ("H", _i32), ("D", _i32), ("layers", _i32)]
+
+
+# entry points of specverify_pass.h
+_S, _C = ctypes.POINTER(_i64), ctypes.POINTER(_CCache)
+_PASS_SIGS = {
+    "sv_kv_page_bytes": ([_i32, _i32, _i32, _S], _i32),
+    "sv_pass_workspace_size": ([_i32, _i32, _i32, _i32, _i32, _i32, ctypes.POINTER(_sz)], _i32),
+    "sv_rope": ([_P, _S, _P, _S, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _P, _f32, _i32, _i32, _P, _P, _P, _P, _S, _P, _S,
+                 _P, _sz, _P], _i32),
+    "sv_rope_frequencies": ([_i32, _i32, _f64, _f64, _i32, _f64, _f64, ctypes.POINTER(_f64), ctypes.POINTER(_f32)], _i32),
+    "sv_kv_write": ([_P, _S, _P, _S, _i32, _C, _P, _P, _i32, _i32, _P, _sz, _P], _i32),
+    "sv_kv_read": ([_C, _P, _P, _i32, _i32, _i32, _P, _S, _P, _S, _P, _sz, _P], _i32),
+    "sv_kv_attention": ([_P, _S, _i32, _C, _P, _P, _P, _i32, _i32, _i32, _f32, _f32, _P, _i32, _P, _S, _P, _P, _sz, _P],
+                        _i32),
+    "sv_kv_commit": ([_C, _P, _P, _P, _i32, _i32, _P, _P, _sz, _P], _i32),
+}
+for _name, (_args, _res) in (*_SIGS.items(), *_DRAFT_SIGS.items(), *_PASS_SIGS.items()):
     _fn = getattr(_lib, _name)
     _fn.argtypes = _args
     _fn.restype = _res
 
 EXPORTED = tuple(_SIGS)
 DRAFT_EXPORTED = tuple(_DRAFT_SIGS)
+PASS_EXPORTED = tuple(_PASS_SIGS)
 
 
 class SpecVerifyError(RuntimeError):
@@ -751,3 +778,225 @@ def sv_beam_reorder(state, parent, pos_dim=None, lens=None, out=None, workspace=
           W, N, H, S, pos, ws.data_ptr(), ws.numel())
     _checked(dev, "sv_beam_reorder", workspace)
     return dst
+
+
+# ---------------------------------------------------------------------------
+# The verifier's pass (specverify_pass.h): the same rules as the drafter's
+# side.  Tensors of a window are [B, N, heads, D] with a unit stride along D.
+# ---------------------------------------------------------------------------
+_PASS_TYPES = {torch.bfloat16: SV_BF16, torch.float16: SV_F16, torch.float32: SV_F32}
+
+
+@functools.lru_cache(maxsize=1024)
+def pass_workspace_size(op, B=0, N=0, Hq=0, H=0, D=0) -> int:
+    n = _sz(0)
+    _check(_lib.sv_pass_workspace_size(op, B, N, Hq, H, D, ctypes.byref(n)), "sv_pass_workspace_size")
+    return n.value
+
+
+def _pass_workspace(dev, *shape):
+    need = pass_workspace_size(*shape)
+    ws = Workspace._cache.get(dev.index)
+    return ws if ws is not None and ws.numel() >= need else Workspace.get(dev, need, in_capture=False)
+
+
+def _window(t, what, types=_PASS_TYPES):
+    """The type's code and the strides of a [B, N, heads, D] tensor."""
+    dt = types.get(t.dtype)
+    if dt is None:
+        raise SpecVerifyError(SV_EDTYPE, f"{what}: {t.dtype}")
+    return dt, _window_strides(t.shape, t.stride(), what)
+
+
+@functools.lru_cache(maxsize=1024)
+def _window_strides(shape, st, what):
+    if len(shape) != 4:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: want [B, N, heads, D], got {tuple(shape)}")
+    if st[3] != 1 and shape[3] > 1:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: a head's values must have unit stride")
+    return (_i64 * 3)(*st[:3])
+
+
+def _int32(t, shape, what):
+    if t is not None:
+        _want(t, torch.int32, shape, what)
+
+
+def kv_page_bytes(H, D, page_tokens) -> int:
+    """Bytes of a page of the 4-bit cache."""
+    n = _i64(0)
+    _check(_lib.sv_kv_page_bytes(int(H), int(D), int(page_tokens), ctypes.byref(n)), "sv_kv_page_bytes")
+    return n.value
+
+
+class KvCache:
+    """A paged 4-bit cache: pool uint8 [pages, bytes] of one layer or [L, pages, bytes] of several (bytes at least
+    kv_page_bytes(H, D, page_tokens), unit stride), pages int32 [B, max_pages] on the same device: sequence b's tokens t lie in page
+    pages[b, t // page_tokens].  The entry points read and write one layer's cache (layer(l) of a pool of several),
+    sv_kv_commit all layers of its pool.  Holds the tensors; what they contain may change between calls."""
+
+    def __init__(self, pool, pages, H, D, page_tokens):
+        H, D, page_tokens = int(H), int(D), int(page_tokens)
+        need = kv_page_bytes(H, D, page_tokens)
+        if pool.dtype is not torch.uint8 or pool.dim() not in (2, 3) or pool.shape[-1] < need or pool.stride(-1) != 1:
+            raise SpecVerifyError(SV_EINVAL, f"pool: want uint8 [pages, {need}] or [L, pages, {need}], got {pool.dtype} "
+                                  f"{tuple(pool.shape)}")
+        if pages.dim() != 2:
+            raise SpecVerifyError(SV_EINVAL, f"pages: want [B, max_pages], got {tuple(pages.shape)}")
+        _want(pages, torch.int32, tuple(pages.shape), "pages")
+        if pages.get_device() != pool.get_device():
+            raise SpecVerifyError(SV_EINVAL, f"KvCache: pool on {pool.device}, pages on {pages.device}")
+        self.pool, self.pages, self.H, self.D, self.page_tokens = pool, pages, H, D, page_tokens
+        self.device = pool.device
+        n, layers = pool.shape[-2], pool.shape[0] if pool.dim() == 3 else 1
+        # a single page or layer has no stride of its own
+        page = pool.stride(-2) if n > 1 else need + -need % 16
+        self._c = _CCache(pool.data_ptr(), pages.data_ptr(), page, pool.stride(0) if layers > 1 and pool.dim() == 3 else 0, n,
+                          pages.shape[1], page_tokens, H, D, layers)
+        self._ref = ctypes.byref(self._c)
+
+    def layer(self, l):
+        """The cache of one layer."""
+        return KvCache(self.pool[l], self.pages, self.H, self.D, self.page_tokens)
+
+    def _one(self, what):
+        if self._c.layers != 1:
+            raise SpecVerifyError(SV_EINVAL, f"{what}: a cache of one layer, not of {self._c.layers} (KvCache.layer)")
+        return self._ref
+
+
+def sv_rope_frequencies(R, theta=10000.0, kind="plain", scale=1.0, original=0, fast=32.0, slow=1.0):
+    """Angles a position of R/2 pairs, float64 [R/2] on the CPU, and the factor for sv_rope.  kind: plain, linear, base or
+    parts (specverify_pass.h)."""
+    if kind not in SV_ROPE_KINDS:
+        raise SpecVerifyError(SV_EINVAL, f"kind {kind!r}: one of {', '.join(SV_ROPE_KINDS)}")
+    R = int(R)
+    out, factor = (_f64 * max(1, R // 2))(), _f32(0)
+    _check(_lib.sv_rope_frequencies(SV_ROPE_KINDS[kind], R, float(theta), float(scale), int(original), float(fast),
+                                    float(slow), out, ctypes.byref(factor)), "sv_rope_frequencies")
+    return torch.tensor(list(out), dtype=torch.float64), factor.value
+
+
+def sv_rope(q, freq, k=None, positions=None, lens=None, parent=None, interleaved=False, factor=1.0, inverse=False,
+            out_q=None, out_k=None, workspace=None):
+    """Rotary positions of q [B, N, Hq, D] and k [B, N, Hk, D] (or None) over the first 2 * len(freq) values of each head;
+    freq float64 on the device.  positions [B, N] int32, or lens [B] int32 (None: 0) + the node's depth in parent [B, N] int32
+    (None: its number).  inverse: the transposed rotation, the gradient.  out_q, out_k: where to write (q, k themselves:
+    in place).  Returns dict(q, k)."""
+    dt, sq = _window(q, "q")
+    B, N, Hq, D = q.shape
+    if freq.dim() != 1:
+        raise SpecVerifyError(SV_EINVAL, f"freq: want [R/2], got {tuple(freq.shape)}")
+    _want(freq, torch.float64, tuple(freq.shape), "freq")
+    _int32(positions, (B, N), "positions")
+    _int32(lens, (B,), "lens")
+    _int32(parent, (B, N), "parent")
+    out_q = torch.empty_like(q, memory_format=torch.contiguous_format) if out_q is None else out_q
+    Hk, sk, sok = 0, None, None
+    if k is not None:
+        if k.dtype is not q.dtype or k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != D:
+            raise SpecVerifyError(SV_EINVAL, f"k: want {q.dtype} [{B}, {N}, heads, {D}], got {k.dtype} {tuple(k.shape)}")
+        Hk, sk = k.shape[2], _window(k, "k")[1]
+        out_k = torch.empty_like(k, memory_format=torch.contiguous_format) if out_k is None else out_k
+        if out_k.dtype is not k.dtype or out_k.shape != k.shape:
+            raise SpecVerifyError(SV_EINVAL, f"out_k: want {k.dtype} {tuple(k.shape)}")
+        sok = _window(out_k, "out_k")[1]
+    elif out_k is not None:
+        raise SpecVerifyError(SV_EINVAL, "out_k: want k with it")
+    if out_q.dtype is not q.dtype or out_q.shape != q.shape:
+        raise SpecVerifyError(SV_EINVAL, f"out_q: want {q.dtype} {tuple(q.shape)}")
+    dev = _one_device("sv_rope", q, freq, k, positions, lens, parent, out_q, out_k, workspace)
+    ws = workspace if workspace is not None else _pass_workspace(dev, SV_PASS_ROPE)
+    _call(dev, _lib.sv_rope, "sv_rope", q.data_ptr(), sq, _at(k), sk, dt, B, N, Hq, Hk, D, 2 * freq.shape[0], freq.data_ptr(),
+          float(factor), bool(interleaved), bool(inverse), _at(positions), _at(lens), _at(parent), out_q.data_ptr(),
+          _window(out_q, "out_q")[1], _at(out_k), sok, ws.data_ptr(), ws.numel())
+    _checked(dev, "sv_rope", workspace)
+    return dict(q=out_q, k=out_k)
+
+
+def _kv_rows(what, cache, k, v, B):
+    """Checks of the keys and values [B, N, H, D] that go with a cache."""
+    dt, sk = _window(k, "k")
+    if v.dtype is not k.dtype or v.shape != k.shape:
+        raise SpecVerifyError(SV_EINVAL, f"v: want {k.dtype} {tuple(k.shape)}, got {v.dtype} {tuple(v.shape)}")
+    if k.shape[0] != B or k.shape[2:] != (cache.H, cache.D):
+        raise SpecVerifyError(SV_EINVAL, f"{what}: want [{B}, N, {cache.H}, {cache.D}], got {tuple(k.shape)}")
+    return dt, sk, _window(v, "v")[1]
+
+
+def sv_kv_write(cache, k, v, lens, news=None, workspace=None):
+    """Keys and values [B, N, H, D] into the cache: token n of sequence b to place lens[b] + n, for n < news[b] (None: N)."""
+    B = cache.pages.shape[0]
+    dt, sk, sv = _kv_rows("k", cache, k, v, B)
+    _int32(lens, (B,), "lens")
+    _int32(news, (B,), "news")
+    dev = _one_device("sv_kv_write", cache.pool, k, v, lens, news, workspace)
+    ws = workspace if workspace is not None else _pass_workspace(dev, SV_PASS_WRITE)
+    _call(dev, _lib.sv_kv_write, "sv_kv_write", k.data_ptr(), sk, v.data_ptr(), sv, dt, cache._one("sv_kv_write"),
+          lens.data_ptr(), _at(news), B, k.shape[1], ws.data_ptr(), ws.numel())
+    _checked(dev, "sv_kv_write", workspace)
+
+
+def sv_kv_read(cache, start, count, k, v, workspace=None):
+    """What the cache holds: tokens start[b] (None: 0) .. + count[b] (None: N) into the first rows of k, v [B, N, H, D] of
+    any type; the others are left as they were.  Returns dict(k, v)."""
+    B = cache.pages.shape[0]
+    dt, sk, sv = _kv_rows("k", cache, k, v, B)
+    _int32(start, (B,), "start")
+    _int32(count, (B,), "count")
+    dev = _one_device("sv_kv_read", cache.pool, k, v, start, count, workspace)
+    ws = workspace if workspace is not None else _pass_workspace(dev, SV_PASS_READ)
+    _call(dev, _lib.sv_kv_read, "sv_kv_read", cache._one("sv_kv_read"), _at(start), _at(count), B, k.shape[1], dt,
+          k.data_ptr(), sk, v.data_ptr(), sv, ws.data_ptr(), ws.numel())
+    _checked(dev, "sv_kv_read", workspace)
+    return dict(k=k, v=v)
+
+
+def sv_kv_attention(cache, q, lens, news=None, parent=None, scale=None, cap=0.0, slopes=None, reach=0, out=None,
+                    want_lse=False, workspace=None):
+    """Attention of a window's nodes q [B, N, Hq, D] (bfloat16 or float16), already written to the cache at places lens[b] + n,
+    over the tokens before the window and each node's ancestors (parent [B, N] int32; None: a chain).  scale None:
+    D^-0.5; cap: scores go through cap * tanh(s / cap); slopes [Hq] float32: minus slope * distance; reach: only keys nearer
+    than that.  Rows from news[b] on are left as they were.  Returns dict(out [B, N, Hq, D], lse [B, N, Hq] or None)."""
+    dt, sq = _window(q, "q")
+    B, N, Hq, D = q.shape
+    if B != cache.pages.shape[0] or D != cache.D:
+        raise SpecVerifyError(SV_EINVAL, f"q: want [{cache.pages.shape[0]}, N, heads, {cache.D}], got {tuple(q.shape)}")
+    _int32(lens, (B,), "lens")
+    _int32(news, (B,), "news")
+    _int32(parent, (B, N), "parent")
+    if slopes is not None:
+        _want(slopes, torch.float32, (Hq,), "slopes")
+    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+    if out.dtype is not q.dtype or out.shape != q.shape:
+        raise SpecVerifyError(SV_EINVAL, f"out: want {q.dtype} {tuple(q.shape)}, got {out.dtype} {tuple(out.shape)}")
+    dev = _one_device("sv_kv_attention", q, cache.pool, lens, news, parent, slopes, out, workspace)
+    ws = workspace if workspace is not None else _pass_workspace(dev, SV_PASS_ATTENTION, B, N, Hq, cache.H, D)
+    lse = torch.empty(B, N, Hq, dtype=torch.float32, device=dev) if want_lse else None
+    _call(dev, _lib.sv_kv_attention, "sv_kv_attention", q.data_ptr(), sq, dt, cache._one("sv_kv_attention"), lens.data_ptr(),
+          _at(news), _at(parent), B, N, Hq, float(D ** -0.5 if scale is None else scale), float(cap), _at(slopes),
+          int(reach), out.data_ptr(), _window(out, "out")[1], _at(lse), ws.data_ptr(), ws.numel())
+    _checked(dev, "sv_kv_attention", workspace)
+    return dict(out=out, lse=lse)
+
+
+def sv_kv_commit(cache, lens, n, path=None, out_lens=None, workspace=None):
+    """After a verification, in all layers of the cache's pool: the root and the accepted path (n [B], path [B, M] int32:
+    sv_verify_tree's len and path; path None: a chain) stay, the path's tokens move next to the root.  n -1 leaves a sequence as
+    it was.  Returns the new lengths lens + 1 + n [B] (out_lens: where to write them, not lens itself)."""
+    B = cache.pages.shape[0]
+    _int32(lens, (B,), "lens")
+    _int32(n, (B,), "n")
+    if path is not None:
+        if path.dim() != 2:
+            raise SpecVerifyError(SV_EINVAL, f"path: want [{B}, M], got {tuple(path.shape)}")
+        _int32(path, (B, path.shape[1]), "path")
+    if out_lens is None:
+        out_lens = torch.empty_like(lens)
+    _int32(out_lens, (B,), "out_lens")
+    dev = _one_device("sv_kv_commit", cache.pool, lens, n, path, out_lens, workspace)
+    ws = workspace if workspace is not None else _pass_workspace(dev, SV_PASS_COMMIT)
+    _call(dev, _lib.sv_kv_commit, "sv_kv_commit", cache._ref, lens.data_ptr(), n.data_ptr(), _at(path), B,
+          path.shape[1] if path is not None else 0, out_lens.data_ptr(), ws.data_ptr(), ws.numel())
+    _checked(dev, "sv_kv_commit", workspace)
+    return out_lens
