@@ -16,6 +16,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kJoinBlocks = 512;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const f32x2 y = {lo, hi};
@@ -48,13 +49,19 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, int64_t b) {
   return s;
 }
 
-// First step of block i.
-__device__ __forceinline__ int64_t start_of(int64_t i, int64_t total, int64_t blocks) {
-  return (int64_t)((uint64_t)i * (uint64_t)total / (uint64_t)blocks);
+// First step of block i; the number of blocks is one or three times a power of
+// two, and blocks take a step each where there are fewer steps.
+__device__ __forceinline__ int64_t start_of(int64_t i, int64_t total, const AttentionParams& p) {
+  if (total < p.blocks) return min(i, total);
+  const uint64_t x = (uint64_t)i * (uint64_t)total >> p.log_blocks;
+  return (int64_t)(p.blocks >> p.log_blocks == 3 ? x / 3 : x);
 }
 // The block that has step x.
-__device__ __forceinline__ int block_of(int64_t x, int64_t total, int64_t blocks) {
-  return (int)((((uint64_t)x + 1) * (uint64_t)blocks - 1) / (uint64_t)total);
+__device__ __forceinline__ int block_of(int64_t x, int64_t total, const AttentionParams& p) {
+  return total < p.blocks ? (int)x : (int)((((uint64_t)x + 1) * (uint64_t)p.blocks - 1) / (uint64_t)total);
+}
+__device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
+  return (uint64_t)x >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
 }
 
 // ---------------------------------------------------------------------------
@@ -85,27 +92,36 @@ struct Tokens {  // what a wave reads of 32 tokens
 template <int D, int PARTS>
 struct Query {
   static constexpr int kSteps = D == 64 ? 1 : D / 128;
-  static constexpr int kWords = D == 64 ? 4 : 8;
-  uint32_t w[PARTS][kSteps][kWords];
-  uint32_t scale;  // the byte of part 0's
+  static constexpr int kHalves = D / 64;  // of 16 values a lane: 4 words
+  u32x4 w[PARTS][kHalves];
+  uint32_t scale;  // the bytes of the parts' scales
 };
 
+template <int D>
+struct QueryRow {  // a lane's 16 values of each 64
+  u32x4 v[D / 64][2];
+};
+template <int D>
+__device__ __forceinline__ void fetch_query(QueryRow<D>* out, const char* row, bool live, int g) {
+#pragma unroll
+  for (int h = 0; h < D / 64; ++h) {
+    const u32x4* at = reinterpret_cast<const u32x4*>(row + (64 * h + 16 * g) * 2);
+    out->v[h][0] = live ? at[0] : u32x4{0, 0, 0, 0};
+    out->v[h][1] = live ? at[1] : u32x4{0, 0, 0, 0};
+  }
+}
 template <int D, int DT, int PARTS>
-__device__ __forceinline__ void load_query(Query<D, PARTS>* out, const char* row, bool live, int g) {
+__device__ __forceinline__ void split_query(Query<D, PARTS>* out, const QueryRow<D>& in, bool turn) {
   constexpr int kHalves = D / 64;  // pieces of 16 values: (64 h + 16 g)
   float x[kHalves][16];
   uint32_t m = 0;
 #pragma unroll
   for (int h = 0; h < kHalves; ++h) {
-    if (live) {
-      Eight<DT> e[2];
-      e[0].load(row + (64 * h + 16 * g) * 2);
-      e[1].load(row + (64 * h + 16 * g + 8) * 2);
-      e[0].get(x[h]);
-      e[1].get(x[h] + 8);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[h][i] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+      Eight<DT> e;
+      e.w[0] = in.v[h][i];
+      e.get(x[h] + 8 * i);
     }
 #pragma unroll
     for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[h][i]) & 0x7fffffffu);
@@ -116,8 +132,8 @@ __device__ __forceinline__ void load_query(Query<D, PARTS>* out, const char* row
   // Rows that are not finite get the scale that stands for NaN.
   const int e = (int)(m >> 23) - 7;
   const int byte = m >= 0x7f800000u ? 255 : min(max(e, 16), 250);
-  out->scale = (uint32_t)byte;
-  const float up = __uint_as_float((uint32_t)(254 - (byte == 255 ? 127 : byte)) << 23);
+  out->scale = byte == 255 ? ~0u : (uint32_t)byte | (uint32_t)(byte - 5) << 8 | (uint32_t)(byte - 10) << 16;
+  const float up = __uint_as_float((uint32_t)(254 - (byte == 255 ? 127 : byte)) << 23 | (turn ? 0x80000000u : 0u));
 #pragma unroll
   for (int h = 0; h < kHalves; ++h)
 #pragma unroll
@@ -130,7 +146,7 @@ __device__ __forceinline__ void load_query(Query<D, PARTS>* out, const char* row
         int w = 0;
         w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], w, false);
         w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
-        out->w[q][h / 2][(h % 2) * 4 + i / 4] = (uint32_t)w;
+        out->w[q][h][i / 4] = (uint32_t)w;
         const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
         y[0] = (y[0] - a[0]) * 32.f;
         y[1] = (y[1] - a[1]) * 32.f;
@@ -140,32 +156,36 @@ __device__ __forceinline__ void load_query(Query<D, PARTS>* out, const char* row
     }
 }
 
-// Scores of tile u's 16 tokens for a tile of rows.
-template <int D, int PARTS>
-__device__ __forceinline__ f32x4 scores(const Tokens<D>& t, int u, const Query<D, PARTS>& q, int g) {
+// Scores of tile u's 16 tokens for a tile of rows.  `words(part, half)`: the
+// query's words.
+template <int D, int PARTS, typename W>
+__device__ __forceinline__ f32x4 scores(const Tokens<D>& t, int u, uint32_t scale, int g, const W& words) {
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  constexpr int kSteps = Query<D, PARTS>::kSteps;
+  constexpr int kSteps = D == 64 ? 1 : D / 128;
 #pragma unroll
   for (int part = PARTS - 1; part >= 0; --part) {  // the smallest first
-    const int sb = q.scale == 255 ? 255 : (int)q.scale - 5 * part;
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      // D = 64: one product's 128 values are two tiles' keys; the queries stand
-      // in the half of this tile, with zeros in the other
       const int at = D == 64 ? 0 : u * kSteps + s;
       const i32x8 a = {t.k[at][0], t.k[at][1], t.k[at][2], t.k[at][3], 0, 0, 0, 0};
-      const uint32_t* w = q.w[part][s];
-      i32x8 b;
       int sa = (int)t.ks[at];
+      u32x4 lo, hi;
       if constexpr (D == 64) {
-        if (g / 2 != u) sa = 127;  // the other tile's scales may be NaN, or too large for sums beside them
-        const i32x8 b0 = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-        const i32x8 b1 = {0, 0, 0, 0, (int)w[0], (int)w[1], (int)w[2], (int)w[3]};
-        b = u ? b1 : b0;
+        // one product's 128 values are two tiles' keys, beside the queries
+        // twice; the other tile's scales are made the smallest, 2^-127, beside
+        // which its products vanish (they may be NaN, or as large as any)
+        lo = hi = words(part, 0);
+        if (g / 2 != u) sa = 0;
       } else {
-        b = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], (int)w[4], (int)w[5], (int)w[6], (int)w[7]};
+        lo = words(part, 2 * s);
+        hi = words(part, 2 * s + 1);
       }
-      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, sa, 0, sb);
+      const i32x8 b = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+      switch (part) {  // byte `part` of the query's scales
+        case 0: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, sa, 0, (int)scale); break;
+        case 1: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, sa, 1, (int)scale); break;
+        default: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, sa, 2, (int)scale);
+      }
     }
   }
   return acc;
@@ -184,10 +204,17 @@ __device__ __forceinline__ uint32_t byte_pair(uint32_t w, float scale, int sel) 
   }
 }
 
+// The scale of token k of 4 from the word that holds their bytes, for a
+// conversion: it takes the exponent's bits alone, so the bits of the
+// neighbouring bytes may stand around them.
+__device__ __forceinline__ float scale_in(uint32_t w, int k) {
+  return __uint_as_float(k == 3 ? w >> 1 : w << (23 - 8 * k));
+}
+
 // Values 2j and 2j + 1 of the lane's sixteenth for its 8 tokens, as the A
 // operands of two products.
 template <int D>
-__device__ __forceinline__ void value_pair(const Tokens<D>& t, const float* scale, int j, u32x4* even, u32x4* odd) {
+__device__ __forceinline__ void value_pair(const Tokens<D>& t, const uint32_t* vs, int j, u32x4* even, u32x4* odd) {
   constexpr int kBytes = D / 32;  // of a token
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
@@ -196,313 +223,556 @@ __device__ __forceinline__ void value_pair(const Tokens<D>& t, const float* scal
       const int at0 = k * kBytes + j, at1 = at0 + kBytes;
       constexpr int kWordsOfTile = kBytes;  // 4 tokens x kBytes / 4
       const int w0 = u * kWordsOfTile + at0 / 4, w1 = u * kWordsOfTile + at1 / 4;
-      const uint32_t a = byte_pair(t.v[w0 / 4][w0 % 4], scale[4 * u + k], at0 % 4);
-      const uint32_t b = byte_pair(t.v[w1 / 4][w1 % 4], scale[4 * u + k + 1], at1 % 4);
+      const uint32_t a = byte_pair(t.v[w0 / 4][w0 % 4], scale_in(vs[u], k), at0 % 4);
+      const uint32_t b = byte_pair(t.v[w1 / 4][w1 % 4], scale_in(vs[u], k + 1), at1 % 4);
       (*even)[2 * u + k / 2] = __builtin_amdgcn_perm(b, a, 0x05040100u);
       (*odd)[2 * u + k / 2] = __builtin_amdgcn_perm(b, a, 0x07060302u);
     }
   }
 }
 
-// The state of a tile of rows in a wave.  m is the reference of the row's
-// exponentials (-inf: none yet), `base` what is subtracted (m, or 0).
+// The state of a tile of rows in a wave: `base` is the reference of the row's
+// exponentials, `limit` the score beyond which it moves (-inf: there is no
+// reference yet, base is 0).
 template <int D>
 struct Rows16 {
   f32x4 o[D / 16];
   f32x4 l;  // sums of the probabilities, the same in all four
-  float m, base;
+  float base, limit;
+  __device__ __forceinline__ float reference() const { return limit > kNegInf ? base : kNegInf; }
 };
 
-// ---------------------------------------------------------------------------
-// The tree: for each node of the group of rows its ancestors, as bits, and
-// each node's depth.
-// ---------------------------------------------------------------------------
-struct TreeShared {
-  int32_t parent[SV_MAX_N];
+// The kernel's arguments, read again from where they lie, and the thread's
+// number as if it were new: what a phase does not use is not kept in registers
+// through it, and nothing of one phase is formed ahead of another.
+__device__ __forceinline__ const AttentionParams& arguments() {
+  uint64_t u = (uint64_t)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(u));
+  return *(const AttentionParams*)(const __attribute__((address_space(4))) AttentionParams*)u;
+}
+__device__ __forceinline__ int thread() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+__device__ __forceinline__ uint32_t opaque(uint32_t x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+constexpr int kStaged = 1024;               // page numbers at a time, -1 for one that is none of the pool
+constexpr int kChunks = SV_MAX_N / 32 + 1;  // steps of 32 tokens that hold nodes
+
+// What the waves of a block share.  QUERY: words of queries kept here.
+template <int D, int ROWS, int QUERY>
+struct Shared {
+  static constexpr int kRows = ROWS;
+  union {
+    struct {  // while a segment is worked on
+      u32x4 q[QUERY ? QUERY : 1];  // queries of many rows (the waves' are the same)
+      uint32_t q_scale[QUERY ? ROWS / kTile * kWave : 1];
+      int32_t page[kStaged];
+      int32_t parent[SV_MAX_N];  // a tree's window
+    };
+    float o[kWaves][kTile][D + 4];  // as it ends
+  };
+  float m[kWaves][ROWS], l[kWaves][ROWS];
+  // trees: the nodes' depths, and what the group's rows see of the last tokens
+  // before the window and of its nodes: bit i of sees[r][k] stands for token
+  // 32 (len / 32 + k) + i
   int32_t depth[SV_MAX_N];
+  uint32_t sees[ROWS][kChunks];
+  int32_t pos[ROWS];   // the rows' positions
+  float slope[ROWS];   // and slopes, of exponents of 2
+  // where the block stands: steps of all, the next one, the last + 1, those
+  // before sequence b, and that sequence
+  int64_t scan[kWaves];
+  int64_t total, at, end, line, units;
+  int32_t b, len, news, u0;
+  int32_t open;  // whether the last item goes on in the next block
+  // the segment at hand
+  int32_t first, stop, h, group, slot, whole;
 };
 
-template <int D, int TILES, int DT>
-__global__ __launch_bounds__(kThreads, TILES * D <= 256 ? 2 : 1) void attention_kernel(const AttentionParams p) {
-  constexpr int kParts = DT == SV_F16 ? 3 : 2;
-  constexpr int kProbs = DT == SV_F16 ? 2 : 1;
-  constexpr int kRows = TILES * kTile;
-  constexpr int kStride = D + 4;
-  __shared__ __align__(16) float s_o[kWaves][kTile][kStride];
-  __shared__ float s_m[kWaves][kRows], s_l[kWaves][kRows];
-  __shared__ TreeShared s_tree;
-  __shared__ uint32_t s_bits[kRows][SV_MAX_N / 32];
-  __shared__ int64_t s_scan[kWaves];
-  __shared__ int64_t s_first[2];  // the block's first sequence, steps before it
-
-  const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int l = lane % 16, g = lane / 16;
+// All sequences' steps, and the place that the block begins in; false: none.
+template <typename S>
+__device__ __forceinline__ bool plan(const AttentionParams& p, S& sh) {
+  const int tid = thread(), lane = tid % kWave, wave = tid / kWave;
   const int64_t each = (int64_t)p.c.H * p.groups;  // items of a sequence
-  AttentionItem* const desc = static_cast<AttentionItem*>(p.desc);
-
-  // all sequences' steps, and the one this block begins in
   int64_t total = 0;
   for (int pass = 0; pass < 2; ++pass) {
-    int64_t before = 0;
-    int64_t begin = 0, blocks = 0;
+    int64_t before = 0, begin = 0;
     if (pass) {
-      blocks = min((int64_t)gridDim.x, total);
-      if ((int64_t)blockIdx.x >= blocks) break;
-      begin = start_of(blockIdx.x, total, blocks);
+      begin = start_of(blockIdx.x, total, p);
+      if (begin >= total) return false;
+      if (tid == 0) {
+        sh.total = total;
+        sh.at = begin;
+        sh.end = start_of(blockIdx.x + 1, total, p);
+        sh.open = 0;
+      }
     }
     for (int64_t b0 = 0; b0 < p.B; b0 += kThreads) {
       const int64_t b = b0 + tid;
+      Span s;
       int64_t mine = 0;
       if (b < p.B) {
-        const Span s = span_of(p, b);
+        s = span_of(p, b);
         mine = s.units * each;
         if (s.news < 0 && pass == 0 && blockIdx.x == 0) flag(p.err, SV_DERR_RANGE);
       }
       int64_t incl = mine;
+      if (p.B > 1) {
 #pragma unroll
-      for (int o = 1; o < kWave; o <<= 1) {
-        const int64_t up = __shfl_up(incl, o, kWave);
-        if (lane >= o) incl += up;
+        for (int o = 1; o < kWave; o <<= 1) {
+          const int64_t up = __shfl_up(incl, o, kWave);
+          if (lane >= o) incl += up;
+        }
       }
-      if (lane == kWave - 1) s_scan[wave] = incl;
+      if (p.B > 1 ? lane == kWave - 1 : tid == 0) sh.scan[wave] = incl;
       __syncthreads();
-      for (int w = 0; w < wave; ++w) incl += s_scan[w];
+      const int waves = min((int)((p.B - b0 + kWave - 1) / kWave), kWaves);
       int64_t sum = 0;
-      for (int w = 0; w < kWaves; ++w) sum += s_scan[w];
-      if (pass && mine && before + incl - mine <= begin && begin < before + incl) {
-        s_first[0] = b;
-        s_first[1] = before + incl - mine;
+      for (int w = 0; w < waves; ++w) {
+        if (w < wave) incl += sh.scan[w];
+        sum += sh.scan[w];
+      }
+      if (p.B <= kThreads) {  // one look is enough
+        total = sum;
+        begin = start_of(blockIdx.x, total, p);
+        if (begin >= total) return false;
+        if (tid == 0) {
+          sh.total = total;
+          sh.at = begin;
+          sh.end = start_of(blockIdx.x + 1, total, p);
+          sh.open = 0;
+        }
+      }
+      if ((pass || p.B <= kThreads) && mine && before + incl - mine <= begin && begin < before + incl) {
+        sh.b = (int32_t)b;
+        sh.line = before + incl - mine;
+        sh.units = s.units;
+        sh.len = s.len;
+        sh.news = s.news;
+        sh.u0 = (int32_t)s.u0;
       }
       before += sum;
       __syncthreads();
     }
     total = before;
+    if (p.B <= kThreads) return total > 0;
   }
-  const int64_t blocks = min((int64_t)gridDim.x, total);
-  if ((int64_t)blockIdx.x >= blocks) {
-    if (tid == 0) desc[blockIdx.x].b = -1;
+  return true;
+}
+
+// The next segment: the part of an item that the block does.
+template <typename S>
+__device__ __forceinline__ void segment(const AttentionParams& p, S& sh) {
+  if (thread() == 0) {
+    const int64_t each = (int64_t)p.c.H * p.groups;
+    const int64_t at = sh.at;
+    int64_t line = sh.line, units = sh.units;
+    if (at >= line + units * each) {
+      int b = sh.b;
+      Span span;
+      do {
+        line += units * each;
+        span = span_of(p, ++b);
+        units = span.units;
+      } while (at >= line + units * each);
+      sh.b = b;
+      sh.line = line;
+      sh.units = units;
+      sh.len = span.len;
+      sh.news = span.news;
+      sh.u0 = (int32_t)span.u0;
+    }
+    const int64_t item = divide(at - line, units), first = line + item * units;  // the item's first step
+    const int64_t last = first + units, stop = min(last, sh.end);
+    const int h = (int)((uint32_t)item / (uint32_t)p.groups), group = (int)item - h * p.groups;
+    const int slot = 2 * (int)blockIdx.x + (at == start_of(blockIdx.x, sh.total, p) ? 0 : 1);
+    sh.h = h;
+    sh.group = group;
+    sh.first = sh.u0 + (int)(at - first);
+    sh.stop = sh.u0 + (int)(stop - first);
+    sh.whole = at == first && stop == last;
+    sh.slot = slot;
+    sh.at = stop;
+    if (at == first && stop < last) {  // the item goes on: its first block describes it
+      AttentionItem d;
+      d.b = sh.b;
+      d.h = h;
+      d.group = group;
+      d.slot = slot;
+      d.last = last - 1;
+      d.total = sh.total;
+      static_cast<AttentionItem*>(p.desc)[blockIdx.x] = d;
+      sh.open = 1;
+    }
+  }
+  __syncthreads();
+}
+
+// What a tree's rows see, and the nodes' depths.
+template <typename S>
+__device__ __forceinline__ void tree(const AttentionParams& p, S& sh) {
+  constexpr int ROWS = S::kRows;
+  const int tid = thread(), len = sh.len, news = sh.news;
+  const int32_t* parent = p.parent + (int64_t)sh.b * p.N;
+  for (int i = tid; i < news; i += kThreads) {
+    const int32_t a = i ? parent[i] : -1;
+    const bool bad = i && (a < 0 || a >= i);
+    sh.parent[i] = bad ? -1 : a;
+    if (bad) flag(p.err, SV_DERR_TREE);
+  }
+  const int row0 = sh.group * ROWS, lead = len % 32;  // tokens of the first of these steps that stand before the window
+  const int chunks = (lead + news + 31) / 32;
+  for (int i = tid; i < ROWS * chunks; i += kThreads) {
+    const int r = i / chunks, k = i - r * chunks;
+    sh.sees[r][k] = k == 0 && (row0 + r) / p.G < news ? (1u << lead) - 1 : 0u;
+  }
+  __syncthreads();
+  for (int i = tid; i < news; i += kThreads) {
+    int d = 0;
+    for (int n = sh.parent[i]; n >= 0; n = sh.parent[n]) ++d;
+    sh.depth[i] = d;
+  }
+  for (int r = tid; r < ROWS; r += kThreads) {
+    const int n = (row0 + r) / p.G;
+    if (n < news) {
+      int most = p.reach > 0 ? p.reach : SV_MAX_N + 1;
+      for (int a = n; a >= 0 && most > 0; a = sh.parent[a], --most)
+        sh.sees[r][(lead + a) / 32] |= 1u << ((lead + a) % 32);
+    }
+  }
+  __syncthreads();
+}
+
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
+
+// What a part's sums count beside others whose largest reference is m.  A part
+// that saw nothing has zeros, or NaN, which stay NaN.
+__device__ __forceinline__ float part_weight(float own, float m) {
+  return own > kNegInf ? __builtin_amdgcn_exp2f(own - m) : (m > kNegInf ? 0.f : 1.f);
+}
+
+// The largest of three, NaN aside; one instruction (fmaxf first quiets each of
+// its operands).
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
+// COUNT (4, 8 or 16) of a row's sums from `col` on, and its statistics, as
+// output: o / l, and the logarithm of the sum of e^s.  Biases are held relative
+// to the root's distances.
+template <int D, int DT, int COUNT>
+__device__ __forceinline__ void finish(const AttentionParams& p, int b, int n, int head, int col, const float* o, float m,
+                                       float l, int depth) {
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  char* out = p.out + b * p.os[0] + n * p.os[1] + head * p.os[2] + col * 2;
+#pragma unroll
+  for (int i = 0; i < COUNT; i += 4) {
+    uint64_t w = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float y = l == 0.f ? 0.f : o[i + k] * inv;
+      const uint16_t e = DT == SV_F16 ? __builtin_bit_cast(uint16_t, (_Float16)y) : __builtin_bit_cast(uint16_t, (__bf16)y);
+      w |= (uint64_t)e << (16 * k);
+    }
+    *reinterpret_cast<uint64_t*>(out + i * 2) = w;
+  }
+  if (p.lse && col == 0) {
+    float x = l == 0.f ? kNegInf : ((m > kNegInf ? m : 0.f) + __builtin_amdgcn_logf(l)) / kLog2e;
+    if (p.slopes) x -= p.slopes[head] * (float)depth;
+    p.lse[((int64_t)b * p.N + n) * p.Hq + head] = x;
+  }
+}
+
+// Waves of a SIMD that the registers leave room for: one tile of rows takes up
+// to 128 registers at D = 64, 168 at 128 and 256 at 256; more waves count for
+// more than a few registers spilled (D = 128, four tiles: 325 us of 1024 nodes
+// with 2 waves and 36 registers spilled, 400 with 1), but not for a hundred
+// (D = 256, two tiles: 290 us with 1 wave, 510 with 2).
+constexpr int kernel_waves(int D, int tiles) {
+  return tiles == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : tiles * D <= 256 || D < 256 ? 2 : 1;
+}
+
+template <int D, int TILES, int DT>
+__global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_kernel(const AttentionParams) {
+  constexpr int kParts = DT == SV_F16 ? 3 : 2;
+  constexpr int kProbs = DT == SV_F16 ? 2 : 1;
+  constexpr int kRows = TILES * kTile;
+  constexpr bool kQueryLds = TILES * D > 256 || TILES > 2;
+  constexpr int kHalves = Query<D, kParts>::kHalves;
+  __shared__ __align__(16) Shared<D, kRows, kQueryLds ? TILES * kParts * kHalves * kWave : 0> sh;
+
+  if (!plan(arguments(), sh)) {
+    if (threadIdx.x == 0) static_cast<AttentionItem*>(arguments().desc)[blockIdx.x].b = -1;
     return;
   }
-  const int64_t begin = start_of(blockIdx.x, total, blocks), end = start_of(blockIdx.x + 1, total, blocks);
-  int64_t b = s_first[0], line = s_first[1];  // steps before sequence b
-  int64_t at = begin;
-  Span span = span_of(p, b);
-  bool open = false;  // whether the last item goes on in the next block
-
-  while (at < end) {
-    while (at >= line + span.units * each) {
-      line += span.units * each;
-      span = span_of(p, ++b);
-    }
-    const int64_t item = (at - line) / span.units;
-    const int64_t first = line + item * span.units;  // the item's first step
-    const int64_t stop = min(first + span.units, end);
-    const int h = (int)(item / p.groups), group = (int)(item % p.groups);
-    const int64_t u0 = span.u0 + (at - first), u1 = span.u0 + (stop - first);
-    const bool whole = at == first && stop == first + span.units;
-    const int slot = 2 * (int)blockIdx.x + (at == begin ? 0 : 1);
-    const int len = span.len, news = span.news;
+  bool more;
+  do {
+    segment(arguments(), sh);
+    const int len = uniform(sh.len), news = uniform(sh.news);
     const int hi = len + news;  // tokens and nodes
-    const int row0 = group * kRows;
+    const int u0 = uniform(sh.first), u1 = uniform(sh.stop);
 
     // ---- the rows
-    __syncthreads();
-    const int node0 = row0 / p.G;  // first node of the group
-    const int nodes = min((row0 + kRows - 1) / p.G, p.N - 1) - node0 + 1;
-    if (p.parent) {
-      const int32_t* parent = p.parent + b * p.N;
-      for (int i = tid; i < news; i += kThreads) s_tree.parent[i] = i ? parent[i] : -1;
-      for (int i = tid; i < nodes * (SV_MAX_N / 32); i += kThreads) (&s_bits[0][0])[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < news; i += kThreads) {
-        int n = i, d = 0;
-        bool bad = false;
-        for (;;) {
-          const int up = s_tree.parent[n];
-          if (n == 0) break;
-          if (up < 0 || up >= n) {
-            bad = true;
-            break;
-          }
-          n = up;
-          ++d;
-        }
-        if (bad) flag(p.err, SV_DERR_TREE);
-        s_tree.depth[i] = d;
-        if (i >= node0 && i < node0 + nodes) {
-          uint32_t* bits = s_bits[i - node0];
-          int a = i;
-          for (int k = 0; k <= d; ++k) {
-            bits[a / 32] |= 1u << (a % 32);
-            a = a ? s_tree.parent[a] : 0;
-          }
+    u32x4 q[kQueryLds ? 1 : TILES][kParts][kHalves];
+    uint32_t q_scale[kQueryLds ? 1 : TILES];
+    Rows16<D> rows[TILES];
+    {
+      const AttentionParams& p = arguments();
+      const int tid = thread(), lane = tid % kWave, wave = uniform(tid / kWave), l = lane % 16, g = lane / 16;
+      const char* const q_at = p.q + sh.b * p.qs[0];
+      const auto query = [&](int t, QueryRow<D>* out) {
+        const int row = sh.group * kRows + t * kTile + l;
+        const int n = row / p.G, head = sh.h * p.G + row - n * p.G;
+        fetch_query<D>(out, q_at + n * p.qs[1] + head * p.qs[2], n < news, g);
+      };
+      constexpr int kMine = kQueryLds ? (TILES + kWaves - 1) / kWaves : TILES;
+      QueryRow<D> in[kMine];
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int t = kQueryLds ? wave + i * kWaves : i;
+        if (t < TILES) query(t, &in[i]);
+      }
+      if (p.parent && (u1 * kAttentionUnit > len / 32 * 32 || p.reach > 0)) tree(p, sh);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int t = kQueryLds ? wave + i * kWaves : i;
+        if (t < TILES) {
+          Query<D, kParts> mine;
+          split_query<D, DT, kParts>(&mine, in[i], p.scale < 0.f);
+#pragma unroll
+          for (int part = 0; part < kParts; ++part)
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+              if constexpr (kQueryLds)
+                sh.q[((t * kParts + part) * kHalves + h) * kWave + lane] = mine.w[part][h];
+              else
+                q[i][part][h] = mine.w[part][h];
+            }
+          if constexpr (kQueryLds)
+            sh.q_scale[t * kWave + lane] = mine.scale;
+          else
+            q_scale[i] = mine.scale;
         }
       }
-      __syncthreads();
-    }
-    Query<D, kParts> q[TILES];
-    Rows16<D> rows[TILES];
-    int node[TILES], pos[TILES];
-    float slope[TILES];
+      if (tid < kRows) {
+        const int row = sh.group * kRows + tid;
+        const int n = row / p.G, head = sh.h * p.G + row - n * p.G;
+        const bool live = n < news;
+        sh.pos[tid] = len + (!live ? 0 : p.parent && p.reach > 0 ? sh.depth[n] : n);
+        sh.slope[tid] = live && p.slopes ? p.slopes[head] * kLog2e : 0.f;
+      }
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      const int row = row0 + t * kTile + l;
-      const int n = row / p.G, head = h * p.G + row % p.G;
-      const bool live = n < news;
-      node[t] = live ? n : -1;
-      pos[t] = len + (live ? (p.parent ? s_tree.depth[n] : n) : 0);
-      slope[t] = live && p.slopes ? p.slopes[head] * kLog2e : 0.f;
-      load_query<D, DT, kParts>(&q[t], p.q + b * p.qs[0] + n * p.qs[1] + head * p.qs[2], live, g);
+      for (int t = 0; t < TILES; ++t) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) rows[t].o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      rows[t].l = f32x4{0.f, 0.f, 0.f, 0.f};
-      rows[t].m = kNegInf;
-      rows[t].base = 0.f;
+        for (int i = 0; i < D / 16; ++i) rows[t].o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        rows[t].l = f32x4{0.f, 0.f, 0.f, 0.f};
+        rows[t].limit = kNegInf;
+        rows[t].base = 0.f;
+      }
     }
 
     // ---- the tokens
-    const int32_t* pages = p.c.pages + b * p.c.max_pages;
-    const int64_t in_page = ((int64_t)1 << p.c.pshift) - 1;
+    const AttentionParams& p = arguments();
+    const int tid = thread(), lane = tid % kWave, wave = uniform(tid / kWave), l = lane % 16, g = lane / 16;
+    // Scores are held as exponents of 2: s * unit, with s the product, or (bent)
+    // already so where a cap, a bias or a scale of 0 comes first.  A negative
+    // scale has turned the queries.
+    const float c = fabsf(p.scale) * kLog2e;
+    const bool bent = p.cap > 0.f || p.slopes || c == 0.f;
+    const float unit = bent ? 1.f : c, per_unit = 1.f / unit;
+    const bool is_tree = p.parent != nullptr;
+    const int reach = p.reach;
+    const char* const pool = p.c.pool + uniform(sh.h) * p.c.head;
+    const int64_t page_stride = p.c.page_stride;
+    const int pshift = p.c.pshift, in_page = (1 << pshift) - 1;
+    const uint32_t off_ks = (uint32_t)p.c.ks, off_vc = (uint32_t)p.c.vc, off_vs = (uint32_t)p.c.vs;
     const int last_tile = (hi - 1) / kTile * kTile;
-    const auto page_at = [&](int64_t token) {
-      return __builtin_amdgcn_readfirstlane(pages[token >> p.c.pshift]);
-    };
-    const auto tile_at = [&](int64_t u, int tile) {
-      return (int)min(u * kAttentionUnit + wave * kWaveTokens + tile * kTile, (int64_t)last_tile);
-    };
-    const auto fetch = [&](int64_t u, Tokens<D>* t, int* bad) {
-      *bad = 0;
+    int page0 = 0;  // page that sh.page[0] stands for
+    // Offsets of a lane within a tile: 32 bits beside a wave's base address.
+    const uint32_t lane_k = D == 64 ? l * (D / 2) + (g % 2) * 16 : l * (D / 2) + g * 16;
+    const uint32_t lane_ks = D == 64 ? l * (D / 32) + g % 2 : l * (D / 32) + g;
+    const uint32_t lane_v = (g * 16 + l) * (D / 8), lane_vs = (g * (D / 32) + l * (D / 16) / 32) * 4;
+    const auto fetch = [&](int u, Tokens<D>* t) {
       const char* base[2];
-      int64_t s[2];
+      uint32_t s[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int tt = tile_at(u, i);
-        int id = page_at(tt);
-        if ((uint32_t)id >= (uint32_t)p.c.num_pages) {
-          id = 0;
-          *bad |= 1 << i;
-        }
-        base[i] = p.c.pool + id * p.c.page_stride + h * p.c.head;
-        s[i] = tt & in_page;
+        const int tt = min(u * kAttentionUnit + wave * kWaveTokens + i * kTile, last_tile);
+        const int id = max(uniform(sh.page[(tt >> pshift) - page0]), 0);
+        base[i] = pool + id * page_stride;
+        s[i] = (uint32_t)(tt & in_page);
       }
+      const uint32_t at_k = opaque(lane_k), at_ks = opaque(lane_ks), at_v = opaque(lane_v), at_vs = opaque(lane_vs);
       if constexpr (D == 64) {
-        const int i = g / 2;
-        const char* kb = i ? base[1] : base[0];
-        const int64_t row = (i ? s[1] : s[0]) + l;
-        t->k[0] = *reinterpret_cast<const i32x4*>(kb + row * (D / 2) + (g % 2) * 16);
-        t->ks[0] = (uint8_t)kb[p.c.ks + row * (D / 32) + g % 2];
+        const char* k0 = base[0] + s[0] * (D / 2);
+        const char* k1 = base[1] + s[1] * (D / 2);
+        t->k[0] = *reinterpret_cast<const i32x4*>((g / 2 ? k1 : k0) + at_k);
+        const char* s0 = base[0] + off_ks + s[0] * (D / 32);
+        const char* s1 = base[1] + off_ks + s[1] * (D / 32);
+        t->ks[0] = (uint8_t)(g / 2 ? s1 : s0)[at_ks];
       } else {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int k = 0; k < D / 128; ++k) {
-            t->k[i * (D / 128) + k] = *reinterpret_cast<const i32x4*>(base[i] + (s[i] + l) * (D / 2) + k * 64 + g * 16);
-            t->ks[i * (D / 128) + k] = (uint8_t)base[i][p.c.ks + (s[i] + l) * (D / 32) + k * 4 + g];
+            t->k[i * (D / 128) + k] = *reinterpret_cast<const i32x4*>(base[i] + s[i] * (D / 2) + k * 64 + at_k);
+            t->ks[i * (D / 128) + k] = (uint8_t)(base[i] + off_ks + s[i] * (D / 32) + k * 4)[at_ks];
           }
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const char* vb = base[i] + p.c.vc + ((s[i] / 4 + g) * 16 + l) * (D / 8);
+        const char* vb = base[i] + off_vc + s[i] * (D / 2);
         if constexpr (D == 64) {
-          const uint64_t w = *reinterpret_cast<const uint64_t*>(vb);
+          const uint64_t w = *reinterpret_cast<const uint64_t*>(vb + at_v);
           t->v[0][2 * i] = (uint32_t)w;
           t->v[0][2 * i + 1] = (uint32_t)(w >> 32);
         } else {
 #pragma unroll
-          for (int k = 0; k < D / 128; ++k) t->v[i * (D / 128) + k] = reinterpret_cast<const u32x4*>(vb)[k];
+          for (int k = 0; k < D / 128; ++k) t->v[i * (D / 128) + k] = *reinterpret_cast<const u32x4*>(vb + k * 16 + at_v);
         }
-        t->vs[i] = *reinterpret_cast<const uint32_t*>(base[i] + p.c.vs +
-                                                      ((s[i] / 4 + g) * (D / 32) + l * (D / 16) / 32) * 4);
+        t->vs[i] = *reinterpret_cast<const uint32_t*>(base[i] + off_vs + s[i] * (D / 32) + at_vs);
       }
     };
 
-    const auto step = [&](int64_t u, Tokens<D>& t, int bad) {
-      const int t0 = (int)(u * kAttentionUnit) + wave * kWaveTokens;
+    // One step of a wave: 32 tokens.  `masked`: some row may not see some of them.
+    const auto step = [&](int u, const Tokens<D>& t, bool masked) {
+      const int t0 = u * kAttentionUnit + wave * kWaveTokens;
       if (t0 >= hi) return;
-      if (bad && lane == 0) flag(p.err, SV_DERR_RANGE);
-      // some row does not see some of these tokens
-      const bool partial = bad || t0 + kWaveTokens > len || (p.reach > 0 && t0 <= hi - 1 - p.reach);
-      float scale[8];
+      if (kQueryLds) asm volatile("" ::: "memory");  // the queries are read where they are used
+      masked = masked || t0 + kWaveTokens > len || (reach > 0 && t0 <= hi - 1 - reach);
+      uint32_t vs[2] = {t.vs[0], t.vs[1]};
+      uint32_t gone = 0;  // tokens without a page
       bool nan = false;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t s = (t.vs[i / 4] >> (8 * (i % 4))) & 255u;
-        // beyond the largest scale there is only NaN, and bytes never written,
+      if (masked) {
+        // Beyond the largest scale there is only NaN, and bytes never written,
         // whose values may overflow: they are added where they are seen
-        nan = nan || s > 252;
-        if (partial && s > 252) s = 127;
-        scale[i] = scale_of(s);
-      }
-      nan = partial && __any(nan);
-      u32x4 pr[TILES][kProbs];
-      uint32_t seen[TILES];  // bit i: row l sees token i of the lane's 8
 #pragma unroll
-      for (int r = 0; r < TILES; ++r) {
-        float x[8];
+        for (int i = 0; i < 8; ++i)
+          if ((vs[i / 4] >> (8 * (i % 4)) & 255u) > 252u) {
+            nan = true;
+            vs[i / 4] &= ~(255u << (8 * (i % 4)));
+          }
+        nan = __any(nan);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (sh.page[(min(t0 + i * kTile, last_tile) >> pshift) - page0] < 0) gone |= 0xffffu << (16 * i);
+      }
+      // what row l of tile r sees of the lane's tokens: bits 0 .. 3 and 16 .. 19
+      const auto seen = [&](int r) {
+        uint32_t w = ~gone;
+        const int pos = sh.pos[r * kTile + l];
+        if (t0 + kWaveTokens > len)
+          w &= is_tree ? sh.sees[r * kTile + l][t0 / 32 - len / 32] : bits_below(pos + 1 - t0);
+        // (a node's place is no lower than its position: what this lets through of a tree is masked above)
+        if (reach > 0) w &= ~bits_below(pos - reach + 1 - t0);
+        return w >> (4 * g);
+      };
+      float x[TILES][8];
+#pragma unroll
+      for (int r = 0; r < TILES; ++r)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const f32x4 s = scores<D, kParts>(t, i, q[r], g);
+          uint32_t qs;
+          if constexpr (kQueryLds)
+            qs = sh.q_scale[r * kWave + lane];
+          else
+            qs = q_scale[r];
+          const f32x4 s = scores<D, kParts>(t, i, qs, g, [&](int part, int h) {
+            if constexpr (kQueryLds)
+              return sh.q[((r * kParts + part) * kHalves + h) * kWave + lane];
+            else
+              return q[r][part][h];
+          });
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[4 * i + k] = s[k] * p.scale;
+          for (int k = 0; k < 4; ++k) x[r][4 * i + k] = s[k];
         }
-        if (p.cap > 0.f) {
+      if (bent) {
+        const AttentionParams& a = arguments();
+        const float cap = a.cap * kLog2e, up = 2.f / a.cap;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            // cap tanh(s / cap) = cap (1 - 2 / (1 + e^(2 s / cap)))
-            const float e = __builtin_amdgcn_exp2f(x[i] * (2.f * kLog2e / p.cap));
-            x[i] = p.cap - 2.f * p.cap * __builtin_amdgcn_rcpf(1.f + e);
+        for (int r = 0; r < TILES; ++r) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[r][i] *= c;
+          if (a.cap > 0.f) {  // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              x[r][i] = fmaf(-2.f * cap, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[r][i] * up)), cap);
           }
         }
+        if (a.slopes) {  // relative to the root's distances, which all of a row's scores share
+          const int t1 = t0 + 4 * g - len;
+          float d[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= kLog2e;
-        seen[r] = 0xffu;
-        if (partial || p.slopes) {
+          for (int i = 0; i < 8; ++i) d[i] = (float)(t1 + (i / 4) * kTile + i % 4);
+          if (is_tree && t0 + kWaveTokens > len) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int tok = t0 + (i / 4) * kTile + 4 * g + i % 4;
-            const int j = tok - len;  // node of the window, if not before it
-            int at_pos = tok;
-            bool see = node[r] >= 0 && tok < hi && !(bad >> (i / 4) & 1);
-            if (see && j >= 0) {
-              if (p.parent) {
-                see = s_bits[node[r] - node0][j / 32] >> (j % 32) & 1;
-                at_pos = len + s_tree.depth[j];
-              } else {
-                see = j <= node[r];
-              }
-            }
-            const int d = pos[r] - at_pos;
-            if (p.reach > 0) see = see && d < p.reach;
-            x[i] -= slope[r] * (float)d;
-            if (!see) {
-              x[i] = kNegInf;
-              seen[r] &= ~(1u << i);
+            for (int i = 0; i < 8; ++i) {
+              const int at = t1 + (i / 4) * kTile + i % 4;
+              if (at >= 0 && at < news) d[i] = (float)sh.depth[at];
             }
           }
-        }
-        float top = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-        // A new reference only where a row's scores pass the old one by 2^8:
-        // probabilities up to that are as exact
-        if (__any(top > rows[r].m + 8.f)) {
-          top = fmaxf(top, __shfl_xor(top, 16, kWave));
-          top = fmaxf(top, __shfl_xor(top, 32, kWave));
-          const float m = fmaxf(rows[r].m, top);
-          const float base = m > kNegInf ? m : 0.f;
-          const float f = __builtin_amdgcn_exp2f(rows[r].m - base);
-          rows[r].m = m;
-          rows[r].base = base;
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) rows[r].o[i] *= f;
-          rows[r].l *= f;
-        }
+          for (int r = 0; r < TILES; ++r) {
+            const float slope = sh.slope[r * kTile + l];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __builtin_amdgcn_exp2f(x[i] - rows[r].base);
+            for (int i = 0; i < 8; ++i) x[r][i] = fmaf(slope, d[i], x[r][i]);
+          }
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int r = 0; r < TILES; ++r) {
+          const uint32_t w = seen(r);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[r][i] = w >> (16 * (i / 4) + i % 4) & 1 ? x[r][i] : kNegInf;
+        }
+      }
+      // New references only where a row's scores pass the old one by 2^8:
+      // probabilities up to that are as exact
+      float top[TILES];
+      bool move = false;
+#pragma unroll
+      for (int r = 0; r < TILES; ++r) {
+        top[r] = max3(max3(x[r][0], x[r][1], x[r][2]), x[r][3], max3(x[r][4], x[r][5], max3(x[r][6], x[r][7], x[r][7])));
+        move = move || top[r] > rows[r].limit;
+      }
+      if (__any(move)) {
+#pragma unroll
+        for (int r = 0; r < TILES; ++r) {
+          float m = fmaxf(top[r], __shfl_xor(top[r], 16, kWave));
+          m = fmaxf(m, __shfl_xor(m, 32, kWave)) * unit;
+          const float old = rows[r].reference();
+          m = fmaxf(old, m);
+          if (m > kNegInf) {
+            const float f = __builtin_amdgcn_exp2f(old - m);
+            rows[r].base = m;
+            rows[r].limit = (m + 8.f) * per_unit;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) rows[r].o[i] *= f;
+            rows[r].l *= f;
+          }
+        }
+      }
+      u32x4 pr[TILES][kProbs];
+#pragma unroll
+      for (int r = 0; r < TILES; ++r) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[r][i] = __builtin_amdgcn_exp2f(fmaf(x[r][i], unit, -rows[r].base));
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          pr[r][0][i] = pack_bf16(x[2 * i], x[2 * i + 1]);
+          pr[r][0][i] = pack_bf16(x[r][2 * i], x[r][2 * i + 1]);
           if constexpr (kProbs == 2) {
-            const float lo = x[2 * i] - __uint_as_float(pr[r][0][i] << 16);
-            const float up = x[2 * i + 1] - __uint_as_float(pr[r][0][i] & 0xffff0000u);
+            const float lo = x[r][2 * i] - __uint_as_float(pr[r][0][i] << 16);
+            const float up = x[r][2 * i + 1] - __uint_as_float(pr[r][0][i] & 0xffff0000u);
             pr[r][1][i] = pack_bf16(lo, up);
           }
         }
@@ -511,21 +781,21 @@ __global__ __launch_bounds__(kThreads, TILES * D <= 256 ? 2 : 1) void attention_
 #pragma unroll
       for (int r = 0; r < TILES; ++r)
 #pragma unroll
-        for (int c = kProbs - 1; c >= 0; --c)
+        for (int e = kProbs - 1; e >= 0; --e)
           rows[r].l = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones),
-                                                              __builtin_bit_cast(bf16x8, pr[r][c]), rows[r].l, 0, 0, 0);
+                                                              __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].l, 0, 0, 0);
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         u32x4 va, vb;
-        value_pair<D>(t, scale, j, &va, &vb);
+        value_pair<D>(t, vs, j, &va, &vb);
 #pragma unroll
         for (int r = 0; r < TILES; ++r)
 #pragma unroll
-          for (int c = kProbs - 1; c >= 0; --c) {
+          for (int e = kProbs - 1; e >= 0; --e) {
             rows[r].o[2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, va), __builtin_bit_cast(bf16x8, pr[r][c]), rows[r].o[2 * j], 0, 0, 0);
+                __builtin_bit_cast(bf16x8, va), __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].o[2 * j], 0, 0, 0);
             rows[r].o[2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, vb), __builtin_bit_cast(bf16x8, pr[r][c]), rows[r].o[2 * j + 1], 0, 0, 0);
+                __builtin_bit_cast(bf16x8, vb), __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].o[2 * j + 1], 0, 0, 0);
           }
       }
       if (nan) {
@@ -534,13 +804,14 @@ __global__ __launch_bounds__(kThreads, TILES * D <= 256 ? 2 : 1) void attention_
         u32x4 va = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          if (((t.vs[i / 4] >> (8 * (i % 4))) & 255u) > 252) va[i / 2] |= 0x3f80u << (16 * (i % 2));
+          if ((t.vs[i / 4] >> (8 * (i % 4)) & 255u) > 252u) va[i / 2] |= 0x3f80u << (16 * (i % 2));
 #pragma unroll
         for (int r = 0; r < TILES; ++r) {
+          const uint32_t w = seen(r);
           u32x4 vb = {0, 0, 0, 0};
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (seen[r] >> i & 1) vb[i / 2] |= 0x3f80u << (16 * (i % 2));
+            if (w >> (16 * (i / 4) + i % 4) & 1) vb[i / 2] |= 0x3f80u << (16 * (i % 2));
           const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
           const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, va),
                                                                     __builtin_bit_cast(bf16x8, vb), zero, 0, 0, 0);
@@ -555,163 +826,232 @@ __global__ __launch_bounds__(kThreads, TILES * D <= 256 ? 2 : 1) void attention_
     };
 
     {
-      Tokens<D> now, next;
-      int bad, bad_next = 0;
-      fetch(u0, &now, &bad);
-      for (int64_t u = u0; u < u1; ++u) {
-        if (u + 1 < u1) fetch(u + 1, &next, &bad_next);
-        step(u, now, bad);
-        now = next;
-        bad = bad_next;
+      const int at_once = min(kStaged << min(pshift, 12) >> 7, 1 << 15);  // steps whose pages are staged
+      for (int v0 = u0; v0 < u1; v0 += at_once) {
+        const int v1 = min(v0 + at_once, u1);
+        page0 = v0 * kAttentionUnit >> pshift;
+        bool lost = false;
+        {
+          const AttentionParams& a = arguments();
+          const int32_t* pages = a.c.pages + (int64_t)sh.b * a.c.max_pages + page0;
+          const int staged = (min(v1 * kAttentionUnit - 1, last_tile) >> pshift) - page0 + 1;
+          if (v0 > u0) __syncthreads();  // (the first time, a segment's end was one)
+          for (int i = thread(); i < staged; i += kThreads) {
+            const int32_t id = pages[i];
+            const bool bad = (uint32_t)id >= (uint32_t)a.c.num_pages;
+            lost = lost || bad;
+            sh.page[i] = bad ? -1 : id;
+          }
+          if (lost) flag(a.err, SV_DERR_RANGE);
+          lost = __syncthreads_or(lost);
+        }
+        // The next step's loads fly while this one is worked on; behind the last
+        // it is read again, so that the number of loads in flight is known.
+        Tokens<D> even, odd;
+        fetch(v0, &even);
+        for (int u = v0;;) {
+          fetch(min(u + 1, v1 - 1), &odd);
+          step(u, even, lost);
+          if (++u >= v1) break;
+          fetch(min(u + 1, v1 - 1), &even);
+          step(u, odd, lost);
+          if (++u >= v1) break;
+        }
       }
     }
 
     // ---- the waves' sums together, a tile of rows at a time
+    {
+      const AttentionParams& a = arguments();
+      const int id = thread(), wave = uniform(id / kWave), l = id % 16, g = id % kWave / 16;
+      const int b = sh.b, row0 = sh.group * kRows, slot = sh.slot;
+      const bool whole = sh.whole;
+      more = sh.at < sh.end;  // read ahead of the barriers behind which the next segment is planned
 #pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      if (g == 0) {
-        s_m[wave][t * kTile + l] = rows[t].m;
-        s_l[wave][t * kTile + l] = rows[t].l[0];
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int t = 0; t < TILES; ++t) {
-      float m = kNegInf;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) m = fmaxf(m, s_m[w][t * kTile + l]);
-      const float f = rows[t].m > kNegInf ? __builtin_amdgcn_exp2f(rows[t].m - m) : (m > kNegInf ? 0.f : 1.f);
-      // NaN scores leave m at -inf: their sums are NaN, times anything
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int i = 0; i < D / 16; i += 4) {
-          const f32x4 v = {rows[t].o[i][k] * f, rows[t].o[i + 1][k] * f, rows[t].o[i + 2][k] * f, rows[t].o[i + 3][k] * f};
-          *reinterpret_cast<f32x4*>(&s_o[wave][l][(4 * g + k) * (D / 16) + i]) = v;
+      for (int t = 0; t < TILES; ++t) {
+        if (g == 0) {
+          sh.m[wave][t * kTile + l] = rows[t].reference();
+          sh.l[wave][t * kTile + l] = rows[t].l[0];
         }
+      }
       __syncthreads();
-      // a row to 16 threads, D/16 neighbouring values each
-      const int r = tid / 16, c = tid % 16;
-      const int rr = t * kTile + r, row = row0 + rr;
-      const int n = row / p.G, head = h * p.G + row % p.G;
-      float mm = kNegInf, ll = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, s_m[w][rr]);
+      for (int t = 0; t < TILES; ++t) {
+        float m = kNegInf;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) {
-        const float mw = s_m[w][rr];
-        ll += s_l[w][rr] * (mw > kNegInf ? __builtin_amdgcn_exp2f(mw - mm) : (mm > kNegInf ? 0.f : 1.f));
-      }
-      float o[D / 16];
+        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sh.m[w][t * kTile + l]);
+        // NaN scores leave m at -inf: their sums are NaN, times anything
+        const float f = part_weight(rows[t].reference(), m);
 #pragma unroll
-      for (int i = 0; i < D / 16; i += 4) {
-        f32x4 v = *reinterpret_cast<const f32x4*>(&s_o[0][r][c * (D / 16) + i]);
+        for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(&s_o[w][r][c * (D / 16) + i]);
+          for (int i = 0; i < D / 16; i += 4) {
+            const f32x4 v = {rows[t].o[i][k] * f, rows[t].o[i + 1][k] * f, rows[t].o[i + 2][k] * f, rows[t].o[i + 3][k] * f};
+            *reinterpret_cast<f32x4*>(&sh.o[wave][l][(4 * g + k) * (D / 16) + i]) = v;
+          }
+        __syncthreads();
+        // a row to 16 threads, D/16 neighbouring values each
+        const int r = id / 16, col = id % 16;
+        const int rr = t * kTile + r, row = row0 + rr;
+        const int n = row / a.G, head = sh.h * a.G + row - n * a.G;
+        if (n < sh.news) {
+          float mm = kNegInf, ll = 0.f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[i + k] = v[k];
-      }
-      if (whole) {
-        if (n < news) {
-          const float inv = ll == 0.f ? 0.f : 1.f / ll;
+          for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, sh.m[w][rr]);
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) o[i] = ll == 0.f ? 0.f : o[i] * inv;
-          char* out = p.out + b * p.os[0] + n * p.os[1] + head * p.os[2] + c * (D / 16) * 2;
-          if constexpr (D == 64) {
-            uint64_t w = 0;
+          for (int w = 0; w < kWaves; ++w) {
+            const float mw = sh.m[w][rr];
+            ll += sh.l[w][rr] * part_weight(mw, mm);
+          }
+          float o[D / 16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint16_t e = DT == SV_F16 ? __builtin_bit_cast(uint16_t, (_Float16)o[i])
-                                              : __builtin_bit_cast(uint16_t, (__bf16)o[i]);
-              w |= (uint64_t)e << (16 * i);
-            }
-            *reinterpret_cast<uint64_t*>(out) = w;
+          for (int i = 0; i < D / 16; i += 4) {
+            f32x4 v = *reinterpret_cast<const f32x4*>(&sh.o[0][r][col * (D / 16) + i]);
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(&sh.o[w][r][col * (D / 16) + i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i + k] = v[k];
+          }
+          if (whole) {
+            finish<D, DT, D / 16>(a, b, n, head, col * (D / 16), o, mm, ll, a.parent ? sh.depth[n] : n);
           } else {
+            float* po = a.part_o + ((int64_t)slot * kRows + rr) * D + col * (D / 16);
 #pragma unroll
-            for (int i = 0; i < D / 16; i += 8) {
-              Eight<DT> e;
-              e.set(o + i);
-              *reinterpret_cast<u32x4*>(out + i * 2) = e.w[0];
+            for (int i = 0; i < D / 16; i += 4)
+              *reinterpret_cast<f32x4*>(po + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+            if (col == 0) {
+              a.part_ml[((int64_t)slot * kRows + rr) * 2] = mm;
+              a.part_ml[((int64_t)slot * kRows + rr) * 2 + 1] = ll;
             }
           }
-          if (p.lse && c == 0)
-            p.lse[((int64_t)b * p.N + n) * p.Hq + head] =
-                ll == 0.f ? kNegInf : (mm > kNegInf ? mm : 0.f) / kLog2e + __builtin_amdgcn_logf(ll) / kLog2e;
         }
-      } else {
-        float* po = p.part_o + ((int64_t)slot * kRows + rr) * D + c * (D / 16);
-#pragma unroll
-        for (int i = 0; i < D / 16; i += 4)
-          *reinterpret_cast<f32x4*>(po + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
-        if (c == 0) {
-          p.part_ml[((int64_t)slot * kRows + rr) * 2] = mm;
-          p.part_ml[((int64_t)slot * kRows + rr) * 2 + 1] = ll;
-        }
-      }
-      __syncthreads();
-    }
-    if (at == first && stop < first + span.units) {  // the item goes on: its first block describes it
-      open = true;
-      if (tid == 0) {
-        AttentionItem d;
-        d.b = (int)b;
-        d.h = h;
-        d.group = group;
-        d.first = blockIdx.x;
-        d.last = block_of(first + span.units - 1, total, blocks);
-        d.slot = slot;
-        d.pad[0] = d.pad[1] = 0;
-        desc[blockIdx.x] = d;
+        __syncthreads();
       }
     }
-    at = stop;
-  }
-  if (!open && tid == 0) desc[blockIdx.x].b = -1;
+  } while (more);
+  if (threadIdx.x == 0 && !sh.open) static_cast<AttentionItem*>(arguments().desc)[blockIdx.x].b = -1;
 }
 
 // ---------------------------------------------------------------------------
 // Items that several blocks share: their parts together.
 // ---------------------------------------------------------------------------
+// Blocks take some rows of an item in turn.  D/4 threads stand beside one
+// another for a row's values, so a block has kSlices of them: where the item has
+// few parts each takes a row and adds them up by itself; where it has many they
+// take a row together, a slice of the parts each, whose sums are added up in LDS
+// in a fixed order.
 template <int D, int DT>
 __global__ __launch_bounds__(kThreads) void join_kernel(const AttentionParams p) {
-  const AttentionItem it = static_cast<const AttentionItem*>(p.desc)[blockIdx.x];
-  if (it.b < 0) return;
-  const int rows = p.tiles * kTile;
-  const int r = blockIdx.y * kTile + threadIdx.x / 16, c = threadIdx.x % 16;
-  const int row = it.group * rows + r;
-  const int n = row / p.G, head = it.h * p.G + row % p.G;
-  const int news = p.news ? p.news[it.b] : p.N;
-  if (n >= news) return;
-  const auto slot_of = [&](int j) { return (int64_t)(j == it.first ? it.slot : 2 * j) * rows + r; };
-  float m = kNegInf;
-  for (int j = it.first; j <= it.last; ++j) m = fmaxf(m, p.part_ml[slot_of(j) * 2]);
-  float o[D / 16], l = 0.f;
+  constexpr int kCols = D / 4, kSlices = kThreads / kCols, kFew = 8;
+  __shared__ f32x4 s_sum[kSlices][kCols];
+  __shared__ float s_l[kSlices], s_m[kSlices];
+  __shared__ int32_t s_end[kAttentionBlocks];  // pieces of work up to a block's item
+  __shared__ int32_t s_scan[kWaves];
+  const AttentionItem* const items = static_cast<const AttentionItem*>(p.desc);
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, rows = p.tiles * kTile;
+  const auto last_of = [&](const AttentionItem& it) { return block_of(it.last, it.total, p); };
+  // every block's item, if one begins there and goes on, and the pieces it makes
+  int32_t pieces = 0;
+  for (int i0 = 0; i0 < p.blocks; i0 += kThreads) {
+    const int i = i0 + tid;
+    int mine = 0;
+    if (i < p.blocks && items[i].b >= 0) mine = last_of(items[i]) - i < kFew ? (rows + kSlices - 1) / kSlices : rows;
+    int incl = mine;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) o[i] = 0.f;
-  for (int j = it.first; j <= it.last; ++j) {
-    const int64_t s = slot_of(j);
-    const float mj = p.part_ml[s * 2];
-    const float f = mj > kNegInf ? __builtin_amdgcn_exp2f(mj - m) : (m > kNegInf ? 0.f : 1.f);
-    l += p.part_ml[s * 2 + 1] * f;
-    const float* po = p.part_o + s * D + c * (D / 16);
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int up = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += up;
+    }
+    if (lane == kWave - 1) s_scan[wave] = incl;
+    __syncthreads();
+    int sum = 0;
+    for (int w = 0; w < kWaves; ++w) {
+      if (w < wave) incl += s_scan[w];
+      sum += s_scan[w];
+    }
+    s_end[i] = pieces + incl;
+    pieces += sum;
+    __syncthreads();
+  }
+  const int col = tid % kCols, slice = tid / kCols;
+  for (int x = blockIdx.x; x < pieces; x += gridDim.x) {
+    int lo = 0;  // the first block whose pieces end behind x
+    for (int step = kAttentionBlocks / 2; step > 0; step /= 2)
+      if (lo + step <= p.blocks && s_end[lo + step - 1] <= x) lo += step;
+    const int first = lo, piece = x - (lo ? s_end[lo - 1] : 0);
+    const AttentionItem it = items[first];
+    const int last = last_of(it);
+    const bool few = last - first < kFew;
+    const int r = few ? piece * kSlices + slice : piece;
+    const int row = it.group * rows + r;
+    const int n = row / p.G, head = it.h * p.G + row - n * p.G;
+    const bool live = r < rows && n < (p.news ? p.news[it.b] : p.N);
+    const auto slot_of = [&](int j) { return (int64_t)(j == first ? it.slot : 2 * j) * rows + r; };
+    const int from = few ? first : first + slice, by = few ? 1 : kSlices;
+    f32x4 o = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f, m = kNegInf;
+    for (int j0 = from; j0 <= last; j0 += kFew * by) {  // kFew parts' loads at a time
+      f32x2 ml[kFew];
+      f32x4 v[kFew];
+      float top = m;
 #pragma unroll
-    for (int i = 0; i < D / 16; i += 4) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(po + i);
+      for (int i = 0; i < kFew; ++i) {
+        const int j = min(j0 + i * by, last);
+        const int64_t s = slot_of(j);
+        ml[i] = live ? reinterpret_cast<const f32x2*>(p.part_ml)[s] : f32x2{kNegInf, 0.f};
+        v[i] = live ? *reinterpret_cast<const f32x4*>(p.part_o + s * D + col * 4) : f32x4{0.f, 0.f, 0.f, 0.f};
+      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[i + k] += v[k] * f;
+      for (int i = 0; i < kFew; ++i) top = fmaxf(top, ml[i][0]);
+      const float keep = part_weight(m, top);
+      o *= keep;
+      l *= keep;
+      m = top;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
+        if (j0 + i * by > last) continue;
+        const float f = part_weight(ml[i][0], m);
+        o += v[i] * f;
+        l += ml[i][1] * f;
+      }
+    }
+    if (!few) {
+      s_sum[slice][col] = o;
+      if (col == 0) {
+        s_l[slice] = l;
+        s_m[slice] = m;
+      }
+      __syncthreads();
+      if (slice == 0) {
+#pragma unroll
+        for (int i = 1; i < kSlices; ++i) m = fmaxf(m, s_m[i]);
+        const float keep = part_weight(s_m[0], m);
+        o *= keep;
+        l *= keep;
+#pragma unroll
+        for (int i = 1; i < kSlices; ++i) {
+          const float f = part_weight(s_m[i], m);
+          o += s_sum[i][col] * f;
+          l += s_l[i] * f;
+        }
+      }
+      __syncthreads();
+    }
+    if (live && (few || slice == 0)) {
+      int depth = n;
+      if (p.lse && p.slopes && p.parent && col == 0) {
+        const int32_t* parent = p.parent + (int64_t)it.b * p.N;
+        depth = 0;
+        for (int a = n; a > 0; ++depth) {
+          const int up = parent[a];
+          if (up < 0 || up >= a) break;
+          a = up;
+        }
+      }
+      const float y[4] = {o[0], o[1], o[2], o[3]};
+      finish<D, DT, 4>(p, it.b, n, head, col * 4, y, m, l, depth);
     }
   }
-  const float inv = 1.f / l;
-  char* out = p.out + it.b * p.os[0] + n * p.os[1] + head * p.os[2] + c * (D / 16) * 2;
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    const float y = l == 0.f ? 0.f : o[i] * inv;
-    reinterpret_cast<uint16_t*>(out)[i] =
-        DT == SV_F16 ? __builtin_bit_cast(uint16_t, (_Float16)y) : __builtin_bit_cast(uint16_t, (__bf16)y);
-  }
-  if (p.lse && c == 0)
-    p.lse[((int64_t)it.b * p.N + n) * p.Hq + head] =
-        l == 0.f ? kNegInf : (m > kNegInf ? m : 0.f) / kLog2e + __builtin_amdgcn_logf(l) / kLog2e;
 }
 
 template <int D, int DT>
@@ -730,16 +1070,19 @@ hipError_t attention(const AttentionParams& p, hipStream_t s) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  join_kernel<D, DT><<<dim3((uint32_t)p.blocks, (uint32_t)p.tiles), kThreads, 0, s>>>(p);
+  join_kernel<D, DT><<<kJoinBlocks, kThreads, 0, s>>>(p);
   return hipGetLastError();
+}
+
+template <int D>
+hipError_t attention(const AttentionParams& p, sv_dtype dt, hipStream_t s) {
+  return dt == SV_BF16 ? attention<D, SV_BF16>(p, s) : attention<D, SV_F16>(p, s);
 }
 
 }  // namespace
 
 hipError_t launch_kv_attention(const AttentionParams& p, sv_dtype dt, int D, hipStream_t s) {
-  if (dt == SV_BF16)
-    return D == 64 ? attention<64, SV_BF16>(p, s) : D == 128 ? attention<128, SV_BF16>(p, s) : attention<256, SV_BF16>(p, s);
-  return D == 64 ? attention<64, SV_F16>(p, s) : D == 128 ? attention<128, SV_F16>(p, s) : attention<256, SV_F16>(p, s);
+  return D == 64 ? attention<64>(p, dt, s) : D == 128 ? attention<128>(p, dt, s) : attention<256>(p, dt, s);
 }
 
 }  // namespace sv

@@ -70,7 +70,7 @@ struct AttentionParams {
   int32_t reach;
   int32_t* err;
   int32_t tiles, groups;  // tiles of 16 rows in a group of rows, groups
-  int32_t blocks;
+  int32_t blocks, log_blocks;
   float* part_o;  // [2 * blocks][tiles * 16][D]
   float* part_ml; // [2 * blocks][tiles * 16][2]
   void* desc;     // [blocks] of AttentionItem
@@ -78,10 +78,9 @@ struct AttentionParams {
 
 // An item (a sequence's key head and group of rows) that several blocks share.
 struct AttentionItem {
-  int32_t b, h, group;      // b = -1: none
-  int32_t first, last;      // blocks
-  int32_t slot;             // of the first block's part
-  int32_t pad[2];
+  int32_t b, h, group;  // b = -1: none
+  int32_t slot;         // of the first block's part
+  int64_t last, total;  // its last step, and how many steps there are
 };
 
 hipError_t launch_rope(const RopeParams& p, sv_dtype dt, hipStream_t s);
@@ -92,7 +91,7 @@ hipError_t launch_kv_attention(const AttentionParams& p, sv_dtype dt, int D, hip
 
 // Rows of nodes x heads are taken in groups of up to this many tiles of 16.
 inline int attention_tiles(int D) { return D == 256 ? 2 : 4; }
-constexpr int kAttentionBlocks = 512;
+constexpr int kAttentionBlocks = 1024;  // at most
 constexpr int kAttentionUnit = 128;  // tokens of a step: 32 for each of a block's 4 waves
 
 }  // namespace sv

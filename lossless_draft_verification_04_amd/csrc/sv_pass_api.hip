@@ -114,7 +114,7 @@ sv_status plan_attention(int32_t B, int32_t N, int32_t Hq, int32_t H, int32_t D,
   pl->groups = (tiles + attention_tiles(D) - 1) / attention_tiles(D);
   pl->tiles = (tiles + pl->groups - 1) / pl->groups;
   pl->groups = (tiles + pl->tiles - 1) / pl->tiles;
-  pl->blocks = kAttentionBlocks;
+  pl->blocks = pl->tiles > 1 || D == 256 ? 512 : D == 64 ? 1024 : 768;
   const size_t rows = (size_t)2 * pl->blocks * pl->tiles * 16;
   size_t off = kWsFixed;
   pl->off_desc = off;
@@ -338,6 +338,7 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
   p.tiles = pl.tiles;
   p.groups = pl.groups;
   p.blocks = pl.blocks;
+  p.log_blocks = __builtin_ctz((unsigned)pl.blocks);
   p.desc = w + pl.off_desc;
   p.part_ml = reinterpret_cast<float*>(w + pl.off_ml);
   p.part_o = reinterpret_cast<float*>(w + pl.off_o);
