@@ -53,6 +53,7 @@ enum {
 
 #define SV_MAX_HEADS 1024       /* query heads, key heads */
 #define SV_MAX_PAGE_TOKENS (1 << 20)
+#define SV_MAX_LAYERS 65536     /* layers of a commit */
 
 /* Device error-word bits of these entry points: SV_DERR_TREE (a parent not
  * before its node, a path that does not rise) and SV_DERR_RANGE (a length, a

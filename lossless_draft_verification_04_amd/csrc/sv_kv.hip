@@ -24,17 +24,12 @@ __host__ __device__ inline int64_t slot_groups(int N) { return ((int64_t)N + 6) 
 
 template <int D>
 __device__ __forceinline__ bool place_of(const KvMoveParams& p, Place* at, int64_t* len, int* count, bool* first) {
-  const int64_t per = slot_groups(p.N) * p.c.H * 4 * (D / 8);  // of a sequence
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  const int64_t b = i / per;
-  if (b >= p.B) return false;
-  const int64_t in = i - b * per;
-  at->b = (int)b;
+  const uint32_t in = blockIdx.x * kThreads + threadIdx.x;  // of the sequence
+  const int b = blockIdx.y;
+  at->b = b;
   at->d8 = (int)(in % (D / 8));
-  const int64_t row = in / (D / 8);
-  const int64_t gh = row / 4;
-  at->h = (int)(gh % p.c.H);
-  const int64_t g = gh / p.c.H;
+  const uint32_t row = in / (D / 8), gh = row / 4, g = gh / (uint32_t)p.c.H;
+  at->h = (int)(gh - g * p.c.H);
   *len = p.lens ? p.lens[b] : 0;
   *count = p.news ? p.news[b] : p.N;
   *first = in == 0;
@@ -133,20 +128,34 @@ __global__ __launch_bounds__(kThreads) void read_kernel(const KvMoveParams p) {
   out.store(p.v + at.b * p.st[1][0] + at.n * p.st[1][1] + at.h * p.st[1][2] + at.d8 * 8 * es);
 }
 
-// A block moves one sequence's path in one layer's head, tokens in the path's
-// order: a place is written after everything that stood in it and moves has
-// been read, because a token moves to a lower place, past none of those behind
-// it.  Threads of a pass take (token, piece): pieces of 4 bytes of the
-// keys' codes, a sixteenth of the values', one byte of the scales.
+// A block moves one sequence's path in one head of several layers, tokens in
+// the path's order: a place is written after everything that stood in it and
+// moves has been read, because a token moves to a lower place, past none of
+// those behind it.  A thread takes one piece of a token -- 16 bytes of the keys'
+// codes, a sixteenth of the values', the keys' scales, one of the values' -- and
+// reads it from all of the block's layers before it writes: what a layer moves
+// is little (8 tokens of 136 bytes), so the time is that of the loads one after
+// another (lengths, path, pages, pieces), and layers share it.
+constexpr int kLayers = 8;
+
+template <int BYTES>
+struct Bits;
+template <>
+struct Bits<1> { using T = uint8_t; };
+template <>
+struct Bits<2> { using T = uint16_t; };
+template <>
+struct Bits<4> { using T = uint32_t; };
+template <>
+struct Bits<8> { using T = uint64_t; };
+
 template <int D>
 __global__ __launch_bounds__(kThreads) void commit_kernel(const KvCommitParams p) {
   const int h = blockIdx.x % p.c.H;
-  const int64_t lb = blockIdx.x / p.c.H;
-  const int b = (int)(lb % p.B);
-  const int64_t layer = lb / p.B;
+  const int b = (int)(blockIdx.x / p.c.H);
+  const int layer0 = blockIdx.y * kLayers, layers = min(kLayers, p.c.layers - layer0);
   const int64_t len = p.lens[b];
   const int n = p.n[b];
-  const bool speaks = h == 0 && layer == 0;  // the sequence's first block writes its length and flags
   const int32_t* path = p.path ? p.path + (int64_t)b * p.M : nullptr;
   const int32_t* pages = p.c.pages + (int64_t)b * p.c.max_pages;
   // n is not bounded by M where there is no path
@@ -165,71 +174,80 @@ __global__ __launch_bounds__(kThreads) void commit_kernel(const KvCommitParams p
       }
     }
   }
-  range = __syncthreads_or(range);
-  tree = __syncthreads_or(tree);
-  if (speaks && threadIdx.x == 0) {
-    p.out_lens[b] = range || tree || n < 0 ? (int32_t)len : (int32_t)(len + 1 + n);
-    if (range) flag(p.err, SV_DERR_RANGE);
-    if (tree) flag(p.err, SV_DERR_TREE);
+  const int bad = __syncthreads_or((range ? 1 : 0) | (tree ? 2 : 0));
+  if (h == 0 && layer0 == 0 && threadIdx.x == 0) {  // the sequence's first block writes its length and flags
+    p.out_lens[b] = bad || n < 0 ? (int32_t)len : (int32_t)(len + 1 + n);
+    if (bad) flag(p.err, (bad & 1 ? SV_DERR_RANGE : 0) | (bad & 2 ? SV_DERR_TREE : 0));
   }
-  if (range || tree || !path || n <= 0) return;
-  constexpr int kKeys = D / 8, kPieces = kKeys + 16 + 2 * (D / 32);
-  constexpr int kPass = 4;  // pieces of a thread at a time
-  constexpr int kTokens = kThreads * kPass / kPieces;
-  char* base = p.c.pool + layer * p.c.layer_stride + h * p.c.head;
+  if (bad || !path || n <= 0) return;
+  constexpr int w = D / 32;
+  constexpr int kPieces = w + 16 + 1 + w;
+  constexpr int kTokens = kThreads / kPieces;
+  char* const base = p.c.pool + layer0 * p.c.layer_stride + h * p.c.head;
   const int64_t in_page = ((int64_t)1 << p.c.pshift) - 1;
+  const int piece = threadIdx.x % kPieces;
   for (int j0 = 0; j0 < n; j0 += kTokens) {
-    const int some = min(kTokens, n - j0) * kPieces;
-    uint64_t held[kPass];
-    char* to[kPass];
-    int size[kPass];
-#pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-      const int x = i * kThreads + threadIdx.x;
-      size[i] = 0;
-      if (x >= some) continue;
-      const int j = j0 + x / kPieces, piece = x % kPieces;
+    const int j = j0 + threadIdx.x / kPieces;
+    const bool live = (int)threadIdx.x < kTokens * kPieces && j < n && path[min(j, n - 1)] != 1 + j;
+    u32x4 held[kLayers];
+    int64_t to = 0, from = 0;
+    if (live) {
       const int64_t s = len + path[j], d = len + 1 + j;
-      if (s == d) continue;
-      const char* sp = base + pages[s >> p.c.pshift] * p.c.page_stride;
-      char* dp = base + pages[d >> p.c.pshift] * p.c.page_stride;
       const int64_t ss = s & in_page, ds = d & in_page;
-      if (piece < kKeys) {
-        size[i] = 4;
-        held[i] = *reinterpret_cast<const uint32_t*>(sp + key_at<D>(ss, piece));
-        to[i] = dp + key_at<D>(ds, piece);
-      } else if (piece < kKeys + 16) {
-        constexpr int w = D / 32;
-        const int c = piece - kKeys;
-        const char* f = sp + p.c.vc + ((ss / 4 * 16 + c) * 4 + ss % 4) * w;
-        to[i] = dp + p.c.vc + ((ds / 4 * 16 + c) * 4 + ds % 4) * w;
-        size[i] = w;
-        if constexpr (w == 2) held[i] = *reinterpret_cast<const uint16_t*>(f);
-        if constexpr (w == 4) held[i] = *reinterpret_cast<const uint32_t*>(f);
-        if constexpr (w == 8) held[i] = *reinterpret_cast<const uint64_t*>(f);
+      if (piece < w) {
+        from = ss * (D / 2) + piece * 16;
+        to = ds * (D / 2) + piece * 16;
+      } else if (piece < w + 16) {
+        from = p.c.vc + ((ss / 4 * 16 + piece - w) * 4 + ss % 4) * w;
+        to = p.c.vc + ((ds / 4 * 16 + piece - w) * 4 + ds % 4) * w;
+      } else if (piece == w + 16) {
+        from = p.c.ks + ss * w;
+        to = p.c.ks + ds * w;
       } else {
-        const int c = (piece - kKeys - 16) / 2;
-        const bool key = (piece - kKeys - 16) % 2 == 0;
-        size[i] = 1;
-        held[i] = (uint8_t)(key ? sp[p.c.ks + key_scale_at<D>(ss, c)] : sp[p.c.vs + value_scale_at<D>(ss, c)]);
-        to[i] = key ? dp + p.c.ks + key_scale_at<D>(ds, c) : dp + p.c.vs + value_scale_at<D>(ds, c);
+        from = p.c.vs + value_scale_at<D>(ss, piece - w - 17);
+        to = p.c.vs + value_scale_at<D>(ds, piece - w - 17);
+      }
+      from += pages[s >> p.c.pshift] * p.c.page_stride;
+      to += pages[d >> p.c.pshift] * p.c.page_stride;
+#pragma unroll
+      for (int i = 0; i < kLayers; ++i) {
+        const char* at = base + min(i, layers - 1) * p.c.layer_stride + from;
+        if (piece < w)
+          held[i] = *reinterpret_cast<const u32x4*>(at);
+        else if (piece > w + 16)
+          held[i][0] = (uint8_t)*at;
+        else if constexpr (w == 8) {
+          const uint64_t x = *reinterpret_cast<const uint64_t*>(at);
+          held[i][0] = (uint32_t)x;
+          held[i][1] = (uint32_t)(x >> 32);
+        } else {
+          held[i][0] = *reinterpret_cast<const typename Bits<w>::T*>(at);
+        }
       }
     }
     __syncthreads();
+    if (live) {
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-      if (size[i] == 1) *to[i] = (char)held[i];
-      if (size[i] == 2) *reinterpret_cast<uint16_t*>(to[i]) = (uint16_t)held[i];
-      if (size[i] == 4) *reinterpret_cast<uint32_t*>(to[i]) = (uint32_t)held[i];
-      if (size[i] == 8) *reinterpret_cast<uint64_t*>(to[i]) = held[i];
+      for (int i = 0; i < kLayers; ++i) {
+        if (i >= layers) break;
+        char* at = base + i * p.c.layer_stride + to;
+        if (piece < w)
+          *reinterpret_cast<u32x4*>(at) = held[i];
+        else if (piece > w + 16)
+          *at = (char)held[i][0];
+        else if constexpr (w == 8)
+          *reinterpret_cast<uint64_t*>(at) = held[i][0] | (uint64_t)held[i][1] << 32;
+        else
+          *reinterpret_cast<typename Bits<w>::T*>(at) = (typename Bits<w>::T)held[i][0];
+      }
     }
   }
 }
 
 template <int D>
 hipError_t move(const KvMoveParams& p, sv_dtype dt, bool write, hipStream_t s) {
-  const int64_t threads = (int64_t)p.B * slot_groups(p.N) * p.c.H * 4 * (D / 8);
-  const dim3 grid((uint32_t)((threads + kThreads - 1) / kThreads));
+  const int64_t threads = slot_groups(p.N) * p.c.H * 4 * (D / 8);  // of a sequence
+  const dim3 grid((uint32_t)((threads + kThreads - 1) / kThreads), (uint32_t)p.B);
   switch (dt) {
     case SV_BF16:
       write ? write_kernel<D, SV_BF16><<<grid, kThreads, 0, s>>>(p) : read_kernel<D, SV_BF16><<<grid, kThreads, 0, s>>>(p);
@@ -253,9 +271,8 @@ hipError_t launch_kv_write(const KvMoveParams& p, sv_dtype dt, int D, hipStream_
 hipError_t launch_kv_read(const KvMoveParams& p, sv_dtype dt, int D, hipStream_t s) { return move(p, dt, D, false, s); }
 
 hipError_t launch_kv_commit(const KvCommitParams& p, int D, hipStream_t s) {
-  // without a path nothing moves: one block a sequence
-  const int64_t blocks = p.path ? (int64_t)p.c.layers * p.B * p.c.H : (int64_t)p.B * p.c.H;
-  const dim3 grid((uint32_t)blocks);
+  // without a path nothing moves
+  const dim3 grid((uint32_t)p.B * p.c.H, p.path ? (uint32_t)(p.c.layers + kLayers - 1) / kLayers : 1);
   if (D == 64) commit_kernel<64><<<grid, kThreads, 0, s>>>(p);
   if (D == 128) commit_kernel<128><<<grid, kThreads, 0, s>>>(p);
   if (D == 256) commit_kernel<256><<<grid, kThreads, 0, s>>>(p);

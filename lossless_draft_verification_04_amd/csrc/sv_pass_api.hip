@@ -149,8 +149,8 @@ sv_status kv_move(const void* k, const int64_t* ks, const void* v, const int64_t
   if ((st = check_tensor(v, vs, B, N, cache->H, cache->D, type_bytes(dt), true, p.st[1], &nv, &av)) != SV_OK) return st;
   if (!write && (!ak || !av || overlap(k, nk, v, nv))) return SV_EINVAL;
   if ((st = check_space(ws, ws_bytes, kWsFixed)) != SV_OK) return st;
-  // a launch takes fewer than 2^31 blocks, each 2048 values of keys
-  if ((double)B * (N + 6.0) * cache->H * cache->D > 2048.0 * INT32_MAX) return SV_EUNSUPPORTED;
+  // threads of a sequence, 8 values of keys each, are counted in 32 bits
+  if (((int64_t)N + 6) * cache->H * cache->D / 8 > INT32_MAX - 1024) return SV_EUNSUPPORTED;
   p.k = static_cast<char*>(const_cast<void*>(k));
   p.v = static_cast<char*>(const_cast<void*>(v));
   p.lens = lens;
@@ -352,7 +352,7 @@ sv_status sv_kv_commit(const sv_kv_cache* cache, const int32_t* lens, const int3
   if (st != SV_OK) return st;
   if (B < 0 || M < 0) return SV_EINVAL;
   if (B > SV_MAX_SEQ || M > SV_MAX_N) return SV_EUNSUPPORTED;
-  if ((int64_t)p.c.layers * B > INT32_MAX / cache->H) return SV_EUNSUPPORTED;
+  if (p.c.layers > SV_MAX_LAYERS) return SV_EUNSUPPORTED;
   if (B == 0) return SV_OK;
   if (!lens || !n || !out_lens) return SV_EINVAL;
   if (overlap(lens, (int64_t)B * 4, out_lens, (int64_t)B * 4)) return SV_EINVAL;

@@ -1,11 +1,12 @@
 // sv_rope.hip -- rotary positions of a window's queries and keys.
 //
 // y = factor * R(t f_i) x on the pairs (x_i, y_i) of each head; the gradient is
-// the transposed rotation.  A block takes some tokens: it forms their angles
-// once, in 64 bits and reduced to a turn (t f_i has far more digits than 32
-// bits hold at distant positions), puts sine and cosine into LDS, and turns
-// all heads with them.  Reads and writes each value once: bound by memory for
-// many tokens, by the launch for few.
+// the transposed rotation.  A thread takes 16 bytes of a head's row (twice,
+// where a pair's halves lie R/2 apart) in up to 8 heads of a token one after
+// another: it forms the angles of its pairs once for them, in 64 bits and
+// reduced to a turn (t f_i has far more digits than 32 bits hold at distant
+// positions), and needs neither LDS nor a barrier.  Reads and writes each value
+// once: bound by memory for many tokens, by the launch for few.
 #include "sv_kv.hpp"
 
 namespace sv {
@@ -13,7 +14,6 @@ namespace sv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAngles = 4096;  // of a block at most (32 KB of LDS)
 
 template <int DT>
 struct Elem;
@@ -47,7 +47,7 @@ __device__ __forceinline__ Pack<T, V> take(const char* at) {
     return {{*reinterpret_cast<const T*>(at)}};
   } else {
     static_assert(sizeof(T) * V == 16, "a vector");
-    return __builtin_bit_cast(Pack<T, V>, *reinterpret_cast<const u32x4*>(at));
+    return __builtin_bit_cast(Pack<T, V>, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at)));
   }
 }
 template <typename T, int V>
@@ -55,7 +55,7 @@ __device__ __forceinline__ void put(char* at, const Pack<T, V>& x) {
   if constexpr (V == 1)
     *reinterpret_cast<T*>(at) = x.v[0];
   else
-    *reinterpret_cast<u32x4*>(at) = __builtin_bit_cast(u32x4, x);
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, x), reinterpret_cast<u32x4*>(at));
 }
 
 // Items of a head's row: V pairs each where pairs are (i, i + R/2), V / 2 (one
@@ -73,91 +73,113 @@ __host__ __device__ inline Rows rows_of(int D, int R, int V, bool interleaved, b
   return r;
 }
 
-template <int DT, int V>
-__global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p, const int tokens, const bool copy) {
+// Threads stand (slot, item): `slots` of a block take `run` rows (token, head) one
+// after another each, `wide` items of a row beside one another.
+struct Shape {
+  int32_t wide, slots, run, copy;
+};
+
+// SPLIT: a pair's halves lie R/2 apart.
+template <int DT, int V, bool SPLIT>
+__global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p, const Shape shape) {
   using T = typename Elem<DT>::T;
-  extern __shared__ float s_angle[];  // [tokens][R/2] cosines, then as many sines
-  const int half = p.R / 2;
-  const int64_t all = (int64_t)p.B * p.N;
-  const int64_t t0 = (int64_t)blockIdx.x * tokens;
-  const int some = (int)min((int64_t)tokens, all - t0);
-  float* const s_cos = s_angle;
-  float* const s_sin = s_angle + tokens * half;
-  for (int x = threadIdx.x; x < some * half; x += kThreads) {
-    const int i = x % half;
-    const int64_t t = t0 + x / half;
-    int64_t pos;
-    if (p.positions) {
-      pos = p.positions[t];
-    } else {
-      const int64_t b = t / p.N;
-      int n = (int)(t - b * p.N);
-      pos = p.lens ? p.lens[b] : 0;
-      if (p.parent) {
-        const int32_t* parent = p.parent + b * p.N;
-        while (n > 0) {  // at most N steps: a parent stands before its node
-          const int up = parent[n];
-          if (up < 0 || up >= n) {
-            if (i == 0) flag(p.err, SV_DERR_TREE);
-            break;
-          }
-          n = up;
-          ++pos;
-        }
-      } else {
-        pos += n;
-      }
-    }
-    const double turns = (double)pos * (p.freq[i] * 0.15915494309189535);
-    float s, c;
-    sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-    s_cos[x] = c * p.factor;
-    s_sin[x] = (p.inverse ? -s : s) * p.factor;
-  }
-  __syncthreads();
-  const Rows rows = rows_of(p.D, p.R, V, p.interleaved, copy);
-  const int heads = p.heads[0] + p.heads[1];
-  const int items = some * heads * rows.all;
   constexpr int es = sizeof(T);
-  for (int x = threadIdx.x; x < items; x += kThreads) {
-    const int row = x / rows.all, item = x - row * rows.all;
-    const int t = row / heads;
-    int h = row - t * heads;
-    const int which = h >= p.heads[0];
-    h -= which ? p.heads[0] : 0;
-    const int64_t b = (t0 + t) / p.N, n = t0 + t - b * p.N;
-    const char* in = p.in[which] + b * p.is[which][0] + n * p.is[which][1] + h * p.is[which][2];
-    char* out = p.out[which] + b * p.os[which][0] + n * p.os[which][1] + h * p.os[which][2];
-    if (item >= rows.turned) {
-      const int64_t at = (p.R + (int64_t)(item - rows.turned) * V) * es;
-      put<T, V>(out + at, take<T, V>(in + at));
-      continue;
-    }
-    const int i0 = item * rows.pairs;
-    const float* c = s_cos + t * half + i0;
-    const float* s = s_sin + t * half + i0;
-    if (p.interleaved && V > 1) {
-      const int64_t at = (int64_t)i0 * 2 * es;
-      Pack<T, V> v = take<T, V>(in + at);
+  constexpr int kPairs = SPLIT || V == 1 ? V : V / 2;  // of an item
+  constexpr int kAhead = 4;                            // rows' loads at a time
+  const int half = p.R / 2, heads = p.heads[0] + p.heads[1];
+  const Rows rows = rows_of(p.D, p.R, V, !SPLIT, shape.copy);
+  const int slot = threadIdx.x / shape.wide, lane = threadIdx.x - slot * shape.wide;
+  // a tree's parents, of the block's first sequence
+  __shared__ int32_t s_parent[SV_MAX_N];
+  int64_t staged = -1;
+  if (p.parent && !p.positions) {
+    staged = (int64_t)blockIdx.x * shape.slots * shape.run / heads / p.N;
+    for (int i = threadIdx.x; i < p.N; i += kThreads) s_parent[i] = p.parent[staged * p.N + i];
+    __syncthreads();
+  }
+  if (slot >= shape.slots) return;
+  const int64_t all = (int64_t)p.B * p.N * heads;
+  const int64_t row0 = ((int64_t)blockIdx.x * shape.slots + slot) * shape.run;
+  const int64_t row1 = min(row0 + shape.run, all);
+  if (row0 >= row1) return;
+  for (int item = blockIdx.y * shape.wide + lane; item < rows.all; item += gridDim.y * shape.wide) {
+    const bool turned = item < rows.turned;
+    const int64_t at0 = (turned ? (int64_t)item * (SPLIT ? V : 2 * kPairs) : p.R + (int64_t)(item - rows.turned) * V) * es;
+    const int64_t at1 = at0 + (SPLIT ? half : 1) * es;  // the other half, where it is a vector of its own
+    int64_t t = row0 / heads;
+    int h = (int)(row0 - t * heads);
+    int64_t b = t / p.N;
+    int n = (int)(t - b * p.N);
+    bool fresh = true;
+    float c[kPairs], s[kPairs];
+    for (int64_t row = row0; row < row1;) {
+      Pack<T, V> v[kAhead], w[kAhead];
+      char* out[kAhead];
+      const int count = (int)min((int64_t)min(kAhead, heads - h), row1 - row);  // of the same token
 #pragma unroll
-      for (int j = 0; j < V / 2; ++j) {
-        const float a = Elem<DT>::get(v.v[2 * j]), d = Elem<DT>::get(v.v[2 * j + 1]);
-        v.v[2 * j] = Elem<DT>::set(a * c[j] - d * s[j]);
-        v.v[2 * j + 1] = Elem<DT>::set(d * c[j] + a * s[j]);
+      for (int a = 0; a < kAhead; ++a) {
+        if (a >= count) break;
+        const int which = h + a >= p.heads[0];
+        const int hh = h + a - (which ? p.heads[0] : 0);
+        const char* in = p.in[which] + b * p.is[which][0] + n * p.is[which][1] + hh * p.is[which][2];
+        out[a] = p.out[which] + b * p.os[which][0] + n * p.os[which][1] + hh * p.os[which][2];
+        v[a] = take<T, V>(in + at0);
+        if ((SPLIT || V == 1) && turned) w[a] = take<T, V>(in + at1);
       }
-      put<T, V>(out + at, v);
-    } else {
-      const int64_t ax = (int64_t)(p.interleaved ? 2 * i0 : i0) * es;
-      const int64_t ay = (int64_t)(p.interleaved ? 2 * i0 + 1 : i0 + half) * es;
-      Pack<T, V> v = take<T, V>(in + ax), w = take<T, V>(in + ay);
+      if (fresh && turned) {  // while the first loads fly
+        int64_t pos;
+        if (p.positions) {
+          pos = p.positions[b * p.N + n];
+        } else {
+          pos = p.lens ? p.lens[b] : 0;
+          if (p.parent) {
+            const int32_t* parent = p.parent + b * p.N;
+            for (int i = n; i > 0; ++pos) {  // at most N steps: a parent stands before its node
+              const int up = b == staged ? s_parent[i] : parent[i];
+              if (up < 0 || up >= i) {
+                if (item == 0) flag(p.err, SV_DERR_TREE);
+                break;
+              }
+              i = up;
+            }
+          } else {
+            pos += n;
+          }
+        }
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const float a = Elem<DT>::get(v.v[j]), d = Elem<DT>::get(w.v[j]);
-        v.v[j] = Elem<DT>::set(a * c[j] - d * s[j]);
-        w.v[j] = Elem<DT>::set(d * c[j] + a * s[j]);
+        for (int j = 0; j < kPairs; ++j) {
+          const double turns = (double)pos * (p.freq[item * kPairs + j] * 0.15915494309189535);
+          sincospif(2.0f * (float)(turns - rint(turns)), &s[j], &c[j]);
+          c[j] *= p.factor;
+          s[j] *= p.inverse ? -p.factor : p.factor;
+        }
       }
-      put<T, V>(out + ax, v);
-      put<T, V>(out + ay, w);
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        if (a >= count) break;
+        if (turned) {
+#pragma unroll
+          for (int j = 0; j < kPairs; ++j) {
+            T& first = v[a].v[SPLIT || V == 1 ? j : 2 * j];
+            T& second = SPLIT || V == 1 ? w[a].v[j] : v[a].v[V == 1 ? 0 : 2 * j + 1];
+            const float x = Elem<DT>::get(first), y = Elem<DT>::get(second);
+            first = Elem<DT>::set(x * c[j] - y * s[j]);
+            second = Elem<DT>::set(y * c[j] + x * s[j]);
+          }
+          if (SPLIT || V == 1) put<T, V>(out[a] + at1, w[a]);
+        }
+        put<T, V>(out[a] + at0, v[a]);
+      }
+      row += count;
+      h += count;
+      fresh = h == heads;
+      if (fresh) {
+        h = 0;
+        if (++n == p.N) {
+          n = 0;
+          ++b;
+        }
+      }
     }
   }
 }
@@ -175,25 +197,35 @@ bool vectors(const RopeParams& p, int es) {
   return true;
 }
 
+template <int DT, int V>
+void run(const RopeParams& p, const Shape& shape, dim3 grid, hipStream_t s) {
+  if (p.interleaved)
+    rope_kernel<DT, V, false><<<grid, kThreads, 0, s>>>(p, shape);
+  else
+    rope_kernel<DT, V, true><<<grid, kThreads, 0, s>>>(p, shape);
+}
+
 template <int DT>
 hipError_t rope(const RopeParams& p, hipStream_t s) {
   constexpr int es = sizeof(typename Elem<DT>::T);
   const bool vec = vectors(p, es);
-  bool copy = false;  // in place, what does not turn stays
-  for (int w = 0; w < 2; ++w) copy = copy || (p.heads[w] && p.in[w] != p.out[w]);
-  const Rows rows = rows_of(p.D, p.R, vec ? 16 / es : 1, p.interleaved, copy);
-  // a block's tokens: enough for every thread to have an item or two, as far as their angles fit
-  const int64_t per = (int64_t)(p.heads[0] + p.heads[1]) * rows.all;
-  int tokens = (int)(1 + 2 * kThreads / (per + 1));
-  const int most = kAngles / (p.R / 2) > 1 ? kAngles / (p.R / 2) : 1;
-  if (tokens > most) tokens = most;
-  const int64_t all = (int64_t)p.B * p.N;
-  const dim3 grid((uint32_t)((all + tokens - 1) / tokens));
-  const size_t lds = (size_t)tokens * (p.R / 2) * 2 * sizeof(float);
+  Shape shape;
+  shape.copy = 0;  // in place, what does not turn stays
+  for (int w = 0; w < 2; ++w) shape.copy |= p.heads[w] && p.in[w] != p.out[w];
+  const Rows rows = rows_of(p.D, p.R, vec ? 16 / es : 1, p.interleaved, shape.copy);
+  shape.wide = rows.all < kThreads ? rows.all : kThreads;
+  shape.slots = kThreads / shape.wide;
+  const int64_t all = (int64_t)p.B * p.N * (p.heads[0] + p.heads[1]);
+  // Rows of a slot: one where there are few, up to 8 for as many as fill the device.
+  const int64_t fill = all / (2048 * (int64_t)shape.slots);
+  shape.run = fill < 1 ? 1 : fill > 8 ? 8 : (int)fill;
+  const int64_t blocks = (all + (int64_t)shape.slots * shape.run - 1) / ((int64_t)shape.slots * shape.run);
+  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid((uint32_t)blocks, (uint32_t)((rows.all + shape.wide - 1) / shape.wide));
   if (vec)
-    rope_kernel<DT, 16 / es><<<grid, kThreads, lds, s>>>(p, tokens, copy);
+    run<DT, 16 / es>(p, shape, grid, s);
   else
-    rope_kernel<DT, 1><<<grid, kThreads, lds, s>>>(p, tokens, copy);
+    run<DT, 1>(p, shape, grid, s);
   return hipGetLastError();
 }
 

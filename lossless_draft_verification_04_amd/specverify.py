@@ -800,9 +800,9 @@ def _pass_workspace(dev, *shape):
     return ws if ws is not None and ws.numel() >= need else Workspace.get(dev, need, in_capture=False)
 
 
-def _window(t, what, types=_PASS_TYPES):
+def _window(t, what):
     """The type's code and the strides of a [B, N, heads, D] tensor."""
-    dt = types.get(t.dtype)
+    dt = _PASS_TYPES.get(t.dtype)
     if dt is None:
         raise SpecVerifyError(SV_EDTYPE, f"{what}: {t.dtype}")
     return dt, _window_strides(t.shape, t.stride(), what)
@@ -877,39 +877,58 @@ def sv_rope_frequencies(R, theta=10000.0, kind="plain", scale=1.0, original=0, f
     return torch.tensor(list(out), dtype=torch.float64), factor.value
 
 
+@functools.lru_cache(maxsize=1024)
+def _rope_layout(q, qst, out_q, out_qst, k=None, kst=None, out_k=None, out_kst=None):
+    """(B, N, Hq, D, Hk) and the strides of q, out_q, k, out_k."""
+    sq, soq, sk, sok = _window_strides(q, qst, "q"), _window_strides(out_q, out_qst, "out_q"), None, None
+    if out_q != q:
+        raise SpecVerifyError(SV_EINVAL, f"out_q: want {tuple(q)}, got {tuple(out_q)}")
+    if k is not None:
+        sk, sok = _window_strides(k, kst, "k"), _window_strides(out_k, out_kst, "out_k")
+        if k[:2] != q[:2] or k[3] != q[3] or out_k != k:
+            raise SpecVerifyError(SV_EINVAL, f"k: want {(*q[:2], 'heads', q[3])} twice, got {tuple(k)} and {tuple(out_k)}")
+    return (*q, 0 if k is None else k[2]), (sq, soq, sk, sok)
+
+
 def sv_rope(q, freq, k=None, positions=None, lens=None, parent=None, interleaved=False, factor=1.0, inverse=False,
             out_q=None, out_k=None, workspace=None):
     """Rotary positions of q [B, N, Hq, D] and k [B, N, Hk, D] (or None) over the first 2 * len(freq) values of each head;
     freq float64 on the device.  positions [B, N] int32, or lens [B] int32 (None: 0) + the node's depth in parent [B, N] int32
     (None: its number).  inverse: the transposed rotation, the gradient.  out_q, out_k: where to write (q, k themselves:
     in place).  Returns dict(q, k)."""
-    dt, sq = _window(q, "q")
-    B, N, Hq, D = q.shape
+    dt = _PASS_TYPES.get(q.dtype)
+    if dt is None:
+        raise SpecVerifyError(SV_EDTYPE, f"q: {q.dtype}")
+    if out_q is None:
+        out_q = torch.empty_like(q)
+    if k is None:
+        if out_k is not None:
+            raise SpecVerifyError(SV_EINVAL, "out_k: want k with it")
+        layout = _rope_layout(q.shape, q.stride(), out_q.shape, out_q.stride())
+    else:
+        if out_k is None:
+            out_k = torch.empty_like(k)
+        if k.dtype is not q.dtype or out_k.dtype is not q.dtype:
+            raise SpecVerifyError(SV_EINVAL, f"k: want {q.dtype}, got {k.dtype} and {out_k.dtype}")
+        layout = _rope_layout(q.shape, q.stride(), out_q.shape, out_q.stride(), k.shape, k.stride(), out_k.shape,
+                              out_k.stride())
+    if out_q.dtype is not q.dtype:
+        raise SpecVerifyError(SV_EINVAL, f"out_q: want {q.dtype}, got {out_q.dtype}")
+    (B, N, Hq, D, Hk), (sq, soq, sk, sok) = layout
     if freq.dim() != 1:
         raise SpecVerifyError(SV_EINVAL, f"freq: want [R/2], got {tuple(freq.shape)}")
-    _want(freq, torch.float64, tuple(freq.shape), "freq")
-    _int32(positions, (B, N), "positions")
-    _int32(lens, (B,), "lens")
-    _int32(parent, (B, N), "parent")
-    out_q = torch.empty_like(q, memory_format=torch.contiguous_format) if out_q is None else out_q
-    Hk, sk, sok = 0, None, None
-    if k is not None:
-        if k.dtype is not q.dtype or k.dim() != 4 or k.shape[:2] != q.shape[:2] or k.shape[3] != D:
-            raise SpecVerifyError(SV_EINVAL, f"k: want {q.dtype} [{B}, {N}, heads, {D}], got {k.dtype} {tuple(k.shape)}")
-        Hk, sk = k.shape[2], _window(k, "k")[1]
-        out_k = torch.empty_like(k, memory_format=torch.contiguous_format) if out_k is None else out_k
-        if out_k.dtype is not k.dtype or out_k.shape != k.shape:
-            raise SpecVerifyError(SV_EINVAL, f"out_k: want {k.dtype} {tuple(k.shape)}")
-        sok = _window(out_k, "out_k")[1]
-    elif out_k is not None:
-        raise SpecVerifyError(SV_EINVAL, "out_k: want k with it")
-    if out_q.dtype is not q.dtype or out_q.shape != q.shape:
-        raise SpecVerifyError(SV_EINVAL, f"out_q: want {q.dtype} {tuple(q.shape)}")
+    _want(freq, torch.float64, freq.shape, "freq")
+    if positions is not None:
+        _want(positions, torch.int32, (B, N), "positions")
+    if lens is not None:
+        _want(lens, torch.int32, (B,), "lens")
+    if parent is not None:
+        _want(parent, torch.int32, (B, N), "parent")
     dev = _one_device("sv_rope", q, freq, k, positions, lens, parent, out_q, out_k, workspace)
     ws = workspace if workspace is not None else _pass_workspace(dev, SV_PASS_ROPE)
     _call(dev, _lib.sv_rope, "sv_rope", q.data_ptr(), sq, _at(k), sk, dt, B, N, Hq, Hk, D, 2 * freq.shape[0], freq.data_ptr(),
-          float(factor), bool(interleaved), bool(inverse), _at(positions), _at(lens), _at(parent), out_q.data_ptr(),
-          _window(out_q, "out_q")[1], _at(out_k), sok, ws.data_ptr(), ws.numel())
+          float(factor), bool(interleaved), bool(inverse), _at(positions), _at(lens), _at(parent), out_q.data_ptr(), soq,
+          _at(out_k), sok, ws.data_ptr(), ws.numel())
     _checked(dev, "sv_rope", workspace)
     return dict(q=out_q, k=out_k)
 
@@ -967,7 +986,7 @@ def sv_kv_attention(cache, q, lens, news=None, parent=None, scale=None, cap=0.0,
     _int32(parent, (B, N), "parent")
     if slopes is not None:
         _want(slopes, torch.float32, (Hq,), "slopes")
-    out = torch.empty_like(q, memory_format=torch.contiguous_format) if out is None else out
+    out = torch.empty_like(q) if out is None else out
     if out.dtype is not q.dtype or out.shape != q.shape:
         raise SpecVerifyError(SV_EINVAL, f"out: want {q.dtype} {tuple(q.shape)}, got {out.dtype} {tuple(out.shape)}")
     dev = _one_device("sv_kv_attention", q, cache.pool, lens, news, parent, slopes, out, workspace)

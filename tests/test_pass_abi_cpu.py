@@ -133,7 +133,7 @@ def test_commit_argument_checks():
         assert f(c=cache(**kw)) == svx.SV_EINVAL, kw
     assert f(c=cache(layers=2, layer_stride=10 * page + 8)) == svx.SV_EALIGN
     assert f(c=cache(layers=1 << 20), B=32768) == svx.SV_EINVAL  # no layer stride
-    assert f(c=cache(layers=1 << 20, layer_stride=1 << 30), B=32768) == svx.SV_EUNSUPPORTED
+    assert f(c=cache(layers=65537, layer_stride=1 << 30)) == svx.SV_EUNSUPPORTED
     for name in ("lens", "n", "out"):
         assert f(**{name: None}) == svx.SV_EINVAL, name
     assert f(out=A) == svx.SV_EINVAL and f(out=P(0x100000008)) == svx.SV_EINVAL
