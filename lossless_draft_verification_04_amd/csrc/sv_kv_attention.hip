@@ -5,8 +5,6 @@ namespace sv {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / kWave;
 constexpr int kTile = 16;       // tokens of a tile, rows of a tile
 constexpr int kWaveTokens = 32; // tokens of a wave's step: two tiles
 
@@ -16,7 +14,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kJoinBlocks = 512;
+constexpr int kJoinBlocks = 512, kJoinThreads = 256;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const f32x2 y = {lo, hi};
@@ -24,15 +22,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // ---------------------------------------------------------------------------
-// Which part of the work a block does: all steps (128 tokens of a sequence for
-// one key head and group of rows) stand in one line, sequence by sequence,
-// and block i of W takes steps [i T / W, (i + 1) T / W).
+// Which part of the work a block does: all steps (32 tokens of a sequence for
+// each of the block's streams, for one key head and group of rows) stand in one
+// line, sequence by sequence, and block i of W takes steps [i T / W, (i + 1) T / W).
 // ---------------------------------------------------------------------------
 struct Span {
   int32_t len, news;  // news = 0: nothing to do
   int64_t u0, units;  // first step of the sequence's tokens, number of steps
 };
 
+template <int UNIT>
 __device__ __forceinline__ Span span_of(const AttentionParams& p, int64_t b) {
   Span s;
   s.len = p.lens[b];
@@ -44,8 +43,8 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, int64_t b) {
   }
   if (s.news == 0) return s;
   const int64_t lo = p.reach > 0 ? max((int64_t)s.len - p.reach + 1, (int64_t)0) : 0;
-  s.u0 = lo / kAttentionUnit;
-  s.units = ((int64_t)s.len + s.news + kAttentionUnit - 1) / kAttentionUnit - s.u0;
+  s.u0 = lo / UNIT;
+  s.units = ((int64_t)s.len + s.news + UNIT - 1) / UNIT - s.u0;
   return s;
 }
 
@@ -264,10 +263,28 @@ __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirs
 constexpr int kStaged = 1024;               // page numbers at a time, -1 for one that is none of the pool
 constexpr int kChunks = SV_MAX_N / 32 + 1;  // steps of 32 tokens that hold nodes
 
+template <int N>
+struct Number {
+  static constexpr int value = N;
+};
+
+// A block's waves: `SPLIT` of them take rows, TILES tiles of 16 each, beside one
+// another, and there are so many streams of tokens.  Waves of the same stream
+// read the same tokens, the second one out of the cache beside it.
+template <int TILES, int SPLIT>
+struct Form {
+  static constexpr int kStreams = SPLIT == 1 ? 4 : 8 / SPLIT;
+  static constexpr int kWaves = SPLIT * kStreams, kThreads = kWaves * kWave;
+  static constexpr int kUnit = kStreams * kWaveTokens;  // tokens of a step
+  static constexpr int kRows = SPLIT * TILES * kTile;
+};
+
 // What the waves of a block share.  QUERY: words of queries kept here.
-template <int D, int ROWS, int QUERY>
-struct Shared {
-  static constexpr int kRows = ROWS;
+template <int D, typename FORM, int QUERY>
+struct Shared : FORM {
+  using FORM::kRows;
+  using FORM::kWaves;
+  static constexpr int ROWS = kRows;
   union {
     struct {  // while a segment is worked on
       u32x4 q[QUERY ? QUERY : 1];  // queries of many rows (the waves' are the same)
@@ -288,7 +305,7 @@ struct Shared {
   // where the block stands: steps of all, the next one, the last + 1, those
   // before sequence b, and that sequence
   int64_t scan[kWaves];
-  int64_t total, at, end, line, units;
+  int64_t total, begin, at, end, line, units;
   int32_t b, len, news, u0;
   int32_t open;  // whether the last item goes on in the next block
   // the segment at hand
@@ -298,6 +315,7 @@ struct Shared {
 // All sequences' steps, and the place that the block begins in; false: none.
 template <typename S>
 __device__ __forceinline__ bool plan(const AttentionParams& p, S& sh) {
+  constexpr int kThreads = S::kThreads, kWaves = S::kWaves;
   const int tid = thread(), lane = tid % kWave, wave = tid / kWave;
   const int64_t each = (int64_t)p.c.H * p.groups;  // items of a sequence
   int64_t total = 0;
@@ -318,7 +336,7 @@ __device__ __forceinline__ bool plan(const AttentionParams& p, S& sh) {
       Span s;
       int64_t mine = 0;
       if (b < p.B) {
-        s = span_of(p, b);
+        s = span_of<S::kUnit>(p, b);
         mine = s.units * each;
         if (s.news < 0 && pass == 0 && blockIdx.x == 0) flag(p.err, SV_DERR_RANGE);
       }
@@ -378,7 +396,7 @@ __device__ __forceinline__ void segment(const AttentionParams& p, S& sh) {
       Span span;
       do {
         line += units * each;
-        span = span_of(p, ++b);
+        span = span_of<S::kUnit>(p, ++b);
         units = span.units;
       } while (at >= line + units * each);
       sh.b = b;
@@ -417,7 +435,7 @@ __device__ __forceinline__ void segment(const AttentionParams& p, S& sh) {
 // What a tree's rows see, and the nodes' depths.
 template <typename S>
 __device__ __forceinline__ void tree(const AttentionParams& p, S& sh) {
-  constexpr int ROWS = S::kRows;
+  constexpr int ROWS = S::kRows, kThreads = S::kThreads;
   const int tid = thread(), len = sh.len, news = sh.news;
   const int32_t* parent = p.parent + (int64_t)sh.b * p.N;
   for (int i = tid; i < news; i += kThreads) {
@@ -493,22 +511,24 @@ __device__ __forceinline__ void finish(const AttentionParams& p, int b, int n, i
 }
 
 // Waves of a SIMD that the registers leave room for: one tile of rows takes up
-// to 128 registers at D = 64, 168 at 128 and 256 at 256; more waves count for
-// more than a few registers spilled (D = 128, four tiles: 325 us of 1024 nodes
-// with 2 waves and 36 registers spilled, 400 with 1), but not for a hundred
-// (D = 256, two tiles: 290 us with 1 wave, 510 with 2).
-constexpr int kernel_waves(int D, int tiles) {
-  return tiles == 1 ? (D == 64 ? 4 : D == 128 ? 3 : 2) : tiles * D <= 256 || D < 256 ? 2 : 1;
+// to 128 registers at D = 64, 168 at 128 and 256 at 256, three at 128 take 256.
+// Registers spilled, or one wave a SIMD, cost more than rows split over waves
+// (32 chains of 17 nodes, D = 128, three tiles a wave: 120 us with 2 waves, 195
+// with 1).
+constexpr int kernel_waves(int D, int tiles, int split) {
+  return split > 1 || tiles > 1 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
 }
 
-template <int D, int TILES, int DT>
-__global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_kernel(const AttentionParams) {
+template <int D, int TILES, int SPLIT, int DT>
+__global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TILES, SPLIT))) void attention_kernel(
+    const AttentionParams) {
+  using F = Form<TILES, SPLIT>;
   constexpr int kParts = DT == SV_F16 ? 3 : 2;
   constexpr int kProbs = DT == SV_F16 ? 2 : 1;
-  constexpr int kRows = TILES * kTile;
-  constexpr bool kQueryLds = TILES * D > 256 || TILES > 2;
+  constexpr int kRows = F::kRows, kWaves = F::kWaves, kStreams = F::kStreams, kThreads = F::kThreads, kUnit = F::kUnit;
+  constexpr bool kQueryLds = TILES * D > 256 || TILES > 2 || (SPLIT > 1 && D == 128);
   constexpr int kHalves = Query<D, kParts>::kHalves;
-  __shared__ __align__(16) Shared<D, kRows, kQueryLds ? TILES * kParts * kHalves * kWave : 0> sh;
+  __shared__ __align__(16) Shared<D, F, kQueryLds ? SPLIT * TILES * kParts * kHalves * kWave : 0> sh;
 
   if (!plan(arguments(), sh)) {
     if (threadIdx.x == 0) static_cast<AttentionItem*>(arguments().desc)[blockIdx.x].b = -1;
@@ -524,7 +544,9 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
     // ---- the rows
     u32x4 q[kQueryLds ? 1 : TILES][kParts][kHalves];
     uint32_t q_scale[kQueryLds ? 1 : TILES];
-    Rows16<D> rows[TILES];
+    // pages of at least 16 tokens: so many steps at a time
+    constexpr int kAtOnce = kStaged * kTile / kUnit;
+    const int last_tile = (hi - 1) / kTile * kTile;
     {
       const AttentionParams& p = arguments();
       const int tid = thread(), lane = tid % kWave, wave = uniform(tid / kWave), l = lane % 16, g = lane / 16;
@@ -534,18 +556,19 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
         const int n = row / p.G, head = sh.h * p.G + row - n * p.G;
         fetch_query<D>(out, q_at + n * p.qs[1] + head * p.qs[2], n < news, g);
       };
-      constexpr int kMine = kQueryLds ? (TILES + kWaves - 1) / kWaves : TILES;
+      constexpr int kAll = SPLIT * TILES;
+      constexpr int kMine = kQueryLds ? (kAll + kWaves - 1) / kWaves : TILES;
       QueryRow<D> in[kMine];
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int t = kQueryLds ? wave + i * kWaves : i;
-        if (t < TILES) query(t, &in[i]);
+        const int t = kQueryLds ? wave + i * kWaves : SPLIT > 1 ? wave / kStreams * TILES + i : i;
+        if (t < kAll) query(t, &in[i]);
       }
-      if (p.parent && (u1 * kAttentionUnit > len / 32 * 32 || p.reach > 0)) tree(p, sh);
+      if (p.parent && (u1 * kUnit > len / 32 * 32 || p.reach > 0)) tree(p, sh);
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
-        const int t = kQueryLds ? wave + i * kWaves : i;
-        if (t < TILES) {
+        const int t = kQueryLds ? wave + i * kWaves : SPLIT > 1 ? wave / kStreams * TILES + i : i;
+        if (t < kAll) {
           Query<D, kParts> mine;
           split_query<D, DT, kParts>(&mine, in[i], p.scale < 0.f);
 #pragma unroll
@@ -570,19 +593,23 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
         sh.pos[tid] = len + (!live ? 0 : p.parent && p.reach > 0 ? sh.depth[n] : n);
         sh.slope[tid] = live && p.slopes ? p.slopes[head] * kLog2e : 0.f;
       }
-#pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) rows[t].o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        rows[t].l = f32x4{0.f, 0.f, 0.f, 0.f};
-        rows[t].limit = kNegInf;
-        rows[t].base = 0.f;
-      }
     }
 
-    // ---- the tokens
+    // ---- the tokens, for a wave of TT tiles of rows, from tile `tile0` of the group on
+    const auto body = [&](auto count) {
+    constexpr int TT = decltype(count)::value;
+    Rows16<D> rows[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) rows[t].o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+      rows[t].l = f32x4{0.f, 0.f, 0.f, 0.f};
+      rows[t].limit = kNegInf;
+      rows[t].base = 0.f;
+    }
     const AttentionParams& p = arguments();
     const int tid = thread(), lane = tid % kWave, wave = uniform(tid / kWave), l = lane % 16, g = lane / 16;
+    const int stream = wave % kStreams, tile0 = wave / kStreams * TILES;
     // Scores are held as exponents of 2: s * unit, with s the product, or (bent)
     // already so where a cap, a bias or a scale of 0 comes first.  A negative
     // scale has turned the queries.
@@ -595,7 +622,6 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
     const int64_t page_stride = p.c.page_stride;
     const int pshift = p.c.pshift, in_page = (1 << pshift) - 1;
     const uint32_t off_ks = (uint32_t)p.c.ks, off_vc = (uint32_t)p.c.vc, off_vs = (uint32_t)p.c.vs;
-    const int last_tile = (hi - 1) / kTile * kTile;
     int page0 = 0;  // page that sh.page[0] stands for
     // Offsets of a lane within a tile: 32 bits beside a wave's base address.
     const uint32_t lane_k = D == 64 ? l * (D / 2) + (g % 2) * 16 : l * (D / 2) + g * 16;
@@ -606,7 +632,7 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
       uint32_t s[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int tt = min(u * kAttentionUnit + wave * kWaveTokens + i * kTile, last_tile);
+        const int tt = min(u * kUnit + stream * kWaveTokens + i * kTile, last_tile);
         const int id = max(uniform(sh.page[(tt >> pshift) - page0]), 0);
         base[i] = pool + id * page_stride;
         s[i] = (uint32_t)(tt & in_page);
@@ -645,7 +671,7 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
 
     // One step of a wave: 32 tokens.  `masked`: some row may not see some of them.
     const auto step = [&](int u, const Tokens<D>& t, bool masked) {
-      const int t0 = u * kAttentionUnit + wave * kWaveTokens;
+      const int t0 = u * kUnit + stream * kWaveTokens;
       if (t0 >= hi) return;
       if (kQueryLds) asm volatile("" ::: "memory");  // the queries are read where they are used
       masked = masked || t0 + kWaveTokens > len || (reach > 0 && t0 <= hi - 1 - reach);
@@ -669,26 +695,26 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
       // what row l of tile r sees of the lane's tokens: bits 0 .. 3 and 16 .. 19
       const auto seen = [&](int r) {
         uint32_t w = ~gone;
-        const int pos = sh.pos[r * kTile + l];
+        const int pos = sh.pos[(tile0 + r) * kTile + l];
         if (t0 + kWaveTokens > len)
-          w &= is_tree ? sh.sees[r * kTile + l][t0 / 32 - len / 32] : bits_below(pos + 1 - t0);
+          w &= is_tree ? sh.sees[(tile0 + r) * kTile + l][t0 / 32 - len / 32] : bits_below(pos + 1 - t0);
         // (a node's place is no lower than its position: what this lets through of a tree is masked above)
         if (reach > 0) w &= ~bits_below(pos - reach + 1 - t0);
         return w >> (4 * g);
       };
-      float x[TILES][8];
+      float x[TT][8];
 #pragma unroll
-      for (int r = 0; r < TILES; ++r)
+      for (int r = 0; r < TT; ++r)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           uint32_t qs;
           if constexpr (kQueryLds)
-            qs = sh.q_scale[r * kWave + lane];
+            qs = sh.q_scale[(tile0 + r) * kWave + lane];
           else
             qs = q_scale[r];
           const f32x4 s = scores<D, kParts>(t, i, qs, g, [&](int part, int h) {
             if constexpr (kQueryLds)
-              return sh.q[((r * kParts + part) * kHalves + h) * kWave + lane];
+              return sh.q[(((tile0 + r) * kParts + part) * kHalves + h) * kWave + lane];
             else
               return q[r][part][h];
           });
@@ -699,7 +725,7 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
         const AttentionParams& a = arguments();
         const float cap = a.cap * kLog2e, up = 2.f / a.cap;
 #pragma unroll
-        for (int r = 0; r < TILES; ++r) {
+        for (int r = 0; r < TT; ++r) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[r][i] *= c;
           if (a.cap > 0.f) {  // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
@@ -721,8 +747,8 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
             }
           }
 #pragma unroll
-          for (int r = 0; r < TILES; ++r) {
-            const float slope = sh.slope[r * kTile + l];
+          for (int r = 0; r < TT; ++r) {
+            const float slope = sh.slope[(tile0 + r) * kTile + l];
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[r][i] = fmaf(slope, d[i], x[r][i]);
           }
@@ -730,7 +756,7 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
       }
       if (masked) {
 #pragma unroll
-        for (int r = 0; r < TILES; ++r) {
+        for (int r = 0; r < TT; ++r) {
           const uint32_t w = seen(r);
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[r][i] = w >> (16 * (i / 4) + i % 4) & 1 ? x[r][i] : kNegInf;
@@ -738,16 +764,17 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
       }
       // New references only where a row's scores pass the old one by 2^8:
       // probabilities up to that are as exact
-      float top[TILES];
+      float top[TT];
       bool move = false;
 #pragma unroll
-      for (int r = 0; r < TILES; ++r) {
+      for (int r = 0; r < TT; ++r) {
         top[r] = max3(max3(x[r][0], x[r][1], x[r][2]), x[r][3], max3(x[r][4], x[r][5], max3(x[r][6], x[r][7], x[r][7])));
         move = move || top[r] > rows[r].limit;
       }
       if (__any(move)) {
 #pragma unroll
-        for (int r = 0; r < TILES; ++r) {
+        for (int r = 0; r < TT; ++r) {
+          if (!__any(top[r] > rows[r].limit)) continue;
           float m = fmaxf(top[r], __shfl_xor(top[r], 16, kWave));
           m = fmaxf(m, __shfl_xor(m, 32, kWave)) * unit;
           const float old = rows[r].reference();
@@ -762,9 +789,9 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
           }
         }
       }
-      u32x4 pr[TILES][kProbs];
+      u32x4 pr[TT][kProbs];
 #pragma unroll
-      for (int r = 0; r < TILES; ++r) {
+      for (int r = 0; r < TT; ++r) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[r][i] = __builtin_amdgcn_exp2f(fmaf(x[r][i], unit, -rows[r].base));
 #pragma unroll
@@ -779,7 +806,7 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
       }
       const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
-      for (int r = 0; r < TILES; ++r)
+      for (int r = 0; r < TT; ++r)
 #pragma unroll
         for (int e = kProbs - 1; e >= 0; --e)
           rows[r].l = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones),
@@ -789,7 +816,7 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
         u32x4 va, vb;
         value_pair<D>(t, vs, j, &va, &vb);
 #pragma unroll
-        for (int r = 0; r < TILES; ++r)
+        for (int r = 0; r < TT; ++r)
 #pragma unroll
           for (int e = kProbs - 1; e >= 0; --e) {
             rows[r].o[2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -806,7 +833,7 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
         for (int i = 0; i < 8; ++i)
           if ((t.vs[i / 4] >> (8 * (i % 4)) & 255u) > 252u) va[i / 2] |= 0x3f80u << (16 * (i % 2));
 #pragma unroll
-        for (int r = 0; r < TILES; ++r) {
+        for (int r = 0; r < TT; ++r) {
           const uint32_t w = seen(r);
           u32x4 vb = {0, 0, 0, 0};
 #pragma unroll
@@ -826,15 +853,14 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
     };
 
     {
-      const int at_once = min(kStaged << min(pshift, 12) >> 7, 1 << 15);  // steps whose pages are staged
-      for (int v0 = u0; v0 < u1; v0 += at_once) {
-        const int v1 = min(v0 + at_once, u1);
-        page0 = v0 * kAttentionUnit >> pshift;
+      for (int v0 = u0; v0 < u1; v0 += kAtOnce) {
+        const int v1 = min(v0 + kAtOnce, u1);
+        page0 = v0 * kUnit >> pshift;
         bool lost = false;
         {
           const AttentionParams& a = arguments();
           const int32_t* pages = a.c.pages + (int64_t)sh.b * a.c.max_pages + page0;
-          const int staged = (min(v1 * kAttentionUnit - 1, last_tile) >> pshift) - page0 + 1;
+          const int staged = (min(v1 * kUnit - 1, last_tile) >> pshift) - page0 + 1;
           if (v0 > u0) __syncthreads();  // (the first time, a segment's end was one)
           for (int i = thread(); i < staged; i += kThreads) {
             const int32_t id = pages[i];
@@ -843,7 +869,7 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
             sh.page[i] = bad ? -1 : id;
           }
           if (lost) flag(a.err, SV_DERR_RANGE);
-          lost = __syncthreads_or(lost);
+          lost = uniform(__syncthreads_or(lost));
         }
         // The next step's loads fly while this one is worked on; behind the last
         // it is read again, so that the number of loads in flight is known.
@@ -860,15 +886,16 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
       }
     }
 
-    // ---- the waves' sums together, a tile of rows at a time
+    // ---- the streams' sums together, a tile of rows at a time
     {
       const AttentionParams& a = arguments();
-      const int id = thread(), wave = uniform(id / kWave), l = id % 16, g = id % kWave / 16;
-      const int b = sh.b, row0 = sh.group * kRows, slot = sh.slot;
+      const int id = thread(), l = id % 16, g = id % kWave / 16;
+      const int w0 = wave - stream;  // the wave of the first stream
+      const int b = sh.b, row0 = sh.group * kRows + tile0 * kTile, slot = sh.slot;
       const bool whole = sh.whole;
       more = sh.at < sh.end;  // read ahead of the barriers behind which the next segment is planned
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) {
+      for (int t = 0; t < TT; ++t) {
         if (g == 0) {
           sh.m[wave][t * kTile + l] = rows[t].reference();
           sh.l[wave][t * kTile + l] = rows[t].l[0];
@@ -876,57 +903,69 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
       }
       __syncthreads();
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        float m = kNegInf;
+      for (int t = 0; t < TILES; ++t) {  // as many barriers for every wave
+        if (t < TT) {
+          const Rows16<D>& mine = rows[t < TT ? t : 0];
+            float m = kNegInf;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, sh.m[w][t * kTile + l]);
-        // NaN scores leave m at -inf: their sums are NaN, times anything
-        const float f = part_weight(rows[t].reference(), m);
+            for (int w = 0; w < kStreams; ++w) m = fmaxf(m, sh.m[w0 + w][t * kTile + l]);
+            const float f = part_weight(mine.reference(), m);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int i = 0; i < D / 16; i += 4) {
-            const f32x4 v = {rows[t].o[i][k] * f, rows[t].o[i + 1][k] * f, rows[t].o[i + 2][k] * f, rows[t].o[i + 3][k] * f};
-            *reinterpret_cast<f32x4*>(&sh.o[wave][l][(4 * g + k) * (D / 16) + i]) = v;
-          }
+              for (int i = 0; i < D / 16; i += 4) {
+                const f32x4 v = {mine.o[i][k] * f, mine.o[i + 1][k] * f, mine.o[i + 2][k] * f, mine.o[i + 3][k] * f};
+                *reinterpret_cast<f32x4*>(&sh.o[wave][l][(4 * g + k) * (D / 16) + i]) = v;
+              }
+        }
         __syncthreads();
-        // a row to 16 threads, D/16 neighbouring values each
-        const int r = id / 16, col = id % 16;
+        // a row to 4 threads of each stream, neighbouring values each
+        constexpr int kCols = 4 * kStreams, kCount = D / kCols;
+        const int in = id - w0 * kWave;
+        const int r = in / kCols, col = in % kCols * kCount;
         const int rr = t * kTile + r, row = row0 + rr;
         const int n = row / a.G, head = sh.h * a.G + row - n * a.G;
-        if (n < sh.news) {
+        if (t < TT && n < sh.news) {
           float mm = kNegInf, ll = 0.f;
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) mm = fmaxf(mm, sh.m[w][rr]);
+          for (int w = 0; w < kStreams; ++w) mm = fmaxf(mm, sh.m[w0 + w][rr]);
 #pragma unroll
-          for (int w = 0; w < kWaves; ++w) {
-            const float mw = sh.m[w][rr];
-            ll += sh.l[w][rr] * part_weight(mw, mm);
-          }
-          float o[D / 16];
+          for (int w = 0; w < kStreams; ++w) ll += sh.l[w0 + w][rr] * part_weight(sh.m[w0 + w][rr], mm);
+          float o[kCount];
 #pragma unroll
-          for (int i = 0; i < D / 16; i += 4) {
-            f32x4 v = *reinterpret_cast<const f32x4*>(&sh.o[0][r][col * (D / 16) + i]);
+          for (int i = 0; i < kCount; i += 4) {
+            f32x4 v = *reinterpret_cast<const f32x4*>(&sh.o[w0][r][col + i]);
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w) v += *reinterpret_cast<const f32x4*>(&sh.o[w][r][col * (D / 16) + i]);
+            for (int w = 1; w < kStreams; ++w) v += *reinterpret_cast<const f32x4*>(&sh.o[w0 + w][r][col + i]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) o[i + k] = v[k];
           }
           if (whole) {
-            finish<D, DT, D / 16>(a, b, n, head, col * (D / 16), o, mm, ll, a.parent ? sh.depth[n] : n);
+            finish<D, DT, kCount>(a, b, n, head, col, o, mm, ll, a.parent ? sh.depth[n] : n);
           } else {
-            float* po = a.part_o + ((int64_t)slot * kRows + rr) * D + col * (D / 16);
+            const int64_t part = (int64_t)slot * kRows + tile0 * kTile + rr;
+            float* po = a.part_o + part * D + col;
 #pragma unroll
-            for (int i = 0; i < D / 16; i += 4)
-              *reinterpret_cast<f32x4*>(po + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+            for (int i = 0; i < kCount; i += 4) *reinterpret_cast<f32x4*>(po + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
             if (col == 0) {
-              a.part_ml[((int64_t)slot * kRows + rr) * 2] = mm;
-              a.part_ml[((int64_t)slot * kRows + rr) * 2 + 1] = ll;
+              a.part_ml[part * 2] = mm;
+              a.part_ml[part * 2 + 1] = ll;
             }
           }
         }
         __syncthreads();
       }
+    }
+    };
+    // the last rows' waves may have fewer tiles
+    if constexpr (SPLIT > 1 && TILES > 1) {
+      const int wave = uniform(thread() / kWave);
+      if (arguments().all_tiles - (sh.group * SPLIT + wave / kStreams) * TILES < TILES)
+        body(Number<TILES - 1>{});
+      else
+        body(Number<TILES>{});
+    } else {
+      body(Number<TILES>{});
     }
   } while (more);
   if (threadIdx.x == 0 && !sh.open) static_cast<AttentionItem*>(arguments().desc)[blockIdx.x].b = -1;
@@ -941,14 +980,15 @@ __global__ __launch_bounds__(kThreads, kernel_waves(D, TILES)) void attention_ke
 // take a row together, a slice of the parts each, whose sums are added up in LDS
 // in a fixed order.
 template <int D, int DT>
-__global__ __launch_bounds__(kThreads) void join_kernel(const AttentionParams p) {
+__global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttentionParams p) {
+  constexpr int kThreads = kJoinThreads, kWaves = kThreads / kWave;
   constexpr int kCols = D / 4, kSlices = kThreads / kCols, kFew = 8;
   __shared__ f32x4 s_sum[kSlices][kCols];
   __shared__ float s_l[kSlices], s_m[kSlices];
   __shared__ int32_t s_end[kAttentionBlocks];  // pieces of work up to a block's item
   __shared__ int32_t s_scan[kWaves];
   const AttentionItem* const items = static_cast<const AttentionItem*>(p.desc);
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, rows = p.tiles * kTile;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, rows = p.split * p.tiles * kTile;
   const auto last_of = [&](const AttentionItem& it) { return block_of(it.last, it.total, p); };
   // every block's item, if one begins there and goes on, and the pieces it makes
   int32_t pieces = 0;
@@ -1054,23 +1094,28 @@ __global__ __launch_bounds__(kThreads) void join_kernel(const AttentionParams p)
   }
 }
 
+template <int D, int DT, int TILES, int SPLIT>
+bool run(const AttentionParams& p, hipStream_t s) {
+  if (p.tiles != TILES || p.split != SPLIT) return false;
+  attention_kernel<D, TILES, SPLIT, DT><<<(uint32_t)p.blocks, Form<TILES, SPLIT>::kThreads, 0, s>>>(p);
+  return true;
+}
+
+// The forms that attention_form() chooses among.
 template <int D, int DT>
 hipError_t attention(const AttentionParams& p, hipStream_t s) {
-  const dim3 grid((uint32_t)p.blocks);
-  switch (p.tiles) {
-    case 1: attention_kernel<D, 1, DT><<<grid, kThreads, 0, s>>>(p); break;
-    case 2: attention_kernel<D, 2, DT><<<grid, kThreads, 0, s>>>(p); break;
-    default:
-      if constexpr (D != 256) {
-        if (p.tiles == 3)
-          attention_kernel<D, 3, DT><<<grid, kThreads, 0, s>>>(p);
-        else
-          attention_kernel<D, 4, DT><<<grid, kThreads, 0, s>>>(p);
-      }
-  }
+  bool ran = run<D, DT, 1, 1>(p, s);
+  if constexpr (D == 64)
+    ran = ran || run<D, DT, 2, 1>(p, s) || run<D, DT, 3, 1>(p, s) || run<D, DT, 4, 1>(p, s) || run<D, DT, 3, 2>(p, s) ||
+          run<D, DT, 4, 2>(p, s) || run<D, DT, 3, 4>(p, s) || run<D, DT, 4, 4>(p, s);
+  if constexpr (D == 128)
+    ran = ran || run<D, DT, 2, 1>(p, s) || run<D, DT, 3, 1>(p, s) || run<D, DT, 2, 2>(p, s) || run<D, DT, 3, 2>(p, s) ||
+          run<D, DT, 2, 4>(p, s) || run<D, DT, 3, 4>(p, s);
+  if constexpr (D == 256) ran = ran || run<D, DT, 1, 2>(p, s) || run<D, DT, 1, 4>(p, s);
+  if (!ran) return hipErrorInvalidValue;
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  join_kernel<D, DT><<<kJoinBlocks, kThreads, 0, s>>>(p);
+  join_kernel<D, DT><<<kJoinBlocks, kJoinThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 

@@ -69,7 +69,8 @@ struct AttentionParams {
   const float* slopes;
   int32_t reach;
   int32_t* err;
-  int32_t tiles, groups;  // tiles of 16 rows in a group of rows, groups
+  int32_t tiles, split;  // a block's rows: `split` waves beside one another with so many tiles of 16 each
+  int32_t groups, all_tiles;  // groups of so many rows, and all tiles
   int32_t blocks, log_blocks;
   float* part_o;  // [2 * blocks][tiles * 16][D]
   float* part_ml; // [2 * blocks][tiles * 16][2]
@@ -89,9 +90,24 @@ hipError_t launch_kv_read(const KvMoveParams& p, sv_dtype dt, int D, hipStream_t
 hipError_t launch_kv_commit(const KvCommitParams& p, int D, hipStream_t s);
 hipError_t launch_kv_attention(const AttentionParams& p, sv_dtype dt, int D, hipStream_t s);
 
-// Rows of nodes x heads are taken in groups of up to this many tiles of 16.
-inline int attention_tiles(int D) { return D == 256 ? 2 : 4; }
+// How `all` tiles of 16 rows (nodes x heads of a key head) are taken: as many
+// in a wave as its registers hold (`most`), more by two or four waves beside one
+// another, which share the tokens they read, more still by several blocks.
+struct AttentionForm {
+  int tiles, split, groups, blocks;
+};
+inline AttentionForm attention_form(int D, int all) {
+  const int most = D == 64 ? 4 : D == 128 ? 3 : 1;
+  AttentionForm f;
+  f.groups = (all + 4 * most - 1) / (4 * most);
+  const int each = (all + f.groups - 1) / f.groups;
+  f.split = each <= most ? 1 : each <= 2 * most ? 2 : 4;
+  f.tiles = (each + f.split - 1) / f.split;
+  f.groups = (all + f.split * f.tiles - 1) / (f.split * f.tiles);
+  // as many blocks as are resident at once
+  f.blocks = f.split > 1 ? 256 : f.tiles > 1 || D == 256 ? 512 : D == 64 ? 1024 : 768;
+  return f;
+}
 constexpr int kAttentionBlocks = 1024;  // at most
-constexpr int kAttentionUnit = 128;  // tokens of a step: 32 for each of a block's 4 waves
 
 }  // namespace sv

@@ -102,7 +102,8 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
 
 struct PassPlan {
   size_t bytes;
-  int32_t tiles, groups, blocks;
+  AttentionForm form;
+  int32_t tiles;
   size_t off_desc, off_ml, off_o;
 };
 
@@ -111,14 +112,12 @@ sv_status plan_attention(int32_t B, int32_t N, int32_t Hq, int32_t H, int32_t D,
   if (D != 64 && D != 128 && D != 256) return SV_EUNSUPPORTED;
   if (B > SV_MAX_SEQ || N > SV_MAX_N || Hq > SV_MAX_HEADS) return SV_EUNSUPPORTED;
   const int tiles = (N * (Hq / H) + 15) / 16;
-  pl->groups = (tiles + attention_tiles(D) - 1) / attention_tiles(D);
-  pl->tiles = (tiles + pl->groups - 1) / pl->groups;
-  pl->groups = (tiles + pl->tiles - 1) / pl->tiles;
-  pl->blocks = pl->tiles > 1 || D == 256 ? 512 : D == 64 ? 1024 : 768;
-  const size_t rows = (size_t)2 * pl->blocks * pl->tiles * 16;
+  pl->form = attention_form(D, tiles);
+  pl->tiles = tiles;
+  const size_t rows = (size_t)2 * pl->form.blocks * pl->form.split * pl->form.tiles * 16;
   size_t off = kWsFixed;
   pl->off_desc = off;
-  off = align_up(off + (size_t)pl->blocks * sizeof(AttentionItem), 256);
+  off = align_up(off + (size_t)pl->form.blocks * sizeof(AttentionItem), 256);
   pl->off_ml = off;
   off = align_up(off + rows * 2 * sizeof(float), 256);
   pl->off_o = off;
@@ -335,10 +334,12 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
   p.slopes = slopes;
   p.reach = reach;
   p.err = reinterpret_cast<int32_t*>(w);
-  p.tiles = pl.tiles;
-  p.groups = pl.groups;
-  p.blocks = pl.blocks;
-  p.log_blocks = __builtin_ctz((unsigned)pl.blocks);
+  p.tiles = pl.form.tiles;
+  p.split = pl.form.split;
+  p.groups = pl.form.groups;
+  p.all_tiles = pl.tiles;
+  p.blocks = pl.form.blocks;
+  p.log_blocks = __builtin_ctz((unsigned)pl.form.blocks);
   p.desc = w + pl.off_desc;
   p.part_ml = reinterpret_cast<float*>(w + pl.off_ml);
   p.part_o = reinterpret_cast<float*>(w + pl.off_o);
