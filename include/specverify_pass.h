@@ -115,10 +115,12 @@ sv_status sv_pass_workspace_size(sv_pass_op op, int32_t B, int32_t N, int32_t Hq
  *   interleaved: pairs are (2i, 2i+1), else (i, i + R/2)
  *   positions [B, N] int32; or NULL: lens[b] (NULL: 0) + depth of the node in
  *     parent [B, N] (NULL: its number); with parent, N <= SV_MAX_N
- * out_q, out_k may be q, k (the same pointer and strides: in place); they must
- * not overlap them otherwise.  Angles are formed in 64 bits and reduced to a
+ * out_q, out_k may be q, k (the same pointer and strides: in place) and must
+ * not overlap them otherwise; all may be views of different heads of one tensor
+ * (a fused projection), with equal strides.  Angles are formed in 64 bits and reduced to a
  * turn before their sine is taken, so far positions keep their digits.  A
- * node whose parent is not before it sets SV_DERR_TREE and has depth 0.
+ * node whose parent is not before it sets SV_DERR_TREE and has depth 0.  All N
+ * nodes turn, padding too.
  */
 sv_status sv_rope(const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride, sv_dtype dt,
                   int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D, int32_t R, const double* freq, float factor,
@@ -189,7 +191,8 @@ sv_status sv_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32
  *   lens [B], news [B] (NULL: N) int32: nodes news[b] .. N - 1 are padding,
  *     their outputs are left as they were
  *   parent [B, N] or NULL (a chain); N <= SV_MAX_N
- *   slopes [Hq] float or NULL; out_lse [B, N, Hq] float or NULL
+ *   slopes [Hq] float or NULL; out_lse [B, N, Hq] float or NULL, apart from
+ *     q and out
  * Hq is a multiple of cache->H.  A sequence whose length or count is out of
  * range sets SV_DERR_RANGE and is left as it was.  A page outside [0,
  * num_pages) sets it too; its tokens count as masked.  A row that sees
@@ -198,8 +201,8 @@ sv_status sv_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32
  * token that a row does not see does not reach it; queries are finite (a row
  * with a NaN or an infinity is NaN).
  *
- * The cache is read once for all query heads of a key head and up to 64 rows
- * (32 at D = 256) of nodes x heads.  Keys are multiplied in 4 bits as they are,
+ * The cache is read once for all query heads of a key head and up to 256 rows
+ * (192 at D = 128, 64 at D = 256) of nodes x heads.  Keys are multiplied in 4 bits as they are,
  * by queries split exactly into two (fp16: three) parts of 8 bits; products,
  * sums and the softmax are held in 32 bits, probabilities are rounded to the
  * 8 bits of bf16 (fp16: 16 bits) before they multiply the values, and are summed
@@ -218,7 +221,7 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
  *   n [B], path [B, M]: out_len and out_path of sv_verify_tree (M its
  *     max_depth; what stands behind n[b] is not read); path NULL: a chain
  *     (out_n of sv_verify_chain), nothing moves
- *   out_lens [B] must not overlap lens
+ *   out_lens [B] must not overlap lens, n or path
  * n[b] = -1 leaves a sequence as it was (it took no part), out_lens[b] =
  * lens[b].  So does a path that does not rise from 1 on within SV_MAX_N nodes,
  * which sets SV_DERR_TREE, and n outside [-1, M] (a chain: n < -1), a length out

@@ -174,10 +174,12 @@ __global__ __launch_bounds__(kThreads) void commit_kernel(const KvCommitParams p
       }
     }
   }
-  const int bad = __syncthreads_or((range ? 1 : 0) | (tree ? 2 : 0));
+  range = __syncthreads_or(range);
+  tree = path && __syncthreads_or(tree);
+  const bool bad = range || tree;
   if (h == 0 && layer0 == 0 && threadIdx.x == 0) {  // the sequence's first block writes its length and flags
     p.out_lens[b] = bad || n < 0 ? (int32_t)len : (int32_t)(len + 1 + n);
-    if (bad) flag(p.err, (bad & 1 ? SV_DERR_RANGE : 0) | (bad & 2 ? SV_DERR_TREE : 0));
+    if (bad) flag(p.err, (range ? SV_DERR_RANGE : 0) | (tree ? SV_DERR_TREE : 0));
   }
   if (bad || !path || n <= 0) return;
   constexpr int w = D / 32;

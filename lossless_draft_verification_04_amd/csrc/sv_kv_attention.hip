@@ -302,10 +302,10 @@ struct Shared : FORM {
   uint32_t sees[ROWS][kChunks];
   int32_t pos[ROWS];   // the rows' positions
   float slope[ROWS];   // and slopes, of exponents of 2
-  // where the block stands: steps of all, the next one, the last + 1, those
+  // where the block stands: steps of all, its next one, its last + 1, those
   // before sequence b, and that sequence
   int64_t scan[kWaves];
-  int64_t total, begin, at, end, line, units;
+  int64_t total, at, end, line, units;
   int32_t b, len, news, u0;
   int32_t open;  // whether the last item goes on in the next block
   // the segment at hand
@@ -488,8 +488,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // output: o / l, and the logarithm of the sum of e^s.  Biases are held relative
 // to the root's distances.
 template <int D, int DT, int COUNT>
-__device__ __forceinline__ void finish(const AttentionParams& p, int b, int n, int head, int col, const float* o, float m,
-                                       float l, int depth) {
+__device__ __forceinline__ void finish(const AttentionParams& p, int b, int n, int head, int col, const float* o,
+                                       float m, float l, int depth) {
   const float inv = l == 0.f ? 0.f : 1.f / l;
   char* out = p.out + b * p.os[0] + n * p.os[1] + head * p.os[2] + col * 2;
 #pragma unroll
@@ -498,7 +498,8 @@ __device__ __forceinline__ void finish(const AttentionParams& p, int b, int n, i
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const float y = l == 0.f ? 0.f : o[i + k] * inv;
-      const uint16_t e = DT == SV_F16 ? __builtin_bit_cast(uint16_t, (_Float16)y) : __builtin_bit_cast(uint16_t, (__bf16)y);
+      const uint16_t e =
+          DT == SV_F16 ? __builtin_bit_cast(uint16_t, (_Float16)y) : __builtin_bit_cast(uint16_t, (__bf16)y);
       w |= (uint64_t)e << (16 * k);
     }
     *reinterpret_cast<uint64_t*>(out + i * 2) = w;
@@ -597,262 +598,263 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
 
     // ---- the tokens, for a wave of TT tiles of rows, from tile `tile0` of the group on
     const auto body = [&](auto count) {
-    constexpr int TT = decltype(count)::value;
-    Rows16<D> rows[TT];
+      constexpr int TT = decltype(count)::value;
+      Rows16<D> rows[TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t) {
+      for (int t = 0; t < TT; ++t) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) rows[t].o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-      rows[t].l = f32x4{0.f, 0.f, 0.f, 0.f};
-      rows[t].limit = kNegInf;
-      rows[t].base = 0.f;
-    }
-    const AttentionParams& p = arguments();
-    const int tid = thread(), lane = tid % kWave, wave = uniform(tid / kWave), l = lane % 16, g = lane / 16;
-    const int stream = wave % kStreams, tile0 = wave / kStreams * TILES;
-    // Scores are held as exponents of 2: s * unit, with s the product, or (bent)
-    // already so where a cap, a bias or a scale of 0 comes first.  A negative
-    // scale has turned the queries.
-    const float c = fabsf(p.scale) * kLog2e;
-    const bool bent = p.cap > 0.f || p.slopes || c == 0.f;
-    const float unit = bent ? 1.f : c, per_unit = 1.f / unit;
-    const bool is_tree = p.parent != nullptr;
-    const int reach = p.reach;
-    const char* const pool = p.c.pool + uniform(sh.h) * p.c.head;
-    const int64_t page_stride = p.c.page_stride;
-    const int pshift = p.c.pshift, in_page = (1 << pshift) - 1;
-    const uint32_t off_ks = (uint32_t)p.c.ks, off_vc = (uint32_t)p.c.vc, off_vs = (uint32_t)p.c.vs;
-    int page0 = 0;  // page that sh.page[0] stands for
-    // Offsets of a lane within a tile: 32 bits beside a wave's base address.
-    const uint32_t lane_k = D == 64 ? l * (D / 2) + (g % 2) * 16 : l * (D / 2) + g * 16;
-    const uint32_t lane_ks = D == 64 ? l * (D / 32) + g % 2 : l * (D / 32) + g;
-    const uint32_t lane_v = (g * 16 + l) * (D / 8), lane_vs = (g * (D / 32) + l * (D / 16) / 32) * 4;
-    const auto fetch = [&](int u, Tokens<D>* t) {
-      const char* base[2];
-      uint32_t s[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int tt = min(u * kUnit + stream * kWaveTokens + i * kTile, last_tile);
-        const int id = max(uniform(sh.page[(tt >> pshift) - page0]), 0);
-        base[i] = pool + id * page_stride;
-        s[i] = (uint32_t)(tt & in_page);
+        for (int i = 0; i < D / 16; ++i) rows[t].o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        rows[t].l = f32x4{0.f, 0.f, 0.f, 0.f};
+        rows[t].limit = kNegInf;
+        rows[t].base = 0.f;
       }
-      const uint32_t at_k = opaque(lane_k), at_ks = opaque(lane_ks), at_v = opaque(lane_v), at_vs = opaque(lane_vs);
-      if constexpr (D == 64) {
-        const char* k0 = base[0] + s[0] * (D / 2);
-        const char* k1 = base[1] + s[1] * (D / 2);
-        t->k[0] = *reinterpret_cast<const i32x4*>((g / 2 ? k1 : k0) + at_k);
-        const char* s0 = base[0] + off_ks + s[0] * (D / 32);
-        const char* s1 = base[1] + off_ks + s[1] * (D / 32);
-        t->ks[0] = (uint8_t)(g / 2 ? s1 : s0)[at_ks];
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int k = 0; k < D / 128; ++k) {
-            t->k[i * (D / 128) + k] = *reinterpret_cast<const i32x4*>(base[i] + s[i] * (D / 2) + k * 64 + at_k);
-            t->ks[i * (D / 128) + k] = (uint8_t)(base[i] + off_ks + s[i] * (D / 32) + k * 4)[at_ks];
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const char* vb = base[i] + off_vc + s[i] * (D / 2);
-        if constexpr (D == 64) {
-          const uint64_t w = *reinterpret_cast<const uint64_t*>(vb + at_v);
-          t->v[0][2 * i] = (uint32_t)w;
-          t->v[0][2 * i + 1] = (uint32_t)(w >> 32);
-        } else {
-#pragma unroll
-          for (int k = 0; k < D / 128; ++k) t->v[i * (D / 128) + k] = *reinterpret_cast<const u32x4*>(vb + k * 16 + at_v);
-        }
-        t->vs[i] = *reinterpret_cast<const uint32_t*>(base[i] + off_vs + s[i] * (D / 32) + at_vs);
-      }
-    };
-
-    // One step of a wave: 32 tokens.  `masked`: some row may not see some of them.
-    const auto step = [&](int u, const Tokens<D>& t, bool masked) {
-      const int t0 = u * kUnit + stream * kWaveTokens;
-      if (t0 >= hi) return;
-      if (kQueryLds) asm volatile("" ::: "memory");  // the queries are read where they are used
-      masked = masked || t0 + kWaveTokens > len || (reach > 0 && t0 <= hi - 1 - reach);
-      uint32_t vs[2] = {t.vs[0], t.vs[1]};
-      uint32_t gone = 0;  // tokens without a page
-      bool nan = false;
-      if (masked) {
-        // Beyond the largest scale there is only NaN, and bytes never written,
-        // whose values may overflow: they are added where they are seen
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if ((vs[i / 4] >> (8 * (i % 4)) & 255u) > 252u) {
-            nan = true;
-            vs[i / 4] &= ~(255u << (8 * (i % 4)));
-          }
-        nan = __any(nan);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (sh.page[(min(t0 + i * kTile, last_tile) >> pshift) - page0] < 0) gone |= 0xffffu << (16 * i);
-      }
-      // what row l of tile r sees of the lane's tokens: bits 0 .. 3 and 16 .. 19
-      const auto seen = [&](int r) {
-        uint32_t w = ~gone;
-        const int pos = sh.pos[(tile0 + r) * kTile + l];
-        if (t0 + kWaveTokens > len)
-          w &= is_tree ? sh.sees[(tile0 + r) * kTile + l][t0 / 32 - len / 32] : bits_below(pos + 1 - t0);
-        // (a node's place is no lower than its position: what this lets through of a tree is masked above)
-        if (reach > 0) w &= ~bits_below(pos - reach + 1 - t0);
-        return w >> (4 * g);
-      };
-      float x[TT][8];
-#pragma unroll
-      for (int r = 0; r < TT; ++r)
+      const AttentionParams& p = arguments();
+      const int tid = thread(), lane = tid % kWave, wave = uniform(tid / kWave), l = lane % 16, g = lane / 16;
+      const int stream = wave % kStreams, tile0 = wave / kStreams * TILES;
+      // Scores are held as exponents of 2: s * unit, with s the product, or (bent)
+      // already so where a cap, a bias or a scale of 0 comes first.  A negative
+      // scale has turned the queries.
+      const float c = fabsf(p.scale) * kLog2e;
+      const bool bent = p.cap > 0.f || p.slopes || c == 0.f;
+      const float unit = bent ? 1.f : c, per_unit = 1.f / unit;
+      const bool is_tree = p.parent != nullptr;
+      const int reach = p.reach;
+      const char* const pool = p.c.pool + uniform(sh.h) * p.c.head;
+      const int64_t page_stride = p.c.page_stride;
+      const int pshift = p.c.pshift, in_page = (1 << pshift) - 1;
+      const uint32_t off_ks = (uint32_t)p.c.ks, off_vc = (uint32_t)p.c.vc, off_vs = (uint32_t)p.c.vs;
+      int page0 = 0;  // page that sh.page[0] stands for
+      // Offsets of a lane within a tile: 32 bits beside a wave's base address.
+      const uint32_t lane_k = D == 64 ? l * (D / 2) + (g % 2) * 16 : l * (D / 2) + g * 16;
+      const uint32_t lane_ks = D == 64 ? l * (D / 32) + g % 2 : l * (D / 32) + g;
+      const uint32_t lane_v = (g * 16 + l) * (D / 8), lane_vs = (g * (D / 32) + l * (D / 16) / 32) * 4;
+      const auto fetch = [&](int u, Tokens<D>* t) {
+        const char* base[2];
+        uint32_t s[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          uint32_t qs;
-          if constexpr (kQueryLds)
-            qs = sh.q_scale[(tile0 + r) * kWave + lane];
-          else
-            qs = q_scale[r];
-          const f32x4 s = scores<D, kParts>(t, i, qs, g, [&](int part, int h) {
-            if constexpr (kQueryLds)
-              return sh.q[(((tile0 + r) * kParts + part) * kHalves + h) * kWave + lane];
-            else
-              return q[r][part][h];
-          });
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[r][4 * i + k] = s[k];
+          const int tt = min(u * kUnit + stream * kWaveTokens + i * kTile, last_tile);
+          const int id = max(uniform(sh.page[(tt >> pshift) - page0]), 0);
+          base[i] = pool + id * page_stride;
+          s[i] = (uint32_t)(tt & in_page);
         }
-      if (bent) {
-        const AttentionParams& a = arguments();
-        const float cap = a.cap * kLog2e, up = 2.f / a.cap;
+        const uint32_t at_k = opaque(lane_k), at_ks = opaque(lane_ks), at_v = opaque(lane_v), at_vs = opaque(lane_vs);
+        if constexpr (D == 64) {
+          const char* k0 = base[0] + s[0] * (D / 2);
+          const char* k1 = base[1] + s[1] * (D / 2);
+          t->k[0] = *reinterpret_cast<const i32x4*>((g / 2 ? k1 : k0) + at_k);
+          const char* s0 = base[0] + off_ks + s[0] * (D / 32);
+          const char* s1 = base[1] + off_ks + s[1] * (D / 32);
+          t->ks[0] = (uint8_t)(g / 2 ? s1 : s0)[at_ks];
+        } else {
 #pragma unroll
-        for (int r = 0; r < TT; ++r) {
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[r][i] *= c;
-          if (a.cap > 0.f) {  // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              x[r][i] = fmaf(-2.f * cap, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[r][i] * up)), cap);
-          }
-        }
-        if (a.slopes) {  // relative to the root's distances, which all of a row's scores share
-          const int t1 = t0 + 4 * g - len;
-          float d[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) d[i] = (float)(t1 + (i / 4) * kTile + i % 4);
-          if (is_tree && t0 + kWaveTokens > len) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int at = t1 + (i / 4) * kTile + i % 4;
-              if (at >= 0 && at < news) d[i] = (float)sh.depth[at];
+            for (int k = 0; k < D / 128; ++k) {
+              t->k[i * (D / 128) + k] = *reinterpret_cast<const i32x4*>(base[i] + s[i] * (D / 2) + k * 64 + at_k);
+              t->ks[i * (D / 128) + k] = (uint8_t)(base[i] + off_ks + s[i] * (D / 32) + k * 4)[at_ks];
             }
-          }
-#pragma unroll
-          for (int r = 0; r < TT; ++r) {
-            const float slope = sh.slope[(tile0 + r) * kTile + l];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[r][i] = fmaf(slope, d[i], x[r][i]);
-          }
         }
-      }
-      if (masked) {
 #pragma unroll
-        for (int r = 0; r < TT; ++r) {
-          const uint32_t w = seen(r);
+        for (int i = 0; i < 2; ++i) {
+          const char* vb = base[i] + off_vc + s[i] * (D / 2);
+          if constexpr (D == 64) {
+            const uint64_t w = *reinterpret_cast<const uint64_t*>(vb + at_v);
+            t->v[0][2 * i] = (uint32_t)w;
+            t->v[0][2 * i + 1] = (uint32_t)(w >> 32);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) x[r][i] = w >> (16 * (i / 4) + i % 4) & 1 ? x[r][i] : kNegInf;
-        }
-      }
-      // New references only where a row's scores pass the old one by 2^8:
-      // probabilities up to that are as exact
-      float top[TT];
-      bool move = false;
-#pragma unroll
-      for (int r = 0; r < TT; ++r) {
-        top[r] = max3(max3(x[r][0], x[r][1], x[r][2]), x[r][3], max3(x[r][4], x[r][5], max3(x[r][6], x[r][7], x[r][7])));
-        move = move || top[r] > rows[r].limit;
-      }
-      if (__any(move)) {
-#pragma unroll
-        for (int r = 0; r < TT; ++r) {
-          if (!__any(top[r] > rows[r].limit)) continue;
-          float m = fmaxf(top[r], __shfl_xor(top[r], 16, kWave));
-          m = fmaxf(m, __shfl_xor(m, 32, kWave)) * unit;
-          const float old = rows[r].reference();
-          m = fmaxf(old, m);
-          if (m > kNegInf) {
-            const float f = __builtin_amdgcn_exp2f(old - m);
-            rows[r].base = m;
-            rows[r].limit = (m + 8.f) * per_unit;
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) rows[r].o[i] *= f;
-            rows[r].l *= f;
+            for (int k = 0; k < D / 128; ++k)
+              t->v[i * (D / 128) + k] = *reinterpret_cast<const u32x4*>(vb + k * 16 + at_v);
           }
+          t->vs[i] = *reinterpret_cast<const uint32_t*>(base[i] + off_vs + s[i] * (D / 32) + at_vs);
         }
-      }
-      u32x4 pr[TT][kProbs];
+      };
+
+      // One step of a wave: 32 tokens.  `masked`: some row may not see some of them.
+      const auto step = [&](int u, const Tokens<D>& t, bool masked) {
+        const int t0 = u * kUnit + stream * kWaveTokens;
+        if (t0 >= hi) return;
+        if (kQueryLds) asm volatile("" ::: "memory");  // the queries are read where they are used
+        masked = masked || t0 + kWaveTokens > len || (reach > 0 && t0 <= hi - 1 - reach);
+        uint32_t vs[2] = {t.vs[0], t.vs[1]};
+        uint32_t gone = 0;  // tokens without a page
+        bool nan = false;
+        if (masked) {
+          // Beyond the largest scale there is only NaN, and bytes never written,
+          // whose values may overflow: they are added where they are seen
 #pragma unroll
-      for (int r = 0; r < TT; ++r) {
+          for (int i = 0; i < 8; ++i)
+            if ((vs[i / 4] >> (8 * (i % 4)) & 255u) > 252u) {
+              nan = true;
+              vs[i / 4] &= ~(255u << (8 * (i % 4)));
+            }
+          nan = __any(nan);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[r][i] = __builtin_amdgcn_exp2f(fmaf(x[r][i], unit, -rows[r].base));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          pr[r][0][i] = pack_bf16(x[r][2 * i], x[r][2 * i + 1]);
-          if constexpr (kProbs == 2) {
-            const float lo = x[r][2 * i] - __uint_as_float(pr[r][0][i] << 16);
-            const float up = x[r][2 * i + 1] - __uint_as_float(pr[r][0][i] & 0xffff0000u);
-            pr[r][1][i] = pack_bf16(lo, up);
-          }
+          for (int i = 0; i < 2; ++i)
+            if (sh.page[(min(t0 + i * kTile, last_tile) >> pshift) - page0] < 0) gone |= 0xffffu << (16 * i);
         }
-      }
-      const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
-#pragma unroll
-      for (int r = 0; r < TT; ++r)
-#pragma unroll
-        for (int e = kProbs - 1; e >= 0; --e)
-          rows[r].l = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones),
-                                                              __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].l, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        u32x4 va, vb;
-        value_pair<D>(t, vs, j, &va, &vb);
+        // what row l of tile r sees of the lane's tokens: bits 0 .. 3 and 16 .. 19
+        const auto seen = [&](int r) {
+          uint32_t w = ~gone;
+          const int pos = sh.pos[(tile0 + r) * kTile + l];
+          if (t0 + kWaveTokens > len)
+            w &= is_tree ? sh.sees[(tile0 + r) * kTile + l][t0 / 32 - len / 32] : bits_below(pos + 1 - t0);
+          // (a node's place is no lower than its position: what this lets through of a tree is masked above)
+          if (reach > 0) w &= ~bits_below(pos - t0 + 1 - reach);
+          return w >> (4 * g);
+        };
+        float x[TT][8];
 #pragma unroll
         for (int r = 0; r < TT; ++r)
 #pragma unroll
-          for (int e = kProbs - 1; e >= 0; --e) {
-            rows[r].o[2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, va), __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].o[2 * j], 0, 0, 0);
-            rows[r].o[2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, vb), __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].o[2 * j + 1], 0, 0, 0);
-          }
-      }
-      if (nan) {
-        // the NaN blocks among tokens that not all rows see: a product of what
-        // is NaN with what is seen says which sums they reach
-        u32x4 va = {0, 0, 0, 0};
+          for (int i = 0; i < 2; ++i) {
+            uint32_t qs;
+            if constexpr (kQueryLds)
+              qs = sh.q_scale[(tile0 + r) * kWave + lane];
+            else
+              qs = q_scale[r];
+            const f32x4 s = scores<D, kParts>(t, i, qs, g, [&](int part, int h) {
+              if constexpr (kQueryLds)
+                return sh.q[(((tile0 + r) * kParts + part) * kHalves + h) * kWave + lane];
+              else
+                return q[r][part][h];
+            });
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if ((t.vs[i / 4] >> (8 * (i % 4)) & 255u) > 252u) va[i / 2] |= 0x3f80u << (16 * (i % 2));
+            for (int k = 0; k < 4; ++k) x[r][4 * i + k] = s[k];
+          }
+        if (bent) {
+          const AttentionParams& a = arguments();
+          const float cap = a.cap * kLog2e, up = 2.f / a.cap;
+#pragma unroll
+          for (int r = 0; r < TT; ++r) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[r][i] *= c;
+            if (a.cap > 0.f) {  // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                x[r][i] = fmaf(-2.f * cap, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[r][i] * up)), cap);
+            }
+          }
+          if (a.slopes) {  // relative to the root's distances, which all of a row's scores share
+            const int t1 = t0 + 4 * g - len;
+            float d[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) d[i] = (float)(t1 + (i / 4) * kTile + i % 4);
+            if (is_tree && t0 + kWaveTokens > len) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int at = t1 + (i / 4) * kTile + i % 4;
+                if (at >= 0 && at < news) d[i] = (float)sh.depth[at];
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < TT; ++r) {
+              const float slope = sh.slope[(tile0 + r) * kTile + l];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[r][i] = fmaf(slope, d[i], x[r][i]);
+            }
+          }
+        }
+        if (masked) {
+#pragma unroll
+          for (int r = 0; r < TT; ++r) {
+            const uint32_t w = seen(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[r][i] = w >> (16 * (i / 4) + i % 4) & 1 ? x[r][i] : kNegInf;
+          }
+        }
+        // New references only where a row's scores pass the old one by 2^8:
+        // probabilities up to that are as exact
+        float top[TT];
+        bool move = false;
 #pragma unroll
         for (int r = 0; r < TT; ++r) {
-          const uint32_t w = seen(r);
-          u32x4 vb = {0, 0, 0, 0};
+          const float last = max3(x[r][4], x[r][5], max3(x[r][6], x[r][7], x[r][7]));
+          top[r] = max3(max3(x[r][0], x[r][1], x[r][2]), x[r][3], last);
+          move = move || top[r] > rows[r].limit;
+        }
+        if (__any(move)) {
+#pragma unroll
+          for (int r = 0; r < TT; ++r) {
+            if (!__any(top[r] > rows[r].limit)) continue;
+            float m = fmaxf(top[r], __shfl_xor(top[r], 16, kWave));
+            m = fmaxf(m, __shfl_xor(m, 32, kWave)) * unit;
+            const float old = rows[r].reference();
+            m = fmaxf(old, m);
+            if (m > kNegInf) {
+              const float f = __builtin_amdgcn_exp2f(old - m);
+              rows[r].base = m;
+              rows[r].limit = (m + 8.f) * per_unit;
+#pragma unroll
+              for (int i = 0; i < D / 16; ++i) rows[r].o[i] *= f;
+              rows[r].l *= f;
+            }
+          }
+        }
+        u32x4 pr[TT][kProbs];
+#pragma unroll
+        for (int r = 0; r < TT; ++r) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[r][i] = __builtin_amdgcn_exp2f(fmaf(x[r][i], unit, -rows[r].base));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            pr[r][0][i] = pack_bf16(x[r][2 * i], x[r][2 * i + 1]);
+            if constexpr (kProbs == 2) {
+              const float lo = x[r][2 * i] - __uint_as_float(pr[r][0][i] << 16);
+              const float up = x[r][2 * i + 1] - __uint_as_float(pr[r][0][i] & 0xffff0000u);
+              pr[r][1][i] = pack_bf16(lo, up);
+            }
+          }
+        }
+        const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
+#pragma unroll
+        for (int r = 0; r < TT; ++r)
+#pragma unroll
+          for (int e = kProbs - 1; e >= 0; --e)
+            rows[r].l = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, ones),
+                                                                __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].l, 0, 0, 0);
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          u32x4 va, vb;
+          value_pair<D>(t, vs, j, &va, &vb);
+#pragma unroll
+          for (int r = 0; r < TT; ++r)
+#pragma unroll
+            for (int e = kProbs - 1; e >= 0; --e) {
+              rows[r].o[2 * j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, va), __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].o[2 * j], 0, 0, 0);
+              rows[r].o[2 * j + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, vb), __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].o[2 * j + 1], 0, 0, 0);
+            }
+        }
+        if (nan) {
+          // the NaN blocks among tokens that not all rows see: a product of what
+          // is NaN with what is seen says which sums they reach
+          u32x4 va = {0, 0, 0, 0};
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            if (w >> (16 * (i / 4) + i % 4) & 1) vb[i / 2] |= 0x3f80u << (16 * (i % 2));
-          const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-          const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, va),
-                                                                    __builtin_bit_cast(bf16x8, vb), zero, 0, 0, 0);
-          // a lane's sixteenth lies in one block: its sums all have it
+            if ((t.vs[i / 4] >> (8 * (i % 4)) & 255u) > 252u) va[i / 2] |= 0x3f80u << (16 * (i % 2));
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)
+          for (int r = 0; r < TT; ++r) {
+            const uint32_t w = seen(r);
+            u32x4 vb = {0, 0, 0, 0};
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (hit[k] > 0.f) rows[r].o[i][k] = __builtin_nanf("");
+            for (int i = 0; i < 8; ++i)
+              if (w >> (16 * (i / 4) + i % 4) & 1) vb[i / 2] |= 0x3f80u << (16 * (i % 2));
+            const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+            const f32x4 hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, va),
+                                                                      __builtin_bit_cast(bf16x8, vb), zero, 0, 0, 0);
+            // a lane's sixteenth lies in one block: its sums all have it
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (hit[k] > 0.f) rows[r].o[i][k] = __builtin_nanf("");
+          }
         }
-      }
-    };
+      };
 
-    {
       for (int v0 = u0; v0 < u1; v0 += kAtOnce) {
         const int v1 = min(v0 + kAtOnce, u1);
         page0 = v0 * kUnit >> pshift;
@@ -884,28 +886,27 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
           if (++u >= v1) break;
         }
       }
-    }
 
-    // ---- the streams' sums together, a tile of rows at a time
-    {
-      const AttentionParams& a = arguments();
-      const int id = thread(), l = id % 16, g = id % kWave / 16;
-      const int w0 = wave - stream;  // the wave of the first stream
-      const int b = sh.b, row0 = sh.group * kRows + tile0 * kTile, slot = sh.slot;
-      const bool whole = sh.whole;
-      more = sh.at < sh.end;  // read ahead of the barriers behind which the next segment is planned
+      // ---- the streams' sums together, a tile of rows at a time
+      {
+        const AttentionParams& a = arguments();
+        const int id = thread(), l = id % 16, g = id % kWave / 16;
+        const int w0 = wave - stream;  // the wave of the first stream
+        const int b = sh.b, row0 = sh.group * kRows + tile0 * kTile, slot = sh.slot;
+        const bool whole = sh.whole;
+        more = sh.at < sh.end;  // read ahead of the barriers behind which the next segment is planned
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        if (g == 0) {
-          sh.m[wave][t * kTile + l] = rows[t].reference();
-          sh.l[wave][t * kTile + l] = rows[t].l[0];
+        for (int t = 0; t < TT; ++t) {
+          if (g == 0) {
+            sh.m[wave][t * kTile + l] = rows[t].reference();
+            sh.l[wave][t * kTile + l] = rows[t].l[0];
+          }
         }
-      }
-      __syncthreads();
+        __syncthreads();
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) {  // as many barriers for every wave
-        if (t < TT) {
-          const Rows16<D>& mine = rows[t < TT ? t : 0];
+        for (int t = 0; t < TILES; ++t) {  // as many barriers for every wave
+          if (t < TT) {
+            const Rows16<D>& mine = rows[t < TT ? t : 0];
             float m = kNegInf;
 #pragma unroll
             for (int w = 0; w < kStreams; ++w) m = fmaxf(m, sh.m[w0 + w][t * kTile + l]);
@@ -917,45 +918,46 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
                 const f32x4 v = {mine.o[i][k] * f, mine.o[i + 1][k] * f, mine.o[i + 2][k] * f, mine.o[i + 3][k] * f};
                 *reinterpret_cast<f32x4*>(&sh.o[wave][l][(4 * g + k) * (D / 16) + i]) = v;
               }
-        }
-        __syncthreads();
-        // a row to 4 threads of each stream, neighbouring values each
-        constexpr int kCols = 4 * kStreams, kCount = D / kCols;
-        const int in = id - w0 * kWave;
-        const int r = in / kCols, col = in % kCols * kCount;
-        const int rr = t * kTile + r, row = row0 + rr;
-        const int n = row / a.G, head = sh.h * a.G + row - n * a.G;
-        if (t < TT && n < sh.news) {
-          float mm = kNegInf, ll = 0.f;
-#pragma unroll
-          for (int w = 0; w < kStreams; ++w) mm = fmaxf(mm, sh.m[w0 + w][rr]);
-#pragma unroll
-          for (int w = 0; w < kStreams; ++w) ll += sh.l[w0 + w][rr] * part_weight(sh.m[w0 + w][rr], mm);
-          float o[kCount];
-#pragma unroll
-          for (int i = 0; i < kCount; i += 4) {
-            f32x4 v = *reinterpret_cast<const f32x4*>(&sh.o[w0][r][col + i]);
-#pragma unroll
-            for (int w = 1; w < kStreams; ++w) v += *reinterpret_cast<const f32x4*>(&sh.o[w0 + w][r][col + i]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) o[i + k] = v[k];
           }
-          if (whole) {
-            finish<D, DT, kCount>(a, b, n, head, col, o, mm, ll, a.parent ? sh.depth[n] : n);
-          } else {
-            const int64_t part = (int64_t)slot * kRows + tile0 * kTile + rr;
-            float* po = a.part_o + part * D + col;
+          __syncthreads();
+          // a row to 4 threads of each stream, neighbouring values each
+          constexpr int kCols = 4 * kStreams, kCount = D / kCols;
+          const int in = id - w0 * kWave;
+          const int r = in / kCols, col = in % kCols * kCount;
+          const int rr = t * kTile + r, row = row0 + rr;
+          const int n = row / a.G, head = sh.h * a.G + row - n * a.G;
+          if (t < TT && n < sh.news) {
+            float mm = kNegInf, ll = 0.f;
 #pragma unroll
-            for (int i = 0; i < kCount; i += 4) *reinterpret_cast<f32x4*>(po + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
-            if (col == 0) {
-              a.part_ml[part * 2] = mm;
-              a.part_ml[part * 2 + 1] = ll;
+            for (int w = 0; w < kStreams; ++w) mm = fmaxf(mm, sh.m[w0 + w][rr]);
+#pragma unroll
+            for (int w = 0; w < kStreams; ++w) ll += sh.l[w0 + w][rr] * part_weight(sh.m[w0 + w][rr], mm);
+            float o[kCount];
+#pragma unroll
+            for (int i = 0; i < kCount; i += 4) {
+              f32x4 v = *reinterpret_cast<const f32x4*>(&sh.o[w0][r][col + i]);
+#pragma unroll
+              for (int w = 1; w < kStreams; ++w) v += *reinterpret_cast<const f32x4*>(&sh.o[w0 + w][r][col + i]);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[i + k] = v[k];
+            }
+            if (whole) {
+              finish<D, DT, kCount>(a, b, n, head, col, o, mm, ll, a.parent ? sh.depth[n] : n);
+            } else {
+              const int64_t part = (int64_t)slot * kRows + tile0 * kTile + rr;
+              float* po = a.part_o + part * D + col;
+#pragma unroll
+              for (int i = 0; i < kCount; i += 4)
+                *reinterpret_cast<f32x4*>(po + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+              if (col == 0) {
+                a.part_ml[part * 2] = mm;
+                a.part_ml[part * 2 + 1] = ll;
+              }
             }
           }
+          __syncthreads();
         }
-        __syncthreads();
       }
-    }
     };
     // the last rows' waves may have fewer tiles
     if constexpr (SPLIT > 1 && TILES > 1) {

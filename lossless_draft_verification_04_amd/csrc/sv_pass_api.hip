@@ -43,6 +43,10 @@ sv_status check_cache(const sv_kv_cache* c, bool layers, Kv* kv) {
       if (c->layer_stride < page || (c->layer_stride < span && c->num_pages > 1 &&
                                      ((c->layers - 1) > (c->page_stride - page) / c->layer_stride)))
         return SV_EINVAL;
+      int64_t end;
+      if (__builtin_mul_overflow((int64_t)c->layers - 1, c->layer_stride, &end) ||
+          __builtin_add_overflow(end, span, &end))
+        return SV_EINVAL;
       if (c->layer_stride % 16) return SV_EALIGN;
       kv->layer_stride = c->layer_stride;
     }
@@ -98,6 +102,22 @@ sv_status check_tensor(const void* base, const int64_t* stride, int64_t B, int64
 bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+// Whether two [B, N, heads, D] tensors that lie within one another share no
+// value: views of one tensor, the heads of one behind those of the other.
+// Strides and rows in bytes.
+bool views_apart(const void* a, const int64_t* as, int64_t ha, const void* b, const int64_t* bs, int64_t hb, int64_t B,
+                 int64_t N, int64_t row) {
+  if (as[0] != bs[0] || as[1] != bs[1]) return false;
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  const int64_t ea = (ha - 1) * as[2] + row, eb = (hb - 1) * bs[2] + row;
+  if (d >= 0 ? d < ea : -d < eb) return false;
+  const int64_t both = d >= 0 ? d + eb : -d + ea;  // what a node's heads of both span
+  const int64_t inner = N > 1 && B > 1 ? std::min(as[0], as[1]) : N > 1 ? as[1] : as[0];
+  const int64_t outer = std::max(as[0], as[1]), count = as[0] < as[1] ? B : N;
+  if (N == 1 && B == 1) return true;
+  return both <= inner && (N == 1 || B == 1 || outer >= (count - 1) * inner + both);
 }
 
 struct PassPlan {
@@ -224,25 +244,22 @@ sv_status sv_rope(const void* q, const int64_t* q_stride, const void* k, const i
     if ((st = check_tensor(out[w], os[w], B, N, heads[w], D, type_bytes(dt), false, p.os[w], &no[w], &ao)) != SV_OK) return st;
     if (!ao) return SV_EINVAL;
   }
+  // nothing that is written is read or written elsewhere; tensors may be views
+  // of the heads of one, as a fused projection's are
+  const int64_t row = (int64_t)D * type_bytes(dt);
   for (int w = 0; w < 2; ++w) {
     if (!heads[w]) continue;
-    bool same = in[w] == out[w];
-    for (int i = 0; i < 3; ++i) same = same && p.is[w][i] == p.os[w][i];
-    if (!same && overlap(in[w], ni[w], out[w], no[w])) return SV_EINVAL;
-    const int x = 1 - w;  // heads of one tensor may lie between the other's: q, k views of one projection, in place
-    if (heads[x] && !same && overlap(in[x], ni[x], out[w], no[w])) return SV_EINVAL;
+    for (int x = 0; x < 2; ++x) {
+      if (!heads[x]) continue;
+      const bool in_place = x == w && in[w] == out[w] && std::equal(p.is[w], p.is[w] + 3, p.os[w]);
+      if (!in_place && overlap(in[x], ni[x], out[w], no[w]) &&
+          !views_apart(in[x], p.is[x], heads[x], out[w], p.os[w], heads[w], B, N, row))
+        return SV_EINVAL;
+    }
   }
-  if (Hq && Hk && overlap(out_q, no[0], out_k, no[1])) {
-    // outputs that interleave: only as views of one tensor whose heads are apart
-    const int es = type_bytes(dt);
-    const int64_t d = static_cast<char*>(out_k) - static_cast<char*>(out_q);
-    bool views = p.os[0][0] == p.os[1][0] && p.os[0][1] == p.os[1][1];
-    const int64_t eq = (int64_t)(Hq - 1) * p.os[0][2] + (int64_t)D * es, ek = (int64_t)(Hk - 1) * p.os[1][2] + (int64_t)D * es;
-    const int64_t unit = N > 1 ? p.os[0][1] : B > 1 ? p.os[0][0] : INT64_MAX;
-    views = views && (d >= 0 ? d >= eq && d + ek <= unit : -d >= ek && -d + eq <= unit);
-    views = views && (N <= 1 || B <= 1 || p.os[0][0] >= (int64_t)(N - 1) * p.os[0][1] + (d >= 0 ? d + ek : -d + eq));
-    if (!views) return SV_EINVAL;
-  }
+  if (Hq && Hk && overlap(out_q, no[0], out_k, no[1]) &&
+      !views_apart(out_q, p.os[0], Hq, out_k, p.os[1], Hk, B, N, row))
+    return SV_EINVAL;
   if ((st = check_space(ws, ws_bytes, kWsFixed)) != SV_OK) return st;
   p.B = B;
   p.N = N;
@@ -303,6 +320,9 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
                           int32_t Hq, float scale, float cap, const float* slopes, int32_t reach, void* out,
                           const int64_t* out_stride, float* out_lse, void* ws, size_t ws_bytes, void* stream) {
   if (dt != SV_BF16 && dt != SV_F16) return SV_EDTYPE;
+  if (B < 0 || N < 1 || Hq < 1) return SV_EINVAL;
+  if (B > SV_MAX_SEQ || N > SV_MAX_N || Hq > SV_MAX_HEADS) return SV_EUNSUPPORTED;
+  if (B == 0) return SV_OK;
   AttentionParams p;
   sv_status st = check_cache(cache, false, &p.c);
   if (st != SV_OK) return st;
@@ -310,13 +330,17 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
   if ((st = plan_attention(B, N, Hq, cache->H, cache->D, &pl)) != SV_OK) return st;
   if (!std::isfinite(scale) || !std::isfinite(cap) || cap < 0 || reach < 0) return SV_EINVAL;
   if (cap > 0 && !std::isfinite(2.9f / cap)) return SV_EINVAL;
-  if (B == 0) return SV_OK;
   if (!lens) return SV_EINVAL;
   int64_t nq, no;
   bool aq, ao;
   if ((st = check_tensor(q, q_stride, B, N, Hq, cache->D, 2, true, p.qs, &nq, &aq)) != SV_OK) return st;
   if ((st = check_tensor(out, out_stride, B, N, Hq, cache->D, 2, true, p.os, &no, &ao)) != SV_OK) return st;
   if (!ao || overlap(q, nq, out, no)) return SV_EINVAL;
+  if (out_lse) {
+    const int64_t nl = (int64_t)B * N * Hq * (int64_t)sizeof(float);
+    if (overlap(out_lse, nl, out, no) || overlap(out_lse, nl, q, nq)) return SV_EINVAL;
+    if (misaligned(out_lse, 4)) return SV_EALIGN;
+  }
   if ((st = check_space(ws, ws_bytes, pl.bytes)) != SV_OK) return st;
   char* w = static_cast<char*>(ws);
   p.q = static_cast<const char*>(q);
@@ -332,7 +356,7 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
   p.scale = scale;
   p.cap = cap;
   p.slopes = slopes;
-  p.reach = reach;
+  p.reach = reach < p.c.room ? reach : 0;  // no two tokens are further apart
   p.err = reinterpret_cast<int32_t*>(w);
   p.tiles = pl.form.tiles;
   p.split = pl.form.split;
@@ -348,15 +372,17 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
 
 sv_status sv_kv_commit(const sv_kv_cache* cache, const int32_t* lens, const int32_t* n, const int32_t* path, int32_t B,
                        int32_t M, int32_t* out_lens, void* ws, size_t ws_bytes, void* stream) {
+  if (B < 0 || M < 0) return SV_EINVAL;
+  if (B > SV_MAX_SEQ || M > SV_MAX_N) return SV_EUNSUPPORTED;
+  if (B == 0) return SV_OK;
   KvCommitParams p;
   sv_status st = check_cache(cache, true, &p.c);
   if (st != SV_OK) return st;
-  if (B < 0 || M < 0) return SV_EINVAL;
-  if (B > SV_MAX_SEQ || M > SV_MAX_N) return SV_EUNSUPPORTED;
   if (p.c.layers > SV_MAX_LAYERS) return SV_EUNSUPPORTED;
-  if (B == 0) return SV_OK;
   if (!lens || !n || !out_lens) return SV_EINVAL;
-  if (overlap(lens, (int64_t)B * 4, out_lens, (int64_t)B * 4)) return SV_EINVAL;
+  const int64_t row = (int64_t)B * (int64_t)sizeof(int32_t);
+  if (overlap(lens, row, out_lens, row) || overlap(n, row, out_lens, row)) return SV_EINVAL;
+  if (path && M && overlap(path, row * M, out_lens, row)) return SV_EINVAL;
   if ((st = check_space(ws, ws_bytes, kWsFixed)) != SV_OK) return st;
   p.lens = lens;
   p.n = n;

@@ -103,11 +103,13 @@ def test_write_and_read_argument_checks():
 def test_attention_argument_checks():
     qs = (5 * 1024, 1024, 128)  # [B, 5, 8, 128]
 
-    def f(q=A, qs=qs, dt=1, c=None, lens=A3, B=3, N=5, Hq=8, scale=0.1, cap=0.0, reach=0, out=A2, os=qs, ws=WS, wsb=BIG):
+    def f(q=A, qs=qs, dt=1, c=None, lens=A3, B=3, N=5, Hq=8, scale=0.1, cap=0.0, reach=0, out=A2, os=qs, lse=None, ws=WS,
+          wsb=BIG):
         return L.sv_kv_attention(q, st(*qs), dt, cache() if c is None else c, lens, None, None, B, N, Hq, scale, cap, None, reach, out, st(*os),
-                                 None, ws, wsb, None)
+                                 lse, ws, wsb, None)
 
     cache_refusals(f)
+    assert f(lse=A) == svx.SV_EINVAL and f(lse=P(0x200000000 + 4)) == svx.SV_EINVAL and f(lse=P(0x500000002)) == svx.SV_EALIGN
     assert f(dt=0) == svx.SV_EDTYPE and f(dt=3) == svx.SV_EDTYPE
     assert f(B=-1) == svx.SV_EINVAL and f(N=0) == svx.SV_EINVAL and f(Hq=6) == svx.SV_EINVAL and f(Hq=0) == svx.SV_EINVAL
     assert f(B=32769) == svx.SV_EUNSUPPORTED and f(N=1025) == svx.SV_EUNSUPPORTED and f(Hq=1028) == svx.SV_EUNSUPPORTED
@@ -137,6 +139,9 @@ def test_commit_argument_checks():
     for name in ("lens", "n", "out"):
         assert f(**{name: None}) == svx.SV_EINVAL, name
     assert f(out=A) == svx.SV_EINVAL and f(out=P(0x100000008)) == svx.SV_EINVAL
+    assert f(out=A2) == svx.SV_EINVAL and f(out=P(0x200000008)) == svx.SV_EINVAL
+    assert f(out=A3) == svx.SV_EINVAL and f(out=P(0x300000000 + 4 * 23)) == svx.SV_EINVAL
+    assert f(c=cache(layers=65536, layer_stride=1 << 48)) == svx.SV_EINVAL
     assert f(B=-1) == svx.SV_EINVAL and f(M=-1) == svx.SV_EINVAL and f(M=1025) == svx.SV_EUNSUPPORTED
     assert f(B=0) == svx.SV_OK
 
@@ -160,6 +165,9 @@ def test_rope_argument_checks():
     assert f(q=P(0x100000001)) == svx.SV_EALIGN and f(freq=P(0x700000004)) == svx.SV_EALIGN
     assert f(ws=None) == svx.SV_EWORKSPACE and f(wsb=16) == svx.SV_EWORKSPACE and f(ws=P(0x40010)) == svx.SV_EALIGN
     assert f(B=0) == svx.SV_OK and f(N=0) == svx.SV_OK and f(Hq=0, Hk=0) == svx.SV_OK
+    # q in place, k apart, where what is read as k is q itself, or one of its heads
+    assert f(oq=A, k=A) == svx.SV_EINVAL and f(oq=A, k=P(0x100000000 + 128 * 2)) == svx.SV_EINVAL
+    assert f(ok=A2, q=A2) == svx.SV_EINVAL and f(ok=A2, q=P(0x200000000 + 512 * 2)) == svx.SV_EINVAL
     # views of one projection whose heads lie across one another
     fused = (5 * 1024, 1024, 128)
     assert f(q=A, qs=fused, k=P(0x100000000 + 256 * 2), ks=fused, oq=A, oqs=fused, ok=P(0x100000000 + 256 * 2), oks=fused) == svx.SV_EINVAL
