@@ -4,6 +4,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -19,7 +21,6 @@ FLAGS = [
     "-O3",
     "-std=c++17",
     "-fPIC",
-    "-shared",
     # explicit fmaf where a fused multiply-add is meant; nothing else contracts
     "-ffp-contract=off",
     # no packed-fp32 instructions in device code
@@ -33,18 +34,28 @@ LIB_TIMELINE = os.path.join(HERE, "libspecverify_timeline.so")
 def build(verbose: bool = False, timeline: bool = False) -> str:
     """Build the library; timeline=True builds the measurement variant with per-block wall-clock stamps
     (libspecverify_timeline.so, -DSV_TIMELINE) beside it."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
     lib = LIB_TIMELINE if timeline else LIB
     tmp = lib + ".tmp"
-    cmd = [HIPCC, *FLAGS, *(["-DSV_TIMELINE"] if timeline else []), "-I" + os.path.join(ROOT, "include"), *srcs,
-           "-o", tmp]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    noise = "is not a recognized feature for this target"
-    err = "\n".join(ln for ln in (res.stdout + res.stderr).splitlines() if noise not in ln)
-    if res.returncode != 0:
-        raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
-    if verbose and err.strip():
-        print(err, file=sys.stderr)
+    flags = [*FLAGS, *(["-DSV_TIMELINE"] if timeline else []), "-I" + os.path.join(ROOT, "include")]
+
+    def hipcc(*args):
+        res = subprocess.run([HIPCC, *args], capture_output=True, text=True)
+        noise = "is not a recognized feature for this target"
+        err = "\n".join(ln for ln in (res.stdout + res.stderr).splitlines() if noise not in ln)
+        if res.returncode != 0:
+            raise RuntimeError(f"hipcc failed ({res.returncode}):\n{err}")
+        if verbose and err.strip():
+            print(err, file=sys.stderr)
+
+    # sources beside one another, the one that takes longest first
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, s + ".o") for s in SOURCES]
+        with ThreadPoolExecutor(min(8, os.cpu_count() or 1)) as pool:
+            jobs = [pool.submit(hipcc, *flags, "-c", os.path.join(CSRC, s), "-o", o)
+                    for s, o in reversed(list(zip(SOURCES, objs)))]
+            for j in jobs:
+                j.result()
+        hipcc("--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp)
     os.replace(tmp, lib)
     return lib
 
