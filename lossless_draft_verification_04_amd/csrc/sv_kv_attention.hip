@@ -422,9 +422,9 @@ __device__ __forceinline__ void segment(const AttentionParams& p, S& sh) {
       d.b = sh.b;
       d.h = h;
       d.group = group;
+      d.news = sh.news;
       d.slot = slot;
-      d.last = last - 1;
-      d.total = sh.total;
+      d.last = block_of(last - 1, sh.total, p);
       static_cast<AttentionItem*>(p.desc)[blockIdx.x] = d;
       sh.open = 1;
     }
@@ -985,49 +985,59 @@ template <int D, int DT>
 __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttentionParams p) {
   constexpr int kThreads = kJoinThreads, kWaves = kThreads / kWave;
   constexpr int kCols = D / 4, kSlices = kThreads / kCols, kFew = 8;
+  constexpr int kItems = kAttentionBlocks / kThreads;  // of a thread
   __shared__ f32x4 s_sum[kSlices][kCols];
   __shared__ float s_l[kSlices], s_m[kSlices];
-  __shared__ int32_t s_end[kAttentionBlocks];  // pieces of work up to a block's item
   __shared__ int32_t s_scan[kWaves];
+  __shared__ int32_t s_first, s_piece;
   const AttentionItem* const items = static_cast<const AttentionItem*>(p.desc);
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, rows = p.split * p.tiles * kTile;
-  const auto last_of = [&](const AttentionItem& it) { return block_of(it.last, it.total, p); };
   // every block's item, if one begins there and goes on, and the pieces it makes
-  int32_t pieces = 0;
-  for (int i0 = 0; i0 < p.blocks; i0 += kThreads) {
-    const int i = i0 + tid;
-    int mine = 0;
-    if (i < p.blocks && items[i].b >= 0) mine = last_of(items[i]) - i < kFew ? (rows + kSlices - 1) / kSlices : rows;
-    int incl = mine;
+  const int each = p.blocks / kThreads, i0 = tid * each;
+  int32_t parts[kItems], end[kItems], count = 0;  // end: of the pieces up to an item, from the thread's first on
 #pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const int up = __shfl_up(incl, o, kWave);
-      if (lane >= o) incl += up;
-    }
-    if (lane == kWave - 1) s_scan[wave] = incl;
-    __syncthreads();
-    int sum = 0;
-    for (int w = 0; w < kWaves; ++w) {
-      if (w < wave) incl += s_scan[w];
-      sum += s_scan[w];
-    }
-    s_end[i] = pieces + incl;
-    pieces += sum;
-    __syncthreads();
+  for (int k = 0; k < kItems; ++k) {
+    const int i = i0 + min(k, each - 1);
+    parts[k] = items[i].b < 0 ? 0 : items[i].last - i;
+  }
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    if (k < each && parts[k]) count += parts[k] < kFew ? (rows + kSlices - 1) / kSlices : rows;
+    end[k] = count;
+  }
+  int32_t incl = count;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int up = __shfl_up(incl, o, kWave);
+    if (lane >= o) incl += up;
+  }
+  if (lane == kWave - 1) s_scan[wave] = incl;
+  __syncthreads();
+  int32_t pieces = 0, before = incl - count;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) before += s_scan[w];
+    pieces += s_scan[w];
   }
   const int col = tid % kCols, slice = tid / kCols;
   for (int x = blockIdx.x; x < pieces; x += gridDim.x) {
-    int lo = 0;  // the first block whose pieces end behind x
-    for (int step = kAttentionBlocks / 2; step > 0; step /= 2)
-      if (lo + step <= p.blocks && s_end[lo + step - 1] <= x) lo += step;
-    const int first = lo, piece = x - (lo ? s_end[lo - 1] : 0);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const int32_t from = k ? end[k - 1] : 0;
+      if (x - before >= from && x - before < end[k]) {
+        s_first = i0 + k;
+        s_piece = x - before - from;
+      }
+    }
+    __syncthreads();
+    const int first = uniform(s_first), piece = uniform(s_piece);
     const AttentionItem it = items[first];
-    const int last = last_of(it);
+    const int last = it.last;
     const bool few = last - first < kFew;
     const int r = few ? piece * kSlices + slice : piece;
     const int row = it.group * rows + r;
     const int n = row / p.G, head = it.h * p.G + row - n * p.G;
-    const bool live = r < rows && n < (p.news ? p.news[it.b] : p.N);
+    const bool live = r < rows && n < it.news;
     const auto slot_of = [&](int j) { return (int64_t)(j == first ? it.slot : 2 * j) * rows + r; };
     const int from = few ? first : first + slice, by = few ? 1 : kSlices;
     f32x4 o = {0.f, 0.f, 0.f, 0.f};
@@ -1077,7 +1087,6 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttentionParam
           l += s_l[i] * f;
         }
       }
-      __syncthreads();
     }
     if (live && (few || slice == 0)) {
       int depth = n;
@@ -1093,6 +1102,7 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttentionParam
       const float y[4] = {o[0], o[1], o[2], o[3]};
       finish<D, DT, 4>(p, it.b, n, head, col * 4, y, m, l, depth);
     }
+    __syncthreads();
   }
 }
 

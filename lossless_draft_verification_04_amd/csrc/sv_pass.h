@@ -80,8 +80,9 @@ struct AttentionParams {
 // An item (a sequence's key head and group of rows) that several blocks share.
 struct AttentionItem {
   int32_t b, h, group;  // b = -1: none
-  int32_t slot;         // of the first block's part
-  int64_t last, total;  // its last step, and how many steps there are
+  int32_t news;         // of the sequence
+  int32_t slot, last;   // of the first block's part; the last block
+  int32_t unused[2];    // 32 bytes
 };
 
 hipError_t launch_rope(const RopeParams& p, sv_dtype dt, hipStream_t s);
