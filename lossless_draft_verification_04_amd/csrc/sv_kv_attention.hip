@@ -807,6 +807,11 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
             }
           }
         }
+        // The second products ahead of the other wave's vector instructions, where
+        // there are many rows: 2 trees of 64 nodes x 16 heads of 256 in fp16 over 65536
+        // tokens 247 to 229 us, 1024 nodes x 32 heads 317 to 308; single tokens, bound by loads, lose by it (67 to 70)
+        constexpr bool kAhead = SPLIT * TILES > 1;
+        if constexpr (kAhead) __builtin_amdgcn_s_setprio(1);
         const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
 #pragma unroll
         for (int r = 0; r < TT; ++r)
@@ -828,6 +833,7 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
                   __builtin_bit_cast(bf16x8, vb), __builtin_bit_cast(bf16x8, pr[r][e]), rows[r].o[2 * j + 1], 0, 0, 0);
             }
         }
+        if constexpr (kAhead) __builtin_amdgcn_s_setprio(0);
         if (nan) {
           // the NaN blocks among tokens that not all rows see: a product of what
           // is NaN with what is seen says which sums they reach
