@@ -559,6 +559,7 @@ def _draft_workspace(dev, *shape):
 # The small calls of decoding take about as long on the host as on the GPU, so
 # these bindings pass addresses as plain integers and ask for the stream's
 # handle without building a Stream object (1.8 us).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -579,7 +580,7 @@ def _one_device(what, first, *others):
 
 def _call(dev, fn, what, *args):
     """One launch with `dev` current, on its current stream."""
-    if dev.index == torch.cuda.current_device():
+    if dev.index == _current_device():  # tensors on a GPU: torch has been initialised
         status = fn(*args, _raw_stream(dev.index))
     else:
         with torch.cuda.device(dev):
@@ -933,14 +934,25 @@ def sv_rope(q, freq, k=None, positions=None, lens=None, parent=None, interleaved
     return dict(q=out_q, k=out_k)
 
 
+@functools.lru_cache(maxsize=1024)
+def _kv_layout(shape, kst, vshape, vst, want, what):
+    """The strides of keys and values [B, N, H, D] that go with a cache."""
+    sk, sv = _window_strides(shape, kst, "k"), _window_strides(vshape, vst, "v")
+    if vshape != shape:
+        raise SpecVerifyError(SV_EINVAL, f"v: want {tuple(shape)}, got {tuple(vshape)}")
+    if (shape[0], *shape[2:]) != want:
+        raise SpecVerifyError(SV_EINVAL, f"{what}: want [{want[0]}, N, {want[1]}, {want[2]}], got {tuple(shape)}")
+    return sk, sv
+
+
 def _kv_rows(what, cache, k, v, B):
-    """Checks of the keys and values [B, N, H, D] that go with a cache."""
-    dt, sk = _window(k, "k")
-    if v.dtype is not k.dtype or v.shape != k.shape:
-        raise SpecVerifyError(SV_EINVAL, f"v: want {k.dtype} {tuple(k.shape)}, got {v.dtype} {tuple(v.shape)}")
-    if k.shape[0] != B or k.shape[2:] != (cache.H, cache.D):
-        raise SpecVerifyError(SV_EINVAL, f"{what}: want [{B}, N, {cache.H}, {cache.D}], got {tuple(k.shape)}")
-    return dt, sk, _window(v, "v")[1]
+    """The type's code and the strides of the keys and values [B, N, H, D] that go with a cache."""
+    dt = _PASS_TYPES.get(k.dtype)
+    if dt is None:
+        raise SpecVerifyError(SV_EDTYPE, f"{what}: {k.dtype}")
+    if v.dtype is not k.dtype:
+        raise SpecVerifyError(SV_EINVAL, f"v: want {k.dtype}, got {v.dtype}")
+    return dt, *_kv_layout(k.shape, k.stride(), v.shape, v.stride(), (B, cache.H, cache.D), what)
 
 
 def sv_kv_write(cache, k, v, lens, news=None, workspace=None):
