@@ -4,7 +4,12 @@
 // a value row: 16 bytes (32 in fp32) on one side, 4 on the other.  Threads are
 // ordered (sequence, group of 4 slots, head, slot, 8 values), because the
 // cache holds sixteenths of value rows for 4 tokens side by side: a wave then
-// writes and reads whole lines of the cache.
+// writes and reads whole lines of the cache.  Bound by memory for many tokens
+// (16 x 2047 tokens of 8 heads of 128 in bf16 written 22 us and read back 19;
+// 8 x 16384 in fp16 read back 97 us, 5.2 TB/s; a copy 4.9), by the launch for few
+// (3 us each).  Sequences are the grid's second dimension, so that a thread finds its place by
+// 32-bit divisions (by 64-bit ones of its number in the whole: 55 us for the former
+// two, 129 us).
 #include "sv_kv.hpp"
 
 namespace sv {
@@ -135,7 +140,8 @@ __global__ __launch_bounds__(kThreads) void read_kernel(const KvMoveParams p) {
 // codes, a sixteenth of the values', the keys' scales, one of the values' -- and
 // reads it from all of the block's layers before it writes: what a layer moves
 // is little (8 tokens of 136 bytes), so the time is that of the loads one after
-// another (lengths, path, pages, pieces), and layers share it.
+// another (lengths, path, pages, pieces), and layers share it: 32 paths of up to 8
+// tokens in 64 layers of 8 heads take 15 us, 55 with a layer a block.
 constexpr int kLayers = 8;
 
 template <int BYTES>

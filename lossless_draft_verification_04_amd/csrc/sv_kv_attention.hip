@@ -1,4 +1,23 @@
 // sv_kv_attention.hip -- attention of a window's nodes over the 4-bit cache.
+//
+// One pass over the tokens with a running reference and sum of each row:
+//   out_i = sum_j 2^(s_ij - m_i) v_j / sum_j 2^(s_ij - m_i),  s in exponents of 2.
+// Rows are nodes x query heads of one key head, in tiles of 16; a step of a wave
+// is 32 tokens.  A wave holds its rows' sums in registers; the waves' streams of
+// tokens and the blocks' parts of a sequence are joined at the end, always in
+// the same order.
+//
+// What bounds it (32 x 8192 tokens and the like; 6.1 TB/s is what a read of HBM
+// reaches, 1147 TFLOP/s what a large bf16 product does):
+//   few rows: memory.  64 sequences of one token, 8 x 128 heads: 428 MB in 97 us,
+//     4.4 TB/s, about 5 once it runs; its start, the blocks' ends and the join are
+//     some 15 us.  Loads two steps ahead instead of one took as long (97.5).
+//   many rows: vector and matrix instructions together.  32 chains of 17 nodes x
+//     32 heads of 128: 109 us, of which memory would need 37 and the products,
+//     at a large product's rate, 48.  The conversion of the values to bf16 is
+//     shared by a wave's tiles, the exponentials are not.
+//   one window: 16 us of dependent loads (lengths, queries, pages, tokens, parts),
+//     5 of them the second launch.
 #include "sv_kv.hpp"
 
 namespace sv {
@@ -14,6 +33,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.4426950408889634f;
+// joins: blocks that all take part in a long sequence's few rows, in many rows' too
 constexpr int kJoinBlocks = 512, kJoinThreads = 256;
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -85,8 +105,9 @@ struct Tokens {  // what a wave reads of 32 tokens
   uint32_t vs[2];   // scales of 4 tokens
 };
 
-// The sum of `parts` such products is Q's exactly: bf16 has 8 bits, an e4m3
-// value 4, fp16 11.  A row has one scale, which takes its largest magnitude
+// The sum of `parts` such products is Q's: bf16 has 8 bits of digits, an e4m3
+// value 4, fp16 11.  Two products of 8 bits take as long as the one of bf16 that
+// they stand for, and the keys need no conversion.  A row has one scale, which takes its largest magnitude
 // to [128, 256); part i holds what the parts before left, times 2^(5 i).
 template <int D, int PARTS>
 struct Query {
@@ -268,7 +289,7 @@ struct Number {
   static constexpr int value = N;
 };
 
-// A block's waves: `SPLIT` of them take rows, TILES tiles of 16 each, beside one
+// A block's waves (attention_form() says which): `SPLIT` of them take rows, TILES tiles of 16 each, beside one
 // another, and there are so many streams of tokens.  Waves of the same stream
 // read the same tokens, the second one out of the cache beside it.
 template <int TILES, int SPLIT>
@@ -764,8 +785,9 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
             for (int i = 0; i < 8; ++i) x[r][i] = w >> (16 * (i / 4) + i % 4) & 1 ? x[r][i] : kNegInf;
           }
         }
-        // New references only where a row's scores pass the old one by 2^8:
-        // probabilities up to that are as exact
+        // New references only where a row's scores pass the old one by 8: up to
+        // 2^8 probabilities and their sums are as exact as up to 1, and what a row
+        // moves at first is most of what it ever moves
         float top[TT];
         bool move = false;
 #pragma unroll
@@ -965,7 +987,8 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
         }
       }
     };
-    // the last rows' waves may have fewer tiles
+    // The last rows' waves may have a tile less to do (5 tiles in 2 x 3: 120 us,
+    // with three in both 142).
     if constexpr (SPLIT > 1 && TILES > 1) {
       const int wave = uniform(thread() / kWave);
       if (arguments().all_tiles - (sh.group * SPLIT + wave / kStreams) * TILES < TILES)

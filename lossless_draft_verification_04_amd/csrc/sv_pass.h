@@ -72,8 +72,8 @@ struct AttentionParams {
   int32_t tiles, split;  // a block's rows: `split` waves beside one another with so many tiles of 16 each
   int32_t groups, all_tiles;  // groups of so many rows, and all tiles
   int32_t blocks, log_blocks;
-  float* part_o;  // [2 * blocks][tiles * 16][D]
-  float* part_ml; // [2 * blocks][tiles * 16][2]
+  float* part_o;  // [2 * blocks][split * tiles * 16][D]: a block's first and last item
+  float* part_ml; // [2 * blocks][split * tiles * 16][2]: reference, sum
   void* desc;     // [blocks] of AttentionItem
 };
 
@@ -92,8 +92,12 @@ hipError_t launch_kv_commit(const KvCommitParams& p, int D, hipStream_t s);
 hipError_t launch_kv_attention(const AttentionParams& p, sv_dtype dt, int D, hipStream_t s);
 
 // How `all` tiles of 16 rows (nodes x heads of a key head) are taken: as many
-// in a wave as its registers hold (`most`), more by two or four waves beside one
-// another, which share the tokens they read, more still by several blocks.
+// in a wave as its registers hold (`most`: two at D = 256 would spill 180 of
+// them), more by two or four waves beside one another, which read the same
+// tokens, more still by several blocks.  Waves beside one another against blocks
+// of their own: 5 tiles of 128 values 112 against 124 us (32 chains of 17 nodes x
+// 4 heads), 16 of 256 values 241 against 280 (trees of 64 x 4, 65536 tokens), 256 of
+// 128 values 320 against 400 (1024 nodes x 4 heads).
 struct AttentionForm {
   int tiles, split, groups, blocks;
 };

