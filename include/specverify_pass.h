@@ -191,6 +191,7 @@ sv_status sv_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32
  *   lens [B], news [B] (NULL: N) int32: nodes news[b] .. N - 1 are padding,
  *     their outputs are left as they were
  *   parent [B, N] or NULL (a chain); N <= SV_MAX_N
+ *   scale, cap finite, below 2^127 in magnitude
  *   slopes [Hq] float or NULL; out_lse [B, N, Hq] float or NULL, apart from
  *     q and out
  * Hq is a multiple of cache->H.  A sequence whose length or count is out of

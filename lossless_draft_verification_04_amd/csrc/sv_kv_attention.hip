@@ -747,15 +747,32 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
         if (bent) {
           const AttentionParams& a = arguments();
           const float cap = a.cap * kLog2e, up = 2.f / a.cap;
+          const auto bend = [&](float s) {  // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+            return fmaf(-2.f * cap, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(s * up)), cap);
+          };
 #pragma unroll
           for (int r = 0; r < TT; ++r) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[r][i] *= c;
-            if (a.cap > 0.f) {  // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap))
+          }
+          if (a.cap > 128.f) {
+            // that is off by 2^-21 of the cap: too much beside small scores under a
+            // large cap, which take the series (its next term: 2^-29 of the score)
+            const float part = 1.f / cap;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                x[r][i] = fmaf(-2.f * cap, __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(x[r][i] * up)), cap);
+            for (int r = 0; r < TT; ++r) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float t = x[r][i] * part, t2 = t * t;
+                const float low = fmaf(t2, fmaf(t2, fmaf(t2, -17.f / 315.f, 2.f / 15.f), -1.f / 3.f), 1.f);
+                x[r][i] = t2 < 1.f / 64.f ? x[r][i] * low : bend(x[r][i]);
+              }
             }
+          } else if (a.cap > 0.f) {
+#pragma unroll
+            for (int r = 0; r < TT; ++r)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) x[r][i] = bend(x[r][i]);
           }
           if (a.slopes) {  // relative to the root's distances, which all of a row's scores share
             const int t1 = t0 + 4 * g - len;

@@ -328,7 +328,8 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
   if (st != SV_OK) return st;
   PassPlan pl;
   if ((st = plan_attention(B, N, Hq, cache->H, cache->D, &pl)) != SV_OK) return st;
-  if (!std::isfinite(scale) || !std::isfinite(cap) || cap < 0 || reach < 0) return SV_EINVAL;
+  // (they are held as exponents of 2)
+  if (!std::isfinite(scale * 1.5f) || !std::isfinite(cap * 1.5f) || cap < 0 || reach < 0) return SV_EINVAL;
   if (cap > 0 && !std::isfinite(2.9f / cap)) return SV_EINVAL;
   if (!lens) return SV_EINVAL;
   int64_t nq, no;

@@ -221,7 +221,7 @@ hipError_t rope(const RopeParams& p, hipStream_t s) {
   const int64_t fill = all / (2048 * (int64_t)shape.slots);
   shape.run = fill < 1 ? 1 : fill > 8 ? 8 : (int)fill;
   const int64_t blocks = (all + (int64_t)shape.slots * shape.run - 1) / ((int64_t)shape.slots * shape.run);
-  if (blocks > INT32_MAX) return hipErrorInvalidValue;
+  if (blocks > UINT32_MAX / kThreads) return hipErrorInvalidValue;  // threads of a launch's dimension
   const dim3 grid((uint32_t)blocks, (uint32_t)((rows.all + shape.wide - 1) / shape.wide));
   if (vec)
     run<DT, 16 / es>(p, shape, grid, s);

@@ -71,6 +71,55 @@ def test_attention_reach_without_end():
         assert torch.equal(check_attention(c, h, q, (0, 300), parent=parent, reach=reach)["out"], tree["out"])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_attention_wide_caps(dtype):
+    """A cap far above the scores changes nothing: s - cap tanh(s / cap) is s^3 / (3 cap^2) at most, 2^-19 for scores up to 40
+    under a cap of 2^17, and its series' roundings are 3 2^-24 of the score, where the tolerance has D 2^-24 and more."""
+    c, h = filled(2, 2, 64, 16, (200, 31), 6, seed=4)
+    q = queries(2, 6, 4, 64, dtype, 4, 1.5)
+    want = check_attention(c, h, q, (200, 31))
+    for cap in (2.0 ** 17, 1e6, 1e30, 1e38):
+        got = svx.sv_kv_attention(h, q.to(DEV), i32(200, 31), cap=cap, want_lse=True)
+        for b, n0 in ((0, 200), (1, 31)):
+            k, v = c.tokens(b, n0 + 6)
+            _, lse, tol, lse_tol, _ = ref.attention(q[b], k, v, n0, None, 64 ** -0.5, 0.0, None, 0, dtype)
+            s = torch.einsum("nhgd,thd->nhgt", q[b].double().unflatten(1, (2, 2)), k) / 8
+            assert 4 < float(s.abs().max()) < 40
+            near(got["out"][b], want["out"][b].cpu(), 2 * tol, f"out of {b}")
+            near(got["lse"][b], lse, lse_tol, f"lse of {b}")
+    for cap in (100.0, 128.0, 129.0, 1000.0):  # on both sides of where the series begins
+        check_attention(c, h, q * 8, (200, 31), cap=cap)
+
+
+def test_attention_scale_of_zero():
+    c, h = filled(2, 1, 128, 16, (200, 0), 6, seed=5)
+    q = queries(2, 6, 2, 128, BF16, 5)
+    for scale in (0.0, -0.0, 1e-44, -1e-30):
+        check_attention(c, h, q, (200, 0), scale=scale)
+
+
+def test_most_heads():
+    """1024 key heads: written, read back, attended to, committed; and as many sequences as blocks of a dimension can be."""
+    H, D, P = 1024, 64, 16
+    c, h = filled(1, H, D, P, (5,), 3, seed=6)
+    check_attention(c, h, queries(1, 3, H, D, BF16, 6), (5,))
+    k = svx.sv_kv_read(h, None, i32(8), *(torch.zeros(1, 8, H, D, device=DEV) for _ in range(2)))["k"]
+    assert torch.equal(k[0].cpu(), c.tokens(0, 8)[0].float())
+    B = 16500
+    many = svx.KvCache(h.pool, torch.zeros(B, 1, dtype=torch.int32, device=DEV), H, D, P)
+    lens, n = torch.arange(B, dtype=torch.int32, device=DEV) % 9, torch.full((B,), 2, dtype=torch.int32, device=DEV)
+    n[-1], lens[-1] = 1, 5
+    before = h.pool.clone()
+    path = torch.tensor([[1, 2]], dtype=torch.int32, device=DEV).repeat(B, 1)  # stays where it is
+    path[-1, 0] = 2
+    new = svx.sv_kv_commit(many, lens, n, path=path)
+    assert torch.equal(new, lens + 1 + n)
+    c.pool[0] = before.cpu()
+    c.pages[0, 0] = 0
+    c.set_raw(0, 6, c.raw(0, 7))
+    assert torch.equal(h.pool.cpu(), c.pool[0])
+
+
 # ---------------------------------------------------------------------------
 # long work for a block
 # ---------------------------------------------------------------------------

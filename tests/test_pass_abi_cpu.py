@@ -113,7 +113,7 @@ def test_attention_argument_checks():
     assert f(dt=0) == svx.SV_EDTYPE and f(dt=3) == svx.SV_EDTYPE
     assert f(B=-1) == svx.SV_EINVAL and f(N=0) == svx.SV_EINVAL and f(Hq=6) == svx.SV_EINVAL and f(Hq=0) == svx.SV_EINVAL
     assert f(B=32769) == svx.SV_EUNSUPPORTED and f(N=1025) == svx.SV_EUNSUPPORTED and f(Hq=1028) == svx.SV_EUNSUPPORTED
-    for v in (INF, -INF, NAN):
+    for v in (INF, -INF, NAN, 3e38):
         assert f(scale=v) == svx.SV_EINVAL and f(cap=v) == svx.SV_EINVAL
     assert f(cap=-1.0) == svx.SV_EINVAL and f(cap=1e-45) == svx.SV_EINVAL and f(reach=-1) == svx.SV_EINVAL
     for name in ("q", "out", "lens"):
