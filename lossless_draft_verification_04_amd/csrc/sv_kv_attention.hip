@@ -497,12 +497,10 @@ __device__ __forceinline__ float part_weight(float own, float m) {
   return own > kNegInf ? __builtin_amdgcn_exp2f(own - m) : (m > kNegInf ? 0.f : 1.f);
 }
 
-// The largest of three, NaN aside; one instruction (fmaxf first quiets each of
-// its operands).
+// The largest of three, NaN where one is: an instruction, where fmaxf first
+// quiets each of its operands.
 __device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 
 // COUNT (4, 8 or 16) of a row's sums from `col` on, and its statistics, as
@@ -809,8 +807,11 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
         bool move = false;
 #pragma unroll
         for (int r = 0; r < TT; ++r) {
-          const float last = max3(x[r][4], x[r][5], max3(x[r][6], x[r][7], x[r][7]));
-          top[r] = max3(max3(x[r][0], x[r][1], x[r][2]), x[r][3], last);
+          // (a row that sees NaN is NaN, whatever its reference)
+          float m = __builtin_elementwise_maximum(x[r][0], x[r][1]);
+#pragma unroll
+          for (int i = 2; i < 8; i += 2) m = max3(m, x[r][i], x[r][i + 1]);
+          top[r] = m;
           move = move || top[r] > rows[r].limit;
         }
         if (__any(move)) {
