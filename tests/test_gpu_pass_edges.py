@@ -146,6 +146,31 @@ def test_attention_pages_staged_more_than_once(D, B, H, T, N, G, dtype):
             near(got["lse"][b, :, rows], lse, lse_tol, f"lse of {b}")
 
 
+@pytest.mark.parametrize("B,N,G,T", [(1100, 16, 9, 90), (32768, 1, 1, 15), (2000, 3, 1, 400)])
+def test_attention_more_sequences_than_threads(B, N, G, T):
+    """Sequences of very different lengths, many without anything to do; their pages are few, in many places."""
+    D, P = 64, 16
+    c, h = filled(1, 1, D, P, (300,), 20, seed=B)
+    g = torch.Generator().manual_seed(B)
+    c.pages = c.pages[0, torch.randint(0, c.pages.shape[1], (B, -(-(T + N) // P)), generator=g)].contiguous()
+    h = svx.KvCache(h.pool, c.pages.to(DEV), 1, D, P)
+    lens = torch.randint(0, T + 1, (B,), generator=g, dtype=torch.int32)
+    news = torch.randint(0, N + 1, (B,), generator=g, dtype=torch.int32)
+    news[B // 3:B // 2] = 0
+    news[-1] = N
+    q = queries(B, N, G, D, BF16, B)
+    out = torch.full((B, N, G, D), 9.0, dtype=BF16, device=DEV)
+    svx.sv_kv_attention(h, q.to(DEV), lens.to(DEV), news=news.to(DEV), out=out)
+    assert bool((out[news.to(DEV) == 0] == 9).all())
+    for b in [0, 1, B // 3 - 1, B // 2, B - 2, B - 1, *torch.randint(0, B, (30,), generator=g).tolist()]:
+        n = int(news[b])
+        if n:
+            k, v = c.tokens(b, int(lens[b]) + n)
+            want, _, tol, _, _ = ref.attention(q[b, :n], k, v, int(lens[b]), None, D ** -0.5, 0.0, None, 0, BF16)
+            near(out[b, :n], want, tol, f"out of {b}")
+        assert bool((out[b, n:] == 9).all())
+
+
 def test_pages_far_apart():
     """Pages and layers that lie past 4 GiB of the pool."""
     H, D, P, B, N = 2, 128, 16, 2, 6
