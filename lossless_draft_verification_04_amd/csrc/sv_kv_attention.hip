@@ -1041,15 +1041,18 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttentionParam
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, rows = p.split * p.tiles * kTile;
   // every block's item, if one begins there and goes on, and the pieces it makes
   const int each = p.blocks / kThreads, i0 = tid * each;
-  int32_t parts[kItems], end[kItems], count = 0;  // end: of the pieces up to an item, from the thread's first on
+  int32_t parts[kItems], some[kItems];  // parts behind the first, rows of nodes
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int i = i0 + min(k, each - 1);
-    parts[k] = items[i].b < 0 ? 0 : items[i].last - i;
+    const AttentionItem& it = items[i];
+    parts[k] = it.b < 0 ? 0 : it.last - i;
+    some[k] = max(min(rows, it.news * p.G - it.group * rows), 0);
   }
+  int32_t end[kItems], count = 0;  // end of the pieces up to an item, from the thread's first on
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    if (k < each && parts[k]) count += parts[k] < kFew ? (rows + kSlices - 1) / kSlices : rows;
+    if (k < each && parts[k] > 0) count += parts[k] < kFew ? (some[k] + kSlices - 1) / kSlices : some[k];
     end[k] = count;
   }
   int32_t incl = count;
@@ -1095,10 +1098,11 @@ __global__ __launch_bounds__(kJoinThreads) void join_kernel(const AttentionParam
       float top = m;
 #pragma unroll
       for (int i = 0; i < kFew; ++i) {
-        const int j = min(j0 + i * by, last);
-        const int64_t s = slot_of(j);
-        ml[i] = live ? reinterpret_cast<const f32x2*>(p.part_ml)[s] : f32x2{kNegInf, 0.f};
-        v[i] = live ? *reinterpret_cast<const f32x4*>(p.part_o + s * D + col * 4) : f32x4{0.f, 0.f, 0.f, 0.f};
+        const int j = j0 + i * by;
+        const bool here = live && (!few || j <= last);
+        const int64_t s = slot_of(min(j, last));
+        ml[i] = here ? reinterpret_cast<const f32x2*>(p.part_ml)[s] : f32x2{kNegInf, 0.f};
+        v[i] = here ? *reinterpret_cast<const f32x4*>(p.part_o + s * D + col * 4) : f32x4{0.f, 0.f, 0.f, 0.f};
       }
 #pragma unroll
       for (int i = 0; i < kFew; ++i) top = fmaxf(top, ml[i][0]);
