@@ -203,11 +203,12 @@ sv_status sv_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32
  * with a NaN or an infinity is NaN).
  *
  * The cache is read once for all query heads of a key head and up to 256 rows
- * (192 at D = 128, 64 at D = 256) of nodes x heads.  Keys are multiplied in 4 bits as they are,
- * by queries split exactly into two (fp16: three) parts of 8 bits; products,
- * sums and the softmax are held in 32 bits, probabilities are rounded to the
- * 8 bits of bf16 (fp16: 16 bits) before they multiply the values, and are summed
- * as rounded.
+ * (192 at D = 128, 64 at D = 256) of nodes x heads.  Keys become bf16 as they are
+ * multiplied, which holds them exactly, and are multiplied by the queries (fp16:
+ * by two parts of bf16 whose sum a query is).  Products, sums and the softmax are
+ * held in 32 bits (a cap is off by 2^-21 of itself); probabilities are rounded to
+ * the 8 bits of bf16 (fp16: 16 bits) before they multiply the values, and are
+ * summed as rounded.
  */
 sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, const sv_kv_cache* cache,
                           const int32_t* lens, const int32_t* news, const int32_t* parent, int32_t B, int32_t N,

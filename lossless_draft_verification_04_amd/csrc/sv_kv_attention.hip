@@ -27,8 +27,6 @@ namespace {
 constexpr int kTile = 16;       // tokens of a tile, rows of a tile
 constexpr int kWaveTokens = 32; // tokens of a wave's step: two tiles
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -88,129 +86,84 @@ __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
 // ---------------------------------------------------------------------------
 // Fragments.  A wave's lane is (l, g): l = lane % 16, g = lane / 16.
 //
-// Scores are made transposed, S^T = K Q^T, by 16x16x128 products of 4-bit keys
-// (row l of a tile, values 32g .. 32g + 31: 16 neighbouring bytes of the cache,
-// with the byte of their scale) and 8-bit queries (row l, values 16g .. + 15 and
-// 64 + 16g .. + 15).  The result has the tile's tokens 4g .. 4g + 3 of row l in a
-// lane, which is the layout that the second product, O^T = V^T P^T in bf16,
-// wants its P in: no lane exchanges anything.  V^T's lane has D/16 neighbouring
-// values (a sixteenth of a row) of tokens 4g .. 4g + 3, which is how the cache
-// holds them.  O^T has values (D/4) g .. of row l in a lane.
+// Scores are made transposed, S^T = K Q^T: the codes of the keys become bf16 as
+// they are multiplied (which holds them exactly), 8 neighbouring values of row l
+// in a lane, beside the same values of a query.  At D = 64 a lane has values
+// 16g .. 16g + 15, else 32g .. 32g + 31 of each 128 (16 neighbouring bytes of the
+// cache); products take them 8 at a time.  The result has the tile's tokens
+// 4g .. 4g + 3 of row l in a lane, which is the layout that the second product,
+// O^T = V^T P^T in bf16, wants its P in: no lane exchanges anything.  V^T's lane
+// has D/16 neighbouring values (a sixteenth of a row) of tokens 4g .. 4g + 3,
+// which is how the cache holds them.  O^T has values (D/4) g .. of row l in a lane.
+//
+// The product of 4 and 8 bits would take the codes as they are, but it is no sum
+// in 32 bits: within a block of 32 it drops what lies some 2^-17 below the largest
+// product (51200 sums of random codes were off by up to 2^-10.4 of it; 76800 of the
+// bf16 product's by 2^-20.5), so that beside one large channel a score is a guess.
+// What bf16 costs: conversions in each wave, and for fp16 two products of 16 bits
+// for three of 8 -- 2 trees of 64 nodes x 16 heads of 256 in fp16 over 65536 tokens
+// 264 us, 233 with 4 and 8 bits; 32 chains of 17 nodes 119 and 117; single tokens
+// and windows the same.
 // ---------------------------------------------------------------------------
 template <int D>
 struct Tokens {  // what a wave reads of 32 tokens
-  static constexpr int kK = D == 64 ? 1 : D / 64;  // 16-byte loads of keys
-  static constexpr int kV = D / 32;                // 8-byte pieces of values
-  i32x4 k[kK];
-  uint32_t ks[kK];  // their scales' bytes
+  static constexpr int kK = D / 64;    // 16 bytes of keys: tile 0's, then tile 1's
+  static constexpr int kS = D == 64 ? 2 : kK;
+  static constexpr int kV = D / 32;    // 8-byte pieces of values
+  u32x4 k[kK];
+  uint32_t ks[kS];  // their scales' bytes
   u32x4 v[kV / 2];  // tile 0's, then tile 1's
   uint32_t vs[2];   // scales of 4 tokens
 };
 
-// The sum of `parts` such products is Q's: bf16 has 8 bits of digits, an e4m3
-// value 4, fp16 11.  Two products of 8 bits take as long as the one of bf16 that
-// they stand for, and the keys need no conversion.  A row has one scale, which takes its largest magnitude
-// to [128, 256); part i holds what the parts before left, times 2^(5 i).
+// A query's values as operands: bf16 as it is, fp16 (11 bits of digits) as two
+// parts of bf16 (8), the second what the first leaves: at most 3 bits, so the sum
+// of their products is Q's.
 template <int D, int PARTS>
 struct Query {
-  static constexpr int kSteps = D == 64 ? 1 : D / 128;
-  static constexpr int kHalves = D / 64;  // of 16 values a lane: 4 words
-  u32x4 w[PARTS][kHalves];
-  uint32_t scale;  // the bytes of the parts' scales
+  static constexpr int kSteps = D / 32;  // products of 32 values
+  u32x4 w[PARTS][kSteps];
 };
 
 template <int D>
-struct QueryRow {  // a lane's 16 values of each 64
-  u32x4 v[D / 64][2];
+struct QueryRow {  // a lane's 8 values for each product
+  u32x4 v[D / 32];
 };
 template <int D>
 __device__ __forceinline__ void fetch_query(QueryRow<D>* out, const char* row, bool live, int g) {
 #pragma unroll
-  for (int h = 0; h < D / 64; ++h) {
-    const u32x4* at = reinterpret_cast<const u32x4*>(row + (64 * h + 16 * g) * 2);
-    out->v[h][0] = live ? at[0] : u32x4{0, 0, 0, 0};
-    out->v[h][1] = live ? at[1] : u32x4{0, 0, 0, 0};
+  for (int s = 0; s < D / 32; ++s) {
+    const int at = D == 64 ? 16 * g + 8 * s : s / 4 * 128 + 32 * g + s % 4 * 8;
+    out->v[s] = live ? *reinterpret_cast<const u32x4*>(row + at * 2) : u32x4{0, 0, 0, 0};
   }
 }
 template <int D, int DT, int PARTS>
 __device__ __forceinline__ void split_query(Query<D, PARTS>* out, const QueryRow<D>& in, bool turn) {
-  constexpr int kHalves = D / 64;  // pieces of 16 values: (64 h + 16 g)
-  float x[kHalves][16];
-  uint32_t m = 0;
+  constexpr uint32_t kInf = DT == SV_F16 ? 0x7c00u : 0x7f80u;
+  const uint32_t sign = turn ? 0x80008000u : 0u;
+  bool bad = false;  // an infinity or NaN in the row
 #pragma unroll
-  for (int h = 0; h < kHalves; ++h) {
+  for (int s = 0; s < D / 32; ++s)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      Eight<DT> e;
-      e.w[0] = in.v[h][i];
-      e.get(x[h] + 8 * i);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[h][i]) & 0x7fffffffu);
-  }
-  m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
-  m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
-  // 2^(e - 7) of a magnitude in [2^e, 2^(e + 1)); parts behind go 2^-10 below it.
-  // Rows that are not finite get the scale that stands for NaN.
-  const int e = (int)(m >> 23) - 7;
-  const int byte = m >= 0x7f800000u ? 255 : min(max(e, 16), 250);
-  out->scale = byte == 255 ? ~0u : (uint32_t)byte | (uint32_t)(byte - 5) << 8 | (uint32_t)(byte - 10) << 16;
-  const float up = __uint_as_float((uint32_t)(254 - (byte == 255 ? 127 : byte)) << 23 | (turn ? 0x80000000u : 0u));
-#pragma unroll
-  for (int h = 0; h < kHalves; ++h)
-#pragma unroll
-    for (int i = 0; i < 16; i += 4) {
-      float y[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) y[j] = byte == 255 ? 0.f : x[h][i + j] * up;
-#pragma unroll
-      for (int q = 0; q < PARTS; ++q) {
-        int w = 0;
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], w, false);
-        w = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
-        out->w[q][h][i / 4] = (uint32_t)w;
-        const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(w, false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w, true);
-        y[0] = (y[0] - a[0]) * 32.f;
-        y[1] = (y[1] - a[1]) * 32.f;
-        y[2] = (y[2] - b[0]) * 32.f;
-        y[3] = (y[3] - b[1]) * 32.f;
-      }
-    }
-}
-
-// Scores of tile u's 16 tokens for a tile of rows.  `words(part, half)`: the
-// query's words.
-template <int D, int PARTS, typename W>
-__device__ __forceinline__ f32x4 scores(const Tokens<D>& t, int u, uint32_t scale, int g, const W& words) {
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  constexpr int kSteps = D == 64 ? 1 : D / 128;
-#pragma unroll
-  for (int part = PARTS - 1; part >= 0; --part) {  // the smallest first
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s) {
-      const int at = D == 64 ? 0 : u * kSteps + s;
-      const i32x8 a = {t.k[at][0], t.k[at][1], t.k[at][2], t.k[at][3], 0, 0, 0, 0};
-      int sa = (int)t.ks[at];
-      u32x4 lo, hi;
-      if constexpr (D == 64) {
-        // one product's 128 values are two tiles' keys, beside the queries
-        // twice; the other tile's scales are made the smallest, 2^-127, beside
-        // which its products vanish (they may be NaN, or as large as any)
-        lo = hi = words(part, 0);
-        if (g / 2 != u) sa = 0;
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = in.v[s][i];
+      bad = bad || (w & kInf) == kInf || (w >> 16 & kInf) == kInf;
+      if constexpr (DT == SV_F16) {
+        const float x = (float)__builtin_bit_cast(_Float16, (uint16_t)(w & 0xffffu));
+        const float y = (float)__builtin_bit_cast(_Float16, (uint16_t)(w >> 16));
+        const uint32_t hi = pack_bf16(x, y);
+        out->w[0][s][i] = hi ^ sign;
+        out->w[1][s][i] = pack_bf16(x - __uint_as_float(hi << 16), y - __uint_as_float(hi & 0xffff0000u)) ^ sign;
       } else {
-        lo = words(part, 2 * s);
-        hi = words(part, 2 * s + 1);
-      }
-      const i32x8 b = {(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-      switch (part) {  // byte `part` of the query's scales
-        case 0: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, sa, 0, (int)scale); break;
-        case 1: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, sa, 1, (int)scale); break;
-        default: acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, 4, 0, 0, sa, 2, (int)scale);
+        out->w[0][s][i] = w ^ sign;
       }
     }
-  }
-  return acc;
+  const uint64_t any = __ballot(bad);  // lanes l, l + 16, .. share a row
+  if (any >> (threadIdx.x % 16) & 0x0001000100010001ull)
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+      for (int s = 0; s < D / 32; ++s) out->w[p][s] = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
 }
 
 template <int SEL>
@@ -223,6 +176,50 @@ __device__ __forceinline__ uint32_t byte_pair(uint32_t w, float scale, int sel) 
     case 1: return two_bf16<1>(w, scale);
     case 2: return two_bf16<2>(w, scale);
     default: return two_bf16<3>(w, scale);
+  }
+}
+
+// The lane's 8 values of tile u's keys for product s, as bf16.
+template <int D>
+__device__ __forceinline__ u32x4 key_step(const Tokens<D>& t, int u, int s) {
+  const int at = D == 64 ? 0 : u * (D / 128) + s / 4;
+  const uint32_t w = t.k[at][D == 64 ? 2 * u + s : s % 4];
+  const float scale = scale_of(t.ks[D == 64 ? u : at]);
+  return u32x4{two_bf16<0>(w, scale), two_bf16<1>(w, scale), two_bf16<2>(w, scale), two_bf16<3>(w, scale)};
+}
+
+// Scores of both tiles' tokens for TT tiles of rows.  `words(r, part, s)`: a
+// query's values.  AHEAD: they are asked for a product ahead (where they lie in LDS
+// and registers are left for them).
+template <int D, int PARTS, int TT, bool AHEAD, typename W>
+__device__ __forceinline__ void scores(const Tokens<D>& t, f32x4 (*acc)[2], const W& words) {
+#pragma unroll
+  for (int r = 0; r < TT; ++r) acc[r][0] = acc[r][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+  u32x4 q[2][TT][PARTS];
+  const auto take = [&](int s) {
+#pragma unroll
+    for (int r = 0; r < TT; ++r)
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part) q[s % 2][r][part] = words(r, part, s);
+  };
+  if constexpr (AHEAD) take(0);
+#pragma unroll
+  for (int s = 0; s < D / 32; ++s) {
+    if constexpr (AHEAD) {
+      if (s + 1 < D / 32) take(s + 1);
+    } else {
+      take(s);
+    }
+    const u32x4 k[2] = {key_step<D>(t, 0, s), key_step<D>(t, 1, s)};
+#pragma unroll
+    for (int r = 0; r < TT; ++r)
+#pragma unroll
+      for (int part = PARTS - 1; part >= 0; --part)  // the smaller first
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          acc[r][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, k[u]),
+                                                              __builtin_bit_cast(bf16x8, q[s % 2][r][part]), acc[r][u], 0, 0, 0);
+    if constexpr (AHEAD) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -311,7 +308,6 @@ struct Shared : FORM {
   union {
     struct {  // while a segment is worked on
       u32x4 q[QUERY ? QUERY : 1];  // queries of many rows (the waves' are the same)
-      uint32_t q_scale[QUERY ? ROWS / kTile * kWave : 1];
       int32_t page[kStaged];
       int32_t parent[SV_MAX_N];  // a tree's window
     };
@@ -545,12 +541,12 @@ template <int D, int TILES, int SPLIT, int DT>
 __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TILES, SPLIT))) void attention_kernel(
     const AttentionParams) {
   using F = Form<TILES, SPLIT>;
-  constexpr int kParts = DT == SV_F16 ? 3 : 2;
+  constexpr int kParts = DT == SV_F16 ? 2 : 1;
   constexpr int kProbs = DT == SV_F16 ? 2 : 1;
   constexpr int kRows = F::kRows, kWaves = F::kWaves, kStreams = F::kStreams, kThreads = F::kThreads, kUnit = F::kUnit;
-  constexpr bool kQueryLds = TILES * D > 256 || TILES > 2 || (SPLIT > 1 && D == 128);
-  constexpr int kHalves = Query<D, kParts>::kHalves;
-  __shared__ __align__(16) Shared<D, F, kQueryLds ? SPLIT * TILES * kParts * kHalves * kWave : 0> sh;
+  constexpr bool kQueryLds = TILES * D > 256 || TILES > 2 || (SPLIT > 1 && D == 128) || (D == 256 && (SPLIT > 1 || DT == SV_F16));
+  constexpr int kSteps = Query<D, kParts>::kSteps;
+  __shared__ __align__(16) Shared<D, F, kQueryLds ? SPLIT * TILES * kParts * kSteps * kWave : 0> sh;
 
   if (!plan(arguments(), sh)) {
     if (threadIdx.x == 0) static_cast<AttentionItem*>(arguments().desc)[blockIdx.x].b = -1;
@@ -564,8 +560,7 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
     const int u0 = uniform(sh.first), u1 = uniform(sh.stop);
 
     // ---- the rows
-    u32x4 q[kQueryLds ? 1 : TILES][kParts][kHalves];
-    uint32_t q_scale[kQueryLds ? 1 : TILES];
+    u32x4 q[kQueryLds ? 1 : TILES][kParts][kSteps];
     // pages of at least 16 tokens: so many steps at a time
     constexpr int kAtOnce = kStaged * kTile / kUnit;
     const int last_tile = (hi - 1) / kTile * kTile;
@@ -596,16 +591,12 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
 #pragma unroll
           for (int part = 0; part < kParts; ++part)
 #pragma unroll
-            for (int h = 0; h < kHalves; ++h) {
+            for (int s = 0; s < kSteps; ++s) {
               if constexpr (kQueryLds)
-                sh.q[((t * kParts + part) * kHalves + h) * kWave + lane] = mine.w[part][h];
+                sh.q[((t * kParts + part) * kSteps + s) * kWave + lane] = mine.w[part][s];
               else
-                q[i][part][h] = mine.w[part][h];
+                q[i][part][s] = mine.w[part][s];
             }
-          if constexpr (kQueryLds)
-            sh.q_scale[t * kWave + lane] = mine.scale;
-          else
-            q_scale[i] = mine.scale;
         }
       }
       if (tid < kRows) {
@@ -646,8 +637,8 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
       const uint32_t off_ks = (uint32_t)p.c.ks, off_vc = (uint32_t)p.c.vc, off_vs = (uint32_t)p.c.vs;
       int page0 = 0;  // page that sh.page[0] stands for
       // Offsets of a lane within a tile: 32 bits beside a wave's base address.
-      const uint32_t lane_k = D == 64 ? l * (D / 2) + (g % 2) * 16 : l * (D / 2) + g * 16;
-      const uint32_t lane_ks = D == 64 ? l * (D / 32) + g % 2 : l * (D / 32) + g;
+      const uint32_t lane_k = l * (D / 2) + (D == 64 ? g * 8 : g * 16);
+      const uint32_t lane_ks = l * (D / 32) + (D == 64 ? g / 2 : g);
       const uint32_t lane_v = (g * 16 + l) * (D / 8), lane_vs = (g * (D / 32) + l * (D / 16) / 32) * 4;
       const auto fetch = [&](int u, Tokens<D>* t) {
         const char* base[2];
@@ -660,21 +651,22 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
           s[i] = (uint32_t)(tt & in_page);
         }
         const uint32_t at_k = opaque(lane_k), at_ks = opaque(lane_ks), at_v = opaque(lane_v), at_vs = opaque(lane_vs);
-        if constexpr (D == 64) {
-          const char* k0 = base[0] + s[0] * (D / 2);
-          const char* k1 = base[1] + s[1] * (D / 2);
-          t->k[0] = *reinterpret_cast<const i32x4*>((g / 2 ? k1 : k0) + at_k);
-          const char* s0 = base[0] + off_ks + s[0] * (D / 32);
-          const char* s1 = base[1] + off_ks + s[1] * (D / 32);
-          t->ks[0] = (uint8_t)(g / 2 ? s1 : s0)[at_ks];
-        } else {
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+        for (int i = 0; i < 2; ++i) {
+          const char* kb = base[i] + s[i] * (D / 2);
+          const char* sb = base[i] + off_ks + s[i] * (D / 32);
+          if constexpr (D == 64) {
+            const uint64_t w = *reinterpret_cast<const uint64_t*>(kb + at_k);
+            t->k[0][2 * i] = (uint32_t)w;
+            t->k[0][2 * i + 1] = (uint32_t)(w >> 32);
+            t->ks[i] = (uint8_t)sb[at_ks];
+          } else {
 #pragma unroll
             for (int k = 0; k < D / 128; ++k) {
-              t->k[i * (D / 128) + k] = *reinterpret_cast<const i32x4*>(base[i] + s[i] * (D / 2) + k * 64 + at_k);
-              t->ks[i * (D / 128) + k] = (uint8_t)(base[i] + off_ks + s[i] * (D / 32) + k * 4)[at_ks];
+              t->k[i * (D / 128) + k] = *reinterpret_cast<const u32x4*>(kb + k * 64 + at_k);
+              t->ks[i * (D / 128) + k] = (uint8_t)(sb + k * 4)[at_ks];
             }
+          }
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -726,24 +718,19 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
           return w >> (4 * g);
         };
         float x[TT][8];
-#pragma unroll
-        for (int r = 0; r < TT; ++r)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            uint32_t qs;
+        {
+          f32x4 sum[TT][2];
+          scores<D, kParts, TT, kQueryLds && D == 256>(t, sum, [&](int r, int part, int at) {
             if constexpr (kQueryLds)
-              qs = sh.q_scale[(tile0 + r) * kWave + lane];
+              return sh.q[(((tile0 + r) * kParts + part) * kSteps + at) * kWave + lane];
             else
-              qs = q_scale[r];
-            const f32x4 s = scores<D, kParts>(t, i, qs, g, [&](int part, int h) {
-              if constexpr (kQueryLds)
-                return sh.q[(((tile0 + r) * kParts + part) * kHalves + h) * kWave + lane];
-              else
-                return q[r][part][h];
-            });
+              return q[r][part][at];
+          });
 #pragma unroll
-            for (int k = 0; k < 4; ++k) x[r][4 * i + k] = s[k];
-          }
+          for (int r = 0; r < TT; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[r][i] = sum[r][i / 4][i % 4];
+        }
         if (bent) {
           const AttentionParams& a = arguments();
           const float cap = a.cap * kLog2e, up = 2.f / a.cap;
