@@ -208,7 +208,8 @@ sv_status sv_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32
  * by two parts of bf16 whose sum a query is).  Products, sums and the softmax are
  * held in 32 bits (a cap is off by 2^-21 of itself); probabilities are rounded to
  * the 8 bits of bf16 (fp16: 16 bits) before they multiply the values, and are
- * summed as rounded.
+ * summed as rounded: a result is off by up to 2^-8 (2^-16) of how far the values
+ * that it averages lie from it, beside the rounding of its own type.
  */
 sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, const sv_kv_cache* cache,
                           const int32_t* lens, const int32_t* news, const int32_t* parent, int32_t B, int32_t N,

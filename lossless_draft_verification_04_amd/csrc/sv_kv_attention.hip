@@ -821,6 +821,14 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
             }
           }
         }
+        // Probabilities are rounded to what the second product takes, and summed as
+        // rounded, so that a row whose tokens' values are alike loses nothing: to
+        // the 8 bits of bf16, whose results are themselves rounded to 8 (off by
+        // 0.0019 to 0.0023 of 64 bits' in all, the rounding of the results alone
+        // 0.0017), in fp16 to two parts, 16 bits, beside results of 11.  Two parts
+        // for bf16 too give 0.0017 and take 144 us instead of 119 for 32 chains of
+        // 17 nodes x 32 heads, 380 instead of 313 for 1024 nodes, 77 instead of 70
+        // for single tokens.
         u32x4 pr[TT][kProbs];
 #pragma unroll
         for (int r = 0; r < TT; ++r) {
