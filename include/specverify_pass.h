@@ -196,11 +196,12 @@ sv_status sv_kv_read(const sv_kv_cache* cache, const int32_t* start, const int32
  *     q and out
  * Hq is a multiple of cache->H.  A sequence whose length or count is out of
  * range sets SV_DERR_RANGE and is left as it was.  A page outside [0,
- * num_pages) sets it too; its tokens count as masked.  A row that sees
- * nothing is 0, its out_lse -inf.  A node whose parent is not before it sets
- * SV_DERR_TREE and sees the tokens before the window and itself.  NaN in a
- * token that a row does not see does not reach it; queries are finite (a row
- * with a NaN or an infinity is NaN).
+ * num_pages) that has a token which the root sees, or one behind it, sets it too;
+ * such a page's tokens count as masked (what lies wholly before the reach may be
+ * gone).  A row that sees nothing is 0, its out_lse -inf.  A node whose parent is
+ * not before it sets SV_DERR_TREE and sees the tokens before the window and itself.
+ * NaN in a token that a row does not see does not reach it; queries are finite (a
+ * row with a NaN or an infinity is NaN).
  *
  * The cache is read once for all query heads of a key head and up to 256 rows
  * (192 at D = 128, 64 at D = 256) of nodes x heads.  Keys become bf16 as they are

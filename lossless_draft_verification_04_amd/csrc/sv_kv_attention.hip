@@ -51,6 +51,11 @@ struct Span {
   int64_t u0, units;  // first step of the sequence's tokens, number of steps
 };
 
+// The first token that a row of the window may see: those of a root at place len.
+__device__ __forceinline__ int64_t first_seen(int32_t len, int32_t reach) {
+  return reach > 0 ? max((int64_t)len - reach + 1, (int64_t)0) : 0;
+}
+
 template <int UNIT>
 __device__ __forceinline__ Span span_of(const AttentionParams& p, int64_t b) {
   Span s;
@@ -62,8 +67,7 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, int64_t b) {
     return s;
   }
   if (s.news == 0) return s;
-  const int64_t lo = p.reach > 0 ? max((int64_t)s.len - p.reach + 1, (int64_t)0) : 0;
-  s.u0 = lo / UNIT;
+  s.u0 = first_seen(s.len, p.reach) / UNIT;
   s.units = ((int64_t)s.len + s.news + UNIT - 1) / UNIT - s.u0;
   return s;
 }
@@ -906,11 +910,13 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
           const AttentionParams& a = arguments();
           const int32_t* pages = a.c.pages + (int64_t)sh.b * a.c.max_pages + page0;
           const int staged = (min(v1 * kUnit - 1, last_tile) >> pshift) - page0 + 1;
+          // pages behind the reach, in the step that it ends in, may be gone
+          const int needed = (int)(first_seen(len, reach) >> pshift) - page0;
           if (v0 > u0) __syncthreads();  // (the first time, a segment's end was one)
           for (int i = thread(); i < staged; i += kThreads) {
             const int32_t id = pages[i];
             const bool bad = (uint32_t)id >= (uint32_t)a.c.num_pages;
-            lost = lost || bad;
+            lost = lost || (bad && i >= needed);
             sh.page[i] = bad ? -1 : id;
           }
           if (lost) flag(a.err, SV_DERR_RANGE);

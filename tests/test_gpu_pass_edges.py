@@ -274,6 +274,31 @@ def test_attention_out_of_range(tree, D):
             assert bool((out[5, 0] == 0).all()) and bool((got["lse"][5, 0] == -math.inf).all())
 
 
+@pytest.mark.parametrize("D,N,G", [(64, 1, 1), (64, 33, 8), (128, 5, 4), (128, 20, 12), (256, 1, 2), (256, 17, 4)])
+@pytest.mark.parametrize("tree", [False, True])
+def test_attention_pages_behind_the_reach(tree, D, N, G):
+    """A window that slides has let its oldest pages go: those without a token that a row can see are no error, whatever step of
+    the tokens they lie in; the first one that has such a token is."""
+    H, P, n0 = 1, 16, 200
+    c, h = filled(1, H, D, P, (n0,), N, seed=D)
+    q = queries(1, N, H * G, D, BF16, N)
+    parent = ref.random_tree(N, 3)[None] if tree else None
+    for reach in (1, 2, 40, 41, 42, 50, 57, 73, 160, 185):
+        first = (n0 - reach + 1) // P  # the page of the first token that the root sees
+        want = check_attention(c, h, q, (n0,), parent=parent, reach=reach)
+        for gone in (-1, c.n, 2 ** 31 - 1):
+            pages = c.pages.clone()
+            pages[0, :first] = gone
+            lost = svx.KvCache(h.pool, pages.to(DEV), H, D, P)
+            got = check_attention(c, lost, q, (n0,), parent=parent, reach=reach)
+            assert errors() == 0, (reach, gone)
+            assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+            pages[0, first] = gone
+            lost = svx.KvCache(h.pool, pages.to(DEV), H, D, P)
+            svx.sv_kv_attention(lost, q.to(DEV), i32(n0), parent=parent.to(DEV) if tree else None, reach=reach)
+            assert errors() == DERR_RANGE, (reach, gone)
+
+
 def masked_attention(q, k, v, n0, parent, keep, dtype):
     """pass_ref.attention without some tokens: each row by itself, over those that it sees."""
     n, Hq, D = q.shape
