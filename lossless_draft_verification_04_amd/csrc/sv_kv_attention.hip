@@ -284,7 +284,6 @@ __device__ __forceinline__ uint32_t opaque(uint32_t x) {
 }
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-constexpr int kStaged = 1024;               // page numbers at a time, -1 for one that is none of the pool
 constexpr int kChunks = SV_MAX_N / 32 + 1;  // steps of 32 tokens that hold nodes
 
 template <int N>
@@ -301,6 +300,7 @@ struct Form {
   static constexpr int kWaves = SPLIT * kStreams, kThreads = kWaves * kWave;
   static constexpr int kUnit = kStreams * kWaveTokens;  // tokens of a step
   static constexpr int kRows = SPLIT * TILES * kTile;
+  static constexpr int kPages = SPLIT == 1 ? 512 : 256;  // page numbers that a wave has at a time
 };
 
 // What the waves of a block share.  QUERY: words of queries kept here.
@@ -312,7 +312,7 @@ struct Shared : FORM {
   union {
     struct {  // while a segment is worked on
       u32x4 q[QUERY ? QUERY : 1];  // queries of many rows (the waves' are the same)
-      int32_t page[kStaged];
+      int32_t page[kWaves][FORM::kPages];  // each wave's own; -1 for one that is none of the pool
       int32_t parent[SV_MAX_N];  // a tree's window
     };
     float o[kWaves][kTile][D + 4];  // as it ends
@@ -565,8 +565,6 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
 
     // ---- the rows
     u32x4 q[kQueryLds ? 1 : TILES][kParts][kSteps];
-    // pages of at least 16 tokens: so many steps at a time
-    constexpr int kAtOnce = kStaged * kTile / kUnit;
     const int last_tile = (hi - 1) / kTile * kTile;
     {
       const AttentionParams& p = arguments();
@@ -611,13 +609,15 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
         sh.slope[tid] = live && p.slopes ? p.slopes[head] * kLog2e : 0.f;
       }
     }
+    __syncthreads();
 
-    // ---- the tokens, for a wave of TT tiles of rows, from tile `tile0` of the group on
+    // ---- the tokens, for a wave of TT tiles of rows, from tile `tile0` of the group
+    // on.  Waves go through this apart: no barriers in it.
+    Rows16<D> rows[TILES];
     const auto body = [&](auto count) {
       constexpr int TT = decltype(count)::value;
-      Rows16<D> rows[TT];
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
+      for (int t = 0; t < TILES; ++t) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) rows[t].o[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         rows[t].l = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -639,7 +639,8 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
       const int64_t page_stride = p.c.page_stride;
       const int pshift = p.c.pshift, in_page = (1 << pshift) - 1;
       const uint32_t off_ks = (uint32_t)p.c.ks, off_vc = (uint32_t)p.c.vc, off_vs = (uint32_t)p.c.vs;
-      int page0 = 0;  // page that sh.page[0] stands for
+      int page0 = 0;  // page that the wave's first number stands for
+      int32_t* const page = sh.page[wave];
       // Offsets of a lane within a tile: 32 bits beside a wave's base address.
       const uint32_t lane_k = l * (D / 2) + (D == 64 ? g * 8 : g * 16);
       const uint32_t lane_ks = l * (D / 32) + (D == 64 ? g / 2 : g);
@@ -650,7 +651,7 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int tt = min(u * kUnit + stream * kWaveTokens + i * kTile, last_tile);
-          const int id = max(uniform(sh.page[(tt >> pshift) - page0]), 0);
+          const int id = max(uniform(page[(tt >> pshift) - page0]), 0);
           base[i] = pool + id * page_stride;
           s[i] = (uint32_t)(tt & in_page);
         }
@@ -709,7 +710,7 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
           nan = __any(nan);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (sh.page[(min(t0 + i * kTile, last_tile) >> pshift) - page0] < 0) gone |= 0xffffu << (16 * i);
+            if (page[(min(t0 + i * kTile, last_tile) >> pshift) - page0] < 0) gone |= 0xffffu << (16 * i);
         }
         // what row l of tile r sees of the lane's tokens: bits 0 .. 3 and 16 .. 19
         const auto seen = [&](int r) {
@@ -902,8 +903,10 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
         }
       };
 
-      for (int v0 = u0; v0 < u1; v0 += kAtOnce) {
-        const int v1 = min(v0 + kAtOnce, u1);
+      // so many steps at a time (they may begin and end inside a page)
+      const int at_once = ((F::kPages - 1) << pshift) / kUnit;
+      for (int v0 = u0; v0 < u1; v0 += at_once) {
+        const int v1 = min(v0 + at_once, u1);
         page0 = v0 * kUnit >> pshift;
         bool lost = false;
         {
@@ -912,15 +915,15 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
           const int staged = (min(v1 * kUnit - 1, last_tile) >> pshift) - page0 + 1;
           // pages behind the reach, in the step that it ends in, may be gone
           const int needed = (int)(first_seen(len, reach) >> pshift) - page0;
-          if (v0 > u0) __syncthreads();  // (the first time, a segment's end was one)
-          for (int i = thread(); i < staged; i += kThreads) {
+          for (int i = lane; i < staged; i += kWave) {
             const int32_t id = pages[i];
             const bool bad = (uint32_t)id >= (uint32_t)a.c.num_pages;
             lost = lost || (bad && i >= needed);
-            sh.page[i] = bad ? -1 : id;
+            page[i] = bad ? -1 : id;
           }
           if (lost) flag(a.err, SV_DERR_RANGE);
-          lost = uniform(__syncthreads_or(lost));
+          lost = __any(lost);
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // a lane reads what others have written
         }
         // The next step's loads fly while this one is worked on; behind the last
         // it is read again, so that the number of loads in flight is known.
@@ -936,88 +939,88 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
         }
       }
 
-      // ---- the streams' sums together, a tile of rows at a time
-      {
-        const AttentionParams& a = arguments();
-        const int id = thread(), l = id % 16, g = id % kWave / 16;
-        const int w0 = wave - stream;  // the wave of the first stream
-        const int b = sh.b, row0 = sh.group * kRows + tile0 * kTile, slot = sh.slot;
-        const bool whole = sh.whole;
-        more = sh.at < sh.end;  // read ahead of the barriers behind which the next segment is planned
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-          if (g == 0) {
-            sh.m[wave][t * kTile + l] = rows[t].reference();
-            sh.l[wave][t * kTile + l] = rows[t].l[0];
-          }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) {  // as many barriers for every wave
-          if (t < TT) {
-            const Rows16<D>& mine = rows[t < TT ? t : 0];
-            float m = kNegInf;
-#pragma unroll
-            for (int w = 0; w < kStreams; ++w) m = fmaxf(m, sh.m[w0 + w][t * kTile + l]);
-            const float f = part_weight(mine.reference(), m);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-              for (int i = 0; i < D / 16; i += 4) {
-                const f32x4 v = {mine.o[i][k] * f, mine.o[i + 1][k] * f, mine.o[i + 2][k] * f, mine.o[i + 3][k] * f};
-                *reinterpret_cast<f32x4*>(&sh.o[wave][l][(4 * g + k) * (D / 16) + i]) = v;
-              }
-          }
-          __syncthreads();
-          // a row to 4 threads of each stream, neighbouring values each
-          constexpr int kCols = 4 * kStreams, kCount = D / kCols;
-          const int in = id - w0 * kWave;
-          const int r = in / kCols, col = in % kCols * kCount;
-          const int rr = t * kTile + r, row = row0 + rr;
-          const int n = row / a.G, head = sh.h * a.G + row - n * a.G;
-          if (t < TT && n < sh.news) {
-            float mm = kNegInf, ll = 0.f;
-#pragma unroll
-            for (int w = 0; w < kStreams; ++w) mm = fmaxf(mm, sh.m[w0 + w][rr]);
-#pragma unroll
-            for (int w = 0; w < kStreams; ++w) ll += sh.l[w0 + w][rr] * part_weight(sh.m[w0 + w][rr], mm);
-            float o[kCount];
-#pragma unroll
-            for (int i = 0; i < kCount; i += 4) {
-              f32x4 v = *reinterpret_cast<const f32x4*>(&sh.o[w0][r][col + i]);
-#pragma unroll
-              for (int w = 1; w < kStreams; ++w) v += *reinterpret_cast<const f32x4*>(&sh.o[w0 + w][r][col + i]);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[i + k] = v[k];
-            }
-            if (whole) {
-              finish<D, DT, kCount>(a, b, n, head, col, o, mm, ll, a.parent ? sh.depth[n] : n);
-            } else {
-              const int64_t part = (int64_t)slot * kRows + tile0 * kTile + rr;
-              float* po = a.part_o + part * D + col;
-#pragma unroll
-              for (int i = 0; i < kCount; i += 4)
-                *reinterpret_cast<f32x4*>(po + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
-              if (col == 0) {
-                a.part_ml[part * 2] = mm;
-                a.part_ml[part * 2 + 1] = ll;
-              }
-            }
-          }
-          __syncthreads();
-        }
-      }
     };
     // The last rows' waves may have a tile less to do (5 tiles in 2 x 3: 120 us,
     // with three in both 142).
-    if constexpr (SPLIT > 1 && TILES > 1) {
-      const int wave = uniform(thread() / kWave);
-      if (arguments().all_tiles - (sh.group * SPLIT + wave / kStreams) * TILES < TILES)
-        body(Number<TILES - 1>{});
-      else
-        body(Number<TILES>{});
-    } else {
+    const auto first_tile = [&](int wave) { return wave / kStreams * TILES; };
+    const bool fewer = SPLIT > 1 && TILES > 1 &&
+                       arguments().all_tiles - sh.group * SPLIT * TILES - first_tile(uniform(thread() / kWave)) < TILES;
+    if (fewer)
+      body(Number<(TILES > 1 ? TILES - 1 : 1)>{});
+    else
       body(Number<TILES>{});
+
+    // ---- the streams' sums together, a tile of rows at a time
+    {
+      const AttentionParams& a = arguments();
+      const int id = thread(), l = id % 16, g = id % kWave / 16, wave = uniform(id / kWave);
+      const int tile0 = first_tile(wave), w0 = wave / kStreams * kStreams;  // the wave of the first stream
+      const int b = sh.b, row0 = sh.group * kRows + tile0 * kTile, slot = sh.slot;
+      const bool whole = sh.whole;
+      more = sh.at < sh.end;  // read ahead of the barriers behind which the next segment is planned
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        if (g == 0) {
+          sh.m[wave][t * kTile + l] = rows[t].reference();
+          sh.l[wave][t * kTile + l] = rows[t].l[0];
+        }
+      }
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < TILES; ++t) {
+        const bool here = t < TILES - 1 || !fewer;
+        if (here) {
+          const Rows16<D>& mine = rows[t];
+          float m = kNegInf;
+#pragma unroll
+          for (int w = 0; w < kStreams; ++w) m = fmaxf(m, sh.m[w0 + w][t * kTile + l]);
+          const float f = part_weight(mine.reference(), m);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < D / 16; i += 4) {
+              const f32x4 v = {mine.o[i][k] * f, mine.o[i + 1][k] * f, mine.o[i + 2][k] * f, mine.o[i + 3][k] * f};
+              *reinterpret_cast<f32x4*>(&sh.o[wave][l][(4 * g + k) * (D / 16) + i]) = v;
+            }
+        }
+        __syncthreads();
+        // a row to 4 threads of each stream, neighbouring values each
+        constexpr int kCols = 4 * kStreams, kCount = D / kCols;
+        const int in = id - w0 * kWave;
+        const int r = in / kCols, col = in % kCols * kCount;
+        const int rr = t * kTile + r, row = row0 + rr;
+        const int n = row / a.G, head = sh.h * a.G + row - n * a.G;
+        if (here && n < sh.news) {
+          float mm = kNegInf, ll = 0.f;
+#pragma unroll
+          for (int w = 0; w < kStreams; ++w) mm = fmaxf(mm, sh.m[w0 + w][rr]);
+#pragma unroll
+          for (int w = 0; w < kStreams; ++w) ll += sh.l[w0 + w][rr] * part_weight(sh.m[w0 + w][rr], mm);
+          float o[kCount];
+#pragma unroll
+          for (int i = 0; i < kCount; i += 4) {
+            f32x4 v = *reinterpret_cast<const f32x4*>(&sh.o[w0][r][col + i]);
+#pragma unroll
+            for (int w = 1; w < kStreams; ++w) v += *reinterpret_cast<const f32x4*>(&sh.o[w0 + w][r][col + i]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[i + k] = v[k];
+          }
+          if (whole) {
+            finish<D, DT, kCount>(a, b, n, head, col, o, mm, ll, a.parent ? sh.depth[n] : n);
+          } else {
+            const int64_t part = (int64_t)slot * kRows + tile0 * kTile + rr;
+            float* po = a.part_o + part * D + col;
+#pragma unroll
+            for (int i = 0; i < kCount; i += 4)
+              *reinterpret_cast<f32x4*>(po + i) = f32x4{o[i], o[i + 1], o[i + 2], o[i + 3]};
+            if (col == 0) {
+              a.part_ml[part * 2] = mm;
+              a.part_ml[part * 2 + 1] = ll;
+            }
+          }
+        }
+        __syncthreads();
+      }
     }
   } while (more);
   if (threadIdx.x == 0 && !sh.open) static_cast<AttentionItem*>(arguments().desc)[blockIdx.x].b = -1;

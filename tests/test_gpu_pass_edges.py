@@ -146,6 +146,36 @@ def test_attention_pages_staged_more_than_once(D, B, H, T, N, G, dtype):
             near(got["lse"][b, :, rows], lse, lse_tol, f"lse of {b}")
 
 
+@pytest.mark.parametrize("D,N,G,B", [(128, 20, 4, 64), (128, 40, 4, 64), (64, 36, 4, 70)])
+def test_attention_lost_pages_where_waves_have_other_rows(D, N, G, B):
+    """A block's waves of which some have fewer rows, each with its own stretches of page numbers, some of them of no page."""
+    T = 17000
+    c, _ = filled(1, 1, D, 16, (4000,), 96, seed=D + N, sigma=0.5)
+    h = handle(c)
+    g = torch.Generator().manual_seed(N)
+    many = -(-(T + N) // 16)
+    c.pages = c.pages[0, torch.randint(0, c.pages.shape[1], (B, many), generator=g)].contiguous()
+    lens = T - torch.randint(0, 999, (B,), generator=g, dtype=torch.int32)
+    lost = {1: [0, 3, 254, 255, 256, 511, 512, 700, 990], B - 1: [1, 253, 254, 600]}
+    pages = c.pages.clone()
+    for b, at in lost.items():
+        pages[b, at] = torch.tensor([-1, c.n], dtype=torch.int32).repeat(9)[:len(at)]
+    h = svx.KvCache(h.pool, pages.to(DEV), 1, D, 16)
+    q = queries(B, N, G, D, BF16, B)
+    got = svx.sv_kv_attention(h, q.to(DEV), lens.to(DEV), want_lse=True)
+    assert errors() == DERR_RANGE
+    for b in (0, 1, B - 1):
+        n0 = int(lens[b])
+        k, v = c.tokens(b, n0 + N)
+        keep = torch.ones(n0 + N, dtype=torch.bool)
+        for p in lost.get(b, ()):
+            keep[16 * p:16 * p + 16] = False
+        assert bool(keep[n0:].all())
+        want, lse, tol, lse_tol, _ = ref.attention(q[b], k[keep], v[keep], int(keep[:n0].sum()), None, D ** -0.5, 0.0, None, 0, BF16)
+        near(got["out"][b], want, tol, f"out of {b}")
+        near(got["lse"][b], lse, lse_tol, f"lse of {b}")
+
+
 @pytest.mark.parametrize("B,N,G,T", [(1100, 16, 9, 90), (32768, 1, 1, 15), (2000, 3, 1, 400)])
 def test_attention_more_sequences_than_threads(B, N, G, T):
     """Sequences of very different lengths, many without anything to do; their pages are few, in many places."""
