@@ -1027,7 +1027,9 @@ def sv_kv_commit(cache, lens, n, path=None, out_lens=None, workspace=None):
     _int32(out_lens, (B,), "out_lens")
     dev = _one_device("sv_kv_commit", cache.pool, lens, n, path, out_lens, workspace)
     ws = workspace if workspace is not None else _pass_workspace(dev, SV_PASS_COMMIT)
-    _call(dev, _lib.sv_kv_commit, "sv_kv_commit", cache._ref, lens.data_ptr(), n.data_ptr(), _at(path), B,
-          path.shape[1] if path is not None else 0, out_lens.data_ptr(), ws.data_ptr(), ws.numel())
+    # a path without places has no address, and none would say a chain: any other will do, nothing of it is read
+    M, at = (0, None) if path is None else (path.shape[1], path.data_ptr() or lens.data_ptr())
+    _call(dev, _lib.sv_kv_commit, "sv_kv_commit", cache._ref, lens.data_ptr(), n.data_ptr(), at, B, M, out_lens.data_ptr(),
+          ws.data_ptr(), ws.numel())
     _checked(dev, "sv_kv_commit", workspace)
     return out_lens

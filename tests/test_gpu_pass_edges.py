@@ -450,6 +450,18 @@ def test_commit_out_of_range(layers):
     assert chain.tolist() == [9] * (B - 4) + [-1, 48, 47, 46] and errors() == DERR_RANGE
 
 
+def test_commit_of_paths_without_places():
+    """A path [B, 0] is a path, not a chain: only n of 0 and -1 are in range."""
+    c = ref.Cache(4, 1, 64, 16, 2, seed=1)
+    h = handle(c)
+    path = torch.zeros(4, 0, dtype=torch.int32, device=DEV)
+    assert svx.sv_kv_commit(h, i32(5, 6, 7, 8), i32(0, -1, 0, 0), path=path).tolist() == [6, 6, 8, 9]
+    assert errors() == 0
+    assert svx.sv_kv_commit(h, i32(5, 6, 7, 8), i32(1, 0, 9, -2), path=path).tolist() == [5, 7, 7, 8]
+    assert errors() == DERR_RANGE
+    assert torch.equal(h.pool.cpu(), c.pool[0])
+
+
 def test_nothing_to_do():
     c, h = filled(3, 1, 64, 16, (5, 9, 0), 4, seed=1)
     q = queries(3, 4, 2, 64, BF16, 1).to(DEV)
