@@ -1006,7 +1006,7 @@ def sv_kv_attention(cache, q, lens, news=None, parent=None, scale=None, cap=0.0,
     lse = torch.empty(B, N, Hq, dtype=torch.float32, device=dev) if want_lse else None
     _call(dev, _lib.sv_kv_attention, "sv_kv_attention", q.data_ptr(), sq, dt, cache._one("sv_kv_attention"), lens.data_ptr(),
           _at(news), _at(parent), B, N, Hq, float(D ** -0.5 if scale is None else scale), float(cap), _at(slopes),
-          int(reach), out.data_ptr(), _window(out, "out")[1], _at(lse), ws.data_ptr(), ws.numel())
+          max(-1, min(int(reach), 2 ** 31 - 1)), out.data_ptr(), _window(out, "out")[1], _at(lse), ws.data_ptr(), ws.numel())
     _checked(dev, "sv_kv_attention", workspace)
     return dict(out=out, lse=lse)
 

@@ -2,6 +2,7 @@
 than once, offsets past 32 bits, bad pages, lengths, parents and paths, captured calls, streams, and the calls of a round
 together."""
 import math
+import sys
 
 import pytest
 import torch
@@ -69,6 +70,19 @@ def test_attention_reach_without_end():
     for reach in (305, 320, 1 << 20, 2 ** 31 - 2, 2 ** 31 - 1):
         assert torch.equal(check_attention(c, h, q, (0, 300), reach=reach)["out"], want["out"])
         assert torch.equal(check_attention(c, h, q, (0, 300), parent=parent, reach=reach)["out"], tree["out"])
+
+
+def test_attention_reach_beyond_32_bits():
+    """A reach of any size is one: no number of 64 bits becomes a smaller one, or one below 0, on its way."""
+    c, h = filled(1, 1, 64, 16, (300,), 5, seed=3)
+    q = queries(1, 5, 2, 64, BF16, 3).to(DEV)
+    want = svx.sv_kv_attention(h, q, i32(300))["out"]
+    for reach in (2 ** 31, 2 ** 32 - 1, 2 ** 32, 2 ** 32 + 5, sys.maxsize, 10 ** 30):
+        assert torch.equal(svx.sv_kv_attention(h, q, i32(300), reach=reach)["out"], want), reach
+    for reach in (-1, -2 ** 31, -2 ** 32, 5 - 2 ** 32, -10 ** 30):
+        with pytest.raises(svx.SpecVerifyError) as e:
+            svx.sv_kv_attention(h, q, i32(300), reach=reach)
+        assert e.value.status == svx.SV_EINVAL
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
