@@ -288,6 +288,7 @@ sv_status sv_rope_frequencies(sv_rope_kind kind, int32_t R, double theta, double
     const auto pair = [&](double n) { return R * std::log(original / (n * 2 * M_PI)) / (2 * std::log(theta)); };
     low = std::max(std::floor(pair(fast)), 0.0);
     high = std::min(std::ceil(pair(slow)), (double)(R - 1));
+    if (pair(slow) < 0) low = high = -1;  // the first pair is slow: all are
   }
   if (kind == SV_ROPE_BASE && R > 2) theta *= std::pow(scale, (double)R / (R - 2));
   for (int i = 0; i < R / 2; ++i) {

@@ -187,6 +187,19 @@ def test_rope_frequencies_refuse():
         assert f(**kw) == svx.SV_EINVAL, kw
 
 
+def test_rope_frequencies_by_parts_where_all_are_slow():
+    """Angles of less than `slow` turns over `original` positions are divided by the scale, the first pair's among them."""
+    for R, original, fast, slow in ((64, 4096, 2000.0, 1000.0), (64, 4, 32.0, 1.0), (2, 6, 2.0, 1.0), (128, 100, 40.0, 16.0)):
+        plain, _ = svx.sv_rope_frequencies(R)
+        assert float(original * plain[0]) / (2 * math.pi) < slow
+        f, _ = svx.sv_rope_frequencies(R, kind="parts", scale=4.0, original=original, fast=fast, slow=slow)
+        assert torch.allclose(f, plain / 4, rtol=1e-15, atol=0)
+    for R, original, fast, slow in ((64, 4096, 600.0, 1.0), (64, 128, 32.0, 1.0), (64, 7, 32.0, 1.0)):  # the first pair turns more than that
+        plain, _ = svx.sv_rope_frequencies(R)
+        f, _ = svx.sv_rope_frequencies(R, kind="parts", scale=4.0, original=original, fast=fast, slow=slow)
+        assert f[0] == 1.0 and f[-1] == plain[-1] / 4
+
+
 def test_binding_refuses_layouts():
     B, H, D, N = 2, 2, 64, 3
     pool = torch.zeros(6, svx.kv_page_bytes(H, D, 16), dtype=torch.uint8)
