@@ -169,3 +169,50 @@ def test_ordinary_scores(n, G, D, dtype):
     k = torch.randn(T, H, D, generator=g)
     k[..., ::16] *= 4
     check(k, values(T, H, D, 5), queries(1, n, H * G, D, dtype, 5)[0], P=16)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,G", [(4, 1), (30, 4)])
+def test_what_is_not_finite(n, G, D, dtype):
+    """An infinity or NaN anywhere in a query makes its row NaN (also where all scores would be -inf, as beside keys of one sign),
+    one in a key the rows that see its token, and no other row or head."""
+    H, T, P = 2, 150 + n, 16
+    g = torch.Generator().manual_seed(D + n)
+    k, v = torch.rand(T, H, D, generator=g) + 0.5, values(T, H, D, 6)
+    q = torch.randn(n, H * G, D, generator=g)
+    c = ref.Cache(1, H, D, P, -(-T // P), seed=1)
+    h = handle(c)
+    for bad in (math.inf, -math.inf, math.nan):
+        for at in (0, 1, 17, D // 2 + 7, D - 1):
+            qq = q.clone()
+            qq[n - 1, H * G - 1] = 0.0
+            qq[n - 1, H * G - 1, at] = qq[0, 0, at] = bad
+            svx.sv_kv_write(h, k[None].to(DEV), v[None].to(DEV), i32(0))
+            got = svx.sv_kv_attention(h, qq[None].to(dtype).to(DEV), i32(T - n), want_lse=True)
+            nan = torch.zeros(n, H * G, dtype=torch.bool)
+            nan[n - 1, H * G - 1] = nan[0, 0] = True
+            assert torch.equal(got["out"][0].cpu().isnan(), nan[..., None].expand(n, H * G, D)), (bad, at)
+            assert torch.equal(got["lse"][0].cpu().isnan(), nan), (bad, at)
+            # a key of the last head, of a node in the middle
+            kk = k.clone()
+            kk[T - n + n // 2, H - 1, at] = bad
+            svx.sv_kv_write(h, kk[None].to(DEV), v[None].to(DEV), i32(0))
+            got = svx.sv_kv_attention(h, q[None].to(dtype).to(DEV), i32(T - n), want_lse=True)
+            nan = torch.zeros(n, H * G, dtype=torch.bool)
+            nan[n // 2:, (H - 1) * G:] = True
+            assert torch.equal(got["out"][0].cpu().isnan(), nan[..., None].expand(n, H * G, D)), (bad, at)
+            assert torch.equal(got["lse"][0].cpu().isnan(), nan), (bad, at)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_least_and_largest_magnitudes(D, dtype):
+    """Keys near the ends of the scales' range beside queries that bring their scores to ordinary size, and the type's least
+    values beside large keys: nothing is flushed, nothing overflows."""
+    H, G, n, T = 2, 2, 3, 100
+    g = torch.Generator().manual_seed(D)
+    for size in (2.0 ** -100, 2.0 ** 100) if dtype is BF16 else (2.0 ** -13, 2.0 ** 22):
+        k = torch.randint(-3, 4, (T, H, D), generator=g) * size
+        q = torch.randint(-4, 5, (n, H * G, D), generator=g) / size
+        check(k.float(), values(T, H, D, 7), q.to(dtype), exact=True)
