@@ -117,10 +117,10 @@ sv_status sv_pass_workspace_size(sv_pass_op op, int32_t B, int32_t N, int32_t Hq
  *     parent [B, N] (NULL: its number); with parent, N <= SV_MAX_N
  * out_q, out_k may be q, k (the same pointer and strides: in place) and must
  * not overlap them otherwise; all may be views of different heads of one tensor
- * (a fused projection), with equal strides.  Angles are formed in 64 bits and reduced to a
- * turn before their sine is taken, so far positions keep their digits.  A
- * node whose parent is not before it sets SV_DERR_TREE and has depth 0.  All N
- * nodes turn, padding too.
+ * (a fused projection), with equal strides.  Angles are formed in 64 bits and
+ * reduced to a turn, so far positions keep their digits; sine, cosine and products
+ * are of 32 bits (off by 2^-21 of |x| + |y| at most).  A node whose parent is not
+ * before it sets SV_DERR_TREE and has depth 0.  All N nodes turn, padding too.
  */
 sv_status sv_rope(const void* q, const int64_t* q_stride, const void* k, const int64_t* k_stride, sv_dtype dt,
                   int32_t B, int32_t N, int32_t Hq, int32_t Hk, int32_t D, int32_t R, const double* freq, float factor,
@@ -229,8 +229,9 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
  * n[b] = -1 leaves a sequence as it was (it took no part), out_lens[b] =
  * lens[b].  So does a path that does not rise from 1 on within SV_MAX_N nodes,
  * which sets SV_DERR_TREE, and n outside [-1, M] (a chain: n < -1), a length out
- * of range or a page outside [0, num_pages), which sets SV_DERR_RANGE.
- * 0 <= M <= SV_MAX_N.
+ * of range or a page outside [0, num_pages) that a token moves from or to, which
+ * sets SV_DERR_RANGE.  0 <= M <= SV_MAX_N; a path of M = 0 (any pointer but NULL,
+ * not read) lets the root alone stay.
  */
 sv_status sv_kv_commit(const sv_kv_cache* cache, const int32_t* lens, const int32_t* n, const int32_t* path, int32_t B,
                        int32_t M, int32_t* out_lens, void* ws, size_t ws_bytes, void* stream);

@@ -7,16 +7,20 @@
 // tokens and the blocks' parts of a sequence are joined at the end, always in
 // the same order.
 //
-// What bounds it (32 x 8192 tokens and the like; 6.1 TB/s is what a read of HBM
-// reaches, 1147 TFLOP/s what a large bf16 product does):
-//   few rows: memory.  64 sequences of one token, 8 x 128 heads: 428 MB in 95 us,
+// What bounds it (6.1 TB/s is what a read of HBM reaches, 1147 TFLOP/s what a large
+// bf16 product does; busy: shares of the kernel's time by counters; the times of
+// this file, one build against another in turn on one device, belong together):
+//   few rows: memory.  64 sequences of one token, 8 x 128 heads: 428 MB in 96 us,
 //     4.5 TB/s, about 5 once it runs; its start, the blocks' ends and the join are
-//     some 15 us.  Loads two steps ahead instead of one took as long (97.5).
-//   many rows: vector and matrix instructions together.  32 chains of 17 nodes x
-//     32 heads of 128: 105 to 115 us, of which memory would need 37 and the products,
-//     at a large product's rate, 48.  The conversion of the values to bf16 is
-//     shared by a wave's tiles, the exponentials are not.
-//   one window: 16 us of dependent loads (lengths, queries, pages, tokens, parts),
+//     some 15 us.  With heads of 64 (214 MB, 70 to 75 us with a bias) a step has half
+//     the bytes for as many addresses, scores and exponentials: vector instructions
+//     busy 58%, matrix 9%.
+//   many rows: vector and matrix instructions, in part one after the other.  32
+//     chains of 17 nodes x 32 heads of 128: 117 to 120 us, of which memory would need
+//     37 and the products, at a large product's rate, 48; busy 45% and 26%.  The
+//     conversions of keys and values are shared by a wave's tiles, the exponentials
+//     are not.  Trees of heads of 256 in fp16, with a cap: 61% and 36%.
+//   one window: 16.5 us of dependent loads (lengths, queries, pages, tokens, parts),
 //     5 of them the second launch.
 #include "sv_kv.hpp"
 
@@ -32,7 +36,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 // Blocks of the join, each of which looks through all items: 256, 512, 1024, 2048
-// take 16.0, 16.5, 18.2, 21.1 us in all for one window, 119, 114, 118, 120 for 32
+// take 15.9, 16.5, 17.8, 19.8 us in all for one window, 124, 119, 121, 125 for 32
 // chains of 17 nodes x 32 heads.
 constexpr int kJoinBlocks = 512, kJoinThreads = 256;
 
@@ -106,7 +110,7 @@ __device__ __forceinline__ int64_t divide(int64_t x, int64_t y) {
 // bf16 product's by 2^-20.5), so that beside one large channel a score is a guess.
 // What bf16 costs: conversions in each wave, and for fp16 two products of 16 bits
 // for three of 8 -- 2 trees of 64 nodes x 16 heads of 256 in fp16 over 65536 tokens
-// 264 us, 233 with 4 and 8 bits; 32 chains of 17 nodes 119 and 117; single tokens
+// 265 us, 231 with 4 and 8 bits; 32 chains of 17 nodes 119 and 117; single tokens
 // and windows the same.
 // ---------------------------------------------------------------------------
 template <int D>
@@ -194,7 +198,7 @@ __device__ __forceinline__ u32x4 key_step(const Tokens<D>& t, int u, int s) {
 
 // Scores of both tiles' tokens for TT tiles of rows.  `words(r, part, s)`: a
 // query's values.  AHEAD: they are asked for a product ahead (where they lie in LDS
-// and registers are left for them).
+// and registers are left for them: trees of heads of 256 in fp16 274 to 265 us).
 template <int D, int PARTS, int TT, bool AHEAD, typename W>
 __device__ __forceinline__ void scores(const Tokens<D>& t, f32x4 (*acc)[2], const W& words) {
 #pragma unroll
@@ -535,8 +539,7 @@ __device__ __forceinline__ void finish(const AttentionParams& p, int b, int n, i
 // Waves of a SIMD that the registers leave room for: one tile of rows takes up
 // to 128 registers at D = 64, 168 at 128 and 256 at 256, three at 128 take 256.
 // Registers spilled, or one wave a SIMD, cost more than rows split over waves
-// (32 chains of 17 nodes, D = 128, three tiles a wave: 120 us with 2 waves, 195
-// with 1).
+// (32 windows of 5 nodes, D = 128, two tiles a wave: 65 us with 2 waves, 94 with 1).
 constexpr int kernel_waves(int D, int tiles, int split) {
   return split > 1 || tiles > 1 ? 2 : D == 64 ? 4 : D == 128 ? 3 : 2;
 }
@@ -832,7 +835,7 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
         // 0.0019 to 0.0023 of 64 bits' in all, the rounding of the results alone
         // 0.0017), in fp16 to two parts, 16 bits, beside results of 11.  Two parts
         // for bf16 too give 0.0017 and take 144 us instead of 119 for 32 chains of
-        // 17 nodes x 32 heads, 380 instead of 313 for 1024 nodes, 77 instead of 70
+        // 17 nodes x 32 heads, 377 instead of 313 for 1024 nodes, 77 instead of 73
         // for single tokens.
         u32x4 pr[TT][kProbs];
 #pragma unroll
@@ -851,7 +854,8 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
         }
         // The second products ahead of the other wave's vector instructions, where
         // there are many rows: 2 trees of 64 nodes x 16 heads of 256 in fp16 over 65536
-        // tokens 247 to 229 us, 1024 nodes x 32 heads 317 to 308; single tokens, bound by loads, lose by it (67 to 70)
+        // tokens 278 to 265 us, 1024 nodes x 32 heads 322 to 313; single tokens gain
+        // nothing
         constexpr bool kAhead = SPLIT * TILES > 1;
         if constexpr (kAhead) __builtin_amdgcn_s_setprio(1);
         const u32x4 ones = {0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u};
@@ -938,10 +942,9 @@ __global__ __launch_bounds__((Form<TILES, SPLIT>::kThreads), (kernel_waves(D, TI
           if (++u >= v1) break;
         }
       }
-
     };
-    // The last rows' waves may have a tile less to do (5 tiles in 2 x 3: 120 us,
-    // with three in both 142).
+    // The last rows' waves may have a tile less to do (5 tiles in 2 x 3: 119 us,
+    // with three in both 131).
     const auto first_tile = [&](int wave) { return wave / kStreams * TILES; };
     const bool fewer = SPLIT > 1 && TILES > 1 &&
                        arguments().all_tiles - sh.group * SPLIT * TILES - first_tile(uniform(thread() / kWave)) < TILES;

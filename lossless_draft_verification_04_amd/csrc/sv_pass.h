@@ -95,9 +95,9 @@ hipError_t launch_kv_attention(const AttentionParams& p, sv_dtype dt, int D, hip
 // in a wave as its registers hold (`most`: two at D = 256 would spill 180 of
 // them), more by two or four waves beside one another, which read the same
 // tokens, more still by several blocks.  Waves beside one another against blocks
-// of their own: 5 tiles of 128 values 112 against 124 us (32 chains of 17 nodes x
-// 4 heads), 16 of 256 values 241 against 280 (trees of 64 x 4, 65536 tokens), 256 of
-// 128 values 320 against 400 (1024 nodes x 4 heads).
+// of their own: 5 tiles of 128 values 119 against 127 us (32 chains of 17 nodes x
+// 4 heads), 16 of 256 values 265 against 278 (trees of 64 x 4, 65536 tokens), 256 of
+// 128 values as long (1024 nodes x 4 heads: 313 and 309).
 struct AttentionForm {
   int tiles, split, groups, blocks;
 };

@@ -150,6 +150,9 @@ __global__ __launch_bounds__(kThreads) void rope_kernel(const RopeParams p, cons
 #pragma unroll
         for (int j = 0; j < kPairs; ++j) {
           const double turns = (double)pos * (p.freq[item * kPairs + j] * 0.15915494309189535);
+          // the rest of a turn to 32 bits, off by 2^-26 turns at most: about what sine,
+          // cosine and products of 32 bits are off by (5.1e-8 in all; 3.5e-8 with sine
+          // and cosine in 64)
           sincospif(2.0f * (float)(turns - rint(turns)), &s[j], &c[j]);
           c[j] *= p.factor;
           s[j] *= p.inverse ? -p.factor : p.factor;
