@@ -92,8 +92,8 @@ hipError_t launch_kv_commit(const KvCommitParams& p, int D, hipStream_t s);
 hipError_t launch_kv_attention(const AttentionParams& p, sv_dtype dt, int D, hipStream_t s);
 
 // How `all` tiles of 16 rows (nodes x heads of a key head) are taken: as many
-// in a wave as its registers hold (`most`: two at D = 256 would spill 180 of
-// them), more by two or four waves beside one another, which read the same
+// in a wave as its registers hold (`most`: two at D = 256 would spill 114 to 198
+// of them), more by two or four waves beside one another, which read the same
 // tokens, more still by several blocks.  Waves beside one another against blocks
 // of their own: 5 tiles of 128 values 119 against 127 us (32 chains of 17 nodes x
 // 4 heads), 16 of 256 values 265 against 278 (trees of 64 x 4, 65536 tokens), 256 of

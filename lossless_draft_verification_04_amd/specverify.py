@@ -857,7 +857,7 @@ class KvCache:
         self._ref = ctypes.byref(self._c)
 
     def layer(self, l):
-        """The cache of one layer."""
+        """The cache of one layer: a handle to keep (making one takes about as long as a small call)."""
         return KvCache(self.pool[l], self.pages, self.H, self.D, self.page_tokens)
 
     def _one(self, what):
