@@ -29,7 +29,8 @@
  * Values are SV_BF16, SV_F16 or, where said, SV_F32.  Tensors [B, N, heads, D]
  * have a unit stride along D; `stride` points to 3 host values, the strides in
  * elements of sequence, node and head.  Strides are not negative and what is
- * written must not overlap itself.
+ * written must not overlap itself; different heads of one tensor, of equal strides,
+ * do not overlap.
  */
 #ifndef SPECVERIFY_PASS_H
 #define SPECVERIFY_PASS_H

@@ -166,7 +166,10 @@ sv_status kv_move(const void* k, const int64_t* ks, const void* v, const int64_t
   bool ak, av;
   if ((st = check_tensor(k, ks, B, N, cache->H, cache->D, type_bytes(dt), true, p.st[0], &nk, &ak)) != SV_OK) return st;
   if ((st = check_tensor(v, vs, B, N, cache->H, cache->D, type_bytes(dt), true, p.st[1], &nv, &av)) != SV_OK) return st;
-  if (!write && (!ak || !av || overlap(k, nk, v, nv))) return SV_EINVAL;
+  if (!write && (!ak || !av)) return SV_EINVAL;
+  if (!write && overlap(k, nk, v, nv) &&
+      !views_apart(k, p.st[0], cache->H, v, p.st[1], cache->H, B, N, (int64_t)cache->D * type_bytes(dt)))
+    return SV_EINVAL;
   if ((st = check_space(ws, ws_bytes, kWsFixed)) != SV_OK) return st;
   // threads of a sequence, 8 values of keys each, are counted in 32 bits
   if (((int64_t)N + 6) * cache->H * cache->D / 8 > INT32_MAX - 1024) return SV_EUNSUPPORTED;
@@ -337,7 +340,8 @@ sv_status sv_kv_attention(const void* q, const int64_t* q_stride, sv_dtype dt, c
   bool aq, ao;
   if ((st = check_tensor(q, q_stride, B, N, Hq, cache->D, 2, true, p.qs, &nq, &aq)) != SV_OK) return st;
   if ((st = check_tensor(out, out_stride, B, N, Hq, cache->D, 2, true, p.os, &no, &ao)) != SV_OK) return st;
-  if (!ao || overlap(q, nq, out, no)) return SV_EINVAL;
+  if (!ao) return SV_EINVAL;
+  if (overlap(q, nq, out, no) && !views_apart(q, p.qs, Hq, out, p.os, Hq, B, N, (int64_t)cache->D * 2)) return SV_EINVAL;
   if (out_lse) {
     const int64_t nl = (int64_t)B * N * Hq * (int64_t)sizeof(float);
     if (overlap(out_lse, nl, out, no) || overlap(out_lse, nl, q, nq)) return SV_EINVAL;

@@ -476,6 +476,38 @@ def test_commit_of_paths_without_places():
     assert torch.equal(h.pool.cpu(), c.pool[0])
 
 
+@pytest.mark.parametrize("B,N", [(1, 1), (3, 1), (1, 5), (3, 5)])
+@pytest.mark.parametrize("turned", [False, True])
+def test_views_of_one_tensor(turned, B, N):
+    """Keys and values read into the heads of one tensor, and attention's results into heads beside its queries."""
+    H, G, D, P = 2, 3, 64, 16
+    c, h = filled(B, H, D, P, (40,) * B, N, seed=B + N)
+    lens = i32(*[40] * B)
+
+    def heads(n):
+        if turned:  # tokens before sequences in memory
+            return torch.full((N, B, n, D), 7.0, dtype=BF16, device=DEV).transpose(0, 1)
+        return torch.full((B, N, n, D), 7.0, dtype=BF16, device=DEV)
+
+    want = svx.sv_kv_read(h, lens, None, heads(H), heads(H))
+    x = heads(2 * H + 1)
+    svx.sv_kv_read(h, lens, None, x[:, :, :H], x[:, :, H:2 * H])
+    assert torch.equal(x[:, :, :H], want["k"]) and torch.equal(x[:, :, H:2 * H], want["v"]) and bool((x[:, :, 2 * H:] == 7).all())
+    q = queries(B, N, H * G, D, BF16, 1).to(DEV)
+    want = svx.sv_kv_attention(h, q, lens)["out"]
+    x = heads(2 * H * G + 1)
+    for at, out in ((0, H * G), (H * G + 1, 1)):
+        x.fill_(7.0)
+        x[:, :, at:at + H * G] = q
+        svx.sv_kv_attention(h, x[:, :, at:at + H * G], lens, out=x[:, :, out:out + H * G])
+        assert torch.equal(x[:, :, out:out + H * G], want) and torch.equal(x[:, :, at:at + H * G], q)
+    for a, b in ((0, 1), (H * G, 1), (0, H * G - 1)):
+        with pytest.raises(svx.SpecVerifyError):
+            svx.sv_kv_attention(h, x[:, :, a:a + H * G], lens, out=x[:, :, b:b + H * G])
+    with pytest.raises(svx.SpecVerifyError):
+        svx.sv_kv_read(h, lens, None, x[:, :, :H], x[:, :, 1:1 + H])
+
+
 def test_nothing_to_do():
     c, h = filled(3, 1, 64, 16, (5, 9, 0), 4, seed=1)
     q = queries(3, 4, 2, 64, BF16, 1).to(DEV)
